@@ -195,7 +195,9 @@ const char* gc_phase_name(int phase) {
       "ef_hist", "collect", "write", "ef_add", "quant_fused", "quant_stats",
       "quant_combine", "quant_apply", "dequant", "psgd_mq", "psgd_mtp", "psgd_resid",
       "refine", "bk_hist", "bk_collect", "bk_refine", "bk_write", "bk_quant", "agg_bounds",
-      "agg_accumulate", "randk_mark", "randk_write", "bk_diag", "bk_flush", "psgd_thin"};
+      "agg_accumulate", "randk_mark", "randk_write", "bk_diag", "bk_flush", "psgd_thin",
+      "ckpt_save", "ckpt_restore", "act_forward", "act_backward", "norm_forward",
+      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join"};
   return (phase >= 0 && phase < GC_PHASE_COUNT) ? names[phase] : "?";
 }
 
@@ -252,6 +254,7 @@ gc_status gc_ctx_destroy(gc_ctx* ctx) {
   free_timing(ctx);
   if (ctx->ws_base) cudaFree(ctx->ws_base);
   if (ctx->psgd_base) cudaFree(ctx->psgd_base);
+  if (ctx->scratch) cudaFree(ctx->scratch);
   gc::free_buckets(ctx);
   free(ctx);
   return st;
@@ -608,6 +611,217 @@ gc_status gc_ef_randk(gc_ctx* ctx, const float* grad, float* err, int64_t n, flo
   if (!guard.ok) return GC_ERR_CUDA;
   return gc::launch_ef_randk(ctx, grad, err, n, p, seed, step, idx_out, val_out, capacity,
                              count_out);
+}
+
+namespace {
+constexpr int64_t kMaxCols = (int64_t)1 << 30;
+
+bool valid_dtype(int dtype) { return dtype == GC_F32 || dtype == GC_BF16 || dtype == GC_F16; }
+
+bool valid_sizes(int64_t rows, int64_t cols) {
+  return rows >= 0 && rows <= INT32_MAX && cols >= 0 && cols <= kMaxCols;
+}
+
+// Sizes, type and stride of a [rows, cols] matrix.  The stride bound keeps
+// every byte offset within 63 bits.
+gc_status check_matrix(int64_t rows, int64_t cols, int dtype, int64_t ld) {
+  if (!valid_sizes(rows, cols) || !valid_dtype(dtype)) return GC_ERR_INVALID_ARG;
+  if (ld < cols || ld > ((int64_t)1 << 30)) return GC_ERR_INVALID_ARG;
+  return GC_OK;
+}
+
+// A checkpoint: both buffers, or neither where it is optional.
+gc_status check_ckpt(const void* codes, const void* scales, bool used, bool optional) {
+  if (optional && !codes && !scales) return GC_OK;
+  if (!codes != !scales) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_buf(codes, used));
+  return check_buf(scales, used);
+}
+}  // namespace
+
+int64_t gc_ckpt_codes_bytes(int64_t rows, int64_t cols) {
+  if (!valid_sizes(rows, cols)) return -1;
+  return rows * round_up(cols, 32);
+}
+
+int64_t gc_ckpt_scales_bytes(int64_t rows, int64_t cols) {
+  if (!valid_sizes(rows, cols)) return -1;
+  return rows * round_up(ceil_div(cols, 32), 16);
+}
+
+gc_status gc_ctx_reserve_scratch(gc_ctx* ctx, int64_t bytes) {
+  if (!ctx || bytes < 0) return GC_ERR_INVALID_ARG;
+  if (bytes <= ctx->scratch_bytes) return GC_OK;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  if (cudaStreamSynchronize(ctx->stream) != cudaSuccess) return GC_ERR_CUDA;
+  if (ctx->scratch) cudaFree(ctx->scratch);
+  ctx->scratch = nullptr;
+  ctx->scratch_bytes = 0;
+  void* base = nullptr;
+  const cudaError_t e = cudaMalloc(&base, (size_t)bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? GC_ERR_NO_MEMORY : GC_ERR_CUDA;
+  }
+  ctx->scratch = base;
+  ctx->scratch_bytes = bytes;
+  return GC_OK;
+}
+
+gc_status gc_ckpt_save(gc_ctx* ctx, const void* x, int dtype, int64_t rows, int64_t cols,
+                       int64_t ldx, uint8_t* codes, uint8_t* scales) {
+  if (!ctx) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, ldx));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(x, used));
+  GC_TRY(check_ckpt(codes, scales, used, false));
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_ckpt_save(ctx, x, dtype, rows, cols, ldx, codes, scales);
+}
+
+gc_status gc_ckpt_restore(gc_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int dtype,
+                          int64_t rows, int64_t cols, void* x_out, int64_t ldx) {
+  if (!ctx) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, ldx));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(x_out, used));
+  GC_TRY(check_ckpt(codes, scales, used, false));
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_ckpt_restore(ctx, codes, scales, dtype, rows, cols, x_out, ldx);
+}
+
+gc_status gc_act_forward(gc_ctx* ctx, int act, const void* x, int64_t ldx, const void* gate,
+                         int64_t ldgate, int dtype, int64_t rows, int64_t cols, void* y,
+                         int64_t ldy, uint8_t* codes, uint8_t* scales, uint8_t* gate_codes,
+                         uint8_t* gate_scales) {
+  if (!ctx || (act != GC_GELU && act != GC_SILU)) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, ldx));
+  GC_TRY(check_matrix(rows, cols, dtype, ldy));
+  if (gate) GC_TRY(check_matrix(rows, cols, dtype, ldgate));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(x, used));
+  if (gate) GC_TRY(check_buf(gate, used));
+  GC_TRY(check_buf(y, used));
+  GC_TRY(check_ckpt(codes, scales, used, true));
+  // the gate's checkpoint comes with the input's, or not at all
+  if (gate && codes)
+    GC_TRY(check_ckpt(gate_codes, gate_scales, used, false));
+  else if (gate_codes || gate_scales)
+    return GC_ERR_INVALID_ARG;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_act_forward(ctx, act, x, ldx, gate, ldgate, dtype, rows, cols, y, ldy, codes,
+                                scales, gate_codes, gate_scales);
+}
+
+gc_status gc_act_backward(gc_ctx* ctx, int act, const void* dy, int64_t lddy,
+                          const uint8_t* codes, const uint8_t* scales, const uint8_t* gate_codes,
+                          const uint8_t* gate_scales, int dtype, int64_t rows, int64_t cols,
+                          void* dx, int64_t lddx, void* dgate, int64_t lddgate) {
+  if (!ctx || (act != GC_GELU && act != GC_SILU)) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, lddy));
+  GC_TRY(check_matrix(rows, cols, dtype, lddx));
+  if (dgate) GC_TRY(check_matrix(rows, cols, dtype, lddgate));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(dy, used));
+  GC_TRY(check_buf(dx, used));
+  if (dgate) GC_TRY(check_buf(dgate, used));
+  GC_TRY(check_ckpt(codes, scales, used, false));
+  // dgate and the gate's checkpoint come together
+  if (dgate)
+    GC_TRY(check_ckpt(gate_codes, gate_scales, used, false));
+  else if (gate_codes || gate_scales)
+    return GC_ERR_INVALID_ARG;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_act_backward(ctx, act, dy, lddy, codes, scales, gate_codes, gate_scales, dtype,
+                                 rows, cols, dx, lddx, dgate, lddgate);
+}
+
+gc_status gc_layernorm_forward(gc_ctx* ctx, const void* x, int64_t ldx, int dtype, int64_t rows,
+                               int64_t cols, const void* gamma, const void* beta, int ptype,
+                               float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                               uint8_t* codes, uint8_t* scales) {
+  if (!ctx || !valid_dtype(ptype) || !(eps >= 0.0f)) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, ldx));
+  GC_TRY(check_matrix(rows, cols, dtype, ldy));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(x, used));
+  GC_TRY(check_buf(y, used));
+  GC_TRY(check_buf(mean, used));
+  GC_TRY(check_buf(rstd, used));
+  if (gamma) GC_TRY(check_buf(gamma, used));
+  if (beta) GC_TRY(check_buf(beta, used));
+  GC_TRY(check_ckpt(codes, scales, used, true));
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_norm_forward(ctx, x, dtype, rows, cols, ldx, gamma, beta, ptype, eps, y, ldy,
+                                 mean, rstd, codes, scales);
+}
+
+int64_t gc_layernorm_scratch_bytes(int64_t rows, int64_t cols) {
+  if (!valid_sizes(rows, cols)) return -1;
+  return gc::norm_scratch_bytes(rows, cols);
+}
+
+gc_status gc_layernorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* x,
+                                int64_t ldx, const uint8_t* codes, const uint8_t* scales,
+                                int dtype, int64_t rows, int64_t cols, const void* gamma,
+                                int ptype, const float* mean, const float* rstd, void* dx,
+                                int64_t lddx, float* dgamma, float* dbeta, int accumulate) {
+  if (!ctx || !valid_dtype(ptype)) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, lddy));
+  GC_TRY(check_matrix(rows, cols, dtype, lddx));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(dy, used));
+  GC_TRY(check_buf(dx, used));
+  GC_TRY(check_buf(mean, used));
+  GC_TRY(check_buf(rstd, used));
+  if (gamma) GC_TRY(check_buf(gamma, used));
+  // the input, or its checkpoint
+  if (x) {
+    if (codes || scales) return GC_ERR_INVALID_ARG;
+    GC_TRY(check_matrix(rows, cols, dtype, ldx));
+    GC_TRY(check_buf(x, used));
+  } else {
+    GC_TRY(check_ckpt(codes, scales, used, false));
+  }
+  if (dgamma) GC_TRY(check_buf(dgamma, cols > 0));
+  if (dbeta) GC_TRY(check_buf(dbeta, cols > 0));
+  if ((dgamma || dbeta) && used && ctx->scratch_bytes < gc::norm_scratch_bytes(rows, cols))
+    return GC_ERR_WORKSPACE;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_norm_backward(ctx, dy, lddy, x, ldx, codes, scales, dtype, rows, cols, gamma,
+                                  ptype, mean, rstd, dx, lddx, dgamma, dbeta, accumulate,
+                                  static_cast<float*>(ctx->scratch));
+}
+
+int64_t gc_linear_wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype) {
+  if (!valid_sizes(rows, out) || !valid_sizes(rows, in) || !valid_dtype(dtype)) return -1;
+  return gc::wgrad_scratch_bytes(rows, out, in, dtype);
+}
+
+gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
+                          const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t out,
+                          int64_t in, float* dw, int64_t lddw, float* db, int accumulate) {
+  if (!ctx) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, out, dtype, lddy));
+  GC_TRY(check_matrix(out, in, GC_F32, lddw));
+  const bool used = rows > 0 && out > 0 && in > 0;
+  GC_TRY(check_buf(dy, rows > 0 && out > 0));
+  GC_TRY(check_ckpt(codes, scales, used, false));
+  GC_TRY(check_buf(dw, out > 0 && in > 0));
+  if (db) GC_TRY(check_buf(db, out > 0));
+  if (used && ctx->scratch_bytes < gc::wgrad_scratch_bytes(rows, out, in, dtype))
+    return GC_ERR_WORKSPACE;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_wgrad(ctx, dy, dtype, lddy, codes, scales, rows, out, in, dw, lddw, db,
+                          accumulate, ctx->scratch);
 }
 
 }  // extern "C"

@@ -196,6 +196,9 @@ struct gc_ctx {
   gc::BucketWs bk;
   int bk_defer;             // deferred residual write-back of the bucketed hybrid
   float* bk_pending;        // error buffer whose kept-entry residuals are pending
+  // scratch of the backward-pass calls (gc_ctx_reserve_scratch)
+  void* scratch;
+  int64_t scratch_bytes;
 };
 
 namespace gc {
@@ -555,6 +558,38 @@ int64_t aggregate_scratch_ints(int W, int64_t n);
 int aggregate_max_ranks();
 // Opts the aggregation kernels into their shared memory (once per device).
 gc_status prepare_aggregate_kernels();
+
+// 8-bit activation checkpoints and the activation functions (gc_ckpt.cu).
+gc_status launch_ckpt_save(gc_ctx* ctx, const void* x, int dtype, int64_t rows, int64_t cols,
+                           int64_t ldx, uint8_t* codes, uint8_t* scales);
+gc_status launch_ckpt_restore(gc_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int dtype,
+                              int64_t rows, int64_t cols, void* x_out, int64_t ldx);
+gc_status launch_act_forward(gc_ctx* ctx, int kind, const void* x, int64_t ldx, const void* gate,
+                             int64_t ldgate, int dtype, int64_t rows, int64_t cols, void* y,
+                             int64_t ldy, uint8_t* codes, uint8_t* scales, uint8_t* gate_codes,
+                             uint8_t* gate_scales);
+gc_status launch_act_backward(gc_ctx* ctx, int kind, const void* dy, int64_t lddy,
+                              const uint8_t* codes, const uint8_t* scales,
+                              const uint8_t* gate_codes, const uint8_t* gate_scales, int dtype,
+                              int64_t rows, int64_t cols, void* dx, int64_t lddx, void* dgate,
+                              int64_t lddgate);
+// Layer norm (gc_norm.cu); `part` is the scratch of the column sums.
+constexpr int kNormMaxParts = 304;  // partial rows of the column sums
+int64_t norm_scratch_bytes(int64_t rows, int64_t cols);
+gc_status launch_norm_forward(gc_ctx* ctx, const void* x, int dtype, int64_t rows, int64_t cols,
+                              int64_t ldx, const void* gamma, const void* beta, int ptype,
+                              float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                              uint8_t* codes, uint8_t* scales);
+gc_status launch_norm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* x,
+                               int64_t ldx, const uint8_t* codes, const uint8_t* scales, int dtype,
+                               int64_t rows, int64_t cols, const void* gamma, int ptype,
+                               const float* mean, const float* rstd, void* dx, int64_t lddx,
+                               float* dgamma, float* dbeta, int accumulate, float* part);
+// Weight gradient of a linear layer (gc_wgrad.cu).
+int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype);
+gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, const uint8_t* codes,
+                       const uint8_t* scales, int64_t rows, int64_t out, int64_t in, float* dw,
+                       int64_t lddw, float* db, int accumulate, void* scratch);
 
 // Builds the device plan of nb buckets (synchronous; frees the previous).
 gc_status plan_buckets(gc_ctx* ctx, int nb, const int64_t* bucket_n, const int64_t* bucket_k);

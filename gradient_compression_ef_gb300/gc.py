@@ -20,7 +20,12 @@ NEAREST_EVEN, STOCHASTIC = 0, 1
 MODES = {"minmax": MINMAX, "qsgd": QSGD, "tern": TERN, "log": LOG}
 ROUNDINGS = {"nearest_even": NEAREST_EVEN, "stochastic": STOCHASTIC}
 
-PHASE_COUNT = 25
+F32, BF16, F16 = 0, 1, 2
+DTYPES = {"f32": F32, "bf16": BF16, "f16": F16}
+GELU, SILU = 0, 1
+ACTS = {"gelu": GELU, "silu": SILU}
+
+PHASE_COUNT = 35
 
 OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE = -1, -2, -3, -4
@@ -71,6 +76,23 @@ SIGNATURES = [
                            _vp]),
     ("gc_topk_aggregate", _int, [_vp, _int, _i64, _vp, _vp, _i64, _vp]),
     ("gc_topk_quant_aggregate", _int, [_vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp]),
+    ("gc_ckpt_codes_bytes", _i64, [_i64, _i64]),
+    ("gc_ckpt_scales_bytes", _i64, [_i64, _i64]),
+    ("gc_ctx_reserve_scratch", _int, [_vp, _i64]),
+    ("gc_ckpt_save", _int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp]),
+    ("gc_ckpt_restore", _int, [_vp, _vp, _vp, _int, _i64, _i64, _vp, _i64]),
+    ("gc_act_forward", _int, [_vp, _int, _vp, _i64, _vp, _i64, _int, _i64, _i64, _vp, _i64,
+                              _vp, _vp, _vp, _vp]),
+    ("gc_act_backward", _int, [_vp, _int, _vp, _i64, _vp, _vp, _vp, _vp, _int, _i64, _i64, _vp,
+                               _i64, _vp, _i64]),
+    ("gc_layernorm_forward", _int, [_vp, _vp, _i64, _int, _i64, _i64, _vp, _vp, _int,
+                                    ctypes.c_float, _vp, _i64, _vp, _vp, _vp, _vp]),
+    ("gc_layernorm_scratch_bytes", _i64, [_i64, _i64]),
+    ("gc_layernorm_backward", _int, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _int, _i64, _i64, _vp,
+                                     _int, _vp, _vp, _vp, _i64, _vp, _vp, _int]),
+    ("gc_linear_wgrad_scratch_bytes", _i64, [_i64, _i64, _i64, _int]),
+    ("gc_linear_wgrad", _int, [_vp, _vp, _int, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
+                               _int]),
 ]
 
 # largest n of gc_ef_topk_noalloc (GC_NOALLOC_MAX_N in include/gc.h)
@@ -160,6 +182,11 @@ class Context:
     def reserve_powersgd(self, max_m, max_n, max_r):
         _check(lib.gc_ctx_reserve_powersgd(self.handle, max_m, max_n, max_r),
                "gc_ctx_reserve_powersgd")
+
+    def reserve_scratch(self, nbytes):
+        """At least nbytes of scratch for layernorm_backward and linear_wgrad
+        (their *_scratch_bytes); synchronises when it grows."""
+        _check(lib.gc_ctx_reserve_scratch(self.handle, nbytes), "gc_ctx_reserve_scratch")
 
     def check(self):
         _check(lib.gc_ctx_check(self.handle), "gc_ctx_check")
@@ -347,3 +374,171 @@ def ef_randk(ctx, grad, err, p, seed, step, idx_out, val_out, count_out, n=None,
     _check(lib.gc_ef_randk(ctx.handle, _ptr(grad), _ptr(err), n, float(p), seed, step,
                            _ptr(idx_out), _ptr(val_out), capacity, _ptr(count_out)),
            "gc_ef_randk")
+
+
+# --- the backward pass that fills the flat gradient: 8-bit activation
+# checkpoints, activation functions, layer norm, linear weight gradients ----
+
+def _dtype(t):
+    """GC_* type of a torch tensor, a torch dtype or a name."""
+    if isinstance(t, str):
+        return DTYPES[t]
+    name = str(getattr(t, "dtype", t))
+    try:
+        return _TORCH_DTYPES[name]
+    except KeyError:
+        raise TypeError("unsupported element type %s (float32, bfloat16 or float16)" % name)
+
+
+_TORCH_DTYPES = {"torch.float32": F32, "torch.bfloat16": BF16, "torch.float16": F16}
+
+
+def _matrix(t, what, like=None):
+    """(rows, cols, row stride) of a 2-D tensor with contiguous columns,
+    which must have the shape and type of `like` if given."""
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D, got %d-D" % (what, t.dim()))
+    rows, cols = t.shape
+    sr, sc = t.stride()
+    if cols > 1 and sc != 1:
+        raise ValueError("%s: columns must be contiguous (stride %d)" % (what, sc))
+    if rows <= 1:
+        sr = cols
+    if sr < cols:
+        raise ValueError("%s: overlapping rows (stride %d, %d columns)" % (what, sr, cols))
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError("%s: %s %s, expected %s %s" % (
+            what, tuple(t.shape), t.dtype, tuple(like.shape), like.dtype))
+    return rows, cols, sr
+
+
+def _flat(t, n, what, name):
+    """A contiguous tensor (or None) of at least n elements of a type."""
+    if t is None:
+        return None
+    if t.numel() < n or not t.is_contiguous() or str(t.dtype) != name:
+        raise ValueError("%s: needs %d contiguous %s" % (what, n, name))
+    return t.data_ptr()
+
+
+def _ckpt(codes, scales, rows, cols):
+    return (_flat(codes, rows * (-(-cols // 32) * 32), "codes", "torch.uint8"),
+            _flat(scales, rows * (-(-cols // 512) * 16), "scales", "torch.uint8"))
+
+
+def _param(t, cols, what):
+    if t is None:
+        return None
+    if t.numel() != cols or not t.is_contiguous():
+        raise ValueError("%s: needs %d contiguous values" % (what, cols))
+    return t.data_ptr()
+
+
+def ckpt_codes_bytes(rows, cols):
+    return int(lib.gc_ckpt_codes_bytes(rows, cols))
+
+
+def ckpt_scales_bytes(rows, cols):
+    return int(lib.gc_ckpt_scales_bytes(rows, cols))
+
+
+def ckpt_save(ctx, x, codes, scales):
+    """Saves x [rows, cols] as an 8-bit checkpoint."""
+    rows, cols, ldx = _matrix(x, "x")
+    c, s = _ckpt(codes, scales, rows, cols)
+    _check(lib.gc_ckpt_save(ctx.handle, x.data_ptr(), _dtype(x), rows, cols, ldx, c, s),
+           "gc_ckpt_save")
+
+
+def ckpt_restore(ctx, codes, scales, x_out):
+    """Writes the values a checkpoint stands for into x_out [rows, cols]."""
+    rows, cols, ldx = _matrix(x_out, "x_out")
+    c, s = _ckpt(codes, scales, rows, cols)
+    _check(lib.gc_ckpt_restore(ctx.handle, c, s, _dtype(x_out), rows, cols, x_out.data_ptr(),
+                               ldx), "gc_ckpt_restore")
+
+
+def act_forward(ctx, act, x, y, codes=None, scales=None, gate=None, gate_codes=None,
+                gate_scales=None):
+    """y = act(x) [* gate]; codes / scales receive the checkpoint of x (and
+    gate_codes / gate_scales that of gate)."""
+    rows, cols, ldx = _matrix(x, "x")
+    _, _, ldy = _matrix(y, "y", x)
+    ldg = _matrix(gate, "gate", x)[2] if gate is not None else 0
+    c, s = _ckpt(codes, scales, rows, cols)
+    gc_, gs = _ckpt(gate_codes, gate_scales, rows, cols)
+    _check(lib.gc_act_forward(ctx.handle, ACTS[act] if isinstance(act, str) else int(act),
+                              x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg,
+                              _dtype(x), rows, cols, y.data_ptr(), ldy, c, s, gc_, gs),
+           "gc_act_forward")
+
+
+def act_backward(ctx, act, dy, dx, codes, scales, dgate=None, gate_codes=None, gate_scales=None):
+    """dx (and dgate) of act_forward from its checkpoints."""
+    rows, cols, lddy = _matrix(dy, "dy")
+    _, _, lddx = _matrix(dx, "dx", dy)
+    ldg = _matrix(dgate, "dgate", dy)[2] if dgate is not None else 0
+    c, s = _ckpt(codes, scales, rows, cols)
+    gc_, gs = _ckpt(gate_codes, gate_scales, rows, cols)
+    _check(lib.gc_act_backward(ctx.handle, ACTS[act] if isinstance(act, str) else int(act),
+                               dy.data_ptr(), lddy, c, s, gc_, gs, _dtype(dy), rows, cols,
+                               dx.data_ptr(), lddx, None if dgate is None else dgate.data_ptr(),
+                               ldg), "gc_act_backward")
+
+
+def layernorm_scratch_bytes(rows, cols):
+    return int(lib.gc_layernorm_scratch_bytes(rows, cols))
+
+
+def layernorm_forward(ctx, x, gamma, beta, eps, y, mean, rstd, codes=None, scales=None):
+    """Layer norm over the columns; gamma / beta may be None; codes / scales
+    receive the checkpoint of x."""
+    rows, cols, ldx = _matrix(x, "x")
+    _, _, ldy = _matrix(y, "y", x)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta differ in type")
+    p = gamma if gamma is not None else beta
+    c, s = _ckpt(codes, scales, rows, cols)
+    _check(lib.gc_layernorm_forward(
+        ctx.handle, x.data_ptr(), ldx, _dtype(x), rows, cols, _param(gamma, cols, "gamma"),
+        _param(beta, cols, "beta"), F32 if p is None else _dtype(p), eps, y.data_ptr(), ldy,
+        _flat(mean, rows, "mean", "torch.float32"), _flat(rstd, rows, "rstd", "torch.float32"),
+        c, s), "gc_layernorm_forward")
+
+
+def layernorm_backward(ctx, dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, codes=None,
+                       scales=None, accumulate=False):
+    """Layer norm backward from x, or (x None) from its checkpoint; dgamma /
+    dbeta: fp32 tensors of cols elements (slices of the flat gradient), or
+    None."""
+    rows, cols, lddy = _matrix(dy, "dy")
+    _, _, lddx = _matrix(dx, "dx", dy)
+    ldx = _matrix(x, "x", dy)[2] if x is not None else 0
+    c, s = _ckpt(codes, scales, rows, cols)
+    _check(lib.gc_layernorm_backward(
+        ctx.handle, dy.data_ptr(), lddy, None if x is None else x.data_ptr(), ldx, c, s,
+        _dtype(dy), rows, cols, _param(gamma, cols, "gamma"),
+        F32 if gamma is None else _dtype(gamma), _flat(mean, rows, "mean", "torch.float32"),
+        _flat(rstd, rows, "rstd", "torch.float32"), dx.data_ptr(), lddx,
+        _flat(dgamma, cols, "dgamma", "torch.float32"),
+        _flat(dbeta, cols, "dbeta", "torch.float32"), 1 if accumulate else 0),
+        "gc_layernorm_backward")
+
+
+def linear_wgrad_scratch_bytes(rows, out_features, in_features, dtype):
+    return int(lib.gc_linear_wgrad_scratch_bytes(rows, out_features, in_features, _dtype(dtype)))
+
+
+def linear_wgrad(ctx, dy, codes, scales, dw, db=None, accumulate=False):
+    """dw [out, in] (and db [out]) of a linear layer, fp32, from dy
+    [rows, out] and the checkpoint of its input [rows, in]."""
+    rows, out, lddy = _matrix(dy, "dy")
+    wo, in_features, lddw = _matrix(dw, "dw")
+    if wo != out or str(dw.dtype) != "torch.float32":
+        raise ValueError("dw: %s %s, expected fp32 with %d rows" % (tuple(dw.shape), dw.dtype,
+                                                                   out))
+    c, s = _ckpt(codes, scales, rows, in_features)
+    _check(lib.gc_linear_wgrad(ctx.handle, dy.data_ptr(), _dtype(dy), lddy, c, s, rows, out,
+                               in_features, dw.data_ptr(), lddw,
+                               _flat(db, out, "db", "torch.float32"), 1 if accumulate else 0),
+           "gc_linear_wgrad")

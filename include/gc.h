@@ -26,7 +26,8 @@
  *  - n <= 2^31 - 1 (indices are int32) and, for calls that use the context's
  *    scratch (Top-K, hybrid, quantisation with groups that do not fit the
  *    single-pass kernel), n <= the context's max_n (GC_ERR_WORKSPACE).
- *  - Finite inputs are a precondition.  Squares and ranges must not
+ *  - Finite inputs are a precondition (except where a call's comment says
+ *    otherwise).  Squares and ranges must not
  *    overflow binary32 (|x| < 1.8e19 for QSGD).
  *  - Arithmetic is IEEE-754 binary32 with one round-to-nearest-even per
  *    operation and no fused multiply-add, so results are bit-identical to a
@@ -90,6 +91,12 @@ typedef enum gc_rounding {
   GC_NEAREST_EVEN = 0, /* round half to even */
   GC_STOCHASTIC = 1    /* unbiased, Philox-4x32-10 keyed by (seed, step, i) */
 } gc_rounding;
+
+/* Element type of an activation or of its gradient. */
+typedef enum gc_dtype { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;
+
+/* Activation function: x Phi(x) (exact GELU), or x / (1 + exp(-x)). */
+typedef enum gc_act { GC_GELU = 0, GC_SILU = 1 } gc_act;
 
 typedef struct gc_ctx gc_ctx;
 
@@ -160,7 +167,17 @@ typedef enum gc_phase {
   GC_PHASE_BK_DIAG = 22,     /* bucketed: per-bucket diagnostics */
   GC_PHASE_BK_FLUSH = 23,    /* bucketed: pending kept-entry residuals into e */
   GC_PHASE_PSGD_THIN = 24,   /* PowerSGD: Q images, the final reduction of Q' */
-  GC_PHASE_COUNT = 25
+  GC_PHASE_CKPT_SAVE = 25,   /* activation -> 8-bit checkpoint */
+  GC_PHASE_CKPT_RESTORE = 26,
+  GC_PHASE_ACT_FORWARD = 27, /* activation function, inputs saved in 8 bits */
+  GC_PHASE_ACT_BACKWARD = 28,
+  GC_PHASE_NORM_FORWARD = 29,/* layer norm */
+  GC_PHASE_NORM_BACKWARD = 30,
+  GC_PHASE_NORM_REDUCE = 31, /* layer norm: column sums of the blocks' partials */
+  GC_PHASE_WGRAD = 32,       /* linear layer: dw from dy and the checkpoint */
+  GC_PHASE_WGRAD_SPLIT = 33, /* linear layer: dy as bf16 planes */
+  GC_PHASE_WGRAD_JOIN = 34,  /* linear layer: sum of the token ranges' partials */
+  GC_PHASE_COUNT = 35
 } gc_phase;
 
 /* Name of a phase ("ef_hist", ...); "?" when out of range. */
@@ -546,6 +563,129 @@ GC_API gc_status gc_ctx_set_deferred_residual(gc_ctx* ctx, int on);
  * none are pending.
  */
 GC_API gc_status gc_bucket_flush(gc_ctx* ctx);
+
+/*
+ * The backward pass that fills the flat gradient.
+ * The bucketed calls compress a gradient "before it leaves GPU memory"
+ * ("gradient-compression-quantization-sparsification" 3.2); these calls
+ * produce it: activations are kept in 8 bits between the forward and the
+ * backward pass, and the backward calls read those checkpoints and write the
+ * parameters' gradients, in fp32, at their places of the flat gradient
+ * (dw, db, dgamma and dbeta may point anywhere into it at a 16-byte
+ * boundary; accumulate != 0 adds to what is there, for gradient
+ * accumulation over micro-batches).
+ *
+ * Matrices are [rows, cols] of one element type (gc_dtype), columns
+ * contiguous, with a row stride ld >= cols in elements; rows need no
+ * alignment (rows that start on 16-byte boundaries run faster).  Unlike the
+ * compressing calls, infinities and NaN are allowed and carry through: a
+ * loss-scaling step must see them.  Products and sums are fp32 (fused
+ * multiply-adds allowed), outputs are rounded once to their type, and every
+ * sum is added in an order that depends on sizes alone, so equal inputs on
+ * one GPU give equal bits.  rows <= 2^31 - 1, cols <= 2^30.
+ *
+ * Checkpoint format: groups of 32 consecutive columns of a row (the last may
+ * be partial) share one scale byte B: the biased binary32 exponent of the
+ * group's largest magnitude plus one, or 0 when that magnitude is below
+ * 2^-120 (every code is then 0), or 255 when it is 2^127 or more, infinite
+ * or NaN (the whole group then restores as NaN).  An element is one byte,
+ * sign << 7 | m with m = min(127, round_half_even(|x| * 2^(134 - B))) and
+ * sign 0 when m = 0, and stands for +-m * 2^(B - 134).  The step is a power
+ * of two: restored values are exact in fp32, in bf16 and (from fp16 inputs)
+ * in fp16, and off by at most half a step, max / 128 (a whole step where m
+ * was clamped).  Row r's codes start at r * round_up(cols, 32) bytes, its
+ * scale bytes at r * round_up(ceil(cols / 32), 16); codes past cols within
+ * the last group are 0.
+ */
+
+/* Bytes of a [rows, cols] checkpoint's codes / scale bytes; -1 for invalid
+ * arguments. */
+GC_API int64_t gc_ckpt_codes_bytes(int64_t rows, int64_t cols);
+GC_API int64_t gc_ckpt_scales_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Reserves (or grows to) `bytes` of scratch for the calls below that state
+ * one; synchronises the stream when it grows, so not during capture.
+ */
+GC_API gc_status gc_ctx_reserve_scratch(gc_ctx* ctx, int64_t bytes);
+
+/* Saves x as a checkpoint; restores the values it stands for, rounded to
+ * dtype. */
+GC_API gc_status gc_ckpt_save(gc_ctx* ctx, const void* x, int dtype, int64_t rows, int64_t cols,
+                              int64_t ldx, uint8_t* codes, uint8_t* scales);
+GC_API gc_status gc_ckpt_restore(gc_ctx* ctx, const uint8_t* codes, const uint8_t* scales,
+                                 int dtype, int64_t rows, int64_t cols, void* x_out,
+                                 int64_t ldx);
+
+/*
+ * y = f(x), or f(x) * gate when gate is not NULL (the gated hidden layer), f
+ * being `act` (gc_act); x (and gate) are saved as checkpoints in the same
+ * pass.  codes / scales may both be NULL (no checkpoint); with a gate,
+ * gate_codes / gate_scales go with them.
+ */
+GC_API gc_status gc_act_forward(gc_ctx* ctx, int act, const void* x, int64_t ldx,
+                                const void* gate, int64_t ldgate, int dtype, int64_t rows,
+                                int64_t cols, void* y, int64_t ldy, uint8_t* codes,
+                                uint8_t* scales, uint8_t* gate_codes, uint8_t* gate_scales);
+
+/*
+ * The backward pass of gc_act_forward from its checkpoints, with x^ and
+ * gate^ the values they stand for: dx = dy * f'(x^) (times gate^, and
+ * dgate = dy * f(x^), when dgate is not NULL).
+ */
+GC_API gc_status gc_act_backward(gc_ctx* ctx, int act, const void* dy, int64_t lddy,
+                                 const uint8_t* codes, const uint8_t* scales,
+                                 const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                 int dtype, int64_t rows, int64_t cols, void* dx, int64_t lddx,
+                                 void* dgate, int64_t lddgate);
+
+/*
+ * Layer norm: per row mean = sum(x) / cols, rstd = 1 / sqrt(sum((x -
+ * mean)^2) / cols + eps), y = (x - mean) * rstd * gamma + beta.  gamma, beta:
+ * [cols] of type ptype, either may be NULL (1, 0).  mean, rstd: fp32[rows]
+ * outputs.  codes / scales: NULL, or receive the checkpoint of x.  eps >= 0.
+ */
+GC_API gc_status gc_layernorm_forward(gc_ctx* ctx, const void* x, int64_t ldx, int dtype,
+                                      int64_t rows, int64_t cols, const void* gamma,
+                                      const void* beta, int ptype, float eps, void* y,
+                                      int64_t ldy, float* mean, float* rstd, uint8_t* codes,
+                                      uint8_t* scales);
+
+/* Scratch bytes of gc_layernorm_backward; -1 for invalid arguments. */
+GC_API int64_t gc_layernorm_scratch_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Layer norm backward from x, or (x NULL) from its checkpoint: with
+ * n = (x - mean) * rstd and d = dy * gamma,
+ *   dx = rstd * (d - mean(d) - n * mean(d * n))   (means over the row),
+ *   dgamma (+)= sum over rows of dy * n,  dbeta (+)= sum over rows of dy.
+ * mean, rstd: the forward call's.  dgamma, dbeta: fp32[cols], either may be
+ * NULL.  GC_ERR_WORKSPACE when less than gc_layernorm_scratch_bytes is
+ * reserved (and dgamma or dbeta is asked for).
+ */
+GC_API gc_status gc_layernorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* x,
+                                       int64_t ldx, const uint8_t* codes, const uint8_t* scales,
+                                       int dtype, int64_t rows, int64_t cols, const void* gamma,
+                                       int ptype, const float* mean, const float* rstd, void* dx,
+                                       int64_t lddx, float* dgamma, float* dbeta,
+                                       int accumulate);
+
+/* Scratch bytes of gc_linear_wgrad; -1 for invalid arguments. */
+GC_API int64_t gc_linear_wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype);
+
+/*
+ * Weight and bias gradients of a linear layer y = x W^T + b, W [out, in],
+ * from dy [rows, out] of type dtype and the checkpoint of x [rows, in]:
+ *   dw[o, i] (+)= sum over rows t of dy[t, o] * x^[t, i],
+ *   db[o]    (+)= sum over rows t of dy[t, o].
+ * dw: fp32, row stride lddw >= in elements; db: fp32[out] or NULL.
+ * rows == 0 writes zeros (or leaves what is there, with accumulate).
+ * GC_ERR_WORKSPACE when less than gc_linear_wgrad_scratch_bytes is reserved.
+ */
+GC_API gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
+                                 const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                 int64_t out, int64_t in, float* dw, int64_t lddw, float* db,
+                                 int accumulate);
 
 /*
  * Largest n accepted by gc_ef_topk_noalloc: its scratch is a fixed device
