@@ -197,7 +197,8 @@ const char* gc_phase_name(int phase) {
       "refine", "bk_hist", "bk_collect", "bk_refine", "bk_write", "bk_quant", "agg_bounds",
       "agg_accumulate", "randk_mark", "randk_write", "bk_diag", "bk_flush", "psgd_thin",
       "ckpt_save", "ckpt_restore", "act_forward", "act_backward", "norm_forward",
-      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join"};
+      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join",
+      "wgrad_bias"};
   return (phase >= 0 && phase < GC_PHASE_COUNT) ? names[phase] : "?";
 }
 
@@ -816,6 +817,8 @@ gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
   GC_TRY(check_ckpt(codes, scales, used, false));
   GC_TRY(check_buf(dw, out > 0 && in > 0));
   if (db) GC_TRY(check_buf(db, out > 0));
+  // tensor-map coordinates are 32 bits; fp32 takes three planes of rows
+  if (dtype == GC_F32 && rows > ((int64_t)1 << 29)) return GC_ERR_UNSUPPORTED;
   if (used && ctx->scratch_bytes < gc::wgrad_scratch_bytes(rows, out, in, dtype))
     return GC_ERR_WORKSPACE;
   DeviceGuard guard(ctx->device);

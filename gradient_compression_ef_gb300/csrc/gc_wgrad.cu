@@ -3,98 +3,839 @@
 //
 //   dw[o][i] (+)= sum over tokens t of dy[t][o] x^[t][i]
 //   db[o]    (+)= sum over tokens t of dy[t][o]
+//
+// A matrix product whose sum runs over the rows of both operands, on the
+// tensor cores (tcgen05, 16-bit operands, fp32 accumulation).  The first MMA
+// operand is x^, the second dy, so that a thread's tensor-memory lane is an
+// input column: 32 lanes store 32 consecutive floats of a row of dw, whatever
+// its stride.  Both operands have the sum's axis as their slow one in memory;
+// the descriptors say so (MN-major) and nothing is transposed.
+//
+// One persistent CTA pair per two SMs (cta_group::2) owns a tile of 256
+// inputs x 256 outputs; each CTA holds 128 input columns of x^ and 128
+// output columns of dy per block of 64 tokens.
+//   producers two threads: TMA of dy (128-byte swizzle); of codes and scale bytes
+//   converter two groups of 4 warps, every second block each: codes -> bf16
+//             (or fp16) operand in shared memory
+//   issuer    one thread of the leader CTA: the MMAs of the pair
+//   read-out  8 warps: tensor memory -> running sums in registers -> dw
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <mutex>
 
 #include "gc_act8.cuh"
+#include "gc_sm100.cuh"
 
 namespace gc {
 namespace {
 
-constexpr int kTile = 64;   // outputs and inputs of a block's tile
-constexpr int kStep = 16;   // tokens per step
+constexpr int kTile = 256;           // inputs and outputs of a pair's tile
+constexpr int kHalf = 128;           // of one CTA
+constexpr int kTok = 64;             // tokens of a block
+constexpr int kStages = 5;
+constexpr uint32_t kOpBytes = kHalf * kTok * 2;     // one CTA's operand, 16 KB
+constexpr uint32_t kCodeBytes = kHalf * kTok;       // 8 KB
+constexpr uint32_t kScaleBytes = 16 * kTok;
+constexpr int kReadWarps = 8, kConvWarps = 8;
+constexpr int kGroups = 2, kGroupWarps = kConvWarps / kGroups;
+constexpr int kDyWarp = kReadWarps + kConvWarps, kIssuerWarp = kDyWarp + 1,
+              kCodeWarp = kDyWarp + 2;
+constexpr int kThreads = 640;        // 5 warpgroups
+constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
+constexpr int kSegBlocks = 8;        // token blocks per accumulator
+constexpr int kMaxPairs = 96;
+constexpr long long kWaitCycles = 4000000000ll;  // bound on each wait: ~2 s
+
+// The work of a call: `tiles` output tiles of `blocks` token blocks.  Pair g
+// takes whole tiles g, g + pairs, ... of the first `full`; the rest, too few
+// for another round, are cut into ranges of `len` blocks of their joint
+// (tile, block) sequence, one range per pair.
+struct Plan {
+  int64_t in_tiles, out_tiles, full, rest;
+  int64_t blocks, tok_blocks;  // per tile (all planes); per plane
+  int64_t len, ranges;
+  int pairs;
+};
 
 struct WgradArgs {
-  const void* dy;
-  const uint8_t *codes, *scales;
-  float *dw, *db;
-  int64_t rows, out, in, lddy, lddw, codes_pitch, scales_pitch;
+  Plan plan;
+  float* dw;
+  float* part;        // [2 * ranges][256 outputs][256 inputs]
+  uint32_t* status;
+  int64_t out, in, lddw;
+  int64_t plane_rows;  // rows from one plane of dy to the next
   int accumulate;
 };
 
-template <int DT>
-__global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs a) {
-  using E = Elem<DT>;
-  __shared__ float sd[kStep][kTile], sx[kStep][kTile];
-  const int64_t o0 = (int64_t)blockIdx.y * kTile, i0 = (int64_t)blockIdx.x * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {}, bias[4] = {};
-  for (int64_t t0 = 0; t0 < a.rows; t0 += kStep) {
-    for (int e = threadIdx.x; e < kStep * kTile; e += 256) {
-      const int r = e / kTile, c = e % kTile;
-      const int64_t t = t0 + r;
-      float d = 0.0f, x = 0.0f;
-      if (t < a.rows && o0 + c < a.out)
-        d = E::to_float(static_cast<const typename E::T*>(a.dy)[t * a.lddy + o0 + c]);
-      if (t < a.rows && i0 + c < a.in)
-        x = decode1(a.codes[t * a.codes_pitch + i0 + c], 0,
-                    (uint32_t)a.scales[t * a.scales_pitch + (i0 + c) / kActGroup] << 23);
-      sd[r][c] = d;
-      sx[r][c] = x;
+// One piece of a pair's work: blocks [k0, k1) of a tile; slot < 0: the whole
+// tile, stored to dw.
+struct Unit {
+  int64_t tile, k0, k1, slot;
+};
+
+struct Work {
+  const Plan& p;
+  int64_t round, r0, r1;
+  int g;
+  __device__ __forceinline__ Work(const Plan& plan, int pair) : p(plan), round(0), g(pair) {
+    r0 = min(p.len * g, p.rest * p.blocks);
+    r1 = min(r0 + p.len, p.rest * p.blocks);
+  }
+  __device__ __forceinline__ bool next(Unit& u) {
+    const int64_t t = round * p.pairs + g;
+    if (t < p.full) {
+      ++round;
+      u = {t, 0, p.blocks, -1};
+      return true;
     }
-    __syncthreads();
+    if (r0 >= r1) return false;
+    const int64_t tile = r0 / p.blocks, k0 = r0 - tile * p.blocks;
+    const int64_t k1 = min(p.blocks, k0 + (r1 - r0));
+    const int64_t first = p.len * g / p.blocks;  // the range's first tile
+    u = {p.full + tile, k0, k1, (k0 == 0 && k1 == p.blocks) ? -1 : 2 * (int64_t)g + (tile - first)};
+    r0 += k1 - k0;
+    return true;
+  }
+};
+
+// Tiles in bands of 8 input tiles, outputs fastest across a band: the tiles
+// that pairs work on at the same time share their operand columns in L2.
+__host__ __device__ inline void tile_place(const Plan& p, int64_t t, int64_t& it, int64_t& ot) {
+  const int64_t per = 8 * p.out_tiles, band = t / per, r = t - band * per;
+  const int64_t w = p.in_tiles - band * 8 < 8 ? p.in_tiles - band * 8 : 8;
+  ot = r / w;
+  it = band * 8 + r - ot * w;
+}
+
+struct Smem {
+  uint32_t a, b, codes, scales;  // shared addresses
+  uint64_t *full, *empty, *cfull, *cempty, *acc_full, *acc_empty, *drain;
+  uint32_t* tmem_slot;
+};
+
+constexpr size_t kSmemBytes =
+    1024 + (size_t)kStages * (2 * kOpBytes + kCodeBytes + kScaleBytes) + 8 * (4 * kStages + 5) + 16;
+
+__device__ __forceinline__ Smem carve(unsigned char* base) {
+  Smem s;
+  const uint32_t at = (sm100::smem_u32(base) + 1023u) & ~1023u;
+  unsigned char* p = base + (at - sm100::smem_u32(base));
+  s.a = at;
+  s.b = s.a + kStages * kOpBytes;
+  s.codes = s.b + kStages * kOpBytes;
+  s.scales = s.codes + kStages * kCodeBytes;
+  uint64_t* bar =
+      reinterpret_cast<uint64_t*>(p + kStages * (2 * kOpBytes + kCodeBytes + kScaleBytes));
+  s.full = bar;
+  s.empty = s.full + kStages;
+  s.cfull = s.empty + kStages;
+  s.cempty = s.cfull + kStages;
+  s.acc_full = s.cempty + kStages;
+  s.acc_empty = s.acc_full + 2;
+  s.drain = s.acc_empty + 2;
+  s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
+  return s;
+}
+
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int by = 1) {
+    st += by;
+    if (st >= kStages) {
+      st -= kStages;
+      ph ^= 1u;
+    }
+  }
+};
+
+// A block's plane of dy and place in it, counted up without divisions.
+struct TokCursor {
+  int32_t tb, per, plane;
+  __device__ __forceinline__ TokCursor(int64_t k, int64_t tok_blocks) : per((int32_t)tok_blocks) {
+    plane = (int32_t)((uint32_t)k / (uint32_t)per);
+    tb = (int32_t)k - plane * per;
+  }
+  __device__ __forceinline__ bool next() {  // true at the end of a plane
+    if (++tb < per) return false;
+    tb = 0;
+    ++plane;
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// Two codes (the bytes that `sel` puts twice each into the halves) as bf16:
+// sign, exponent B and the seven bits m make +-(128 + m) 2^(B - 134); taking
+// +-128 2^(B - 134) off is exact.
+__device__ __forceinline__ uint32_t two_bf16(uint32_t w, uint32_t sel, uint32_t bexp) {
+  const uint32_t v = __byte_perm(w, 0u, sel);
+  const uint32_t x = (v & 0x807F807Fu) | bexp, c = (v & 0x80008000u) | bexp;
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(c));
+  return d;
+}
+
+// The same as fp16: +-(1 + m / 128) * 2 less +-2 is +-m * 2^-6; times
+// 2^(B - 128), a power of two that fp16 holds for every B an fp16 value can
+// have (104 .. 143), subnormals included.
+__device__ __forceinline__ uint32_t two_f16(uint32_t w, uint32_t sel, uint32_t scale) {
+  const uint32_t v = __byte_perm(w, 0u, sel);  // code in the high byte of each half
+  const uint32_t c = (v & 0x80008000u) | 0x40004000u;
+  const uint32_t x = ((v >> 5) & 0x03F803F8u) | c;
+  uint32_t d;
+  asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
+      : "=r"(d)
+      : "r"(x), "r"(c), "r"(scale));
+  return d;
+}
+
+// 2^(B - 128) in both halves; 0 below fp16's range, NaN above it.
+__device__ __forceinline__ uint32_t f16_scale(uint32_t b) {
+  uint32_t h;
+  if (b > 143u) h = 0x7E00u;
+  else if (b >= 114u) h = (b - 113u) << 10;
+  else if (b >= 104u) h = 1u << (b - 104u);
+  else h = 0u;
+  return h | (h << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 eight(uint32_t w0, uint32_t w1, uint32_t s) {
+  if (F16)
+    return make_uint4(two_f16(w0, 0x1404u, s), two_f16(w0, 0x3424u, s), two_f16(w1, 0x1404u, s),
+                      two_f16(w1, 0x3424u, s));
+  return make_uint4(two_bf16(w0, 0x1100u, s), two_bf16(w0, 0x3322u, s), two_bf16(w1, 0x1100u, s),
+                    two_bf16(w1, 0x3322u, s));
+}
+
+template <bool F16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap map_dy,
+                 const __grid_constant__ CUtensorMap map_codes,
+                 const __grid_constant__ CUtensorMap map_scales,
+                 const __grid_constant__ WgradArgs a) {
+  using namespace sm100;
+  extern __shared__ unsigned char wg_smem[];
+  const Smem s = carve(wg_smem);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 2 * kGroupWarps + 1);
+      mbar_init(&s.empty[i], 1);
+      mbar_init(&s.cfull[i], 1);
+      mbar_init(&s.cempty[i], kGroupWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 2 * kReadWarps);
+    }
+    mbar_init(s.drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == kIssuerWarp) {
+    tmem_alloc_pair(s.tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers exist before either CTA arrives on one
+  tc_fence_after_sync();
+  const uint32_t tmem = *s.tmem_slot;
+  bool ok = true;
+  Work work(a.plan, pair);
+  Unit u;
+
+  if (warp >= kDyWarp) {
+    reg_dec<40>();
+    // These three warps run their loops as whole warps (uniform registers);
+    // one elected lane issues.
+    if (warp == kCodeWarp) {
+      Ring ring;
+      uint32_t loads = 0;
+      while (ok && work.next(u)) {
+        int64_t it, ot;
+        tile_place(a.plan, u.tile, it, ot);
+        const int32_t x = (int32_t)(it * kTile) + (int32_t)rank * kHalf;
+        const int32_t xs = x / kActGroup & ~15;
+        TokCursor cur(u.k0, a.plan.tok_blocks);
+        for (int32_t n = (int32_t)(u.k1 - u.k0); n > 0; --n, ring.next(), cur.next()) {
+          const int st = ring.st;
+          if (loads >= kStages) {
+            if (!mbar_wait(&s.cempty[st], ring.ph ^ 1u, kWaitCycles)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+          } else {
+            ++loads;
+          }
+          if (elect_one()) {
+            // the converters read the stage through the generic proxy, TMA
+            // refills it through the asynchronous one
+            fence_proxy_async_smem();
+            const int32_t y = cur.tb * kTok;
+            mbar_arrive_expect_tx(&s.cfull[st], kCodeBytes + kScaleBytes);
+            tma_load_2d(s.codes + st * kCodeBytes, &map_codes, x, y, &s.cfull[st]);
+            tma_load_2d(s.scales + st * kScaleBytes, &map_scales, xs, y, &s.cfull[st]);
+          }
+        }
+      }
+    } else if (warp == kDyWarp) {
+      const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
+      Ring ring;
+      uint32_t loads = 0;
+      while (ok && work.next(u)) {
+        int64_t it, ot;
+        tile_place(a.plan, u.tile, it, ot);
+        const int32_t x = (int32_t)(ot * kTile) + (int32_t)rank * kHalf;
+        TokCursor cur(u.k0, a.plan.tok_blocks);
+        int32_t row0 = (int32_t)(cur.plane * a.plane_rows);
+        for (int32_t n = (int32_t)(u.k1 - u.k0); n > 0; --n, ring.next()) {
+          const int st = ring.st;
+          if (loads >= kStages) {
+            // free once the pair's MMAs read it
+            if (!mbar_wait_cluster(&s.empty[st], ring.ph ^ 1u, kWaitCycles)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+          } else {
+            ++loads;
+          }
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kOpBytes);
+            const int32_t y = row0 + cur.tb * kTok;
+            const uint32_t dst = s.b + st * kOpBytes;
+            tma_load_2d_pair(dst, &map_dy, x, y, bar0 + st * 8);
+            tma_load_2d_pair(dst + kOpBytes / 2, &map_dy, x + 64, y, bar0 + st * 8);
+          }
+          if (cur.next()) row0 += (int32_t)a.plane_rows;
+        }
+      }
+    } else if (warp == kIssuerWarp && rank == 0) {
+      constexpr uint32_t idesc = idesc_f16_mn(kTile, kTile, F16 ? 0 : 1);
+      // MN-major operands: 128-byte rows of 64 columns, 8 tokens per
+      // 1024-byte group, the two blocks of 64 columns 8 KB apart; 16 tokens
+      // (one MMA) are 2048 bytes
+      const uint64_t da = smem_desc_sw128(s.a, kOpBytes / 2, 1024);
+      const uint64_t db = smem_desc_sw128(s.b, kOpBytes / 2, 1024);
+      const uint32_t hi = (uint32_t)(da >> 32);
+      const uint32_t a0 = (uint32_t)da, b0 = (uint32_t)db;
+      Ring ring;
+      uint32_t seg = 0;
+      while (ok && work.next(u)) {
+        int in_seg = 0;
+        for (int32_t n = (int32_t)(u.k1 - u.k0); n > 0; --n, ring.next()) {
+          const int st = ring.st;
+          const uint32_t buf = seg & 1u;
+          if (in_seg == 0 && seg >= 2 &&
+              !mbar_wait_cluster(&s.acc_empty[buf], ((seg >> 1) - 1u) & 1u, kWaitCycles))
+            ok = false;
+          if (ok && !mbar_wait_cluster(&s.full[st], ring.ph, kWaitCycles)) ok = false;
+          if (__any_sync(0xffffffffu, !ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const bool last = in_seg == kSegBlocks - 1 || n == 1;
+          if (elect_one()) {
+            const uint32_t off = (uint32_t)st * (kOpBytes >> 4), d = tmem + buf * kTile;
 #pragma unroll
-    for (int r = 0; r < kStep; ++r) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const float d = sd[r][ty * 4 + p];
-        bias[p] += d;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[p][q] = fmaf(d, sx[r][tx * 4 + q], acc[p][q]);
+            for (int kk = 0; kk < kTok / 16; ++kk)
+              mma_f16_pair(d, a0 + off + kk * (2048 >> 4), b0 + off + kk * (2048 >> 4), hi, idesc,
+                           (in_seg | kk) ? 1u : 0u);
+            mma_commit_pair(&s.empty[st]);
+            if (last) mma_commit_pair(&s.acc_full[buf]);
+          }
+          ++in_seg;
+          if (last) {
+            ++seg;
+            in_seg = 0;
+          }
+        }
       }
     }
-    __syncthreads();
-  }
-  for (int p = 0; p < 4; ++p) {
-    const int64_t o = o0 + ty * 4 + p;
-    if (o >= a.out) continue;
-    for (int q = 0; q < 4; ++q) {
-      const int64_t i = i0 + tx * 4 + q;
-      if (i >= a.in) continue;
-      float* w = a.dw + o * a.lddw + i;
-      *w = a.accumulate ? *w + acc[p][q] : acc[p][q];
+    // MMAs still in flight read both CTAs' shared memory: wait for them (the
+    // commit of the lane that issued them)
+    if (warp == kIssuerWarp) {
+      if (rank == 0 && elect_one()) mma_commit_pair(s.drain);
+      if (!mbar_wait_cluster(s.drain, 0, kWaitCycles)) ok = false;
     }
-    if (a.db && blockIdx.x == 0 && tx == 0)
-      a.db[o] = a.accumulate ? a.db[o] + bias[p] : bias[p];
+  } else if (warp >= kReadWarps) {
+    reg_dec<48>();
+    const int cw = warp - kReadWarps, group = cw / kGroupWarps;
+    const int unit = lane & 7, row0 = (cw % kGroupWarps) * 16 + (lane >> 3);
+    const uint32_t half = (uint32_t)(unit >> 2);
+    const uint32_t full0 = map_to_rank(smem_u32(s.full), 0);
+    Ring ring;
+    ring.next(group);
+    int64_t done = group, skip = group;  // block of this CTA, blocks to pass over
+    while (ok && work.next(u)) {
+      int64_t it, ot;
+      tile_place(a.plan, u.tile, it, ot);
+      const uint32_t sat =
+          (uint32_t)(((it * kTile + rank * kHalf) / kActGroup & 15) + (unit >> 1));
+      int64_t k = u.k0 + skip;
+      for (; k < u.k1; k += kGroups, done += kGroups, ring.next(kGroups)) {
+        const int st = ring.st;
+        bool got = mbar_wait(&s.cfull[st], ring.ph, kWaitCycles);
+        if (got && done >= kStages) got = mbar_wait_cluster(&s.empty[st], ring.ph ^ 1u, kWaitCycles);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        uint4 c[4];
+        uint32_t b[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t r = (uint32_t)(row0 + p * 4);
+          c[p] = lds_u4(s.codes + st * kCodeBytes + r * kHalf + unit * 16);
+          b[p] = lds_u8(s.scales + st * kScaleBytes + r * 16 + sat);
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t r = (uint32_t)(row0 + p * 4);
+          const uint32_t sc = F16 ? f16_scale(b[p]) : b[p] * 0x00800080u;
+          const uint4 lo = eight<F16>(c[p].x, c[p].y, sc), hi = eight<F16>(c[p].z, c[p].w, sc);
+          // 16-byte chunks 2 (unit % 4) and + 1 of the half's 128-byte row r,
+          // swizzled; the upper half's threads store theirs in the other
+          // order, so that eight threads cover all banks at each store
+          const uint32_t row = s.a + st * kOpBytes + half * (kOpBytes / 2) + r * 128;
+          const uint32_t ch = (uint32_t)(unit & 3) * 2;
+          const uint32_t first = ((ch + half) ^ (r & 7u)) << 4;
+          sts_u4(row + first, half ? hi : lo);
+          sts_u4(row + (first ^ 16u), half ? lo : hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s.cempty[st]);
+          mbar_arrive_cluster(full0 + st * 8);
+        }
+        __syncwarp();
+      }
+      skip = k - u.k1;
+    }
+  } else {
+    reg_inc<168>();
+    // warp w reads lanes 32 (w % 4) .. + 31 (inputs) of columns 128 (w / 4)
+    // .. + 127 (outputs) of every accumulator
+    const uint32_t q = (uint32_t)warp & 3u, ch = (uint32_t)warp >> 2;
+    const uint32_t acc_empty0 = map_to_rank(smem_u32(s.acc_empty), 0);
+    uint32_t seg = 0;
+    while (ok && work.next(u)) {
+      float sum[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; ++c) sum[c] = 0.0f;
+      for (int64_t k = u.k0; k < u.k1; k += kSegBlocks, ++seg) {
+        const uint32_t buf = seg & 1u;
+        const bool got = mbar_wait_cluster(&s.acc_full[buf], (seg >> 1) & 1u, kWaitCycles);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t at = tmem + ((q * 32) << 16) + buf * kTile + ch * kHalf;
+#pragma unroll
+        for (int j = 0; j < kHalf / 16; ++j) {
+          float v[16];
+          tmem_ld16(at + j * 16, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sum[j * 16 + c] += v[c];
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0 + buf * 8);
+      }
+      if (!ok) break;
+      int64_t it, ot;
+      tile_place(a.plan, u.tile, it, ot);
+      const uint32_t m = rank * kHalf + q * 32 + lane, n = ch * kHalf;
+      if (u.slot >= 0) {
+        float* dst = a.part + (u.slot * kTile + n) * kTile + m;
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) dst[c * kTile] = sum[c];
+      } else {
+        const int64_t i = it * kTile + m, o = ot * kTile + n;
+        float* w = a.dw + o * a.lddw + i;
+        const int rows = (int)min((int64_t)kHalf, a.out - o);
+        if (i < a.in) {
+          if (a.accumulate) {
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c, w += a.lddw)
+              if (c < rows) *w += sum[c];
+          } else {
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c, w += a.lddw)
+              if (c < rows) *w = sum[c];
+          }
+        }
+      }
+    }
   }
+  if (!ok) {
+    atomicOr(a.status, kStatusWaitTimeout);
+    // a wait ran out: let copies in flight land before the CTA's memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000ll) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == kIssuerWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// Adds the ranges' partials of a cut tile in the order of their tokens and
+// stores it: block (y, x) takes 4 outputs of rest tile y.
+__global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__ WgradArgs a) {
+  const Plan& p = a.plan;
+  const int64_t t = blockIdx.y, b0 = t * p.blocks, b1 = b0 + p.blocks;
+  const int64_t g0 = b0 / p.len, g1 = (b1 - 1) / p.len;
+  if (g0 == g1) return;  // one range held it all and stored it
+  int64_t it, ot;
+  tile_place(p, p.full + t, it, ot);
+  const int64_t i = it * kTile + threadIdx.x;
+  if (i >= a.in) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int n0 = blockIdx.x * 4;
+  // the tile is the second one of its first range if that range begins
+  // before the tile's first block's tile, the first one of every other
+  const float* src = a.part + n0 * kTile + threadIdx.x;
+  const int64_t second = t - p.len * g0 / p.blocks;
+  for (int64_t g = g0; g <= g1; g += 8) {
+    float x[8][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t slot = 2 * (g + e) + (g + e == g0 ? second : 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[e][j] = g + e <= g1 ? src[slot * kTile * kTile + j * kTile] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += x[e][j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t o = ot * kTile + n0 + j;
+    if (o < a.out) {
+      float* w = a.dw + o * a.lddw + i;
+      *w = a.accumulate ? *w + v[j] : v[j];
+    }
+  }
+}
+
+// dy as planes of 16-bit values with 16-byte rows that the tensor maps take:
+// fp32 cut into three bf16 values whose sum it is (8 significant bits each,
+// by truncation, so every remainder is exact and no plane overflows); 16-bit
+// types as they are.  Rows past `rows` and columns past `out` are zero.
+template <int DT>
+__global__ void __launch_bounds__(256) wgrad_split_kernel(const void* dy, int64_t rows,
+                                                          int64_t out, int64_t lddy,
+                                                          uint16_t* planes, int64_t plane_rows,
+                                                          int64_t pitch) {
+  using E = Elem<DT>;
+  const int64_t per = pitch / kChunk, total = plane_rows * per;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total;
+       at += (int64_t)gridDim.x * 256) {
+    const int64_t r = at / per, c = (at - r * per) * kChunk;
+    const int valid = r < rows ? (int)min((int64_t)kChunk, out - c) : 0;
+    const typename E::T* src = static_cast<const typename E::T*>(dy) + r * lddy + c;
+    uint16_t* dst = planes + r * pitch + c;
+    if (DT == GC_F32) {
+      uint32_t w[3][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t p[3][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = 2 * j + e < valid ? E::to_float(src[2 * j + e]) : 0.0f;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            p[k][e] = __float_as_uint(x) & 0xFFFF0000u;
+            x = __fsub_rn(x, __uint_as_float(p[k][e]));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) w[k][j] = (p[k][0] >> 16) | p[k][1];
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(dst + k * plane_rows * pitch) =
+            make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    } else {
+      const uint16_t* s16 = reinterpret_cast<const uint16_t*>(src);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = (2 * j < valid ? s16[2 * j] : 0u) |
+               ((uint32_t)(2 * j + 1 < valid ? s16[2 * j + 1] : 0u) << 16);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Column sums of dy: block (x, y) adds rows y * rows_per .. of 256 columns
+// (32 lanes x 8), eight warps taking every eighth row, into part[y][out], or
+// into db when there is one row range.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) bias_kernel(const void* dy, int64_t rows, int64_t out,
+                                                   int64_t lddy, int64_t rows_per, float* part,
+                                                   float* db, int accumulate) {
+  using E = Elem<DT>;
+  __shared__ float s[8][256 + 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 256 + lane * kChunk;
+  const int valid = (int)max((int64_t)0, min((int64_t)kChunk, out - c));
+  const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(rows, r0 + rows_per);
+  float v[8] = {};
+  if (valid > 0)
+    for (int64_t r = r0 + warp; r < r1; r += 8) {
+      float d[8];
+      load_chunk<DT, VEC>(d, static_cast<const typename E::T*>(dy) + r * lddy + c, valid);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += d[j];
+    }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[warp][lane * 8 + j] = v[j];
+  __syncthreads();
+  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (o >= out) return;
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
+  if (gridDim.y > 1) part[(int64_t)blockIdx.y * out + o] = t;
+  else db[o] = accumulate ? db[o] + t : t;
+}
+
+__global__ void __launch_bounds__(256) bias_join_kernel(const float* part, int parts, int64_t out,
+                                                        float* db, int accumulate) {
+  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (o >= out) return;
+  float t = 0.0f;
+  for (int p = 0; p < parts; ++p) t += part[(int64_t)p * out + o];
+  db[o] = accumulate ? db[o] + t : t;
+}
+
+// --- host ----------------------------------------------------------------------------------------
+
+constexpr int kMaxBiasParts = 64;
+
+int plane_count(int dtype) { return dtype == GC_F32 ? 3 : 1; }
+
+Plan make_plan(int64_t rows, int64_t out, int64_t in, int planes, int pairs) {
+  Plan p;
+  p.in_tiles = ceil_div(in, kTile);
+  p.out_tiles = ceil_div(out, kTile);
+  p.tok_blocks = ceil_div(rows, kTok);
+  p.blocks = p.tok_blocks * planes;
+  p.pairs = std::min(pairs, kMaxPairs);
+  const int64_t tiles = p.in_tiles * p.out_tiles;
+  p.full = tiles / p.pairs * p.pairs;
+  p.rest = tiles - p.full;
+  // the rest over all pairs; a range shorter than an accumulator's blocks
+  // would cost more to join than it saves
+  p.len = std::max(ceil_div(p.rest * p.blocks, (int64_t)p.pairs),
+                   std::min<int64_t>(p.blocks, kSegBlocks));
+  p.ranges = p.rest ? ceil_div(p.rest * p.blocks, p.len) : 0;
+  return p;
+}
+
+int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
+
+int64_t planes_bytes(int64_t rows, int64_t out, int dtype) {
+  return up256((int64_t)plane_count(dtype) * round_up(rows, kTok) * round_up(out, 8) * 2);
+}
+constexpr int64_t kSlotBytes = (int64_t)kTile * kTile * 4;
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+// rows x cols elements of `size` bytes, rows `pitch` bytes apart, read in
+// boxes of kTok rows x box columns; what lies outside reads as zero.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows,
+              int64_t cols, int64_t pitch, uint32_t box, bool swizzle) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t boxes[2] = {box, (cuuint32_t)kTok};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, type, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DT>
+void launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy, float* db,
+                 int accumulate, float* part) {
+  const int64_t bx = ceil_div(out, 256);
+  const int64_t want = std::min<int64_t>({ceil_div((int64_t)ctx->num_sms * 8, bx),
+                                          ceil_div(rows, 64), (int64_t)kMaxBiasParts});
+  const int64_t rows_per = ceil_div(rows, std::max<int64_t>(want, 1));
+  const int64_t by = ceil_div(rows, rows_per);
+  const dim3 g((unsigned)bx, (unsigned)by);
+  constexpr int kSize = DT == GC_F32 ? 4 : 2;
+  {
+    LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
+    if (lddy * kSize % 16 == 0)
+      bias_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(dy, rows, out, lddy, rows_per, part, db,
+                                                        accumulate);
+    else
+      bias_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(dy, rows, out, lddy, rows_per, part, db,
+                                                         accumulate);
+  }
+  if (by > 1) {
+    LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
+    bias_join_kernel<<<(unsigned)bx, 256, 0, ctx->stream>>>(part, (int)by, out, db, accumulate);
+  }
+}
+
+template <int DT>
+void launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
+                  uint16_t* planes, int64_t plane_rows, int64_t pitch) {
+  const int64_t total = plane_rows * (pitch / kChunk);
+  const unsigned g = (unsigned)std::min<int64_t>(ceil_div(total, 256), (int64_t)ctx->num_sms * 8);
+  LaunchScope L(ctx, GC_PHASE_WGRAD_SPLIT);
+  wgrad_split_kernel<DT><<<g, 256, 0, ctx->stream>>>(dy, rows, out, lddy, planes, plane_rows,
+                                                     pitch);
+}
+
+template <bool F16>
+gc_status launch_tiles(gc_ctx* ctx, const CUtensorMap& md, const CUtensorMap& mc,
+                       const CUtensorMap& ms, const WgradArgs& a) {
+  if (cudaFuncSetAttribute(wgrad_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kSmemBytes) != cudaSuccess)
+    return GC_ERR_CUDA;
+  const int64_t pairs =
+      a.plan.full ? a.plan.pairs : std::min<int64_t>(a.plan.pairs, a.plan.ranges);
+  LaunchScope L(ctx, GC_PHASE_WGRAD);
+  wgrad_kernel<F16><<<(unsigned)(2 * pairs), kThreads, kSmemBytes, ctx->stream>>>(md, mc, ms, a);
+  return GC_OK;
 }
 
 }  // namespace
 
-int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype) { return 0; }
+int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype) {
+  if (rows == 0 || out == 0 || in == 0) return 0;
+  // partials of at most two slots per range, never more than one range per
+  // pair; a plane of 16-bit dy in case its rows are not 16-byte aligned
+  const Plan p = make_plan(rows, out, in, plane_count(dtype), kMaxPairs);
+  const int64_t tiles = p.in_tiles * p.out_tiles;
+  const int64_t slots = std::min<int64_t>(2 * kMaxPairs, tiles * p.blocks);
+  return planes_bytes(rows, out, dtype) + slots * kSlotBytes +
+         up256((int64_t)kMaxBiasParts * out * 4);
+}
 
 gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, const uint8_t* codes,
                        const uint8_t* scales, int64_t rows, int64_t out, int64_t in, float* dw,
                        int64_t lddw, float* db, int accumulate, void* scratch) {
   if (out == 0 || in == 0) return GC_OK;
+  if (rows == 0) {
+    if (accumulate) return GC_OK;
+    if (cudaMemset2DAsync(dw, lddw * 4, 0, in * 4, out, ctx->stream) != cudaSuccess ||
+        (db && cudaMemsetAsync(db, 0, out * 4, ctx->stream) != cudaSuccess))
+      return GC_ERR_CUDA;
+    return GC_OK;
+  }
+  char* at = static_cast<char*>(scratch);
+  uint16_t* planes = reinterpret_cast<uint16_t*>(at);
+  at += planes_bytes(rows, out, dtype);
+  float* bias_part = reinterpret_cast<float*>(at);
+  at += up256((int64_t)kMaxBiasParts * out * 4);
+
+  if (db) {
+    if (dtype == GC_F32) launch_bias<GC_F32>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    else if (dtype == GC_BF16)
+      launch_bias<GC_BF16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    else launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+  }
+
   WgradArgs a{};
-  a.dy = dy;
-  a.codes = codes;
-  a.scales = scales;
+  const int np = plane_count(dtype);
+  a.plan = make_plan(rows, out, in, np, ctx->num_sms / 2);
   a.dw = dw;
-  a.db = db;
-  a.rows = rows;
+  a.part = reinterpret_cast<float*>(at);
+  a.status = ctx->ws.status;
   a.out = out;
   a.in = in;
-  a.lddy = lddy;
   a.lddw = lddw;
-  a.codes_pitch = ckpt_codes_pitch(in);
-  a.scales_pitch = ckpt_scales_pitch(in);
+  a.plane_rows = a.plan.tok_blocks * kTok;
   a.accumulate = accumulate;
-  LaunchScope L(ctx, GC_PHASE_WGRAD);
-  const dim3 g((unsigned)ceil_div(in, kTile), (unsigned)ceil_div(out, kTile));
-  if (dtype == GC_F32) wgrad_kernel<GC_F32><<<g, 256, 0, ctx->stream>>>(a);
-  else if (dtype == GC_BF16) wgrad_kernel<GC_BF16><<<g, 256, 0, ctx->stream>>>(a);
-  else wgrad_kernel<GC_F16><<<g, 256, 0, ctx->stream>>>(a);
+
+  // the tensor map takes dy as it lies when its rows start on 16-byte
+  // boundaries
+  const void* d16 = dy;
+  int64_t d_rows = rows, d_cols = out, d_pitch = lddy * 2;
+  if (dtype == GC_F32 || (rows > 1 && lddy * 2 % 16 != 0) ) {
+    d_cols = round_up(out, 8);
+    d_pitch = d_cols * 2;
+    d_rows = np * a.plane_rows;
+    d16 = planes;
+    if (dtype == GC_F32)
+      launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols);
+    else
+      launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols);
+  } else if (rows == 1) {
+    d_pitch = round_up(out * 2, 16);
+  }
+  const bool f16 = dtype == GC_F16;
+  CUtensorMap md, mc, ms;
+  const int64_t cp = ckpt_codes_pitch(in), sp = ckpt_scales_pitch(in);
+  if (!make_map(&md, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d16,
+                d_rows, d_cols, d_pitch, 64, true) ||
+      !make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, rows, cp, cp, kHalf, false) ||
+      !make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, rows, sp, sp, 16, false))
+    return GC_ERR_CUDA;
+  const gc_status st =
+      f16 ? launch_tiles<true>(ctx, md, mc, ms, a) : launch_tiles<false>(ctx, md, mc, ms, a);
+  if (st != GC_OK) return st;
+  if (a.plan.ranges > a.plan.rest) {
+    LaunchScope L(ctx, GC_PHASE_WGRAD_JOIN);
+    wgrad_join_kernel<<<dim3(kTile / 4, (unsigned)a.plan.rest), 256, 0, ctx->stream>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 

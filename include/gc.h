@@ -177,7 +177,8 @@ typedef enum gc_phase {
   GC_PHASE_WGRAD = 32,       /* linear layer: dw from dy and the checkpoint */
   GC_PHASE_WGRAD_SPLIT = 33, /* linear layer: dy as bf16 planes */
   GC_PHASE_WGRAD_JOIN = 34,  /* linear layer: sum of the token ranges' partials */
-  GC_PHASE_COUNT = 35
+  GC_PHASE_WGRAD_BIAS = 35,  /* linear layer: db, column sums of dy */
+  GC_PHASE_COUNT = 36
 } gc_phase;
 
 /* Name of a phase ("ef_hist", ...); "?" when out of range. */
@@ -679,6 +680,14 @@ GC_API int64_t gc_linear_wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t 
  *   dw[o, i] (+)= sum over rows t of dy[t, o] * x^[t, i],
  *   db[o]    (+)= sum over rows t of dy[t, o].
  * dw: fp32, row stride lddw >= in elements; db: fp32[out] or NULL.
+ * Products are exact: a restored value is exact in bf16, a bf16 dy is taken
+ * as it is, an fp32 dy as the three bf16 values it is the sum of (three times
+ * the work).  With dtype GC_F16 the checkpoint must be one of fp16 values,
+ * exact in fp16: groups whose largest magnitude is above fp16's range count
+ * as NaN, below it as 0.  Sums run on the tensor cores over 512 tokens, those
+ * sums in fp32 rounded to nearest.  fp32 dy: rows <= 2^29
+ * (GC_ERR_UNSUPPORTED above).  The scratch size covers a copy of a dy whose
+ * rows do not start on 16-byte boundaries.
  * rows == 0 writes zeros (or leaves what is there, with accumulate).
  * GC_ERR_WORKSPACE when less than gc_linear_wgrad_scratch_bytes is reserved.
  */
