@@ -10,8 +10,9 @@
 // on every machine) and a restored value, 7 bits times a power of two, is
 // exact in binary32, in bf16 and, for values that came from fp16, in fp16.
 //
-// Work unit: a chunk of 8 consecutive columns per thread, so that the four
-// threads of a group of 32 are neighbours in a warp.
+// Work unit: 16 bytes of a row (8 columns of a 16-bit type, 4 of fp32) per
+// thread, so that every load and store of a warp is one run of 512 bytes and
+// the threads of a group of 32 columns (4 or 8) are neighbours in a warp.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,8 +22,7 @@
 
 namespace gc {
 
-constexpr int kChunk = 8;     // columns of one thread's unit
-constexpr int kActGroup = 32; // columns that share a scale byte
+constexpr int kActGroup = 32;  // columns that share a scale byte
 
 inline int64_t ckpt_codes_pitch(int64_t cols) { return round_up(cols, kActGroup); }
 inline int64_t ckpt_scales_pitch(int64_t cols) {
@@ -30,8 +30,7 @@ inline int64_t ckpt_scales_pitch(int64_t cols) {
 }
 
 // ---------------------------------------------------------------------------
-// Typed chunks.  A chunk stays in its own type (Raw) until it is used: 4
-// registers for the 16-bit types.
+// Typed units: 16 bytes as they lie in memory, unpacked to V fp32 values.
 // ---------------------------------------------------------------------------
 template <int DT>
 struct Elem;
@@ -39,47 +38,25 @@ struct Elem;
 template <>
 struct Elem<GC_F32> {
   using T = float;
-  struct Raw { uint4 a, b; };
-  static __device__ __forceinline__ void zero(Raw& r) {
-    r.a = make_uint4(0, 0, 0, 0);
-    r.b = make_uint4(0, 0, 0, 0);
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[V]) {
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z);
+    v[3] = __uint_as_float(r.w);
   }
-  static __device__ __forceinline__ void load(Raw& r, const T* p) {
-    r.a = __ldg(reinterpret_cast<const uint4*>(p));
-    r.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-  }
-  static __device__ __forceinline__ void store(T* p, const Raw& r) {
-    reinterpret_cast<uint4*>(p)[0] = r.a;
-    reinterpret_cast<uint4*>(p)[1] = r.b;
-  }
-  static __device__ __forceinline__ void unpack(const Raw& r, float v[8]) {
-    v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
-    v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
-    v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
-    v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
-  }
-  static __device__ __forceinline__ void pack(Raw& r, const float v[8]) {
-    r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                     __float_as_uint(v[3]));
-    r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                     __float_as_uint(v[7]));
+  static __device__ __forceinline__ uint4 pack(const float (&v)[V]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
   }
   static __device__ __forceinline__ float to_float(T x) { return x; }
-  static __device__ __forceinline__ T from_float(float x) { return x; }
 };
 
 template <>
 struct Elem<GC_BF16> {
   using T = __nv_bfloat16;
-  using Raw = uint4;
-  static __device__ __forceinline__ void zero(Raw& r) { r = make_uint4(0, 0, 0, 0); }
-  static __device__ __forceinline__ void load(Raw& r, const T* p) {
-    r = __ldg(reinterpret_cast<const uint4*>(p));
-  }
-  static __device__ __forceinline__ void store(T* p, const Raw& r) {
-    *reinterpret_cast<uint4*>(p) = r;
-  }
-  static __device__ __forceinline__ void unpack(const Raw& r, float v[8]) {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[V]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -87,31 +64,23 @@ struct Elem<GC_BF16> {
       v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-  static __device__ __forceinline__ void pack(Raw& r, const float v[8]) {
+  static __device__ __forceinline__ uint4 pack(const float (&v)[V]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    r = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
   static __device__ __forceinline__ float to_float(T x) { return __bfloat162float(x); }
-  static __device__ __forceinline__ T from_float(float x) { return __float2bfloat16_rn(x); }
 };
 
 template <>
 struct Elem<GC_F16> {
   using T = __half;
-  using Raw = uint4;
-  static __device__ __forceinline__ void zero(Raw& r) { r = make_uint4(0, 0, 0, 0); }
-  static __device__ __forceinline__ void load(Raw& r, const T* p) {
-    r = __ldg(reinterpret_cast<const uint4*>(p));
-  }
-  static __device__ __forceinline__ void store(T* p, const Raw& r) {
-    *reinterpret_cast<uint4*>(p) = r;
-  }
-  static __device__ __forceinline__ void unpack(const Raw& r, float v[8]) {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[V]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -120,61 +89,272 @@ struct Elem<GC_F16> {
       v[2 * i + 1] = f.y;
     }
   }
-  static __device__ __forceinline__ void pack(Raw& r, const float v[8]) {
+  static __device__ __forceinline__ uint4 pack(const float (&v)[V]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    r = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
   static __device__ __forceinline__ float to_float(T x) { return __half2float(x); }
-  static __device__ __forceinline__ T from_float(float x) { return __float2half_rn(x); }
 };
 
-// Eight columns starting at p of which the first `valid` (1..8) exist; the
-// rest read as zero.  VEC: p is 16-byte aligned.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_chunk(float v[8], const typename Elem<DT>::T* p, int valid) {
-  using E = Elem<DT>;
-  if (VEC && valid >= kChunk) {
-    typename E::Raw r;
-    E::load(r, p);
-    E::unpack(r, v);
-    return;
-  }
+constexpr int elem_size(int dtype) { return dtype == GC_F32 ? 4 : 2; }
+inline bool row_aligned(int64_t ld, int dtype) { return ld * elem_size(dtype) % 16 == 0; }
+
+// ---------------------------------------------------------------------------
+// Units of a row.  `row` is its first byte, `off` the first byte of the
+// thread's unit, `bytes` the row's length; a unit past the end reads as zero
+// and is not stored.
+// ---------------------------------------------------------------------------
+
+// Elements [0, n) of 16 bytes, one by one.  (This and store_some run at the
+// ends of rows only; out of line they keep the kernels within the
+// instruction cache.)
+template <int DT>
+__device__ __noinline__ uint4 load_some(const char* p, int n) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i) v[i] = i < valid ? E::to_float(p[i]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    if (DT == GC_F32) {
+      if (i < n) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      if (2 * i < n) w[i] = h[2 * i];
+      if (2 * i + 1 < n) w[i] |= (uint32_t)h[2 * i + 1] << 16;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_chunk(typename Elem<DT>::T* p, const float v[8], int valid) {
-  using E = Elem<DT>;
-  if (VEC && valid >= kChunk) {
-    typename E::Raw r;
-    E::pack(r, v);
-    E::store(p, r);
+// Elements [lo, hi) of 16 bytes, one by one.
+template <int DT>
+__device__ __noinline__ void store_some(char* p, uint4 r, int lo, int hi) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (DT == GC_F32) {
+      if (i >= lo && i < hi) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    } else {
+      uint16_t* h = reinterpret_cast<uint16_t*>(p);
+      if (2 * i >= lo && 2 * i < hi) h[2 * i] = (uint16_t)w[i];
+      if (2 * i + 1 >= lo && 2 * i + 1 < hi) h[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    }
+  }
+}
+
+// Rows that start on 16-byte boundaries: a thread's own load and store.
+template <int DT>
+__device__ __forceinline__ uint4 load_aligned(const char* row, int64_t off, int64_t bytes) {
+  const int64_t left = bytes - off;
+  if (left >= 16) return __ldg(reinterpret_cast<const uint4*>(row + off));
+  if (left <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  return load_some<DT>(row + off, (int)left / elem_size(DT));
+}
+template <int DT>
+__device__ __forceinline__ void store_aligned(char* row, int64_t off, int64_t bytes,
+                                              const uint4& r) {
+  const int64_t left = bytes - off;
+  if (left >= 16) *reinterpret_cast<uint4*>(row + off) = r;
+  else if (left > 0) store_some<DT>(row + off, r, 0, (int)left / elem_size(DT));
+}
+
+// 16 of the 32 bytes lo ++ hi, from byte `shift` (0..15, even; the same in
+// the whole warp) on.
+__device__ __forceinline__ uint4 funnel(const uint4& lo, const uint4& hi, uint32_t shift) {
+  uint32_t w[5];
+  switch (shift >> 2) {
+    case 0: w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w; w[4] = hi.x; break;
+    case 1: w[0] = lo.y; w[1] = lo.z; w[2] = lo.w; w[3] = hi.x; w[4] = hi.y; break;
+    case 2: w[0] = lo.z; w[1] = lo.w; w[2] = hi.x; w[3] = hi.y; w[4] = hi.z; break;
+    default: w[0] = lo.w; w[1] = hi.x; w[2] = hi.y; w[3] = hi.z; w[4] = hi.w; break;
+  }
+  const uint32_t sh = (shift & 3u) * 8u;
+  return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                    __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+}
+
+// Rows that start anywhere, the warp's 32 units being consecutive in one row
+// (all lanes call; a whole warp may lie past the end).  Memory is read in
+// the aligned 16-byte pieces that cover the units, each once per warp, and
+// the units are cut from neighbouring lanes' pieces.  A piece may hold bytes
+// of the row before (never before the matrix: its first row is aligned) or
+// after; `end` is the matrix's end, past which nothing is read.
+template <int DT>
+__device__ __forceinline__ uint4 load_ragged(const char* row, int64_t off, int64_t bytes,
+                                             const char* end) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  const char* p = row + off - mis;
+  auto piece = [&](const char* q, int64_t at) -> uint4 {  // `at`: q's place in the row
+    if (at >= bytes) return make_uint4(0u, 0u, 0u, 0u);
+    if (end - q >= 16) return __ldg(reinterpret_cast<const uint4*>(q));
+    return load_some<DT>(q, (int)(end - q) / elem_size(DT));
+  };
+  const uint4 a = piece(p, off - mis);
+  uint4 r = a;
+  if (mis) {
+    uint4 next = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 31) next = piece(p + 16, off - mis + 16);
+    const uint4 n = make_uint4(__shfl_down_sync(0xffffffffu, a.x, 1),
+                               __shfl_down_sync(0xffffffffu, a.y, 1),
+                               __shfl_down_sync(0xffffffffu, a.z, 1),
+                               __shfl_down_sync(0xffffffffu, a.w, 1));
+    r = funnel(a, lane == 31 ? next : n, mis);
+  }
+  // columns past the row's end are zero
+  const int64_t left = bytes - off;
+  if (left < 16) {
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (left <= 4 * i) w[i] = 0u;
+      else if (left == 4 * i + 2) w[i] &= 0xFFFFu;
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+
+// The store of such units: pieces that the warp's units fill are stored
+// whole, the elements of the others one by one.
+template <int DT>
+__device__ __forceinline__ void store_ragged(char* row, int64_t off, int64_t bytes,
+                                             const uint4& r) {
+  constexpr int E = elem_size(DT);
+  const int lane = threadIdx.x & 31;
+  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  if (!mis) {
+    store_aligned<DT>(row, off, bytes, r);
     return;
   }
+  const uint4 b = make_uint4(__shfl_up_sync(0xffffffffu, r.x, 1),
+                             __shfl_up_sync(0xffffffffu, r.y, 1),
+                             __shfl_up_sync(0xffffffffu, r.z, 1),
+                             __shfl_up_sync(0xffffffffu, r.w, 1));
+  const uint4 piece = funnel(b, r, 16u - mis);
+  char* p = row + off - mis;                 // the piece that the unit starts in
+  const int64_t left = bytes - (off - mis);  // of the row, from there
+  if (lane > 0 && left >= 16) *reinterpret_cast<uint4*>(p) = piece;
+  else if (left > 0)
+    store_some<DT>(p, piece, lane > 0 ? 0 : (int)mis / E, (int)min(left, (int64_t)16) / E);
+  // the last unit's end lies in a piece that the warp does not fill
+  if (lane == 31 && left > 16)
+    store_some<DT>(p + 16, funnel(r, r, 16u - mis), 0,
+                   (int)min(left - 16, (int64_t)mis) / E);
+}
+
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ uint4 load_unit(const char* row, int64_t off, int64_t bytes,
+                                           const char* end) {
+  return ALIGNED ? load_aligned<DT>(row, off, bytes) : load_ragged<DT>(row, off, bytes, end);
+}
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void store_unit(char* row, int64_t off, int64_t bytes,
+                                           const uint4& r) {
+  if (ALIGNED) store_aligned<DT>(row, off, bytes, r);
+  else store_ragged<DT>(row, off, bytes, r);
+}
+
+// A warp's run: U times 32 consecutive units from byte `at` (a multiple of
+// 512) of a row on; lane l has units l, l + 32, ...  Inside the row (`inner`,
+// the same in the whole warp: at + 512 U + 16 <= bytes) nothing is checked
+// and every address is one base plus a constant.
+template <int DT, bool ALIGNED, int U>
+__device__ __forceinline__ void load_run(uint4 (&r)[U], const char* row, uint32_t at, bool inner,
+                                         int64_t bytes, const char* end) {
+  const uint32_t lane = threadIdx.x & 31u;
+  if (!inner) {
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i)
-    if (i < valid) p[i] = E::from_float(v[i]);
+    for (int i = 0; i < U; ++i) {
+      const int64_t seg = (int64_t)at + i * 512;
+      r[i] = seg < bytes ? load_unit<DT, ALIGNED>(row, seg + lane * 16, bytes, end)
+                         : make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
+  const uint32_t mis = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  const char* p = row + at + lane * 16u - mis;
+#pragma unroll
+  for (int i = 0; i < U; ++i) r[i] = __ldg(reinterpret_cast<const uint4*>(p + i * 512));
+  if (ALIGNED || mis == 0u) return;
+  uint4 last = r[U - 1];  // the piece behind the run, for lane 31
+  if (lane == 31u) last = __ldg(reinterpret_cast<const uint4*>(p + (U - 1) * 512 + 16));
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    // the next lane's piece; lane 31's next is lane 0's of the next segment
+    const uint4 v = (i + 1 < U && lane == 0u) ? r[i + 1 < U ? i + 1 : i] : r[i];
+    const int from = (int)((lane + 1u) & 31u);
+    uint4 n = make_uint4(
+        __shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
+        __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
+    if (i == U - 1 && lane == 31u) n = last;
+    r[i] = funnel(r[i], n, mis);
+  }
+}
+
+template <int DT, bool ALIGNED, int U>
+__device__ __forceinline__ void store_run(char* row, uint32_t at, bool inner, int64_t bytes,
+                                          const uint4 (&r)[U]) {
+  const uint32_t lane = threadIdx.x & 31u;
+  if (!inner) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t seg = (int64_t)at + i * 512;
+      if (seg < bytes) store_unit<DT, ALIGNED>(row, seg + lane * 16, bytes, r[i]);
+    }
+    return;
+  }
+  const uint32_t mis = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  char* p = row + at + lane * 16u - mis;
+  if (ALIGNED || mis == 0u) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) *reinterpret_cast<uint4*>(p + i * 512) = r[i];
+    return;
+  }
+  constexpr int E = elem_size(DT);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    // the lane before's unit; lane 0's is lane 31's of the segment before
+    const uint4 v = (i > 0 && lane == 31u) ? r[i > 0 ? i - 1 : 0] : r[i];
+    const int from = (int)((lane + 31u) & 31u);
+    const uint4 b = make_uint4(
+        __shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
+        __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
+    const uint4 piece = funnel(b, r[i], 16u - mis);
+    if (i > 0 || lane > 0u) *reinterpret_cast<uint4*>(p + i * 512) = piece;
+    else store_some<DT>(p, piece, (int)mis / E, 16 / E);
+  }
+  if (lane == 31u)
+    store_some<DT>(p + (U - 1) * 512 + 16, funnel(r[U - 1], r[U - 1], 16u - mis), 0,
+                   (int)mis / E);
 }
 
 // ---------------------------------------------------------------------------
 // The format.
 // ---------------------------------------------------------------------------
 
-// Largest magnitude (as bits; a NaN compares above infinity) of a thread's
-// chunk, then of the group's four threads.  All 32 lanes take part.
-__device__ __forceinline__ uint32_t group_max_bits(const float v[8]) {
-  uint32_t m = 0;
+// Largest magnitude of a unit's group, as binary32 bits (a NaN compares above
+// infinity).  16-bit types compare their magnitude bits two at a time.  All
+// 32 lanes take part.
+template <int DT>
+__device__ __forceinline__ uint32_t group_max_bits(const uint4& r) {
+  if (DT == GC_F32) {
+    uint32_t m = max(max(r.x & 0x7FFFFFFFu, r.y & 0x7FFFFFFFu),
+                     max(r.z & 0x7FFFFFFFu, r.w & 0x7FFFFFFFu));
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  return m;
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  }
+  uint32_t m = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu),
+                        __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const uint32_t h = max(m & 0xFFFFu, m >> 16);
+  if (DT == GC_BF16) return h << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
 }
 
 __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
@@ -182,45 +362,76 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
   return e < 7u ? 0u : (e >= 254u ? 255u : e + 1u);
 }
 
-// Codes of four values at scale byte b.  |x| * up < 128 + 2^23 addition: the
-// sum's low mantissa bits are the product rounded half to even.
-__device__ __forceinline__ uint32_t encode4(const float v[4], float up) {
+// Codes of four values, up = 2^(134 - B), from the values and the bytes that
+// hold their signs.  The fused multiply-add rounds |x| * up + 2^23 once, to
+// the product rounded half to even in its low byte; 128 (from above 127.5)
+// becomes 127.
+__device__ __forceinline__ uint32_t encode4(const float* v, uint32_t signs, float up) {
   uint32_t q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = __float_as_uint(__fadd_rn(fminf(__fmul_rn(fabsf(v[i]), up), 127.0f), 8388608.0f));
-  const uint32_t lo = __byte_perm(q[0], q[1], 0x0040), hi = __byte_perm(q[2], q[3], 0x0040);
-  const uint32_t m = __byte_perm(lo, hi, 0x5410);
-  const uint32_t slo = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0073);
-  const uint32_t shi = __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0073);
-  const uint32_t sign = __byte_perm(slo, shi, 0x5410);
+  for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(fabsf(v[i]), up, 8388608.0f));
+  uint32_t m = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040),
+                           0x5410);
+  m -= (m >> 7) & 0x01010101u;
   const uint32_t nonzero = m + 0x7F7F7F7Fu;  // bit 7 of each byte: m != 0
-  return m | (sign & nonzero & 0x80808080u);
+  return m | (signs & nonzero & 0x80808080u);
 }
 
-__device__ __forceinline__ uint2 encode8(const float v[8], uint32_t b) {
-  if (b == 0u || b == 255u) return make_uint2(0u, 0u);
-  const float up = __uint_as_float((261u - b) << 23);  // 2^(134 - b)
-  return make_uint2(encode4(v, up), encode4(v + 4, up));
+// A unit's codes (one word for fp32, two for 16-bit types) from its bytes
+// and its values.
+template <int DT>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint4& r,
+                                            const float (&v)[Elem<DT>::V], uint32_t b) {
+  const bool empty = b == 0u || b == 255u;
+  const float up = __uint_as_float((261u - b) << 23);
+  if (DT == GC_F32) {
+    const uint32_t s = __byte_perm(__byte_perm(r.x, r.y, 0x0073), __byte_perm(r.z, r.w, 0x0073),
+                                   0x5410);
+    *reinterpret_cast<uint32_t*>(p) = empty ? 0u : encode4(v, s, up);
+  } else {
+    const uint32_t c0 = encode4(v, __byte_perm(r.x, r.y, 0x7531), up);
+    const uint32_t c1 = encode4(v + Elem<DT>::V - 4, __byte_perm(r.z, r.w, 0x7531), up);
+    *reinterpret_cast<uint2*>(p) = empty ? make_uint2(0u, 0u) : make_uint2(c0, c1);
+  }
 }
 
-// The value of the code in byte i of w: the binary32 word with sign, exponent
-// b and the seven bits m on top of its mantissa is +-(128 + m) * 2^(b - 134);
-// taking +-128 * 2^(b - 134) off it is exact.  b == 255 gives inf - inf = NaN.
-__device__ __forceinline__ float decode1(uint32_t w, int i, uint32_t bexp) {
-  const uint32_t c = __byte_perm(w, 0u, 0x0044u | ((uint32_t)i << 8) | ((uint32_t)i << 12));
-  // c = byte i in bytes 3 and 2 (byte 0, 1 from the zero word)
-  const uint32_t s = c & 0x80000000u;
-  const uint32_t x = s | bexp | (c & 0x007F0000u);
-  return __fsub_rn(__uint_as_float(x), __uint_as_float(s | bexp));
+template <int V>
+struct Codes {
+  uint32_t w[V / 4];
+};
+template <int V>
+__device__ __forceinline__ Codes<V> load_codes(const uint8_t* p) {
+  Codes<V> c;
+  if (V == 4) c.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  else {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    c.w[0] = u.x;
+    c.w[V / 4 - 1] = u.y;
+  }
+  return c;
 }
 
-__device__ __forceinline__ void decode8(float v[8], uint2 w, uint32_t b) {
-  const uint32_t bexp = b << 23;
+// Two codes (the bytes that `sel` puts twice each into the halves) as bf16:
+// sign, exponent B and the seven bits m make +-(128 + m) 2^(B - 134); taking
+// +-128 2^(B - 134) off is exact.  bexp: B in both exponents; B = 255 gives
+// inf - inf = NaN.
+__device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t sel, uint32_t bexp) {
+  const uint32_t v = __byte_perm(w, 0u, sel);
+  const uint32_t x = (v & 0x807F807Fu) | bexp, c = (v & 0x80008000u) | bexp;
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(c));
+  return d;
+}
+
+template <int V>
+__device__ __forceinline__ void decode(float (&v)[V], const Codes<V>& c, uint32_t b) {
+  const uint32_t bexp = b * 0x00800080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = decode1(w.x, i, bexp);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[4 + i] = decode1(w.y, i, bexp);
+  for (int i = 0; i < V / 2; ++i) {
+    const uint32_t d = decode2(c.w[i / 2], i & 1 ? 0x3322u : 0x1100u, bexp);
+    v[2 * i] = __uint_as_float(d << 16);
+    v[2 * i + 1] = __uint_as_float(d & 0xFFFF0000u);
+  }
 }
 
 }  // namespace gc

@@ -7,11 +7,15 @@
 //   backward: dx = dy [* gate^] f'(x^), dgate = dy f(x^), with x^ and gate^
 //   the values that the checkpoints stand for.
 //
-// Every kernel is one pass over its tensors, bound by memory: a thread owns a
-// chunk of 8 consecutive columns (one 16-byte load per 16-bit tensor), four
-// neighbouring threads the group of 32 that shares a scale byte.  The chunks
-// of all rows are one index space, so that narrow and wide rows load the GPU
-// alike.
+// Every kernel is one pass over its tensors, bound by memory as long as few
+// instructions are spent per element.  A warp takes a run of U x 32
+// consecutive units of 16 bytes of one row: it divides once, adds constants
+// to one base address per tensor, and issues all its loads before it uses
+// the first.  (A thread that placed each of its units by itself spent 40
+// instructions per element on a gated forward pass, half of them on
+// addresses: 138 us for 8192 x 11008 bf16 against 107 at the copy rate.)
+// Rows that do not start on 16-byte boundaries are read and written in the
+// aligned pieces that cover the run, shifted into place between lanes.
 #include <algorithm>
 
 #include "gc_act8.cuh"
@@ -20,252 +24,285 @@ namespace gc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKindNone = 2;  // save only
+constexpr int kKindNone = 2;  // save, restore
 
-// Position of a thread in the (row, chunk) space, advanced by a fixed stride
-// without a division per step.
-struct Walk {
-  int64_t row;
-  int32_t chunk;
-  int64_t step_rows;
-  int32_t step_chunks, per_row;
-  __device__ __forceinline__ Walk(int64_t first, int64_t stride, int32_t chunks_per_row)
-      : per_row(chunks_per_row) {
-    row = first / per_row;
-    chunk = (int32_t)(first - row * per_row);
-    step_rows = stride / per_row;
-    step_chunks = (int32_t)(stride - step_rows * per_row);
-  }
-  __device__ __forceinline__ void next() {
-    row += step_rows;
-    chunk += step_chunks;
-    if (chunk >= per_row) {
-      chunk -= per_row;
-      ++row;
-    }
-  }
-};
-
-template <int KIND>
-__device__ __forceinline__ float act_value(float x) {
-  if (KIND == GC_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678f));
-  return x / (1.0f + expf(-x));
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// f(x) and f'(x).
-template <int KIND>
-__device__ __forceinline__ void act_both(float x, float& f, float& d) {
+// f(x), and f'(x) if asked.
+//
+// GELU: with a = |x|, Phi(-a) = exp(-a^2 / 2) R(a), where R(a) =
+// exp(a^2 / 2) Phi(-a) is smooth; R is a polynomial of degree 5 in
+// t = 1 / (1 + 0.32 a), fitted to R on [0, 14] so that the largest error of
+// Phi(-a) max(1, a) is least (3.1e-8; iteratively reweighted least squares).
+// x Phi(x) = (x + |x|) / 2 - a Phi(-a) for either sign; a is limited to 14
+// as a factor, where Phi(-a) is 0 in fp32, so that +inf gives +inf.
+template <int KIND, bool DERIV>
+__device__ __forceinline__ void act(float x, float& f, float& d) {
   if (KIND == GC_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(x * 0.70710678f));
-    f = x * cdf;
-    d = fmaf(x * 0.39894228f, expf(-0.5f * x * x), cdf);
+    const float a = fabsf(x);
+    const float t = rcp_approx(fmaf(0.32f, a, 1.0f));
+    float r = fmaf(t, -0.128873349f, 0.491905883f);
+    r = fmaf(r, t, -0.259480187f);
+    r = fmaf(r, t, 0.310232595f);
+    r = fmaf(r, t, 0.0814068223f);
+    r = fmaf(r, t, 0.00480820835f);
+    const float e = exp2_approx(a * a * -0.72134752f);  // exp(-a^2 / 2)
+    const float q = r * e;                              // Phi(-a)
+    f = fmaf(-fminf(a, 14.0f), q, fmaf(0.5f, x, 0.5f * a));
+    if (DERIV) d = fmaf(x * 0.39894228f, e, x < 0.0f ? q : 1.0f - q);
   } else {
-    const float s = 1.0f / (1.0f + expf(-x));
+    const float s = rcp_approx(1.0f + exp2_approx(x * -1.44269504f));
     f = x * s;
-    d = s * fmaf(x, 1.0f - s, 1.0f);
+    if (DERIV) d = fmaf(f, 1.0f - s, s);
   }
 }
 
-struct FwdArgs {
-  const void* x;
-  const void* gate;
-  void* y;
+// One tensor [rows, cols]: base address and row stride in bytes, its end.
+struct Mat {
+  char* p;
+  int64_t pitch;
+  const char* end;
+};
+
+struct Args {
+  Mat x, gate, y;  // forward: inputs, output; backward: dy in x, dgate in gate, dx in y
   uint8_t *codes, *scales, *gate_codes, *gate_scales;
-  int64_t ldx, ldgate, ldy;
-  int64_t total;  // chunks of all rows
-  int64_t cols, codes_pitch, scales_pitch;
+  int64_t row_bytes, codes_pitch, scales_pitch;
+  int64_t total;  // runs of all rows
+  uint32_t runs;  // of one row
 };
 
-template <int DT, int KIND, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kThreads) act_forward_kernel(FwdArgs a) {
-  using T = typename Elem<DT>::T;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  Walk w(first, stride, (int32_t)(a.codes_pitch / kChunk));
-  // whole warps stay in the loop together (group_max_bits); a.total is a
-  // multiple of 4, so a group of 32 columns is wholly inside or outside
-  for (int64_t base = first - (threadIdx.x & 31); base < a.total; base += stride, w.next()) {
-    const bool in = base + (threadIdx.x & 31) < a.total;
-    const int64_t c = (int64_t)w.chunk * kChunk;
-    const int valid = in ? (int)max((int64_t)0, min((int64_t)kChunk, a.cols - c)) : 0;
-    float v[8], g[8];
-    load_chunk<DT, VEC>(v, static_cast<const T*>(a.x) + w.row * a.ldx + c, valid);
-    if (GATED) load_chunk<DT, VEC>(g, static_cast<const T*>(a.gate) + w.row * a.ldgate + c, valid);
-    if (KIND != kKindNone) {
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = act_value<KIND>(v[i]);
-        if (GATED) y[i] *= g[i];
-      }
-      store_chunk<DT, VEC>(static_cast<T*>(a.y) + w.row * a.ldy + c, y, valid);
+// The warp's run: its row, first byte in the row, whether it lies inside.
+template <int U>
+struct Run {
+  int64_t row;
+  uint32_t at;
+  bool any, inner;
+  __device__ __forceinline__ Run(const Args& a) {
+    const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    any = id < a.total;
+    uint32_t run;
+    if (a.total <= 0xFFFFFFFFll) {
+      row = (uint32_t)id / a.runs;
+      run = (uint32_t)id - (uint32_t)row * a.runs;
+    } else {
+      row = id / a.runs;
+      run = (uint32_t)(id - row * a.runs);
     }
-    if (a.codes) {
-      const uint32_t b = scale_byte(group_max_bits(v));
-      const uint32_t bg = GATED ? scale_byte(group_max_bits(g)) : 0u;
-      if (in) {
-        const int64_t at = w.row * a.codes_pitch + c;
-        *reinterpret_cast<uint2*>(a.codes + at) = encode8(v, b);
-        if (GATED) *reinterpret_cast<uint2*>(a.gate_codes + at) = encode8(g, bg);
-        if ((w.chunk & 3) == 0) {
-          const int64_t sat = w.row * a.scales_pitch + (w.chunk >> 2);
-          a.scales[sat] = (uint8_t)b;
-          if (GATED) a.gate_scales[sat] = (uint8_t)bg;
-        }
-      }
-    }
+    at = run * (U * 512u);
+    inner = (int64_t)at + U * 512 + 16 <= a.row_bytes;
   }
-}
-
-struct BwdArgs {
-  const void* dy;
-  void *dx, *dgate;
-  const uint8_t *codes, *scales, *gate_codes, *gate_scales;
-  int64_t lddy, lddx, lddgate;
-  int64_t total, cols, codes_pitch, scales_pitch;
 };
 
-__device__ __forceinline__ void restore_chunk(float v[8], const uint8_t* codes,
-                                              const uint8_t* scales, int64_t row, int32_t chunk,
-                                              int64_t cp, int64_t sp) {
-  const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + row * cp + (int64_t)chunk * kChunk));
-  decode8(v, c, __ldg(scales + row * sp + (chunk >> 2)));
-}
-
-template <int DT, int KIND, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kThreads) act_backward_kernel(BwdArgs a) {
-  using T = typename Elem<DT>::T;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  Walk w(first, stride, (int32_t)(a.codes_pitch / kChunk));
-  for (int64_t at = first; at < a.total; at += stride, w.next()) {
-    const int64_t c = (int64_t)w.chunk * kChunk;
-    const int valid = (int)min((int64_t)kChunk, a.cols - c);
-    if (valid <= 0) continue;
-    float dy[8], x[8], g[8];
-    load_chunk<DT, VEC>(dy, static_cast<const T*>(a.dy) + w.row * a.lddy + c, valid);
-    restore_chunk(x, a.codes, a.scales, w.row, w.chunk, a.codes_pitch, a.scales_pitch);
-    if (GATED)
-      restore_chunk(g, a.gate_codes, a.gate_scales, w.row, w.chunk, a.codes_pitch,
-                    a.scales_pitch);
-    float dx[8], dg[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f, d;
-      act_both<KIND>(x[i], f, d);
-      dx[i] = GATED ? dy[i] * g[i] * d : dy[i] * d;
-      dg[i] = dy[i] * f;
-    }
-    store_chunk<DT, VEC>(static_cast<T*>(a.dx) + w.row * a.lddx + c, dx, valid);
-    if (GATED) store_chunk<DT, VEC>(static_cast<T*>(a.dgate) + w.row * a.lddgate + c, dg, valid);
-  }
-}
-
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) restore_kernel(BwdArgs a) {
-  using T = typename Elem<DT>::T;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  Walk w(first, stride, (int32_t)(a.codes_pitch / kChunk));
-  for (int64_t at = first; at < a.total; at += stride, w.next()) {
-    const int64_t c = (int64_t)w.chunk * kChunk;
-    const int valid = (int)min((int64_t)kChunk, a.cols - c);
-    if (valid <= 0) continue;
-    float x[8];
-    restore_chunk(x, a.codes, a.scales, w.row, w.chunk, a.codes_pitch, a.scales_pitch);
-    store_chunk<DT, VEC>(static_cast<T*>(a.dx) + w.row * a.lddx + c, x, valid);
-  }
-}
-
-int elem_size(int dtype) { return dtype == GC_F32 ? 4 : 2; }
-
-unsigned grid_for(const gc_ctx* ctx, int64_t total) {
-  return (unsigned)std::max<int64_t>(
-      1, std::min<int64_t>(ceil_div(total, kThreads), (int64_t)ctx->num_sms * 8));
-}
-
-template <int DT, int KIND, bool GATED>
-void forward_dt(gc_ctx* ctx, const FwdArgs& a, bool vec) {
-  const unsigned g = grid_for(ctx, a.total);
-  if (vec)
-    act_forward_kernel<DT, KIND, GATED, true><<<g, kThreads, 0, ctx->stream>>>(a);
-  else
-    act_forward_kernel<DT, KIND, GATED, false><<<g, kThreads, 0, ctx->stream>>>(a);
-}
-
-template <int KIND, bool GATED>
-void forward_kind(gc_ctx* ctx, const FwdArgs& a, int dtype, bool vec) {
-  if (dtype == GC_F32) forward_dt<GC_F32, KIND, GATED>(ctx, a, vec);
-  else if (dtype == GC_BF16) forward_dt<GC_BF16, KIND, GATED>(ctx, a, vec);
-  else forward_dt<GC_F16, KIND, GATED>(ctx, a, vec);
-}
-
-template <int DT, int KIND, bool GATED>
-void backward_dt(gc_ctx* ctx, const BwdArgs& a, bool vec) {
-  const unsigned g = grid_for(ctx, a.total);
-  if (vec)
-    act_backward_kernel<DT, KIND, GATED, true><<<g, kThreads, 0, ctx->stream>>>(a);
-  else
-    act_backward_kernel<DT, KIND, GATED, false><<<g, kThreads, 0, ctx->stream>>>(a);
-}
-
-template <int KIND, bool GATED>
-void backward_kind(gc_ctx* ctx, const BwdArgs& a, int dtype, bool vec) {
-  if (dtype == GC_F32) backward_dt<GC_F32, KIND, GATED>(ctx, a, vec);
-  else if (dtype == GC_BF16) backward_dt<GC_BF16, KIND, GATED>(ctx, a, vec);
-  else backward_dt<GC_F16, KIND, GATED>(ctx, a, vec);
-}
-
+// Bytes of codes of a run before unit i * 32 + lane.
 template <int DT>
-void restore_dt(gc_ctx* ctx, const BwdArgs& a, bool vec) {
-  const unsigned g = grid_for(ctx, a.total);
-  if (vec)
-    restore_kernel<DT, true><<<g, kThreads, 0, ctx->stream>>>(a);
-  else
-    restore_kernel<DT, false><<<g, kThreads, 0, ctx->stream>>>(a);
+__device__ __forceinline__ uint32_t code_at(int i) {
+  return (uint32_t)(i * 32 + (threadIdx.x & 31)) * Elem<DT>::V;
 }
 
-bool row_aligned(int64_t ld, int dtype) { return ld * elem_size(dtype) % 16 == 0; }
+template <int DT, int U>
+__device__ __forceinline__ void save_run(const uint4 (&r)[U], uint8_t* codes, uint8_t* scales,
+                                         const Args& a, const Run<U>& run) {
+  constexpr int V = Elem<DT>::V;
+  const int64_t c0 = run.at / elem_size(DT);
+  uint8_t* pc = codes + run.row * a.codes_pitch + c0;
+  uint8_t* ps = scales + run.row * a.scales_pitch + c0 / kActGroup;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float v[V];
+    Elem<DT>::unpack(r[i], v);
+    const uint32_t b = scale_byte(group_max_bits<DT>(r[i])), c = code_at<DT>(i);
+    if (run.inner || c0 + c < a.codes_pitch) {
+      store_codes<DT>(pc + c, r[i], v, b);
+      if ((c & (kActGroup - 1)) == 0) ps[c / kActGroup] = (uint8_t)b;
+    }
+  }
+}
 
-gc_status launched() { return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA; }
+template <int DT, int KIND, bool GATED, bool ALIGNED, int U>
+__global__ void __launch_bounds__(kThreads)
+    act_forward_kernel(const __grid_constant__ Args a) {
+  using E = Elem<DT>;
+  constexpr int V = E::V;
+  const Run<U> run(a);
+  if (!run.any) return;
+  uint4 x[U], g[U];
+  load_run<DT, ALIGNED>(x, a.x.p + run.row * a.x.pitch, run.at, run.inner, a.row_bytes, a.x.end);
+  if (GATED)
+    load_run<DT, ALIGNED>(g, a.gate.p + run.row * a.gate.pitch, run.at, run.inner, a.row_bytes,
+                          a.gate.end);
+  if (a.codes) {
+    save_run<DT>(x, a.codes, a.scales, a, run);
+    if (GATED) save_run<DT>(g, a.gate_codes, a.gate_scales, a, run);
+  }
+  if (KIND == kKindNone) return;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float v[V], w[V], d;
+    E::unpack(x[i], v);
+    if (GATED) E::unpack(g[i], w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float f;
+      act<KIND, false>(v[j], f, d);
+      v[j] = GATED ? f * w[j] : f;
+    }
+    x[i] = E::pack(v);
+  }
+  store_run<DT, ALIGNED>(a.y.p + run.row * a.y.pitch, run.at, run.inner, a.row_bytes, x);
+}
+
+template <int V, int U>
+struct Saved {
+  Codes<V> c[U];
+  uint32_t b[U];
+};
+template <int DT, int U>
+__device__ __forceinline__ void saved_run(Saved<Elem<DT>::V, U>& s, const uint8_t* codes,
+                                          const uint8_t* scales, const Args& a,
+                                          const Run<U>& run) {
+  const int64_t c0 = run.at / elem_size(DT);
+  const uint8_t* pc = codes + run.row * a.codes_pitch + c0;
+  const uint8_t* ps = scales + run.row * a.scales_pitch + c0 / kActGroup;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t c = code_at<DT>(i);
+    s.c[i] = Codes<Elem<DT>::V>{};
+    s.b[i] = 0u;
+    if (run.inner || c0 + c < a.codes_pitch) {
+      s.c[i] = load_codes<Elem<DT>::V>(pc + c);
+      s.b[i] = __ldg(ps + c / kActGroup);
+    }
+  }
+}
+
+// KIND == kKindNone: restore.
+template <int DT, int KIND, bool GATED, bool ALIGNED, int U>
+__global__ void __launch_bounds__(kThreads)
+    act_backward_kernel(const __grid_constant__ Args a) {
+  using E = Elem<DT>;
+  constexpr int V = E::V;
+  const Run<U> run(a);
+  if (!run.any) return;
+  uint4 r[U], h[U];
+  Saved<V, U> sx, sg;
+  if (KIND != kKindNone)
+    load_run<DT, ALIGNED>(r, a.x.p + run.row * a.x.pitch, run.at, run.inner, a.row_bytes,
+                          a.x.end);
+  saved_run<DT>(sx, a.codes, a.scales, a, run);
+  if (GATED) saved_run<DT>(sg, a.gate_codes, a.gate_scales, a, run);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float x[V];
+    decode<V>(x, sx.c[i], sx.b[i]);
+    if (KIND != kKindNone) {
+      float dy[V], g[V], dg[V];
+      E::unpack(r[i], dy);
+      if (GATED) decode<V>(g, sg.c[i], sg.b[i]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float f, d;
+        act<KIND, true>(x[j], f, d);
+        if (GATED) dg[j] = dy[j] * f;
+        x[j] = (GATED ? dy[j] * g[j] : dy[j]) * d;
+      }
+      if (GATED) h[i] = E::pack(dg);
+    }
+    r[i] = E::pack(x);
+  }
+  store_run<DT, ALIGNED>(a.y.p + run.row * a.y.pitch, run.at, run.inner, a.row_bytes, r);
+  if (GATED)
+    store_run<DT, ALIGNED>(a.gate.p + run.row * a.gate.pitch, run.at, run.inner, a.row_bytes, h);
+}
+
+// --- host ----------------------------------------------------------------------------------------
+
+constexpr int kUnroll = 4;
+
+template <int DT, int KIND, bool GATED, bool BACK, bool ALIGNED>
+void launch_sized(gc_ctx* ctx, Args a, int64_t rows) {
+  const int64_t segs = ceil_div(a.codes_pitch / Elem<DT>::V, 32);  // of 32 units, per row
+  // long runs where a row has one and every SM gets at least two blocks of
+  // them; else a unit per lane (17 x 4096 bf16: 34 blocks instead of 9)
+  const int64_t runs = ceil_div(segs, kUnroll);
+  const bool large = segs >= kUnroll && rows * runs >= (int64_t)ctx->num_sms * 16;
+  a.runs = (uint32_t)(large ? runs : segs);
+  a.total = rows * a.runs;
+  const unsigned g = (unsigned)ceil_div(a.total, kThreads / 32);
+  if (BACK) {
+    if (large)
+      act_backward_kernel<DT, KIND, GATED, ALIGNED, kUnroll><<<g, kThreads, 0, ctx->stream>>>(a);
+    else
+      act_backward_kernel<DT, KIND, GATED, ALIGNED, 1><<<g, kThreads, 0, ctx->stream>>>(a);
+  } else {
+    if (large)
+      act_forward_kernel<DT, KIND, GATED, ALIGNED, kUnroll><<<g, kThreads, 0, ctx->stream>>>(a);
+    else
+      act_forward_kernel<DT, KIND, GATED, ALIGNED, 1><<<g, kThreads, 0, ctx->stream>>>(a);
+  }
+}
+
+template <int KIND, bool GATED, bool BACK>
+gc_status launch_typed(gc_ctx* ctx, const Args& a, int64_t rows, int dtype, bool aligned) {
+  if (dtype == GC_F32) {
+    if (aligned) launch_sized<GC_F32, KIND, GATED, BACK, true>(ctx, a, rows);
+    else launch_sized<GC_F32, KIND, GATED, BACK, false>(ctx, a, rows);
+  } else if (dtype == GC_BF16) {
+    if (aligned) launch_sized<GC_BF16, KIND, GATED, BACK, true>(ctx, a, rows);
+    else launch_sized<GC_BF16, KIND, GATED, BACK, false>(ctx, a, rows);
+  } else {
+    if (aligned) launch_sized<GC_F16, KIND, GATED, BACK, true>(ctx, a, rows);
+    else launch_sized<GC_F16, KIND, GATED, BACK, false>(ctx, a, rows);
+  }
+  return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}
+
+Mat mat(const void* p, int64_t ld, int dtype, int64_t rows, int64_t cols) {
+  const int e = elem_size(dtype);
+  char* c = static_cast<char*>(const_cast<void*>(p));
+  return {c, ld * e, c + ((rows - 1) * ld + cols) * e};
+}
+
+Args common(int dtype, int64_t cols) {
+  Args a{};
+  a.row_bytes = cols * elem_size(dtype);
+  a.codes_pitch = ckpt_codes_pitch(cols);
+  a.scales_pitch = ckpt_scales_pitch(cols);
+  return a;
+}
 
 }  // namespace
 
 gc_status launch_ckpt_save(gc_ctx* ctx, const void* x, int dtype, int64_t rows, int64_t cols,
                            int64_t ldx, uint8_t* codes, uint8_t* scales) {
   if (rows == 0 || cols == 0) return GC_OK;
-  FwdArgs a{};
-  a.x = x;
+  Args a = common(dtype, cols);
+  a.x = mat(x, ldx, dtype, rows, cols);
   a.codes = codes;
   a.scales = scales;
-  a.ldx = ldx;
-  a.cols = cols;
-  a.codes_pitch = ckpt_codes_pitch(cols);
-  a.scales_pitch = ckpt_scales_pitch(cols);
-  a.total = rows * (a.codes_pitch / kChunk);
   LaunchScope L(ctx, GC_PHASE_CKPT_SAVE);
-  forward_kind<kKindNone, false>(ctx, a, dtype, row_aligned(ldx, dtype));
-  return launched();
+  return launch_typed<kKindNone, false, false>(ctx, a, rows, dtype, row_aligned(ldx, dtype));
 }
 
 gc_status launch_ckpt_restore(gc_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int dtype,
                               int64_t rows, int64_t cols, void* x_out, int64_t ldx) {
   if (rows == 0 || cols == 0) return GC_OK;
-  BwdArgs a{};
-  a.codes = codes;
-  a.scales = scales;
-  a.dx = x_out;
-  a.lddx = ldx;
-  a.cols = cols;
-  a.codes_pitch = ckpt_codes_pitch(cols);
-  a.scales_pitch = ckpt_scales_pitch(cols);
-  a.total = rows * (a.codes_pitch / kChunk);
-  const bool vec = row_aligned(ldx, dtype);
+  Args a = common(dtype, cols);
+  a.y = mat(x_out, ldx, dtype, rows, cols);
+  a.codes = const_cast<uint8_t*>(codes);
+  a.scales = const_cast<uint8_t*>(scales);
   LaunchScope L(ctx, GC_PHASE_CKPT_RESTORE);
-  if (dtype == GC_F32) restore_dt<GC_F32>(ctx, a, vec);
-  else if (dtype == GC_BF16) restore_dt<GC_BF16>(ctx, a, vec);
-  else restore_dt<GC_F16>(ctx, a, vec);
-  return launched();
+  return launch_typed<kKindNone, false, true>(ctx, a, rows, dtype, row_aligned(ldx, dtype));
 }
 
 gc_status launch_act_forward(gc_ctx* ctx, int kind, const void* x, int64_t ldx, const void* gate,
@@ -273,32 +310,22 @@ gc_status launch_act_forward(gc_ctx* ctx, int kind, const void* x, int64_t ldx, 
                              int64_t ldy, uint8_t* codes, uint8_t* scales, uint8_t* gate_codes,
                              uint8_t* gate_scales) {
   if (rows == 0 || cols == 0) return GC_OK;
-  FwdArgs a{};
-  a.x = x;
-  a.gate = gate;
-  a.y = y;
+  Args a = common(dtype, cols);
+  a.x = mat(x, ldx, dtype, rows, cols);
+  if (gate) a.gate = mat(gate, ldgate, dtype, rows, cols);
+  a.y = mat(y, ldy, dtype, rows, cols);
   a.codes = codes;
   a.scales = scales;
   a.gate_codes = gate_codes;
   a.gate_scales = gate_scales;
-  a.ldx = ldx;
-  a.ldgate = ldgate;
-  a.ldy = ldy;
-  a.cols = cols;
-  a.codes_pitch = ckpt_codes_pitch(cols);
-  a.scales_pitch = ckpt_scales_pitch(cols);
-  a.total = rows * (a.codes_pitch / kChunk);
-  const bool vec = row_aligned(ldx, dtype) && row_aligned(ldy, dtype) &&
-                   (!gate || row_aligned(ldgate, dtype));
+  const bool aligned = row_aligned(ldx, dtype) && row_aligned(ldy, dtype) &&
+                       (!gate || row_aligned(ldgate, dtype));
   LaunchScope L(ctx, GC_PHASE_ACT_FORWARD);
-  if (kind == GC_GELU) {
-    if (gate) forward_kind<GC_GELU, true>(ctx, a, dtype, vec);
-    else forward_kind<GC_GELU, false>(ctx, a, dtype, vec);
-  } else {
-    if (gate) forward_kind<GC_SILU, true>(ctx, a, dtype, vec);
-    else forward_kind<GC_SILU, false>(ctx, a, dtype, vec);
-  }
-  return launched();
+  if (kind == GC_GELU)
+    return gate ? launch_typed<GC_GELU, true, false>(ctx, a, rows, dtype, aligned)
+                : launch_typed<GC_GELU, false, false>(ctx, a, rows, dtype, aligned);
+  return gate ? launch_typed<GC_SILU, true, false>(ctx, a, rows, dtype, aligned)
+              : launch_typed<GC_SILU, false, false>(ctx, a, rows, dtype, aligned);
 }
 
 gc_status launch_act_backward(gc_ctx* ctx, int kind, const void* dy, int64_t lddy,
@@ -307,32 +334,22 @@ gc_status launch_act_backward(gc_ctx* ctx, int kind, const void* dy, int64_t ldd
                               int64_t rows, int64_t cols, void* dx, int64_t lddx, void* dgate,
                               int64_t lddgate) {
   if (rows == 0 || cols == 0) return GC_OK;
-  BwdArgs a{};
-  a.dy = dy;
-  a.dx = dx;
-  a.dgate = dgate;
-  a.codes = codes;
-  a.scales = scales;
-  a.gate_codes = gate_codes;
-  a.gate_scales = gate_scales;
-  a.lddy = lddy;
-  a.lddx = lddx;
-  a.lddgate = lddgate;
-  a.cols = cols;
-  a.codes_pitch = ckpt_codes_pitch(cols);
-  a.scales_pitch = ckpt_scales_pitch(cols);
-  a.total = rows * (a.codes_pitch / kChunk);
-  const bool vec = row_aligned(lddy, dtype) && row_aligned(lddx, dtype) &&
-                   (!dgate || row_aligned(lddgate, dtype));
+  Args a = common(dtype, cols);
+  a.x = mat(dy, lddy, dtype, rows, cols);
+  if (dgate) a.gate = mat(dgate, lddgate, dtype, rows, cols);
+  a.y = mat(dx, lddx, dtype, rows, cols);
+  a.codes = const_cast<uint8_t*>(codes);
+  a.scales = const_cast<uint8_t*>(scales);
+  a.gate_codes = const_cast<uint8_t*>(gate_codes);
+  a.gate_scales = const_cast<uint8_t*>(gate_scales);
+  const bool aligned = row_aligned(lddy, dtype) && row_aligned(lddx, dtype) &&
+                       (!dgate || row_aligned(lddgate, dtype));
   LaunchScope L(ctx, GC_PHASE_ACT_BACKWARD);
-  if (kind == GC_GELU) {
-    if (dgate) backward_kind<GC_GELU, true>(ctx, a, dtype, vec);
-    else backward_kind<GC_GELU, false>(ctx, a, dtype, vec);
-  } else {
-    if (dgate) backward_kind<GC_SILU, true>(ctx, a, dtype, vec);
-    else backward_kind<GC_SILU, false>(ctx, a, dtype, vec);
-  }
-  return launched();
+  if (kind == GC_GELU)
+    return dgate ? launch_typed<GC_GELU, true, true>(ctx, a, rows, dtype, aligned)
+                 : launch_typed<GC_GELU, false, true>(ctx, a, rows, dtype, aligned);
+  return dgate ? launch_typed<GC_SILU, true, true>(ctx, a, rows, dtype, aligned)
+               : launch_typed<GC_SILU, false, true>(ctx, a, rows, dtype, aligned);
 }
 
 }  // namespace gc

@@ -574,7 +574,6 @@ gc_status launch_act_backward(gc_ctx* ctx, int kind, const void* dy, int64_t ldd
                               int64_t rows, int64_t cols, void* dx, int64_t lddx, void* dgate,
                               int64_t lddgate);
 // Layer norm (gc_norm.cu); `part` is the scratch of the column sums.
-constexpr int kNormMaxParts = 304;  // partial rows of the column sums
 int64_t norm_scratch_bytes(int64_t rows, int64_t cols);
 gc_status launch_norm_forward(gc_ctx* ctx, const void* x, int dtype, int64_t rows, int64_t cols,
                               int64_t ldx, const void* gamma, const void* beta, int ptype,

@@ -184,18 +184,7 @@ __device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
                : "memory");
 }
 
-// Two codes (the bytes that `sel` puts twice each into the halves) as bf16:
-// sign, exponent B and the seven bits m make +-(128 + m) 2^(B - 134); taking
-// +-128 2^(B - 134) off is exact.
-__device__ __forceinline__ uint32_t two_bf16(uint32_t w, uint32_t sel, uint32_t bexp) {
-  const uint32_t v = __byte_perm(w, 0u, sel);
-  const uint32_t x = (v & 0x807F807Fu) | bexp, c = (v & 0x80008000u) | bexp;
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(c));
-  return d;
-}
-
-// The same as fp16: +-(1 + m / 128) * 2 less +-2 is +-m * 2^-6; times
+// decode2 in fp16: +-(1 + m / 128) * 2 less +-2 is +-m * 2^-6; times
 // 2^(B - 128), a power of two that fp16 holds for every B an fp16 value can
 // have (104 .. 143), subnormals included.
 __device__ __forceinline__ uint32_t two_f16(uint32_t w, uint32_t sel, uint32_t scale) {
@@ -224,8 +213,8 @@ __device__ __forceinline__ uint4 eight(uint32_t w0, uint32_t w1, uint32_t s) {
   if (F16)
     return make_uint4(two_f16(w0, 0x1404u, s), two_f16(w0, 0x3424u, s), two_f16(w1, 0x1404u, s),
                       two_f16(w1, 0x3424u, s));
-  return make_uint4(two_bf16(w0, 0x1100u, s), two_bf16(w0, 0x3322u, s), two_bf16(w1, 0x1100u, s),
-                    two_bf16(w1, 0x3322u, s));
+  return make_uint4(decode2(w0, 0x1100u, s), decode2(w0, 0x3322u, s), decode2(w1, 0x1100u, s),
+                    decode2(w1, 0x3322u, s));
 }
 
 template <bool F16>
@@ -556,79 +545,69 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__
 // dy as planes of 16-bit values with 16-byte rows that the tensor maps take:
 // fp32 cut into three bf16 values whose sum it is (8 significant bits each,
 // by truncation, so every remainder is exact and no plane overflows); 16-bit
-// types as they are.  Rows past `rows` and columns past `out` are zero.
-template <int DT>
-__global__ void __launch_bounds__(256) wgrad_split_kernel(const void* dy, int64_t rows,
-                                                          int64_t out, int64_t lddy,
-                                                          uint16_t* planes, int64_t plane_rows,
-                                                          int64_t pitch) {
+// types as they are.  Rows past `rows` and columns past `out` are zero.  A
+// warp takes 32 consecutive units of 16 bytes of one row of dy.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(256) wgrad_split_kernel(const char* dy, const char* end,
+                                                          int64_t rows, int64_t row_bytes,
+                                                          int64_t dy_pitch, uint16_t* planes,
+                                                          int64_t plane_rows, int64_t pitch) {
   using E = Elem<DT>;
-  const int64_t per = pitch / kChunk, total = plane_rows * per;
-  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total;
-       at += (int64_t)gridDim.x * 256) {
-    const int64_t r = at / per, c = (at - r * per) * kChunk;
-    const int valid = r < rows ? (int)min((int64_t)kChunk, out - c) : 0;
-    const typename E::T* src = static_cast<const typename E::T*>(dy) + r * lddy + c;
-    uint16_t* dst = planes + r * pitch + c;
+  constexpr int V = E::V;
+  const int64_t segs = (pitch + 32 * V - 1) / (32 * V), total = plane_rows * segs;
+  for (int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); at < total;
+       at += (int64_t)gridDim.x * 8) {
+    const int64_t r = at / segs, u = (at - r * segs) * 32 + (threadIdx.x & 31);
+    const uint4 raw = r < rows ? load_unit<DT, ALIGNED>(dy + r * dy_pitch, u * 16, row_bytes, end)
+                               : make_uint4(0u, 0u, 0u, 0u);
+    if (u * V >= pitch) continue;
+    uint16_t* dst = planes + r * pitch + u * V;
     if (DT == GC_F32) {
-      uint32_t w[3][4];
+      uint32_t rest[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t p[3][2];
+      for (int k = 0; k < 3; ++k) {
+        uint32_t p[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = 2 * j + e < valid ? E::to_float(src[2 * j + e]) : 0.0f;
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            p[k][e] = __float_as_uint(x) & 0xFFFF0000u;
-            x = __fsub_rn(x, __uint_as_float(p[k][e]));
-          }
+        for (int e = 0; e < 4; ++e) {
+          p[e] = rest[e] & 0xFFFF0000u;
+          rest[e] = __float_as_uint(__fsub_rn(__uint_as_float(rest[e]), __uint_as_float(p[e])));
         }
-#pragma unroll
-        for (int k = 0; k < 3; ++k) w[k][j] = (p[k][0] >> 16) | p[k][1];
+        *reinterpret_cast<uint2*>(dst + k * plane_rows * pitch) =
+            make_uint2(__byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
       }
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint4*>(dst + k * plane_rows * pitch) =
-            make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
     } else {
-      const uint16_t* s16 = reinterpret_cast<const uint16_t*>(src);
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = (2 * j < valid ? s16[2 * j] : 0u) |
-               ((uint32_t)(2 * j + 1 < valid ? s16[2 * j + 1] : 0u) << 16);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst) = raw;
     }
   }
 }
 
-// Column sums of dy: block (x, y) adds rows y * rows_per .. of 256 columns
-// (32 lanes x 8), eight warps taking every eighth row, into part[y][out], or
-// into db when there is one row range.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) bias_kernel(const void* dy, int64_t rows, int64_t out,
-                                                   int64_t lddy, int64_t rows_per, float* part,
-                                                   float* db, int accumulate) {
+// Column sums of dy: block (x, y) adds rows y * rows_per .. of 32 units (256
+// columns, 128 of fp32), eight warps taking every eighth row, into
+// part[y][out], or into db when there is one row range.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(256) bias_kernel(const char* dy, const char* end, int64_t rows,
+                                                   int64_t out, int64_t dy_pitch,
+                                                   int64_t rows_per, float* part, float* db,
+                                                   int accumulate) {
   using E = Elem<DT>;
-  __shared__ float s[8][256 + 8];
+  constexpr int V = E::V, W = 32 * V;
+  __shared__ float s[8][W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 256 + lane * kChunk;
-  const int valid = (int)max((int64_t)0, min((int64_t)kChunk, out - c));
+  const int64_t off = ((int64_t)blockIdx.x * 32 + lane) * 16;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(rows, r0 + rows_per);
-  float v[8] = {};
-  if (valid > 0)
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      float d[8];
-      load_chunk<DT, VEC>(d, static_cast<const typename E::T*>(dy) + r * lddy + c, valid);
+  float v[V] = {};
+#pragma unroll 4
+  for (int64_t r = r0 + warp; r < r1; r += 8) {
+    float d[V];
+    E::unpack(load_unit<DT, ALIGNED>(dy + r * dy_pitch, off, out * elem_size(DT), end), d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += d[j];
-    }
+    for (int j = 0; j < V; ++j) v[j] += d[j];
+  }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[warp][lane * 8 + j] = v[j];
+  for (int j = 0; j < V; ++j) s[warp][lane * V + j] = v[j];
   __syncthreads();
-  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (o >= out) return;
+  const int64_t o = (int64_t)blockIdx.x * W + threadIdx.x;
+  if ((int)threadIdx.x >= W || o >= out) return;
   float t = 0.0f;
 #pragma unroll
   for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
@@ -711,36 +690,46 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int6
 template <int DT>
 void launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy, float* db,
                  int accumulate, float* part) {
-  const int64_t bx = ceil_div(out, 256);
+  constexpr int kSize = elem_size(DT);
+  const int64_t bx = ceil_div(out, 32 * Elem<DT>::V);
   const int64_t want = std::min<int64_t>({ceil_div((int64_t)ctx->num_sms * 8, bx),
                                           ceil_div(rows, 64), (int64_t)kMaxBiasParts});
   const int64_t rows_per = ceil_div(rows, std::max<int64_t>(want, 1));
   const int64_t by = ceil_div(rows, rows_per);
   const dim3 g((unsigned)bx, (unsigned)by);
-  constexpr int kSize = DT == GC_F32 ? 4 : 2;
+  const char* p = static_cast<const char*>(dy);
+  const char* end = p + ((rows - 1) * lddy + out) * kSize;
   {
     LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
-    if (lddy * kSize % 16 == 0)
-      bias_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(dy, rows, out, lddy, rows_per, part, db,
-                                                        accumulate);
+    if (row_aligned(lddy, DT))
+      bias_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize, rows_per,
+                                                        part, db, accumulate);
     else
-      bias_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(dy, rows, out, lddy, rows_per, part, db,
-                                                         accumulate);
+      bias_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize,
+                                                         rows_per, part, db, accumulate);
   }
   if (by > 1) {
     LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
-    bias_join_kernel<<<(unsigned)bx, 256, 0, ctx->stream>>>(part, (int)by, out, db, accumulate);
+    bias_join_kernel<<<(unsigned)ceil_div(out, 256), 256, 0, ctx->stream>>>(part, (int)by, out, db,
+                                                                            accumulate);
   }
 }
 
 template <int DT>
 void launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
                   uint16_t* planes, int64_t plane_rows, int64_t pitch) {
-  const int64_t total = plane_rows * (pitch / kChunk);
-  const unsigned g = (unsigned)std::min<int64_t>(ceil_div(total, 256), (int64_t)ctx->num_sms * 8);
+  constexpr int kSize = elem_size(DT);
+  const int64_t total = plane_rows * ceil_div(pitch, 32 * Elem<DT>::V);
+  const unsigned g = (unsigned)std::min<int64_t>(ceil_div(total, 8), (int64_t)ctx->num_sms * 8);
+  const char* p = static_cast<const char*>(dy);
+  const char* end = p + ((rows - 1) * lddy + out) * kSize;
   LaunchScope L(ctx, GC_PHASE_WGRAD_SPLIT);
-  wgrad_split_kernel<DT><<<g, 256, 0, ctx->stream>>>(dy, rows, out, lddy, planes, plane_rows,
-                                                     pitch);
+  if (row_aligned(lddy, DT))
+    wgrad_split_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(
+        p, end, rows, out * kSize, lddy * kSize, planes, plane_rows, pitch);
+  else
+    wgrad_split_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(
+        p, end, rows, out * kSize, lddy * kSize, planes, plane_rows, pitch);
 }
 
 template <bool F16>
