@@ -101,20 +101,48 @@ struct Elem<GC_F16> {
   static __device__ __forceinline__ float to_float(T x) { return __half2float(x); }
 };
 
+// A unit as pairs, for the packed fp32 instructions.
+template <int DT>
+__device__ __forceinline__ void unpack2(const uint4& r, float2 (&v)[Elem<DT>::V / 2]) {
+  float f[Elem<DT>::V];
+  Elem<DT>::unpack(r, f);
+#pragma unroll
+  for (int i = 0; i < Elem<DT>::V / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack2(const float2 (&v)[Elem<DT>::V / 2]) {
+  float f[Elem<DT>::V];
+#pragma unroll
+  for (int i = 0; i < Elem<DT>::V / 2; ++i) {
+    f[2 * i] = v[i].x;
+    f[2 * i + 1] = v[i].y;
+  }
+  return Elem<DT>::pack(f);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 constexpr int elem_size(int dtype) { return dtype == GC_F32 ? 4 : 2; }
 inline bool row_aligned(int64_t ld, int dtype) { return ld * elem_size(dtype) % 16 == 0; }
 
 // ---------------------------------------------------------------------------
-// Units of a row.  `row` is its first byte, `off` the first byte of the
-// thread's unit, `bytes` the row's length; a unit past the end reads as zero
-// and is not stored.
+// Runs of units.  A warp's run is U times 32 consecutive units of a row, from
+// byte `at` (a multiple of 512) of the row on; lane l has units l, l + 32, ...
+// Columns past the row's `bytes` read as zero and are not stored.  Inside the
+// row (`inner`, the same in the whole warp: at + 512 U <= bytes, 16 less where
+// rows are not aligned) nothing is checked and every address is one base plus
+// a constant.
+//
+// Rows that start anywhere are read and written in the aligned 16-byte pieces
+// that cover the run; lanes exchange neighbouring pieces and cut their units
+// from them.  A piece may hold bytes of the row before (never from before the
+// matrix: its first row is aligned) or of the row after; nothing is read past
+// `end`, the matrix's end, and pieces that the run does not fill are stored
+// by elements.
 // ---------------------------------------------------------------------------
 
-// Elements [0, n) of 16 bytes, one by one.  (This and store_some run at the
-// ends of rows only; out of line they keep the kernels within the
-// instruction cache.)
+// Elements [0, n) of 16 bytes, one by one.
 template <int DT>
-__device__ __noinline__ uint4 load_some(const char* p, int n) {
+__device__ __forceinline__ uint4 load_some(const char* p, int n) {
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -131,7 +159,7 @@ __device__ __noinline__ uint4 load_some(const char* p, int n) {
 
 // Elements [lo, hi) of 16 bytes, one by one.
 template <int DT>
-__device__ __noinline__ void store_some(char* p, uint4 r, int lo, int hi) {
+__device__ __forceinline__ void store_some(char* p, const uint4& r, int lo, int hi) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -143,22 +171,6 @@ __device__ __noinline__ void store_some(char* p, uint4 r, int lo, int hi) {
       if (2 * i + 1 >= lo && 2 * i + 1 < hi) h[2 * i + 1] = (uint16_t)(w[i] >> 16);
     }
   }
-}
-
-// Rows that start on 16-byte boundaries: a thread's own load and store.
-template <int DT>
-__device__ __forceinline__ uint4 load_aligned(const char* row, int64_t off, int64_t bytes) {
-  const int64_t left = bytes - off;
-  if (left >= 16) return __ldg(reinterpret_cast<const uint4*>(row + off));
-  if (left <= 0) return make_uint4(0u, 0u, 0u, 0u);
-  return load_some<DT>(row + off, (int)left / elem_size(DT));
-}
-template <int DT>
-__device__ __forceinline__ void store_aligned(char* row, int64_t off, int64_t bytes,
-                                              const uint4& r) {
-  const int64_t left = bytes - off;
-  if (left >= 16) *reinterpret_cast<uint4*>(row + off) = r;
-  else if (left > 0) store_some<DT>(row + off, r, 0, (int)left / elem_size(DT));
 }
 
 // 16 of the 32 bytes lo ++ hi, from byte `shift` (0..15, even; the same in
@@ -176,160 +188,158 @@ __device__ __forceinline__ uint4 funnel(const uint4& lo, const uint4& hi, uint32
                     __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
 }
 
-// Rows that start anywhere, the warp's 32 units being consecutive in one row
-// (all lanes call; a whole warp may lie past the end).  Memory is read in
-// the aligned 16-byte pieces that cover the units, each once per warp, and
-// the units are cut from neighbouring lanes' pieces.  A piece may hold bytes
-// of the row before (never before the matrix: its first row is aligned) or
-// after; `end` is the matrix's end, past which nothing is read.
-template <int DT>
-__device__ __forceinline__ uint4 load_ragged(const char* row, int64_t off, int64_t bytes,
-                                             const char* end) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-  const char* p = row + off - mis;
-  auto piece = [&](const char* q, int64_t at) -> uint4 {  // `at`: q's place in the row
-    if (at >= bytes) return make_uint4(0u, 0u, 0u, 0u);
-    if (end - q >= 16) return __ldg(reinterpret_cast<const uint4*>(q));
-    return load_some<DT>(q, (int)(end - q) / elem_size(DT));
-  };
-  const uint4 a = piece(p, off - mis);
-  uint4 r = a;
-  if (mis) {
-    uint4 next = make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 31) next = piece(p + 16, off - mis + 16);
-    const uint4 n = make_uint4(__shfl_down_sync(0xffffffffu, a.x, 1),
-                               __shfl_down_sync(0xffffffffu, a.y, 1),
-                               __shfl_down_sync(0xffffffffu, a.z, 1),
-                               __shfl_down_sync(0xffffffffu, a.w, 1));
-    r = funnel(a, lane == 31 ? next : n, mis);
-  }
-  // columns past the row's end are zero
-  const int64_t left = bytes - off;
-  if (left < 16) {
-    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ uint4 shfl4(const uint4& v, int from) {
+  return make_uint4(__shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
+                    __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
+}
+
+// The unit with the columns from byte `left` on set to zero.
+__device__ __forceinline__ void cut_unit(uint4& r, int64_t left) {
+  if (left >= 16) return;
+  uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (left <= 4 * i) w[i] = 0u;
-      else if (left == 4 * i + 2) w[i] &= 0xFFFFu;
-    }
-    r = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    if (left <= 4 * i) w[i] = 0u;
+    else if (left == 4 * i + 2) w[i] &= 0xFFFFu;
   }
-  return r;
+  r = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The store of such units: pieces that the warp's units fill are stored
-// whole, the elements of the others one by one.
-template <int DT>
-__device__ __forceinline__ void store_ragged(char* row, int64_t off, int64_t bytes,
-                                             const uint4& r) {
-  constexpr int E = elem_size(DT);
-  const int lane = threadIdx.x & 31;
-  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-  if (!mis) {
-    store_aligned<DT>(row, off, bytes, r);
-    return;
-  }
-  const uint4 b = make_uint4(__shfl_up_sync(0xffffffffu, r.x, 1),
-                             __shfl_up_sync(0xffffffffu, r.y, 1),
-                             __shfl_up_sync(0xffffffffu, r.z, 1),
-                             __shfl_up_sync(0xffffffffu, r.w, 1));
-  const uint4 piece = funnel(b, r, 16u - mis);
-  char* p = row + off - mis;                 // the piece that the unit starts in
-  const int64_t left = bytes - (off - mis);  // of the row, from there
-  if (lane > 0 && left >= 16) *reinterpret_cast<uint4*>(p) = piece;
-  else if (left > 0)
-    store_some<DT>(p, piece, lane > 0 ? 0 : (int)mis / E, (int)min(left, (int64_t)16) / E);
-  // the last unit's end lies in a piece that the warp does not fill
-  if (lane == 31 && left > 16)
-    store_some<DT>(p + 16, funnel(r, r, 16u - mis), 0,
-                   (int)min(left - 16, (int64_t)mis) / E);
-}
-
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ uint4 load_unit(const char* row, int64_t off, int64_t bytes,
-                                           const char* end) {
-  return ALIGNED ? load_aligned<DT>(row, off, bytes) : load_ragged<DT>(row, off, bytes, end);
-}
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void store_unit(char* row, int64_t off, int64_t bytes,
-                                           const uint4& r) {
-  if (ALIGNED) store_aligned<DT>(row, off, bytes, r);
-  else store_ragged<DT>(row, off, bytes, r);
-}
-
-// A warp's run: U times 32 consecutive units from byte `at` (a multiple of
-// 512) of a row on; lane l has units l, l + 32, ...  Inside the row (`inner`,
-// the same in the whole warp: at + 512 U + 16 <= bytes) nothing is checked
-// and every address is one base plus a constant.
 template <int DT, bool ALIGNED, int U>
 __device__ __forceinline__ void load_run(uint4 (&r)[U], const char* row, uint32_t at, bool inner,
                                          int64_t bytes, const char* end) {
+  constexpr int E = elem_size(DT);
   const uint32_t lane = threadIdx.x & 31u;
-  if (!inner) {
+  const uint32_t mis = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  const int64_t o = (int64_t)at + lane * 16u - mis;  // the first piece's place in the row
+  const char* p = row + o;
+  if (inner) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) r[i] = __ldg(reinterpret_cast<const uint4*>(p + i * 512));
+  } else if (ALIGNED && (bytes & 15) == 0) {  // whole units
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      r[i] = o + i * 512 < bytes ? __ldg(reinterpret_cast<const uint4*>(p + i * 512))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+    return;
+  } else {
+    const int64_t e = end - row;
+    int cut = -1;  // the piece that the matrix ends in
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t seg = (int64_t)at + i * 512;
-      r[i] = seg < bytes ? load_unit<DT, ALIGNED>(row, seg + lane * 16, bytes, end)
-                         : make_uint4(0u, 0u, 0u, 0u);
+      const int64_t oi = o + i * 512;
+      r[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (oi < bytes) {
+        if (oi + 16 <= e) r[i] = __ldg(reinterpret_cast<const uint4*>(p + i * 512));
+        else cut = i;
+      }
     }
-    return;
+    if (cut >= 0) {
+      const uint4 v = load_some<DT>(p + cut * 512, (int)(e - o - cut * 512) / E);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (i == cut) r[i] = v;
+    }
   }
-  const uint32_t mis = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-  const char* p = row + at + lane * 16u - mis;
+  if (!ALIGNED && mis) {
+    uint4 last = make_uint4(0u, 0u, 0u, 0u);  // the piece behind the run, for lane 31
+    const int64_t ol = o + (U - 1) * 512 + 16;
+    if (lane == 31u && (inner || ol < bytes)) {
+      if (inner || ol + 16 <= end - row) last = __ldg(reinterpret_cast<const uint4*>(row + ol));
+      else last = load_some<DT>(row + ol, (int)(end - row - ol) / E);
+    }
 #pragma unroll
-  for (int i = 0; i < U; ++i) r[i] = __ldg(reinterpret_cast<const uint4*>(p + i * 512));
-  if (ALIGNED || mis == 0u) return;
-  uint4 last = r[U - 1];  // the piece behind the run, for lane 31
-  if (lane == 31u) last = __ldg(reinterpret_cast<const uint4*>(p + (U - 1) * 512 + 16));
+    for (int i = 0; i < U; ++i) {
+      // the next lane's piece; lane 31's next is lane 0's of the next segment
+      const uint4 v = (i + 1 < U && lane == 0u) ? r[i + 1 < U ? i + 1 : i] : r[i];
+      uint4 n = shfl4(v, (int)((lane + 1u) & 31u));
+      if (i == U - 1 && lane == 31u) n = last;
+      r[i] = funnel(r[i], n, mis);
+    }
+  }
+  if (!inner) {
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    // the next lane's piece; lane 31's next is lane 0's of the next segment
-    const uint4 v = (i + 1 < U && lane == 0u) ? r[i + 1 < U ? i + 1 : i] : r[i];
-    const int from = (int)((lane + 1u) & 31u);
-    uint4 n = make_uint4(
-        __shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
-        __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
-    if (i == U - 1 && lane == 31u) n = last;
-    r[i] = funnel(r[i], n, mis);
+    for (int i = 0; i < U; ++i) cut_unit(r[i], bytes - at - i * 512 - lane * 16);
   }
 }
 
 template <int DT, bool ALIGNED, int U>
 __device__ __forceinline__ void store_run(char* row, uint32_t at, bool inner, int64_t bytes,
                                           const uint4 (&r)[U]) {
+  constexpr int E = elem_size(DT);
   const uint32_t lane = threadIdx.x & 31u;
-  if (!inner) {
+  const uint32_t mis = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+  const int64_t o = (int64_t)at + lane * 16u - mis;
+  char* p = row + o;
+  if (ALIGNED || mis == 0u) {
+    if (inner) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) *reinterpret_cast<uint4*>(p + i * 512) = r[i];
+      return;
+    }
+    if ((bytes & 15) == 0) {  // whole units
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (o + i * 512 < bytes) *reinterpret_cast<uint4*>(p + i * 512) = r[i];
+      return;
+    }
+    int cut = -1;  // the unit that the row ends in
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t seg = (int64_t)at + i * 512;
-      if (seg < bytes) store_unit<DT, ALIGNED>(row, seg + lane * 16, bytes, r[i]);
+      const int64_t left = bytes - o - i * 512;
+      if (left >= 16) {
+        *reinterpret_cast<uint4*>(p + i * 512) = r[i];
+      } else if (left > 0) {
+        cut = i;
+        v = r[i];
+      }
     }
+    if (cut >= 0) store_some<DT>(p + cut * 512, v, 0, (int)(bytes - o - cut * 512) / E);
     return;
   }
-  const uint32_t mis = ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-  char* p = row + at + lane * 16u - mis;
-  if (ALIGNED || mis == 0u) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) *reinterpret_cast<uint4*>(p + i * 512) = r[i];
-    return;
-  }
-  constexpr int E = elem_size(DT);
+  int cut = -1;  // the piece that the row ends in
+  uint4 v = make_uint4(0u, 0u, 0u, 0u), first = v;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     // the lane before's unit; lane 0's is lane 31's of the segment before
-    const uint4 v = (i > 0 && lane == 31u) ? r[i > 0 ? i - 1 : 0] : r[i];
-    const int from = (int)((lane + 31u) & 31u);
-    const uint4 b = make_uint4(
-        __shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
-        __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
-    const uint4 piece = funnel(b, r[i], 16u - mis);
-    if (i > 0 || lane > 0u) *reinterpret_cast<uint4*>(p + i * 512) = piece;
-    else store_some<DT>(p, piece, (int)mis / E, 16 / E);
+    const uint4 u = (i > 0 && lane == 31u) ? r[i > 0 ? i - 1 : 0] : r[i];
+    const uint4 piece = funnel(shfl4(u, (int)((lane + 31u) & 31u)), r[i], 16u - mis);
+    const int64_t left = bytes - o - i * 512;
+    if (i == 0 && lane == 0u) {
+      first = piece;
+    } else if (inner || left >= 16) {
+      *reinterpret_cast<uint4*>(p + i * 512) = piece;
+    } else if (left > 0) {
+      cut = i;
+      v = piece;
+    }
   }
-  if (lane == 31u)
+  if (cut >= 0) store_some<DT>(p + cut * 512, v, 0, (int)(bytes - o - cut * 512) / E);
+  if (lane == 0u)
+    store_some<DT>(p, first, (int)mis / E,
+                   (int)max((int64_t)0, min(bytes - o, (int64_t)16)) / E);
+  // the last unit's end lies in a piece that the run does not fill
+  const int64_t tail = bytes - o - (U - 1) * 512 - 16;
+  if (lane == 31u && tail > 0)
     store_some<DT>(p + (U - 1) * 512 + 16, funnel(r[U - 1], r[U - 1], 16u - mis), 0,
-                   (int)mis / E);
+                   (int)min(tail, (int64_t)mis) / E);
+}
+
+// One unit per lane, `off` being the lane's byte in the row (a whole warp's
+// units are consecutive).
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ uint4 load_unit(const char* row, int64_t off, int64_t bytes,
+                                           const char* end) {
+  uint4 r[1];
+  load_run<DT, ALIGNED>(r, row, (uint32_t)off - (threadIdx.x & 31u) * 16u, false, bytes, end);
+  return r[0];
+}
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void store_unit(char* row, int64_t off, int64_t bytes,
+                                           const uint4& r) {
+  const uint4 u[1] = {r};
+  store_run<DT, ALIGNED>(row, (uint32_t)off - (threadIdx.x & 31u) * 16u, false, bytes, u);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,7 +379,12 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
 __device__ __forceinline__ uint32_t encode4(const float* v, uint32_t signs, float up) {
   uint32_t q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(fabsf(v[i]), up, 8388608.0f));
+  for (int i = 0; i < 4; i += 2) {
+    const float2 m = __ffma2_rn(make_float2(fabsf(v[i]), fabsf(v[i + 1])), both(up),
+                                both(8388608.0f));
+    q[i] = __float_as_uint(m.x);
+    q[i + 1] = __float_as_uint(m.y);
+  }
   uint32_t m = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040),
                            0x5410);
   m -= (m >> 7) & 0x01010101u;
@@ -424,13 +439,22 @@ __device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t sel, uint32_t b
 }
 
 template <int V>
-__device__ __forceinline__ void decode(float (&v)[V], const Codes<V>& c, uint32_t b) {
+__device__ __forceinline__ void decode(float2 (&v)[V / 2], const Codes<V>& c, uint32_t b) {
   const uint32_t bexp = b * 0x00800080u;
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) {
     const uint32_t d = decode2(c.w[i / 2], i & 1 ? 0x3322u : 0x1100u, bexp);
-    v[2 * i] = __uint_as_float(d << 16);
-    v[2 * i + 1] = __uint_as_float(d & 0xFFFF0000u);
+    v[i] = make_float2(__uint_as_float(d << 16), __uint_as_float(d & 0xFFFF0000u));
+  }
+}
+template <int V>
+__device__ __forceinline__ void decode(float (&v)[V], const Codes<V>& c, uint32_t b) {
+  float2 p[V / 2];
+  decode<V>(p, c, b);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    v[2 * i] = p[i].x;
+    v[2 * i + 1] = p[i].y;
   }
 }
 

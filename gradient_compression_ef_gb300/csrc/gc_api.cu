@@ -44,13 +44,15 @@ gc_status check_buf(const void* p, bool used) {
 // Makes the context's device current for the duration of a call.
 struct DeviceGuard {
   int prev = -1;
-  bool ok = true;
+  bool ok = true, moved = false;
   explicit DeviceGuard(int dev) {
     if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+    if (prev == dev) return;
+    if (cudaSetDevice(dev) != cudaSuccess) ok = false;
+    else moved = true;
   }
   ~DeviceGuard() {
-    if (ok && prev >= 0) cudaSetDevice(prev);
+    if (moved) cudaSetDevice(prev);
   }
 };
 

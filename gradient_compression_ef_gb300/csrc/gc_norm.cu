@@ -13,12 +13,12 @@
 // then the output.  All sums are fp32, in an order that sizes alone decide.
 // Both passes are bound by memory; what they need is loads in flight and few
 // instructions per element:
-//   cols <= 1024        a warp per row, up to 4 units of 16 bytes per lane;
-//   wider, while two    a block walks over rows that one thread copies into a
-//   rows fit in shared  ring of stages in shared memory (bulk copies, several
-//   memory              rows ahead); a thread owns 16 or 32 columns for all
-//                       rows: parameters and column sums stay in registers,
-//                       and nothing but the stage changes from row to row;
+//   cols <= 512         a warp per row, up to 4 units of 16 bytes per lane;
+//   wider, while two    a block walks over rows that its producer warp copies
+//   rows fit in shared  into a ring of stages in shared memory (bulk copies,
+//   memory              several rows ahead); a thread owns 16 columns of all
+//                       rows, the column sums stay in its registers, and
+//                       nothing but the stage changes from row to row;
 //   wider still         the row is read again from L2 for each of its passes.
 // The backward pass leaves one partial row of column sums per block; a second
 // small grid adds the partials in block order.
@@ -116,20 +116,116 @@ __device__ __forceinline__ void keep_packed(uint4& r) {
   asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)::"memory");
 }
 
-// K units per thread, unit i of a thread being thread + i * threads.  K == 0:
-// rows wider than the registers hold; the row is read again (from L2) for
-// each of its three passes.
-template <int DT, int K, bool WARP, bool ALIGNED>
-__global__ void __launch_bounds__(WARP ? 256 : 1024)
+// A thread's V parameters of unit i, in shared memory.
+template <int V>
+__device__ __forceinline__ void lds_params(float2 (&g)[V / 2], uint32_t at) {
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    const float4 f = sm100::lds128(at + j * 4);
+    g[j / 2] = make_float2(f.x, f.y);
+    g[j / 2 + 1] = make_float2(f.z, f.w);
+  }
+}
+// A row per warp, K units per lane, no barrier; gamma and beta lie in shared
+// memory, shared by the block's warps.
+template <int DT, int K, bool ALIGNED>
+__global__ void __launch_bounds__(256, 4)
+    norm_forward_warp_kernel(const __grid_constant__ NormArgs a) {
+  using L = Elem<DT>;
+  constexpr int V = L::V, H = V / 2;
+  extern __shared__ __align__(16) float params[];  // gamma, beta: [2][K * 32 * V]
+  for (int c = threadIdx.x * V; c < K * 32 * V; c += 256 * V) {
+    float v[V];
+    load_params<V>(v, a.gamma, a.ptype, c, a.cols, 1.0f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) params[c + j] = v[j];
+    load_params<V>(v, a.beta, a.ptype, c, a.cols, 0.0f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) params[K * 32 * V + c + j] = v[j];
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const uint32_t gam = sm100::smem_u32(params) + lane * (V * 4), bet = gam + K * 32 * V * 4;
+  const float inv_n = 1.0f / (float)a.cols;
+  const bool inner = K * 512 + (ALIGNED ? 0 : 16) <= a.row_bytes;
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows;
+       row += (int64_t)gridDim.x * 8) {
+    uint4 raw[K];
+    load_run<DT, ALIGNED>(raw, a.x + row * a.xpitch, 0u, inner, a.row_bytes, a.xend);
+    float2 s = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      float2 v[H];
+      unpack2<DT>(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < H; ++j) s = __fadd2_rn(s, v[j]);
+    }
+    const float mean = warp_allsum(s.x + s.y) * inv_n;
+    const float2 m = both(-mean);
+    s = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      keep_packed(raw[i]);
+      float2 v[H];
+      unpack2<DT>(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[j] = __fadd2_rn(v[j], m);
+      if (!inner) {
+        const int64_t left = a.row_bytes - (i * 32 + lane) * 16;
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          if (2 * j * elem_size(DT) >= left) v[j].x = 0.0f;
+          if ((2 * j + 1) * elem_size(DT) >= left) v[j].y = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) s = __ffma2_rn(v[j], v[j], s);
+    }
+    const float rstd = rsqrtf(warp_allsum(s.x + s.y) * inv_n + a.eps);
+    if (lane == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    const float2 rs = both(rstd);
+    uint8_t* codes = a.codes + row * a.codes_pitch + lane * V;
+    uint8_t* scales = a.scales + row * a.scales_pitch + lane * V / kActGroup;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      keep_packed(raw[i]);
+      if (a.codes) {
+        float f[V];
+        L::unpack(raw[i], f);
+        const uint32_t sb = scale_byte(group_max_bits<DT>(raw[i]));
+        if (inner || (i * 32 + lane) * V < a.codes_pitch) {
+          store_codes<DT>(codes + i * 32 * V, raw[i], f, sb);
+          if (lane % (kActGroup / V) == 0) scales[i * 32 * V / kActGroup] = (uint8_t)sb;
+        }
+      }
+      float2 v[H], g[H], b[H];
+      unpack2<DT>(raw[i], v);
+      lds_params<V>(g, gam + i * 32 * V * 4);
+      lds_params<V>(b, bet + i * 32 * V * 4);
+#pragma unroll
+      for (int j = 0; j < H; ++j)
+        v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j], m), rs), g[j], b[j]);
+      raw[i] = pack2<DT>(v);
+    }
+    store_run<DT, ALIGNED>(a.out + row * a.outpitch, 0u, inner, a.row_bytes, raw);
+  }
+}
+
+// A row per block, one unit per thread (few rows: the shortest way through),
+// or K == 0: rows wider than the other kernels hold, read again (from L2) for
+// each of the three passes.
+template <int DT, int K, bool ALIGNED>
+__global__ void __launch_bounds__(1024)
     norm_forward_kernel(const __grid_constant__ NormArgs a) {
   using E = Elem<DT>;
   constexpr int V = E::V, KK = K ? K : 1;
   __shared__ float2 slot[2][32];
-  RowSum<WARP> sum{slot};
-  const int nt = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)
-                           : (int64_t)blockIdx.x;
-  if (row >= a.rows) return;  // whole warps only, no barrier follows for WARP
+  RowSum<false> sum{slot};
+  const int nt = blockDim.x, t = threadIdx.x;
+  const int64_t row = blockIdx.x;
   const float inv_n = 1.0f / (float)a.cols;
   const int loops = K ? K : (int)((a.codes_pitch / V + nt - 1) / nt);
   const char* x = a.x + row * a.xpitch;
@@ -196,6 +292,19 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
   }
 }
 
+// A block's column sums go to its partial row, or, when it is the only block,
+// to the gradients.
+__device__ __forceinline__ void put_sums(const NormArgs& a, int64_t part, bool only, int64_t c,
+                                         float g, float b) {
+  if (!only) {
+    a.part[part * 2 * a.cols + c] = g;
+    a.part[(part * 2 + 1) * a.cols + c] = b;
+    return;
+  }
+  if (a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + g : g;
+  if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + b : b;
+}
+
 // A unit's inputs as they lie in memory.
 template <int DT, bool CKPT>
 struct RawUnit {
@@ -212,7 +321,10 @@ template <int DT, bool CKPT, bool ALIGNED>
 __device__ __forceinline__ void load_raw(RawUnit<DT, CKPT>& r, const NormArgs& a, int64_t row,
                                          int64_t off) {
   constexpr int V = Elem<DT>::V;
-  r.dy = load_unit<DT, ALIGNED>(a.dy + row * a.dypitch, off, a.row_bytes, a.dyend);
+  const bool whole = ALIGNED && off + 16 <= a.row_bytes;
+  const char* dy = a.dy + row * a.dypitch;
+  r.dy = whole ? __ldg(reinterpret_cast<const uint4*>(dy + off))
+               : load_unit<DT, ALIGNED>(dy, off, a.row_bytes, a.dyend);
   if constexpr (CKPT) {
     const int64_t c = off / elem_size(DT);
     r.c = Codes<V>{};
@@ -222,7 +334,9 @@ __device__ __forceinline__ void load_raw(RawUnit<DT, CKPT>& r, const NormArgs& a
       r.b = __ldg(a.scales + row * a.scales_pitch + c / kActGroup);
     }
   } else {
-    r.x = load_unit<DT, ALIGNED>(a.x + row * a.xpitch, off, a.row_bytes, a.xend);
+    const char* x = a.x + row * a.xpitch;
+    r.x = whole ? __ldg(reinterpret_cast<const uint4*>(x + off))
+                : load_unit<DT, ALIGNED>(x, off, a.row_bytes, a.xend);
   }
 }
 
@@ -296,8 +410,6 @@ __global__ void __launch_bounds__(256, 2)
   }
 
   if (!a.dgamma && !a.dbeta) return;
-  float* pg = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-  float* pb = pg + a.cols;
   // the block's warps own the same columns: add them in warp order
   extern __shared__ float acc[];  // [2][codes_pitch]
   const int w8 = (int)a.codes_pitch;
@@ -317,16 +429,15 @@ __global__ void __launch_bounds__(256, 2)
     }
     __syncthreads();
   }
-  for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-    pg[c] = acc[c];
-    pb[c] = acc[w8 + c];
-  }
+  for (int c = threadIdx.x; c < a.cols; c += blockDim.x)
+    put_sums(a, blockIdx.x, gridDim.x == 1, c, acc[c], acc[w8 + c]);
 }
 
 // ---------------------------------------------------------------------------
 // Rows through a ring of stages in shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 6;
+constexpr int kCols = 16;  // columns per thread
 constexpr long long kWaitCycles = 4000000000ll;  // bound on each wait: ~2 s
 
 // Copies a row's aligned 16-byte pieces to dst and returns the bytes that the
@@ -391,12 +502,16 @@ __device__ __forceinline__ uint4 lds_u128(uint32_t a) {
   return v;
 }
 
+// How the rows lie: every thread's units inside rows on 16-byte boundaries;
+// rows on such boundaries with a ragged end; rows that start anywhere.
+enum Rows { kFull, kEnds, kAnywhere };
+
 // A unit from a staged row whose first byte lies `mis` bytes into it; `left`
 // of the row's bytes begin at the unit (the columns past them are zero).
-template <int DT, bool ALIGNED>
+template <int DT, int ROWS>
 __device__ __forceinline__ uint4 staged_unit(uint32_t at, uint32_t mis, int left) {
   uint4 r;
-  if (ALIGNED) {
+  if (ROWS != kAnywhere) {
     r = lds_u128(at);
   } else {
     const uint32_t p = at + (mis & ~3u);
@@ -410,7 +525,7 @@ __device__ __forceinline__ uint4 staged_unit(uint32_t at, uint32_t mis, int left
     }
     r = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (left < 16) {
+  if (ROWS != kFull && left < 16) {
     uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -422,20 +537,69 @@ __device__ __forceinline__ uint4 staged_unit(uint32_t at, uint32_t mis, int left
   return r;
 }
 
-// Block-wide sums for the ring kernels; the barrier also carries whether a
-// thread's wait ran out (then every thread leaves its row loop).
-struct BlockSum {
-  float2 (*slot)[32];
+template <int DT, int ROWS>
+__device__ __forceinline__ void put_unit(char* out, uint32_t u, int left, int64_t bytes,
+                                         const uint4& r) {
+  if (ROWS == kFull || (ROWS == kEnds && left == 16))
+    *reinterpret_cast<uint4*>(out + u * 16) = r;
+  else
+    store_unit<DT, ROWS != kAnywhere>(out, (int64_t)u * 16, bytes, r);
+}
+
+// Sums of N (1 or 2) values over the row's warps, for the ring kernels: over
+// a warp's lanes by shuffles, over the warps from shared memory, which every
+// thread reads whole (fewer steps in a row than shuffles again).  `slot`
+// holds zeros past the last warp.  The named barrier leaves the producer warp
+// out, and carries whether a thread's wait ran out (then every thread leaves
+// its row loop).
+template <int N>
+struct RowsSum {
+  float (*slot)[36 * N];
+  int threads;
   int turn = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b, bool& ok) {
-    a = warp_allsum(a);
-    b = warp_allsum(b);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if (lane == 0) slot[turn][warp] = make_float2(a, b);
-    ok = !__syncthreads_or(!ok);
-    const float2 v = lane < nw ? slot[turn][lane] : make_float2(0.0f, 0.0f);
+  __device__ __forceinline__ void operator()(float (&v)[N], bool& ok) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float s = v[0];
+    if (N == 2) {
+      const bool up = lane & 1;
+      const float send = up ? v[0] : v[N - 1], stay = up ? v[N - 1] : v[0];
+      s = stay + __shfl_xor_sync(0xffffffffu, send, 1);
+    }
+#pragma unroll
+    for (int k = N; k < 32; k <<= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane < N) slot[turn][warp * N + lane] = s;
+    uint32_t bad = ok ? 0u : 1u;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(bad)
+        : "r"(bad), "r"(threads)
+        : "memory");
+    ok = bad == 0u;
+    const float4* w = reinterpret_cast<const float4*>(slot[turn]);
+    float2 t = make_float2(0.0f, 0.0f);
+    const int quads = threads / 32 * N / 4;  // whole or not, what lies past them is zero
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) {
+      const float4 f = w[i];
+      t = __fadd2_rn(t, make_float2(f.x, f.y));
+      t = __fadd2_rn(t, make_float2(f.z, f.w));
+    }
+    if (quads > 2 * N - 1)
+      for (int i = 2 * N; i <= quads; ++i) {
+        const float4 f = w[i];
+        t = __fadd2_rn(t, make_float2(f.x, f.y));
+        t = __fadd2_rn(t, make_float2(f.z, f.w));
+      }
     turn ^= 1;
-    return make_float2(warp_allsum(v.x), warp_allsum(v.y));
+    if (N == 2) {
+      v[0] = t.x;
+      v[N - 1] = t.y;
+    } else {
+      v[0] = t.x + t.y;
+    }
   }
 };
 
@@ -450,6 +614,37 @@ struct RingPos {
   }
 };
 
+// The backward kernel's producer warp: copies the block's rows, stage after
+// stage, as the row's warps hand the stages back.  (The copies' address
+// arithmetic, done by a thread of the row's warps between two barriers, kept
+// all of them waiting: 16384 x 4096 bf16 88 -> 82 us.  The forward kernel
+// copies half as much and does without: its extra warp would cost one of the
+// four blocks that an SM's registers hold, 74 -> 83 us.)
+template <int DT, bool CKPT>
+__device__ __forceinline__ bool produce(const NormArgs& a, char* stages, uint64_t* full,
+                                        uint64_t* empty) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    RingPos ring;
+    int filled = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ring.next(a.stages)) {
+      if (filled < a.stages) {
+        ++filled;
+      } else {
+        if (!sm100::mbar_wait(&empty[ring.st], ring.ph ^ 1u, kWaitCycles)) {
+          ok = false;
+          break;
+        }
+        // the warps read the stage through the generic proxy, the copy
+        // refills it through the asynchronous one
+        sm100::fence_proxy_async_smem();
+      }
+      fill_stage<DT, true, CKPT>(a, row, stages + ring.st * a.stage_bytes, &full[ring.st]);
+    }
+  }
+  return ok;
+}
+
 __device__ __forceinline__ void ring_end(bool ok, uint32_t* status) {
   if (ok) return;
   atomicOr(status, kStatusWaitTimeout);
@@ -459,262 +654,315 @@ __device__ __forceinline__ void ring_end(bool ok, uint32_t* status) {
   }
 }
 
-// E columns per thread, unit i of a thread being thread + i * threads.
-template <int DT, int E, bool ALIGNED>
-__global__ void __launch_bounds__(512, 1)
+// kCols columns per thread, unit i of a thread being thread + i * threads.
+// Registers decide how many warps an SM holds, and these kernels live from
+// that: gamma and beta (read by each thread at its own place) are kept in
+// shared memory, a row between its passes packed as it came.  The limits give
+// 8 and 5 warps per scheduler.
+constexpr int kForwardRegs = 64, kBackwardRegs = 96;
+constexpr int kForwardWarps = 32, kBackwardWarps = 20;  // per SM
+
+template <int V>
+__device__ __forceinline__ void sts_params(uint32_t at, const void* p, int ptype, int64_t c,
+                                           int64_t cols, float fill) {
+  float v[V];
+  load_params<V>(v, p, ptype, c, cols, fill);
+#pragma unroll
+  for (int j = 0; j < V; j += 4)
+    sm100::sts128(at + j * 4, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+}
+
+template <int DT, int ROWS>
+__global__ void __maxnreg__(kForwardRegs)
     norm_forward_ring_kernel(const __grid_constant__ NormArgs a) {
   using namespace sm100;
   using L = Elem<DT>;
-  constexpr int V = L::V, K = E / V;
+  constexpr int V = L::V, K = kCols / V, H = V / 2;
   extern __shared__ __align__(128) char stages[];
-  __shared__ float2 slot[2][32];
+  __shared__ __align__(16) float slot[2][36 * 1];
   __shared__ __align__(8) uint64_t full[kMaxStages];
-  BlockSum sum{slot};
   const int t = threadIdx.x, nt = blockDim.x;
-  if (t == 0) {
-    for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
-    mbar_fence_init();
-    int64_t r = blockIdx.x;
-    for (int i = 0; i < a.stages && r < a.rows; ++i, r += gridDim.x)
-      fill_stage<DT, false, false>(a, r, stages + i * a.stage_bytes, &full[i]);
-  }
-  const uint32_t base = smem_u32(stages);
-  const float inv_n = 1.0f / (float)a.cols;
-  float g[K][V], b[K][V];
-  int left[K];  // bytes of the row from the unit on
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int64_t u = t + (int64_t)i * nt;
-    left[i] = (int)max((int64_t)0, min((int64_t)16, a.row_bytes - u * 16));
-    load_params<V>(g[i], a.gamma, a.ptype, u * V, a.cols, 1.0f);
-    load_params<V>(b[i], a.beta, a.ptype, u * V, a.cols, 0.0f);
-  }
-  __syncthreads();
-  bool ok = true;
-  RingPos ring;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ring.next(a.stages)) {
-    ok = mbar_wait(&full[ring.st], ring.ph, kWaitCycles);
-    const uint32_t stage = base + ring.st * a.stage_bytes;
-    const uint32_t mis =
-        ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(a.x + row * a.xpitch) & 15u);
-    uint4 raw[K];
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      raw[i] = left[i] > 0 ? staged_unit<DT, ALIGNED>(stage + (t + i * nt) * 16, mis, left[i])
-                           : make_uint4(0u, 0u, 0u, 0u);
-      float v[V];
-      L::unpack(raw[i], v);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += v[j];
-    }
-    const float mean = sum(s, 0.0f, ok).x * inv_n;
-    if (!ok) break;
-    // every thread holds its part of the row: the stage takes a later one
-    if (t == 0 && row + (int64_t)a.stages * gridDim.x < a.rows) {
-      fence_proxy_async_smem();
-      fill_stage<DT, false, false>(a, row + (int64_t)a.stages * gridDim.x,
-                                   stages + ring.st * a.stage_bytes, &full[ring.st]);
-    }
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      keep_packed(raw[i]);
-      float v[V];
-      L::unpack(raw[i], v);
-      if (left[i] == 16) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) q = fmaf(v[j] - mean, v[j] - mean, q);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j * elem_size(DT) < left[i]) q = fmaf(v[j] - mean, v[j] - mean, q);
-      }
-    }
-    const float rstd = rsqrtf(sum(q, 0.0f, ok).x * inv_n + a.eps);
-    if (t == 0) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
-    char* out = a.out + row * a.outpitch;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      keep_packed(raw[i]);
-      float v[V];
-      L::unpack(raw[i], v);
-      const uint32_t u = t + i * nt;
-      if (a.codes) {
-        const uint32_t sb = scale_byte(group_max_bits<DT>(raw[i]));
-        if (u * V < a.codes_pitch) {
-          store_codes<DT>(a.codes + row * a.codes_pitch + u * V, raw[i], v, sb);
-          if (t % (kActGroup / V) == 0)
-            a.scales[row * a.scales_pitch + u * V / kActGroup] = (uint8_t)sb;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[i][j], b[i][j]);
-      const uint4 r = L::pack(v);
-      if (ALIGNED && left[i] == 16) *reinterpret_cast<uint4*>(out + u * 16) = r;
-      else store_unit<DT, ALIGNED>(out, (int64_t)u * 16, a.row_bytes, r);
-    }
-  }
-  ring_end(ok, a.status);
-}
-
-// E columns per thread.  With 16 a thread keeps d and n between the two
-// passes over the row, and gamma; with 32 it takes them from the stage and
-// from L1 again (the column sums alone are 64 registers).
-template <int DT, int E, bool CKPT, bool ALIGNED>
-__global__ void __launch_bounds__(512, 1)
-    norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
-  using namespace sm100;
-  using L = Elem<DT>;
-  constexpr int V = L::V, K = E / V;
-  constexpr bool KEEP = E == 16;
-  extern __shared__ __align__(128) char stages[];
-  __shared__ float2 slot[2][32];
-  __shared__ __align__(8) uint64_t full[kMaxStages];
-  BlockSum sum{slot};
-  const int t = threadIdx.x, nt = blockDim.x;
+  for (int i = t; i < 72; i += nt) slot[i / 36][i % 36] = 0.0f;
   int64_t fetch = blockIdx.x;  // next row to copy (thread 0)
   if (t == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
     mbar_fence_init();
     for (int i = 0; i < a.stages && fetch < a.rows; ++i, fetch += gridDim.x)
-      fill_stage<DT, true, CKPT>(a, fetch, stages + i * a.stage_bytes, &full[i]);
+      fill_stage<DT, false, false>(a, fetch, stages + i * a.stage_bytes, &full[i]);
   }
-  const uint32_t base = smem_u32(stages);
+  __syncthreads();
+  RowsSum<1> sum{slot, nt};
+  const uint32_t base = smem_u32(stages) + t * 16;
   const float inv_n = 1.0f / (float)a.cols;
-  float sg[K][V], sb[K][V], gk[KEEP ? K : 1][V];
+  // the thread's own gamma, then beta, behind the stages
+  const uint32_t gam = smem_u32(stages) + a.stages * a.stage_bytes + t * (V * 4);
+  const uint32_t bet = gam + nt * (kCols * 4);
+  int left[K];  // bytes of the row from the unit on
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int64_t u = t + (int64_t)i * nt;
+    left[i] = (int)max((int64_t)0, min((int64_t)16, a.row_bytes - u * 16));
+    sts_params<V>(gam + i * nt * (V * 4), a.gamma, a.ptype, u * V, a.cols, 1.0f);
+    sts_params<V>(bet + i * nt * (V * 4), a.beta, a.ptype, u * V, a.cols, 0.0f);
+  }
+  bool ok = true;
+  RingPos ring;
+  const char* x = a.x + blockIdx.x * a.xpitch;
+  char* out = a.out + blockIdx.x * a.outpitch;
+  uint8_t* codes = a.codes + blockIdx.x * a.codes_pitch;
+  uint8_t* scales = a.scales + blockIdx.x * a.scales_pitch;
+  const int64_t hop = gridDim.x;
+  for (int64_t row = blockIdx.x; row < a.rows;
+       row += hop, x += hop * a.xpitch, out += hop * a.outpitch, codes += hop * a.codes_pitch,
+               scales += hop * a.scales_pitch) {
+    ok = mbar_wait(&full[ring.st], ring.ph, kWaitCycles);
+    const uint32_t stage = base + ring.st * a.stage_bytes;
+    const uint32_t mis = ROWS == kAnywhere ? (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15u) : 0u;
+    uint4 raw[K];
+    float2 c = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (ROWS == kFull || left[i] > 0)
+        raw[i] = staged_unit<DT, ROWS>(stage + i * nt * 16, mis, left[i]);
+      float2 v[H];
+      unpack2<DT>(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < H; ++j) c = __fadd2_rn(c, v[j]);
+    }
+    float s[1] = {c.x + c.y};
+    sum(s, ok);
+    if (!ok) break;
+    // every thread holds its part of the row: the stage takes a later one
+    if (t == 0 && fetch < a.rows) {
+      fence_proxy_async_smem();
+      fill_stage<DT, false, false>(a, fetch, stages + ring.st * a.stage_bytes, &full[ring.st]);
+      fetch += hop;
+    }
+    ring.next(a.stages);
+    const float mean = s[0] * inv_n;
+    const float2 m = both(-mean);
+    c = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      keep_packed(raw[i]);
+      float2 v[H];
+      unpack2<DT>(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[j] = __fadd2_rn(v[j], m);
+      if (ROWS != kFull && left[i] < 16) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          if (2 * j * elem_size(DT) >= left[i]) v[j].x = 0.0f;
+          if ((2 * j + 1) * elem_size(DT) >= left[i]) v[j].y = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) c = __ffma2_rn(v[j], v[j], c);
+    }
+    s[0] = c.x + c.y;
+    sum(s, ok);
+    const float rstd = rsqrtf(s[0] * inv_n + a.eps);
+    if (t == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    const float2 rs = both(rstd);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      keep_packed(raw[i]);
+      const uint32_t u = t + i * nt;
+      if (a.codes) {
+        float f[V];
+        L::unpack(raw[i], f);
+        const uint32_t sb = scale_byte(group_max_bits<DT>(raw[i]));
+        if (ROWS == kFull || u * V < a.codes_pitch) {
+          store_codes<DT>(codes + u * V, raw[i], f, sb);
+          if (t % (kActGroup / V) == 0) scales[u * V / kActGroup] = (uint8_t)sb;
+        }
+      }
+      float2 v[H], g[H], b[H];
+      unpack2<DT>(raw[i], v);
+      lds_params<V>(g, gam + i * nt * (V * 4));
+      lds_params<V>(b, bet + i * nt * (V * 4));
+#pragma unroll
+      for (int j = 0; j < H; ++j)
+        v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j], m), rs), g[j], b[j]);
+      put_unit<DT, ROWS>(out, u, left[i], a.row_bytes, pack2<DT>(v));
+    }
+  }
+  ring_end(ok, a.status);
+}
+
+// A thread's part of a row between the two passes, packed: dy, and x or (from
+// a checkpoint) the restored values as bf16, which holds them exactly.
+template <int DT, bool CKPT>
+struct Packed {
+  uint4 dy, x;
+};
+template <>
+struct Packed<GC_F32, true> {
+  uint4 dy;
+  uint2 x;
+};
+
+template <int DT, bool CKPT>
+__device__ __forceinline__ void unpack_x(const Packed<DT, CKPT>& p, float2 (&v)[Elem<DT>::V / 2]) {
+  if constexpr (CKPT) {
+    uint32_t w[Elem<DT>::V / 2];
+    w[0] = p.x.x;
+    w[1] = p.x.y;
+    if constexpr (DT != GC_F32) {
+      w[2] = p.x.z;
+      w[3] = p.x.w;
+    }
+#pragma unroll
+    for (int j = 0; j < Elem<DT>::V / 2; ++j)
+      v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+  } else {
+    unpack2<DT>(p.x, v);
+  }
+}
+
+// Row sums s1 = sum(d), s2 = sum(d (x - mean)), with d = dy gamma; then
+//   dx = rstd d - (s2 rstd^3 / n) (x - mean) - s1 rstd / n.
+template <int DT, bool CKPT, int ROWS>
+__global__ void __maxnreg__(kBackwardRegs)
+    norm_backward_ring_kernel(const __grid_constant__ NormArgs a) {
+  using namespace sm100;
+  constexpr int V = Elem<DT>::V, K = kCols / V, H = V / 2;
+  extern __shared__ __align__(128) char stages[];
+  __shared__ __align__(16) float slot[2][36 * 2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  const int t = threadIdx.x, nt = blockDim.x - 32;  // the last warp is the producer
+  for (int i = t; i < 72 * 2; i += blockDim.x) slot[i / (36 * 2)][i % (36 * 2)] = 0.0f;
+  if (t == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], nt / 32);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  let_next_begin();
+  if (t >= nt) {
+    ring_end(produce<DT, CKPT>(a, stages, full, empty), a.status);
+    return;
+  }
+  RowsSum<2> sum{slot, nt};
+  const uint32_t base = smem_u32(stages);
+  const uint32_t gam = base + a.stages * a.stage_bytes + t * (V * 4);  // the thread's own gamma
+  const float inv_n = 1.0f / (float)a.cols;
+  float2 sg[K][H], sb[K][H];
   int left[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int64_t u = t + (int64_t)i * nt;
     left[i] = (int)max((int64_t)0, min((int64_t)16, a.row_bytes - u * 16));
-    if (KEEP) load_params<V>(gk[KEEP ? i : 0], a.gamma, a.ptype, u * V, a.cols, 1.0f);
+    sts_params<V>(gam + i * nt * (V * 4), a.gamma, a.ptype, u * V, a.cols, 1.0f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) sg[i][j] = sb[i][j] = 0.0f;
+    for (int j = 0; j < H; ++j) sg[i][j] = sb[i][j] = both(0.0f);
   }
-  float mean_n = 0.0f, rstd_n = 0.0f;
+  const int64_t hop = gridDim.x;
+  const char *dyp = a.dy + blockIdx.x * a.dypitch, *xp = a.x + blockIdx.x * a.xpitch;
+  char* out = a.out + blockIdx.x * a.outpitch;
+  float mean = 0.0f, rstd = 0.0f;
   if (blockIdx.x < a.rows) {
-    mean_n = __ldg(a.mean + blockIdx.x);
-    rstd_n = __ldg(a.rstd + blockIdx.x);
+    mean = __ldg(a.mean + blockIdx.x);
+    rstd = __ldg(a.rstd + blockIdx.x);
   }
-  __syncthreads();
   bool ok = true;
   RingPos ring;
-  int last_st = -1;  // the stage of the row before
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ring.next(a.stages)) {
+  for (int64_t row = blockIdx.x; row < a.rows;
+       row += hop, dyp += hop * a.dypitch, xp += hop * a.xpitch, out += hop * a.outpitch) {
+    float mean_n = 0.0f, rstd_n = 0.0f;
+    if (row + hop < a.rows) {
+      mean_n = __ldg(a.mean + row + hop);
+      rstd_n = __ldg(a.rstd + row + hop);
+    }
     ok = mbar_wait(&full[ring.st], ring.ph, kWaitCycles);
     const uint32_t stage = base + ring.st * a.stage_bytes;
-    const float mean = mean_n, rstd = rstd_n;
-    if (row + gridDim.x < a.rows) {
-      mean_n = __ldg(a.mean + row + gridDim.x);
-      rstd_n = __ldg(a.rstd + row + gridDim.x);
-    }
     const uint32_t mis0 =
-        ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(a.dy + row * a.dypitch) & 15u);
+        ROWS == kAnywhere ? (uint32_t)(reinterpret_cast<uintptr_t>(dyp) & 15u) : 0u;
     const uint32_t mis1 =
-        ALIGNED ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(a.x + row * a.xpitch) & 15u);
-    // dy and n = (x - mean) rstd of unit i
-    auto inputs = [&](int i, float (&d)[V], float (&n)[V]) {
-      const uint32_t u = t + i * nt;
-      L::unpack(staged_unit<DT, ALIGNED>(stage + u * 16, mis0, left[i]), d);
-      if (CKPT) {
-        Codes<V> c;
+        ROWS == kAnywhere ? (uint32_t)(reinterpret_cast<uintptr_t>(xp) & 15u) : 0u;
+    const float2 m = both(-mean), rs = both(rstd);
+    Packed<DT, CKPT> in[K];
+    float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
-        for (int w = 0; w < V / 4; ++w) c.w[w] = lds_u32(stage + a.second_at + u * V + 4 * w);
-        uint32_t bb;
+    for (int i = 0; i < K; ++i) {
+      const uint32_t u = t + i * nt;
+      in[i] = Packed<DT, CKPT>{};
+      if (ROWS != kFull && left[i] <= 0) continue;
+      in[i].dy = staged_unit<DT, ROWS>(stage + u * 16, mis0, left[i]);
+      if constexpr (CKPT) {
+        const uint32_t at = stage + a.second_at + u * V;
+        uint32_t b;
         asm volatile("ld.shared.u8 %0, [%1];"
-                     : "=r"(bb)
-                     : "r"(stage + a.scales_at + u * V / kActGroup)
+                     : "=r"(b)
+                     : "r"(stage + a.scales_at + u / (kActGroup / V))
                      : "memory");
-        decode<V>(n, c, bb);
-      } else {
-        L::unpack(staged_unit<DT, ALIGNED>(stage + a.second_at + u * 16, mis1, left[i]), n);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) n[j] = (n[j] - mean) * rstd;
-    };
-    auto gamma = [&](int i, float (&g)[V]) {
-      if (KEEP) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) g[j] = gk[KEEP ? i : 0][j];
-      } else {
-        load_params<V>(g, a.gamma, a.ptype, ((int64_t)t + (int64_t)i * nt) * V, a.cols, 1.0f);
-      }
-    };
-    float dk[KEEP ? K : 1][V], nk[KEEP ? K : 1][V];
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      float (&d)[V] = dk[KEEP ? i : 0];
-      float (&n)[V] = nk[KEEP ? i : 0];
-      if (left[i] > 0) {
-        float g[V];
-        inputs(i, d, n);
-        gamma(i, g);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          sg[i][j] = fmaf(d[j], n[j], sg[i][j]);
-          sb[i][j] += d[j];
-          d[j] *= g[j];  // dy is 0 past the last column
-          s1 += d[j];
-          s2 = fmaf(d[j], n[j], s2);
+        b *= 0x00800080u;
+        const uint32_t c0 = lds_u32(at);
+        in[i].x.x = decode2(c0, 0x1100u, b);
+        in[i].x.y = decode2(c0, 0x3322u, b);
+        if constexpr (DT != GC_F32) {
+          const uint32_t c1 = lds_u32(at + 4);
+          in[i].x.z = decode2(c1, 0x1100u, b);
+          in[i].x.w = decode2(c1, 0x3322u, b);
         }
+      } else {
+        in[i].x = staged_unit<DT, ROWS>(stage + a.second_at + u * 16, mis1, left[i]);
+      }
+      float2 d[H], n[H], g[H];
+      unpack2<DT>(in[i].dy, d);
+      unpack_x<DT, CKPT>(in[i], n);
+      lds_params<V>(g, gam + i * nt * (V * 4));
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        n[j] = __fadd2_rn(n[j], m);
+        sg[i][j] = __ffma2_rn(__fmul2_rn(d[j], rs), n[j], sg[i][j]);
+        sb[i][j] = __fadd2_rn(sb[i][j], d[j]);
+        d[j] = __fmul2_rn(d[j], g[j]);  // dy is 0 past the last column
+        s1 = __fadd2_rn(s1, d[j]);
+        s2 = __ffma2_rn(d[j], n[j], s2);
       }
     }
-    const float2 c12 = sum(s1, s2, ok);
+    // the warp holds its part of the row
+    __syncwarp();
+    if ((t & 31) == 0) mbar_arrive(&empty[ring.st]);
+    ring.next(a.stages);
+    float s[2] = {s1.x + s1.y, s2.x + s2.y};
+    sum(s, ok);
     if (!ok) break;
-    // all threads are past the row before: its stage takes the next row
-    if (t == 0) {
-      if (last_st >= 0 && fetch < a.rows) {
-        fence_proxy_async_smem();
-        fill_stage<DT, true, CKPT>(a, fetch, stages + last_st * a.stage_bytes, &full[last_st]);
-        fetch += gridDim.x;
-      }
-      last_st = ring.st;
-    }
-    const float c1 = c12.x * inv_n * rstd, c2 = c12.y * inv_n * rstd;
-    char* out = a.out + row * a.outpitch;
+    const float2 c1 = both(-s[0] * inv_n * rstd);
+    const float2 c2 = both(-s[1] * inv_n * rstd * rstd * rstd);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const uint32_t u = t + i * nt;
-      float o[V];
-      if (KEEP) {
+      keep_packed(in[i].dy);
+      float2 d[H], n[H], g[H];
+      unpack2<DT>(in[i].dy, d);
+      unpack_x<DT, CKPT>(in[i], n);
+      lds_params<V>(g, gam + i * nt * (V * 4));
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          o[j] = fmaf(rstd, dk[KEEP ? i : 0][j], fmaf(-c2, nk[KEEP ? i : 0][j], -c1));
-      } else {
-        float n[V], g[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = 0.0f;
-        if (left[i] > 0) {
-          inputs(i, o, n);
-          gamma(i, g);
-#pragma unroll
-          for (int j = 0; j < V; ++j) o[j] = fmaf(rstd, o[j] * g[j], fmaf(-c2, n[j], -c1));
-        }
-      }
-      const uint4 r = L::pack(o);
-      if (ALIGNED && left[i] == 16) *reinterpret_cast<uint4*>(out + u * 16) = r;
-      else store_unit<DT, ALIGNED>(out, (int64_t)u * 16, a.row_bytes, r);
+      for (int j = 0; j < H; ++j)
+        d[j] = __ffma2_rn(__fmul2_rn(d[j], g[j]), rs, __ffma2_rn(__fadd2_rn(n[j], m), c2, c1));
+      put_unit<DT, ROWS>(out, t + i * nt, left[i], a.row_bytes, pack2<DT>(d));
     }
+    mean = mean_n;
+    rstd = rstd_n;
   }
   ring_end(ok, a.status);
 
   if (!a.dgamma && !a.dbeta) return;
-  float* pg = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-  float* pb = pg + a.cols;
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int64_t c = ((int64_t)t + (int64_t)i * nt) * V;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (c + j < a.cols) {
-        pg[c + j] = sg[i][j];
-        pb[c + j] = sb[i][j];
-      }
+      if (c + j < a.cols)
+        put_sums(a, blockIdx.x, gridDim.x == 1, c + j, j & 1 ? sg[i][j / 2].y : sg[i][j / 2].x,
+                 j & 1 ? sb[i][j / 2].y : sb[i][j / 2].x);
   }
 }
 
@@ -762,7 +1010,9 @@ __global__ void __launch_bounds__(512)
     const int64_t off = fetch(i, d, n);
 #pragma unroll
     for (int j = 0; j < V; ++j) d[j] = rstd * (d[j] - c1 - n[j] * c2);
-    store_unit<DT, ALIGNED>(a.out + row * a.outpitch, off, a.row_bytes, E::pack(d));
+    char* out = a.out + row * a.outpitch;
+    if (ALIGNED && off + 16 <= a.row_bytes) *reinterpret_cast<uint4*>(out + off) = E::pack(d);
+    else store_unit<DT, ALIGNED>(out, off, a.row_bytes, E::pack(d));
   }
 }
 
@@ -786,39 +1036,36 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
       sb[j] += d[j];
     }
   }
-  float* pg = a.part + (int64_t)blockIdx.y * 2 * a.cols;
 #pragma unroll
   for (int j = 0; j < V; ++j)
-    if (c + j < a.cols) {
-      pg[c + j] = sg[j];
-      pg[a.cols + c + j] = sb[j];
-    }
+    if (c + j < a.cols) put_sums(a, blockIdx.y, gridDim.y == 1, c + j, sg[j], sb[j]);
 }
 
 // out[c] (+)= the sum of part[p][which][c] over p: a block takes 32 columns
-// of one of the two sums; its 16 warps add every 16th partial row in order,
+// of one of the two sums; its 32 warps add every 32nd partial row in order,
 // then the warps' sums are added in warp order.
-__global__ void __launch_bounds__(512) norm_reduce_kernel(const float* part, int parts,
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, int parts,
                                                           int64_t cols, float* dgamma,
                                                           float* dbeta, int accumulate) {
-  __shared__ float s[16][33];
+  __shared__ float s[32][33];
   float* out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.0f;
+  after_previous();
   if (c < cols) {
     const float* p = part + (int64_t)blockIdx.y * cols + c;
     const int64_t pitch = 2 * cols;
 #pragma unroll 4
-    for (int i = warp; i < parts; i += 16) v += p[i * pitch];
+    for (int i = warp; i < parts; i += 32) v += p[i * pitch];
   }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < cols) {
     v = s[0][lane];
 #pragma unroll
-    for (int w = 1; w < 16; ++w) v += s[w][lane];
+    for (int w = 1; w < 32; ++w) v += s[w][lane];
     out[c] = accumulate ? out[c] + v : v;
   }
 }
@@ -827,20 +1074,40 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const float* part, int
 
 constexpr int kMaxSms = 160;  // the scratch is sized for at most so many
 
-// Rows of 1025 .. 16384 columns go through the ring while two stages fit;
-// E columns per thread.
+// Rows of 513 .. 16384 columns (8192 backward) go through the ring while two
+// stages fit.
 struct RingPlan {
-  int e, threads;  // e == 0: not this way
-  uint32_t second_at, scales_at, stage_bytes;
+  int threads;  // of the rows; 0: not this way
+  uint32_t second_at, scales_at, stage_bytes, smem;
   int stages, per_sm;
 };
 
-constexpr uint32_t kRingBytes = 216 * 1024;  // of an SM's shared memory
+// Shared memory that each of n blocks of an SM may use (228 KB, of which the
+// system takes 1 KB a block, and the kernels' static part; one block at most
+// 227 KB).
+int64_t block_smem(int n) {
+  return std::min<int64_t>(228 * 1024 / n - 1024, 226 * 1024) - 512;
+}
+
+// Threads of a row; 0 where rows are too narrow or too wide.  (A wider row's
+// threads would leave an SM a single block of more registers: 11008 columns
+// ran at 31% of the copy rate backward, against 61% for the passes that read
+// a row twice.)
+int ring_threads(int64_t cols, bool back) {
+  const int64_t c = ckpt_codes_pitch(cols);
+  return c <= 512 || c > (back ? 512 : 1024) * kCols ? 0 : (int)round_up(ceil_div(c, kCols), 32);
+}
+
+// Blocks per SM by registers, the backward kernel's producer warp counted.
+int ring_blocks(int threads, bool back) {
+  return back ? kBackwardWarps / (threads / 32 + 1) : kForwardWarps / (threads / 32);
+}
 
 RingPlan ring_plan(int64_t cols, int dtype, bool back, bool ckpt) {
   RingPlan p{};
+  p.threads = ring_threads(cols, back);
+  if (!p.threads) return p;
   const int64_t c = ckpt_codes_pitch(cols);
-  if (c <= 1024 || c > 512 * 32) return p;
   const int64_t row = round_up(cols * elem_size(dtype) + 15, 16) + 16;  // with a shifted start
   p.second_at = (uint32_t)round_up(row, 128);
   int64_t bytes = p.second_at;
@@ -848,13 +1115,14 @@ RingPlan ring_plan(int64_t cols, int dtype, bool back, bool ckpt) {
   p.scales_at = (uint32_t)round_up(bytes, 128);
   if (back && ckpt) bytes = p.scales_at + ckpt_scales_pitch(cols);
   p.stage_bytes = (uint32_t)round_up(bytes, 128);
-  if (2 * p.stage_bytes > kRingBytes) return p;
-  p.e = c <= 512 * 16 ? 16 : 32;
-  p.threads = (int)round_up(ceil_div(c, p.e), 32);
-  // blocks per SM by registers (128 a thread), then as many stages as fit
-  p.per_sm = std::max(1, 512 / p.threads);
-  while (p.per_sm > 1 && 2 * p.stage_bytes > kRingBytes / p.per_sm) --p.per_sm;
-  p.stages = (int)std::min<int64_t>(kMaxStages, kRingBytes / p.per_sm / p.stage_bytes);
+  const int64_t params = (int64_t)p.threads * kCols * (back ? 4 : 8);
+  // as many blocks as registers allow, fewer where two stages do not fit
+  p.per_sm = ring_blocks(p.threads, back);
+  while (p.per_sm > 1 && params + 2 * (int64_t)p.stage_bytes > block_smem(p.per_sm)) --p.per_sm;
+  p.stages =
+      (int)std::min<int64_t>(kMaxStages, (block_smem(p.per_sm) - params) / p.stage_bytes);
+  if (p.stages < 2) return RingPlan{};
+  p.smem = (uint32_t)(p.stages * (int64_t)p.stage_bytes + params);
   return p;
 }
 
@@ -866,59 +1134,77 @@ void apply(NormArgs& a, const RingPlan& p, const gc_ctx* ctx) {
   a.stages = p.stages;
 }
 
-template <class Kernel>
-void launch_ring(Kernel kernel, gc_ctx* ctx, const NormArgs& a, const RingPlan& p, unsigned grid) {
-  const int smem = (int)(p.stage_bytes * p.stages);
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  kernel<<<grid, p.threads, smem, ctx->stream>>>(a);
+template <auto Kernel>
+void launch_ring(gc_ctx* ctx, const NormArgs& a, const RingPlan& p, unsigned grid, int threads) {
+  static uint64_t devices = 0;
+  if (!allow_smem(ctx, Kernel, 226 * 1024, devices)) return;  // the launch's error says so
+  Kernel<<<grid, threads, p.smem, ctx->stream>>>(a);
 }
 
-template <int DT, int K, bool WARP>
-void forward_launch(gc_ctx* ctx, const NormArgs& a, int threads, bool aligned) {
-  const int per_block = WARP ? threads / 32 : 1;
-  const unsigned grid = (unsigned)ceil_div(a.rows, per_block);
+template <int DT, int K>
+void forward_block(gc_ctx* ctx, const NormArgs& a, int threads, bool aligned) {
   if (aligned)
-    norm_forward_kernel<DT, K, WARP, true><<<grid, threads, 0, ctx->stream>>>(a);
+    norm_forward_kernel<DT, K, true><<<(unsigned)a.rows, threads, 0, ctx->stream>>>(a);
   else
-    norm_forward_kernel<DT, K, WARP, false><<<grid, threads, 0, ctx->stream>>>(a);
+    norm_forward_kernel<DT, K, false><<<(unsigned)a.rows, threads, 0, ctx->stream>>>(a);
+}
+
+template <int DT, int K>
+void forward_warp(gc_ctx* ctx, const NormArgs& a, bool aligned) {
+  const unsigned g = (unsigned)std::min<int64_t>(ceil_div(a.rows, 8),
+                                                 (int64_t)ctx->num_sms * 4);
+  const size_t smem = (size_t)K * 32 * Elem<DT>::V * 8;
+  if (aligned)
+    norm_forward_warp_kernel<DT, K, true><<<g, 256, smem, ctx->stream>>>(a);
+  else
+    norm_forward_warp_kernel<DT, K, false><<<g, 256, smem, ctx->stream>>>(a);
+}
+
+template <int DT>
+void forward_ring(gc_ctx* ctx, const NormArgs& a, const RingPlan& p, bool aligned) {
+  const unsigned g = (unsigned)std::min<int64_t>(a.rows, (int64_t)ctx->num_sms * p.per_sm);
+  if (!aligned) launch_ring<norm_forward_ring_kernel<DT, kAnywhere>>(ctx, a, p, g, p.threads);
+  else if (a.cols == (int64_t)p.threads * kCols)
+    launch_ring<norm_forward_ring_kernel<DT, kFull>>(ctx, a, p, g, p.threads);
+  else launch_ring<norm_forward_ring_kernel<DT, kEnds>>(ctx, a, p, g, p.threads);
 }
 
 template <int DT>
 void forward_dt(gc_ctx* ctx, NormArgs& a, bool aligned) {
   const int64_t units = a.codes_pitch / Elem<DT>::V;
-  const RingPlan p = ring_plan(a.cols, DT, false, false);
   // fewer rows than SMs: a block each, one unit per thread
-  if (units <= 1024 && units > 32 && a.rows <= ctx->num_sms) {
-    forward_launch<DT, 1, false>(ctx, a, (int)round_up(units, 32), aligned);
-  } else if (p.e) {
-    apply(a, p, ctx);
-    const unsigned g = (unsigned)std::min<int64_t>(a.rows, (int64_t)ctx->num_sms * p.per_sm);
-    if (p.e == 16) {
-      if (aligned) launch_ring(norm_forward_ring_kernel<DT, 16, true>, ctx, a, p, g);
-      else launch_ring(norm_forward_ring_kernel<DT, 16, false>, ctx, a, p, g);
-    } else {
-      if (aligned) launch_ring(norm_forward_ring_kernel<DT, 32, true>, ctx, a, p, g);
-      else launch_ring(norm_forward_ring_kernel<DT, 32, false>, ctx, a, p, g);
-    }
-  } else if (units <= 32) {
-    forward_launch<DT, 1, true>(ctx, a, 256, aligned);
-  } else if (units <= 64) {
-    forward_launch<DT, 2, true>(ctx, a, 256, aligned);
-  } else if (units <= 128) {
-    forward_launch<DT, 4, true>(ctx, a, 256, aligned);
-  } else if (units <= 256) {  // fp32, 513 .. 1024 columns
-    forward_launch<DT, 8, true>(ctx, a, 256, aligned);
+  if (units > 32 && units <= 1024 && a.rows <= ctx->num_sms) {
+    forward_block<DT, 1>(ctx, a, (int)round_up(units, 32), aligned);
+  } else if (a.codes_pitch <= 512) {
+    if (units <= 32) forward_warp<DT, 1>(ctx, a, aligned);
+    else if (units <= 64) forward_warp<DT, 2>(ctx, a, aligned);
+    else forward_warp<DT, 4>(ctx, a, aligned);
   } else {
-    forward_launch<DT, 0, false>(ctx, a, 1024, aligned);
+    const RingPlan p = ring_plan(a.cols, DT, false, false);
+    if (p.threads) {
+      apply(a, p, ctx);
+      forward_ring<DT>(ctx, a, p, aligned);
+    } else {
+      forward_block<DT, 0>(ctx, a, 1024, aligned);
+    }
   }
 }
 
 // Partial rows of the column sums that a call may leave.
 int64_t max_parts(int64_t cols) {
-  const int64_t c = ckpt_codes_pitch(cols);
-  if (c <= 1024) return kMaxSms * 2;
-  const int threads = (int)round_up(ceil_div(c, c <= 512 * 16 ? 16 : 32), 32);
-  return (int64_t)kMaxSms * std::max(2, 512 / threads);
+  const int threads = ring_threads(cols, true);
+  return (int64_t)kMaxSms * (threads ? ring_blocks(threads, true) : 2);
+}
+
+template <int DT, bool CKPT>
+int backward_ring(gc_ctx* ctx, const NormArgs& a, const RingPlan& p, bool aligned) {
+  const unsigned g =
+      (unsigned)std::min<int64_t>(a.rows, (int64_t)std::min(ctx->num_sms, kMaxSms) * p.per_sm);
+  if (!aligned) launch_ring<norm_backward_ring_kernel<DT, CKPT, kAnywhere>>(ctx, a, p, g, p.threads + 32);
+  else if (a.cols == (int64_t)p.threads * kCols)
+    launch_ring<norm_backward_ring_kernel<DT, CKPT, kFull>>(ctx, a, p, g, p.threads + 32);
+  else launch_ring<norm_backward_ring_kernel<DT, CKPT, kEnds>>(ctx, a, p, g, p.threads + 32);
+  return (int)g;
 }
 
 template <int DT, int K, bool CKPT>
@@ -935,26 +1221,17 @@ template <int DT, bool CKPT>
 int backward_dt(gc_ctx* ctx, NormArgs& a, bool aligned) {
   constexpr int V = Elem<DT>::V;
   const int64_t sms = std::min(ctx->num_sms, kMaxSms);
-  if (a.codes_pitch <= 1024) {
+  if (a.codes_pitch <= 512) {
     LaunchScope L(ctx, GC_PHASE_NORM_BACKWARD);
     const unsigned g = (unsigned)std::min<int64_t>(ceil_div(a.rows, 8), sms * 2);
-    if (a.codes_pitch <= 512) backward_launch<DT, 16 / V, CKPT>(ctx, a, g, aligned);
-    else backward_launch<DT, 32 / V, CKPT>(ctx, a, g, aligned);
+    backward_launch<DT, 16 / V, CKPT>(ctx, a, g, aligned);
     return (int)g;
   }
   const RingPlan p = ring_plan(a.cols, DT, true, CKPT);
-  if (p.e) {
+  if (p.threads) {
     LaunchScope L(ctx, GC_PHASE_NORM_BACKWARD);
     apply(a, p, ctx);
-    const unsigned g = (unsigned)std::min<int64_t>(a.rows, sms * p.per_sm);
-    if (p.e == 16) {
-      if (aligned) launch_ring(norm_backward_ring_kernel<DT, 16, CKPT, true>, ctx, a, p, g);
-      else launch_ring(norm_backward_ring_kernel<DT, 16, CKPT, false>, ctx, a, p, g);
-    } else {
-      if (aligned) launch_ring(norm_backward_ring_kernel<DT, 32, CKPT, true>, ctx, a, p, g);
-      else launch_ring(norm_backward_ring_kernel<DT, 32, CKPT, false>, ctx, a, p, g);
-    }
-    return (int)g;
+    return backward_ring<DT, CKPT>(ctx, a, p, aligned);
   }
   {
     LaunchScope L(ctx, GC_PHASE_NORM_BACKWARD);
@@ -981,10 +1258,12 @@ gc_status backward_all(gc_ctx* ctx, NormArgs& a, bool aligned) {
   int parts = 0;
   if (a.rows > 0)
     parts = a.codes ? backward_dt<DT, true>(ctx, a, aligned) : backward_dt<DT, false>(ctx, a, aligned);
-  if (a.dgamma || a.dbeta) {
+  if ((a.dgamma || a.dbeta) && parts != 1) {
     LaunchScope L(ctx, GC_PHASE_NORM_REDUCE);
-    norm_reduce_kernel<<<dim3((unsigned)ceil_div(a.cols, 32), 2), 512, 0, ctx->stream>>>(
-        a.part, parts, a.cols, a.dgamma, a.dbeta, a.accumulate);
+    if (launch_early(norm_reduce_kernel, dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0,
+                     ctx->stream, a.part, parts, a.cols, a.dgamma, a.dbeta,
+                     a.accumulate) != cudaSuccess)
+      return GC_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }

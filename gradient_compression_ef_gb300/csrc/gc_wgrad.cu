@@ -60,8 +60,10 @@ struct Plan {
 
 struct WgradArgs {
   Plan plan;
-  float* dw;
+  float *dw, *db;
   float* part;        // [2 * ranges][256 outputs][256 inputs]
+  float* bias_part;   // [bias_parts][out]
+  int bias_parts;     // 0: db is done, or not asked for
   uint32_t* status;
   int64_t out, in, lddw;
   int64_t plane_rows;  // rows from one plane of dy to the next
@@ -492,6 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
+  after_previous();  // db's sums, which this kernel may not have waited for
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -502,42 +505,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Adds the ranges' partials of a cut tile in the order of their tokens and
-// stores it: block (y, x) takes 4 outputs of rest tile y.
-__global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__ WgradArgs a) {
+// stores it (16 outputs of a rest tile per block), and the partial rows of db
+// (32 columns per block; the first blocks).
+constexpr int kJoinRows = 16;
+
+__global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__ WgradArgs a,
+                                                         int bias_blocks) {
   const Plan& p = a.plan;
-  const int64_t t = blockIdx.y, b0 = t * p.blocks, b1 = b0 + p.blocks;
+  if ((int)blockIdx.x < bias_blocks) {
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t o = (int64_t)blockIdx.x * 32 + lane;
+    after_previous();
+    float v = 0.0f;
+    if (o < a.out) {
+#pragma unroll 8
+      for (int i = warp; i < a.bias_parts; i += 8) v += a.bias_part[i * a.out + o];
+    }
+    s[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && o < a.out) {
+#pragma unroll
+      for (int w = 1; w < 8; ++w) v += s[w][lane];
+      a.db[o] = a.accumulate ? a.db[o] + v : v;
+    }
+    return;
+  }
+  const int64_t b = blockIdx.x - bias_blocks, t = b / (kTile / kJoinRows);
+  const int n0 = (int)(b - t * (kTile / kJoinRows)) * kJoinRows;
+  const int64_t b0 = t * p.blocks, b1 = b0 + p.blocks;
   const int64_t g0 = b0 / p.len, g1 = (b1 - 1) / p.len;
   if (g0 == g1) return;  // one range held it all and stored it
   int64_t it, ot;
   tile_place(p, p.full + t, it, ot);
   const int64_t i = it * kTile + threadIdx.x;
-  if (i >= a.in) return;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int n0 = blockIdx.x * 4;
-  // the tile is the second one of its first range if that range begins
-  // before the tile's first block's tile, the first one of every other
-  const float* src = a.part + n0 * kTile + threadIdx.x;
+  // the tile is the second one of its first range if that range begins with
+  // another tile, the first one of every other
   const int64_t second = t - p.len * g0 / p.blocks;
-  for (int64_t g = g0; g <= g1; g += 8) {
-    float x[8][4];
+  after_previous();
+  if (i >= a.in) return;
+  for (int n = n0; n < n0 + kJoinRows; n += 4) {
+    const float* src = a.part + n * kTile + threadIdx.x;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t g = g0; g <= g1; g += 4) {
+      float x[4][4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t slot = 2 * (g + e) + (g + e == g0 ? second : 0);
+      for (int e = 0; e < 4; ++e) {
+        const int64_t slot = 2 * (g + e) + (g + e == g0 ? second : 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[e][j] = g + e <= g1 ? src[slot * kTile * kTile + j * kTile] : 0.0f;
+        for (int j = 0; j < 4; ++j)
+          x[e][j] = g + e <= g1 ? src[slot * kTile * kTile + j * kTile] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += x[e][j];
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += x[e][j];
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t o = ot * kTile + n0 + j;
-    if (o < a.out) {
-      float* w = a.dw + o * a.lddw + i;
-      *w = a.accumulate ? *w + v[j] : v[j];
+    for (int j = 0; j < 4; ++j) {
+      const int64_t o = ot * kTile + n + j;
+      if (o < a.out) {
+        float* w = a.dw + o * a.lddw + i;
+        *w = a.accumulate ? *w + v[j] : v[j];
+      }
     }
   }
 }
@@ -579,6 +609,7 @@ __global__ void __launch_bounds__(256) wgrad_split_kernel(const char* dy, const 
       *reinterpret_cast<uint4*>(dst) = raw;
     }
   }
+  after_previous();  // db's sums, which this kernel did not wait for
 }
 
 // Column sums of dy: block (x, y) adds rows y * rows_per .. of 32 units (256
@@ -589,19 +620,43 @@ __global__ void __launch_bounds__(256) bias_kernel(const char* dy, const char* e
                                                    int64_t out, int64_t dy_pitch,
                                                    int64_t rows_per, float* part, float* db,
                                                    int accumulate) {
-  using E = Elem<DT>;
-  constexpr int V = E::V, W = 32 * V;
+  constexpr int V = Elem<DT>::V, W = 32 * V;
   __shared__ float s[8][W];
+  let_next_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t off = ((int64_t)blockIdx.x * 32 + lane) * 16;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(rows, r0 + rows_per);
-  float v[V] = {};
-#pragma unroll 4
-  for (int64_t r = r0 + warp; r < r1; r += 8) {
-    float d[V];
-    E::unpack(load_unit<DT, ALIGNED>(dy + r * dy_pitch, off, out * elem_size(DT), end), d);
+  const int64_t bytes = out * elem_size(DT);
+  float2 v2[V / 2];
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] += d[j];
+  for (int j = 0; j < V / 2; ++j) v2[j] = both(0.0f);
+  auto add = [&](const uint4& raw) {
+    float2 d[V / 2];
+    unpack2<DT>(raw, d);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) v2[j] = __fadd2_rn(v2[j], d[j]);
+  };
+  if (ALIGNED && off + 16 <= bytes) {  // plain loads, eight at a time
+    const char* p = dy + (r0 + warp) * dy_pitch + off;
+    int64_t r = r0 + warp;
+    for (; r + 56 < r1; r += 64, p += 64 * dy_pitch) {
+      uint4 raw[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        raw[k] = __ldg(reinterpret_cast<const uint4*>(p + k * 8 * dy_pitch));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(raw[k]);
+    }
+    for (; r < r1; r += 8, p += 8 * dy_pitch) add(__ldg(reinterpret_cast<const uint4*>(p)));
+  } else {
+    for (int64_t r = r0 + warp; r < r1; r += 8)
+      add(load_unit<DT, ALIGNED>(dy + r * dy_pitch, off, bytes, end));
+  }
+  float v[V];
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) {
+    v[2 * j] = v2[j].x;
+    v[2 * j + 1] = v2[j].y;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) s[warp][lane * V + j] = v[j];
@@ -615,18 +670,9 @@ __global__ void __launch_bounds__(256) bias_kernel(const char* dy, const char* e
   else db[o] = accumulate ? db[o] + t : t;
 }
 
-__global__ void __launch_bounds__(256) bias_join_kernel(const float* part, int parts, int64_t out,
-                                                        float* db, int accumulate) {
-  const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (o >= out) return;
-  float t = 0.0f;
-  for (int p = 0; p < parts; ++p) t += part[(int64_t)p * out + o];
-  db[o] = accumulate ? db[o] + t : t;
-}
-
 // --- host ----------------------------------------------------------------------------------------
 
-constexpr int kMaxBiasParts = 64;
+constexpr int kMaxBiasParts = 304;
 
 int plane_count(int dtype) { return dtype == GC_F32 ? 3 : 1; }
 
@@ -687,9 +733,10 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int6
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches db's sums; returns the partial rows that are left to add.
 template <int DT>
-void launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy, float* db,
-                 int accumulate, float* part) {
+int launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy, float* db,
+                int accumulate, float* part) {
   constexpr int kSize = elem_size(DT);
   const int64_t bx = ceil_div(out, 32 * Elem<DT>::V);
   const int64_t want = std::min<int64_t>({ceil_div((int64_t)ctx->num_sms * 8, bx),
@@ -699,48 +746,52 @@ void launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t
   const dim3 g((unsigned)bx, (unsigned)by);
   const char* p = static_cast<const char*>(dy);
   const char* end = p + ((rows - 1) * lddy + out) * kSize;
-  {
-    LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
-    if (row_aligned(lddy, DT))
-      bias_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize, rows_per,
-                                                        part, db, accumulate);
-    else
-      bias_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize,
-                                                         rows_per, part, db, accumulate);
-  }
-  if (by > 1) {
-    LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
-    bias_join_kernel<<<(unsigned)ceil_div(out, 256), 256, 0, ctx->stream>>>(part, (int)by, out, db,
-                                                                            accumulate);
-  }
+  LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
+  if (row_aligned(lddy, DT))
+    bias_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize, rows_per,
+                                                      part, db, accumulate);
+  else
+    bias_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize, rows_per,
+                                                       part, db, accumulate);
+  return by > 1 ? (int)by : 0;
 }
 
+// early: the kernel before on the stream is db's, of which this one needs
+// nothing.
 template <int DT>
-void launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
-                  uint16_t* planes, int64_t plane_rows, int64_t pitch) {
+gc_status launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
+                       uint16_t* planes, int64_t plane_rows, int64_t pitch, bool early) {
   constexpr int kSize = elem_size(DT);
   const int64_t total = plane_rows * ceil_div(pitch, 32 * Elem<DT>::V);
   const unsigned g = (unsigned)std::min<int64_t>(ceil_div(total, 8), (int64_t)ctx->num_sms * 8);
   const char* p = static_cast<const char*>(dy);
   const char* end = p + ((rows - 1) * lddy + out) * kSize;
+  const auto kernel =
+      row_aligned(lddy, DT) ? wgrad_split_kernel<DT, true> : wgrad_split_kernel<DT, false>;
   LaunchScope L(ctx, GC_PHASE_WGRAD_SPLIT);
-  if (row_aligned(lddy, DT))
-    wgrad_split_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(
-        p, end, rows, out * kSize, lddy * kSize, planes, plane_rows, pitch);
-  else
-    wgrad_split_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(
-        p, end, rows, out * kSize, lddy * kSize, planes, plane_rows, pitch);
+  if (early)
+    return launch_early(kernel, dim3(g), 256, 0, ctx->stream, p, end, rows, out * kSize,
+                        lddy * kSize, planes, plane_rows, pitch) == cudaSuccess
+               ? GC_OK
+               : GC_ERR_CUDA;
+  kernel<<<g, 256, 0, ctx->stream>>>(p, end, rows, out * kSize, lddy * kSize, planes, plane_rows,
+                                     pitch);
+  return GC_OK;
 }
 
 template <bool F16>
 gc_status launch_tiles(gc_ctx* ctx, const CUtensorMap& md, const CUtensorMap& mc,
-                       const CUtensorMap& ms, const WgradArgs& a) {
-  if (cudaFuncSetAttribute(wgrad_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kSmemBytes) != cudaSuccess)
-    return GC_ERR_CUDA;
+                       const CUtensorMap& ms, const WgradArgs& a, bool early) {
+  static uint64_t devices = 0;
+  if (!allow_smem(ctx, wgrad_kernel<F16>, (int)kSmemBytes, devices)) return GC_ERR_CUDA;
   const int64_t pairs =
       a.plan.full ? a.plan.pairs : std::min<int64_t>(a.plan.pairs, a.plan.ranges);
   LaunchScope L(ctx, GC_PHASE_WGRAD);
+  if (early)
+    return launch_early(wgrad_kernel<F16>, dim3((unsigned)(2 * pairs)), kThreads, kSmemBytes,
+                        ctx->stream, md, mc, ms, a) == cudaSuccess
+               ? GC_OK
+               : GC_ERR_CUDA;
   wgrad_kernel<F16><<<(unsigned)(2 * pairs), kThreads, kSmemBytes, ctx->stream>>>(md, mc, ms, a);
   return GC_OK;
 }
@@ -775,38 +826,44 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
   float* bias_part = reinterpret_cast<float*>(at);
   at += up256((int64_t)kMaxBiasParts * out * 4);
 
-  if (db) {
-    if (dtype == GC_F32) launch_bias<GC_F32>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-    else if (dtype == GC_BF16)
-      launch_bias<GC_BF16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-    else launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-  }
-
   WgradArgs a{};
   const int np = plane_count(dtype);
   a.plan = make_plan(rows, out, in, np, ctx->num_sms / 2);
   a.dw = dw;
+  a.db = db;
   a.part = reinterpret_cast<float*>(at);
+  a.bias_part = bias_part;
   a.status = ctx->ws.status;
   a.out = out;
   a.in = in;
   a.lddw = lddw;
   a.plane_rows = a.plan.tok_blocks * kTok;
   a.accumulate = accumulate;
+  if (db) {
+    if (dtype == GC_F32)
+      a.bias_parts = launch_bias<GC_F32>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    else if (dtype == GC_BF16)
+      a.bias_parts = launch_bias<GC_BF16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    else
+      a.bias_parts = launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+  }
+  bool early = db != nullptr;
 
   // the tensor map takes dy as it lies when its rows start on 16-byte
   // boundaries
   const void* d16 = dy;
   int64_t d_rows = rows, d_cols = out, d_pitch = lddy * 2;
-  if (dtype == GC_F32 || (rows > 1 && lddy * 2 % 16 != 0) ) {
+  if (dtype == GC_F32 || (rows > 1 && lddy * 2 % 16 != 0)) {
     d_cols = round_up(out, 8);
     d_pitch = d_cols * 2;
     d_rows = np * a.plane_rows;
     d16 = planes;
-    if (dtype == GC_F32)
-      launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols);
-    else
-      launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols);
+    const gc_status st =
+        dtype == GC_F32
+            ? launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols, early)
+            : launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols, early);
+    if (st != GC_OK) return st;
+    early = false;
   } else if (rows == 1) {
     d_pitch = round_up(out * 2, 16);
   }
@@ -819,11 +876,17 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
       !make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, rows, sp, sp, 16, false))
     return GC_ERR_CUDA;
   const gc_status st =
-      f16 ? launch_tiles<true>(ctx, md, mc, ms, a) : launch_tiles<false>(ctx, md, mc, ms, a);
+      f16 ? launch_tiles<true>(ctx, md, mc, ms, a, early)
+          : launch_tiles<false>(ctx, md, mc, ms, a, early);
   if (st != GC_OK) return st;
-  if (a.plan.ranges > a.plan.rest) {
+  const int64_t tile_blocks =
+      a.plan.ranges > a.plan.rest ? a.plan.rest * (kTile / kJoinRows) : 0;
+  const int64_t bias_blocks = a.bias_parts ? ceil_div(out, 32) : 0;
+  if (tile_blocks + bias_blocks > 0) {
     LaunchScope L(ctx, GC_PHASE_WGRAD_JOIN);
-    wgrad_join_kernel<<<dim3(kTile / 4, (unsigned)a.plan.rest), 256, 0, ctx->stream>>>(a);
+    if (launch_early(wgrad_join_kernel, dim3((unsigned)(tile_blocks + bias_blocks)), 256, 0,
+                     ctx->stream, a, (int)bias_blocks) != cudaSuccess)
+      return GC_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }

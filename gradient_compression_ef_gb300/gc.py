@@ -379,51 +379,77 @@ def ef_randk(ctx, grad, err, p, seed, step, idx_out, val_out, count_out, n=None,
 # --- the backward pass that fills the flat gradient: 8-bit activation
 # checkpoints, activation functions, layer norm, linear weight gradients ----
 
+_TORCH = {}  # torch dtype -> GC_* type, filled when the first tensor comes
+_U8 = _F32 = None
+
+
+def _types():
+    global _U8, _F32
+    import torch
+    _U8, _F32 = torch.uint8, torch.float32
+    _TORCH.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+
+
 def _dtype(t):
     """GC_* type of a torch tensor, a torch dtype or a name."""
     if isinstance(t, str):
         return DTYPES[t]
-    name = str(getattr(t, "dtype", t))
+    dt = getattr(t, "dtype", t)
+    if not _TORCH:
+        _types()
     try:
-        return _TORCH_DTYPES[name]
+        return _TORCH[dt]
     except KeyError:
-        raise TypeError("unsupported element type %s (float32, bfloat16 or float16)" % name)
-
-
-_TORCH_DTYPES = {"torch.float32": F32, "torch.bfloat16": BF16, "torch.float16": F16}
+        raise TypeError("unsupported element type %s (float32, bfloat16 or float16)" % dt) from None
 
 
 def _matrix(t, what, like=None):
     """(rows, cols, row stride) of a 2-D tensor with contiguous columns,
     which must have the shape and type of `like` if given."""
-    if t.dim() != 2:
-        raise ValueError("%s must be 2-D, got %d-D" % (what, t.dim()))
-    rows, cols = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D, got %d-D" % (what, len(shape)))
+    rows, cols = shape
     sr, sc = t.stride()
-    if cols > 1 and sc != 1:
+    if sc != 1 and cols > 1:
         raise ValueError("%s: columns must be contiguous (stride %d)" % (what, sc))
     if rows <= 1:
         sr = cols
-    if sr < cols:
+    elif sr < cols:
         raise ValueError("%s: overlapping rows (stride %d, %d columns)" % (what, sr, cols))
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+    if like is not None and (shape != like.shape or t.dtype != like.dtype):
         raise ValueError("%s: %s %s, expected %s %s" % (
-            what, tuple(t.shape), t.dtype, tuple(like.shape), like.dtype))
+            what, tuple(shape), t.dtype, tuple(like.shape), like.dtype))
     return rows, cols, sr
 
 
-def _flat(t, n, what, name):
-    """A contiguous tensor (or None) of at least n elements of a type."""
+def _floats(t, n, what):
+    """Address of a contiguous fp32 tensor (or None) of at least n elements."""
     if t is None:
         return None
-    if t.numel() < n or not t.is_contiguous() or str(t.dtype) != name:
-        raise ValueError("%s: needs %d contiguous %s" % (what, n, name))
+    if not _TORCH:
+        _types()
+    if t.dtype != _F32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s: needs %d contiguous float32" % (what, n))
     return t.data_ptr()
 
 
 def _ckpt(codes, scales, rows, cols):
-    return (_flat(codes, rows * (-(-cols // 32) * 32), "codes", "torch.uint8"),
-            _flat(scales, rows * (-(-cols // 512) * 16), "scales", "torch.uint8"))
+    """Addresses of a checkpoint's buffers (either may be None)."""
+    if codes is None and scales is None:
+        return None, None
+    if not _TORCH:
+        _types()
+    groups = (cols + 31) >> 5
+    if codes is not None and (codes.dtype != _U8 or codes.numel() < rows * groups * 32
+                              or not codes.is_contiguous()):
+        raise ValueError("codes: needs %d contiguous uint8" % (rows * groups * 32))
+    if scales is not None and (scales.dtype != _U8
+                               or scales.numel() < rows * (((groups + 15) >> 4) << 4)
+                               or not scales.is_contiguous()):
+        raise ValueError("scales: needs %d contiguous uint8" % (rows * (((groups + 15) >> 4) << 4)))
+    return (None if codes is None else codes.data_ptr(),
+            None if scales is None else scales.data_ptr())
 
 
 def _param(t, cols, what):
@@ -432,6 +458,10 @@ def _param(t, cols, what):
     if t.numel() != cols or not t.is_contiguous():
         raise ValueError("%s: needs %d contiguous values" % (what, cols))
     return t.data_ptr()
+
+
+def _act(act):
+    return ACTS[act] if isinstance(act, str) else int(act)
 
 
 def ckpt_codes_bytes(rows, cols):
@@ -467,8 +497,7 @@ def act_forward(ctx, act, x, y, codes=None, scales=None, gate=None, gate_codes=N
     ldg = _matrix(gate, "gate", x)[2] if gate is not None else 0
     c, s = _ckpt(codes, scales, rows, cols)
     gc_, gs = _ckpt(gate_codes, gate_scales, rows, cols)
-    _check(lib.gc_act_forward(ctx.handle, ACTS[act] if isinstance(act, str) else int(act),
-                              x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg,
+    _check(lib.gc_act_forward(ctx.handle, _act(act), x.data_ptr(), ldx, None if gate is None else gate.data_ptr(), ldg,
                               _dtype(x), rows, cols, y.data_ptr(), ldy, c, s, gc_, gs),
            "gc_act_forward")
 
@@ -480,8 +509,7 @@ def act_backward(ctx, act, dy, dx, codes, scales, dgate=None, gate_codes=None, g
     ldg = _matrix(dgate, "dgate", dy)[2] if dgate is not None else 0
     c, s = _ckpt(codes, scales, rows, cols)
     gc_, gs = _ckpt(gate_codes, gate_scales, rows, cols)
-    _check(lib.gc_act_backward(ctx.handle, ACTS[act] if isinstance(act, str) else int(act),
-                               dy.data_ptr(), lddy, c, s, gc_, gs, _dtype(dy), rows, cols,
+    _check(lib.gc_act_backward(ctx.handle, _act(act), dy.data_ptr(), lddy, c, s, gc_, gs, _dtype(dy), rows, cols,
                                dx.data_ptr(), lddx, None if dgate is None else dgate.data_ptr(),
                                ldg), "gc_act_backward")
 
@@ -502,7 +530,7 @@ def layernorm_forward(ctx, x, gamma, beta, eps, y, mean, rstd, codes=None, scale
     _check(lib.gc_layernorm_forward(
         ctx.handle, x.data_ptr(), ldx, _dtype(x), rows, cols, _param(gamma, cols, "gamma"),
         _param(beta, cols, "beta"), F32 if p is None else _dtype(p), eps, y.data_ptr(), ldy,
-        _flat(mean, rows, "mean", "torch.float32"), _flat(rstd, rows, "rstd", "torch.float32"),
+        _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"),
         c, s), "gc_layernorm_forward")
 
 
@@ -518,10 +546,10 @@ def layernorm_backward(ctx, dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=Non
     _check(lib.gc_layernorm_backward(
         ctx.handle, dy.data_ptr(), lddy, None if x is None else x.data_ptr(), ldx, c, s,
         _dtype(dy), rows, cols, _param(gamma, cols, "gamma"),
-        F32 if gamma is None else _dtype(gamma), _flat(mean, rows, "mean", "torch.float32"),
-        _flat(rstd, rows, "rstd", "torch.float32"), dx.data_ptr(), lddx,
-        _flat(dgamma, cols, "dgamma", "torch.float32"),
-        _flat(dbeta, cols, "dbeta", "torch.float32"), 1 if accumulate else 0),
+        F32 if gamma is None else _dtype(gamma), _floats(mean, rows, "mean"),
+        _floats(rstd, rows, "rstd"), dx.data_ptr(), lddx,
+        _floats(dgamma, cols, "dgamma"),
+        _floats(dbeta, cols, "dbeta"), 1 if accumulate else 0),
         "gc_layernorm_backward")
 
 
@@ -534,11 +562,11 @@ def linear_wgrad(ctx, dy, codes, scales, dw, db=None, accumulate=False):
     [rows, out] and the checkpoint of its input [rows, in]."""
     rows, out, lddy = _matrix(dy, "dy")
     wo, in_features, lddw = _matrix(dw, "dw")
-    if wo != out or str(dw.dtype) != "torch.float32":
+    if wo != out or _dtype(dw) != F32:
         raise ValueError("dw: %s %s, expected fp32 with %d rows" % (tuple(dw.shape), dw.dtype,
                                                                    out))
     c, s = _ckpt(codes, scales, rows, in_features)
     _check(lib.gc_linear_wgrad(ctx.handle, dy.data_ptr(), _dtype(dy), lddy, c, s, rows, out,
                                in_features, dw.data_ptr(), lddw,
-                               _flat(db, out, "db", "torch.float32"), 1 if accumulate else 0),
+                               _floats(db, out, "db"), 1 if accumulate else 0),
            "gc_linear_wgrad")
