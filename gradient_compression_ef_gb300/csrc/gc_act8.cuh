@@ -316,14 +316,22 @@ __device__ __forceinline__ void store_run(char* row, uint32_t at, bool inner, in
     }
   }
   if (cut >= 0) store_some<DT>(p + cut * 512, v, 0, (int)(bytes - o - cut * 512) / E);
-  if (lane == 0u)
-    store_some<DT>(p, first, (int)mis / E,
-                   (int)max((int64_t)0, min(bytes - o, (int64_t)16)) / E);
-  // the last unit's end lies in a piece that the run does not fill
-  const int64_t tail = bytes - o - (U - 1) * 512 - 16;
-  if (lane == 31u && tail > 0)
-    store_some<DT>(p + (U - 1) * 512 + 16, funnel(r[U - 1], r[U - 1], 16u - mis), 0,
-                   (int)min(tail, (int64_t)mis) / E);
+  // The two pieces that the run shares with its neighbours, an element per
+  // lane: lane 0's first piece by the lanes of the lower half, the piece
+  // behind lane 31's last unit, which holds that unit's end, by the upper's.
+  const uint4 tail = funnel(r[U - 1], r[U - 1], 16u - mis);
+  const uint4 q = shfl4(lane == 0u ? first : tail, lane < 16u ? 0 : 31);
+  const uint32_t k = lane & 15u, w = k * E / 4;  // the lane's element, its word
+  if (k * E < 16u) {
+    const uint32_t word = w == 0u ? q.x : w == 1u ? q.y : w == 2u ? q.z : q.w;
+    const bool upper = lane >= 16u;
+    // its place in the row
+    const int64_t c = (int64_t)at - mis + (upper ? U * 512 : 0) + k * E;
+    if ((upper ? k * E < mis : k * E >= mis) && c < bytes) {
+      if (DT == GC_F32) *reinterpret_cast<uint32_t*>(row + c) = word;
+      else *reinterpret_cast<uint16_t*>(row + c) = (uint16_t)(k & 1u ? word >> 16 : word);
+    }
+  }
 }
 
 // One unit per lane, `off` being the lane's byte in the row (a whole warp's

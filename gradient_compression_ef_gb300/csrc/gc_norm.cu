@@ -537,13 +537,13 @@ __device__ __forceinline__ uint4 staged_unit(uint32_t at, uint32_t mis, int left
   return r;
 }
 
-template <int DT, int ROWS>
-__device__ __forceinline__ void put_unit(char* out, uint32_t u, int left, int64_t bytes,
-                                         const uint4& r) {
-  if (ROWS == kFull || (ROWS == kEnds && left == 16))
-    *reinterpret_cast<uint4*>(out + u * 16) = r;
-  else
-    store_unit<DT, ROWS != kAnywhere>(out, (int64_t)u * 16, bytes, r);
+// The warp's units, the first lane's first one being u0.
+template <int DT, int ROWS, int K>
+__device__ __forceinline__ void put_units(char* out, uint32_t u0, int64_t bytes,
+                                          const uint4 (&r)[K]) {
+  const bool inner =
+      ROWS == kFull || (int64_t)u0 * 16 + K * 512 + (ROWS == kEnds ? 0 : 16) <= bytes;
+  store_run<DT, ROWS != kAnywhere>(out, u0 * 16, inner, bytes, r);
 }
 
 // Sums of N (1 or 2) values over the row's warps, for the ring kernels: over
@@ -654,7 +654,8 @@ __device__ __forceinline__ void ring_end(bool ok, uint32_t* status) {
   }
 }
 
-// kCols columns per thread, unit i of a thread being thread + i * threads.
+// kCols columns per thread; a warp's units are consecutive, lane l having
+// units l, l + 32, ... of them.
 // Registers decide how many warps an SM holds, and these kernels live from
 // that: gamma and beta (read by each thread at its own place) are kept in
 // shared memory, a row between its passes packed as it came.  The limits give
@@ -692,18 +693,19 @@ __global__ void __maxnreg__(kForwardRegs)
   }
   __syncthreads();
   RowsSum<1> sum{slot, nt};
-  const uint32_t base = smem_u32(stages) + t * 16;
+  const uint32_t u0 = (t & ~31) * K, u1 = u0 + (t & 31);  // the warp's and the thread's first unit
+  const uint32_t base = smem_u32(stages) + u1 * 16;
   const float inv_n = 1.0f / (float)a.cols;
   // the thread's own gamma, then beta, behind the stages
-  const uint32_t gam = smem_u32(stages) + a.stages * a.stage_bytes + t * (V * 4);
+  const uint32_t gam = smem_u32(stages) + a.stages * a.stage_bytes + u1 * (V * 4);
   const uint32_t bet = gam + nt * (kCols * 4);
   int left[K];  // bytes of the row from the unit on
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const int64_t u = t + (int64_t)i * nt;
+    const int64_t u = u1 + i * 32;
     left[i] = (int)max((int64_t)0, min((int64_t)16, a.row_bytes - u * 16));
-    sts_params<V>(gam + i * nt * (V * 4), a.gamma, a.ptype, u * V, a.cols, 1.0f);
-    sts_params<V>(bet + i * nt * (V * 4), a.beta, a.ptype, u * V, a.cols, 0.0f);
+    sts_params<V>(gam + i * 32 * (V * 4), a.gamma, a.ptype, u * V, a.cols, 1.0f);
+    sts_params<V>(bet + i * 32 * (V * 4), a.beta, a.ptype, u * V, a.cols, 0.0f);
   }
   bool ok = true;
   RingPos ring;
@@ -724,7 +726,7 @@ __global__ void __maxnreg__(kForwardRegs)
     for (int i = 0; i < K; ++i) {
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
       if (ROWS == kFull || left[i] > 0)
-        raw[i] = staged_unit<DT, ROWS>(stage + i * nt * 16, mis, left[i]);
+        raw[i] = staged_unit<DT, ROWS>(stage + i * 512, mis, left[i]);
       float2 v[H];
       unpack2<DT>(raw[i], v);
 #pragma unroll
@@ -771,7 +773,7 @@ __global__ void __maxnreg__(kForwardRegs)
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       keep_packed(raw[i]);
-      const uint32_t u = t + i * nt;
+      const uint32_t u = u1 + i * 32;
       if (a.codes) {
         float f[V];
         L::unpack(raw[i], f);
@@ -783,13 +785,14 @@ __global__ void __maxnreg__(kForwardRegs)
       }
       float2 v[H], g[H], b[H];
       unpack2<DT>(raw[i], v);
-      lds_params<V>(g, gam + i * nt * (V * 4));
-      lds_params<V>(b, bet + i * nt * (V * 4));
+      lds_params<V>(g, gam + i * 32 * (V * 4));
+      lds_params<V>(b, bet + i * 32 * (V * 4));
 #pragma unroll
       for (int j = 0; j < H; ++j)
         v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j], m), rs), g[j], b[j]);
-      put_unit<DT, ROWS>(out, u, left[i], a.row_bytes, pack2<DT>(v));
+      raw[i] = pack2<DT>(v);
     }
+    put_units<DT, ROWS>(out, u0, a.row_bytes, raw);
   }
   ring_end(ok, a.status);
 }
@@ -844,22 +847,22 @@ __global__ void __maxnreg__(kBackwardRegs)
     mbar_fence_init();
   }
   __syncthreads();
-  let_next_begin();
   if (t >= nt) {
     ring_end(produce<DT, CKPT>(a, stages, full, empty), a.status);
     return;
   }
   RowsSum<2> sum{slot, nt};
   const uint32_t base = smem_u32(stages);
-  const uint32_t gam = base + a.stages * a.stage_bytes + t * (V * 4);  // the thread's own gamma
+  const uint32_t u0 = (t & ~31) * K, u1 = u0 + (t & 31);  // the warp's and the thread's first unit
+  const uint32_t gam = base + a.stages * a.stage_bytes + u1 * (V * 4);  // the thread's own gamma
   const float inv_n = 1.0f / (float)a.cols;
   float2 sg[K][H], sb[K][H];
   int left[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const int64_t u = t + (int64_t)i * nt;
+    const int64_t u = u1 + i * 32;
     left[i] = (int)max((int64_t)0, min((int64_t)16, a.row_bytes - u * 16));
-    sts_params<V>(gam + i * nt * (V * 4), a.gamma, a.ptype, u * V, a.cols, 1.0f);
+    sts_params<V>(gam + i * 32 * (V * 4), a.gamma, a.ptype, u * V, a.cols, 1.0f);
 #pragma unroll
     for (int j = 0; j < H; ++j) sg[i][j] = sb[i][j] = both(0.0f);
   }
@@ -891,7 +894,7 @@ __global__ void __maxnreg__(kBackwardRegs)
     float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const uint32_t u = t + i * nt;
+      const uint32_t u = u1 + i * 32;
       in[i] = Packed<DT, CKPT>{};
       if (ROWS != kFull && left[i] <= 0) continue;
       in[i].dy = staged_unit<DT, ROWS>(stage + u * 16, mis0, left[i]);
@@ -917,7 +920,7 @@ __global__ void __maxnreg__(kBackwardRegs)
       float2 d[H], n[H], g[H];
       unpack2<DT>(in[i].dy, d);
       unpack_x<DT, CKPT>(in[i], n);
-      lds_params<V>(g, gam + i * nt * (V * 4));
+      lds_params<V>(g, gam + i * 32 * (V * 4));
 #pragma unroll
       for (int j = 0; j < H; ++j) {
         n[j] = __fadd2_rn(n[j], m);
@@ -937,18 +940,20 @@ __global__ void __maxnreg__(kBackwardRegs)
     if (!ok) break;
     const float2 c1 = both(-s[0] * inv_n * rstd);
     const float2 c2 = both(-s[1] * inv_n * rstd * rstd * rstd);
+    uint4 res[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       keep_packed(in[i].dy);
       float2 d[H], n[H], g[H];
       unpack2<DT>(in[i].dy, d);
       unpack_x<DT, CKPT>(in[i], n);
-      lds_params<V>(g, gam + i * nt * (V * 4));
+      lds_params<V>(g, gam + i * 32 * (V * 4));
 #pragma unroll
       for (int j = 0; j < H; ++j)
         d[j] = __ffma2_rn(__fmul2_rn(d[j], g[j]), rs, __ffma2_rn(__fadd2_rn(n[j], m), c2, c1));
-      put_unit<DT, ROWS>(out, t + i * nt, left[i], a.row_bytes, pack2<DT>(d));
+      res[i] = pack2<DT>(d);
     }
+    put_units<DT, ROWS>(out, u0, a.row_bytes, res);
     mean = mean_n;
     rstd = rstd_n;
   }
@@ -957,7 +962,7 @@ __global__ void __maxnreg__(kBackwardRegs)
   if (!a.dgamma && !a.dbeta) return;
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const int64_t c = ((int64_t)t + (int64_t)i * nt) * V;
+    const int64_t c = (int64_t)(u1 + i * 32) * V;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (c + j < a.cols)
@@ -1053,7 +1058,6 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.0f;
-  after_previous();
   if (c < cols) {
     const float* p = part + (int64_t)blockIdx.y * cols + c;
     const int64_t pitch = 2 * cols;
@@ -1260,10 +1264,8 @@ gc_status backward_all(gc_ctx* ctx, NormArgs& a, bool aligned) {
     parts = a.codes ? backward_dt<DT, true>(ctx, a, aligned) : backward_dt<DT, false>(ctx, a, aligned);
   if ((a.dgamma || a.dbeta) && parts != 1) {
     LaunchScope L(ctx, GC_PHASE_NORM_REDUCE);
-    if (launch_early(norm_reduce_kernel, dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0,
-                     ctx->stream, a.part, parts, a.cols, a.dgamma, a.dbeta,
-                     a.accumulate) != cudaSuccess)
-      return GC_ERR_CUDA;
+    norm_reduce_kernel<<<dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0, ctx->stream>>>(
+        a.part, parts, a.cols, a.dgamma, a.dbeta, a.accumulate);
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
