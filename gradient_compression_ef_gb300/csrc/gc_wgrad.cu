@@ -33,12 +33,17 @@ namespace {
 constexpr int kTile = 256;           // inputs and outputs of a pair's tile
 constexpr int kHalf = 128;           // of one CTA
 constexpr int kTok = 64;             // tokens of a block
-constexpr int kStages = 5;
+constexpr int kStages = 4;           // of operands
+constexpr int kCodeStages = 6;       // of codes and scale bytes
 constexpr uint32_t kOpBytes = kHalf * kTok * 2;     // one CTA's operand, 16 KB
 constexpr uint32_t kCodeBytes = kHalf * kTok;       // 8 KB
 constexpr uint32_t kScaleBytes = 16 * kTok;
 constexpr int kReadWarps = 8, kConvWarps = 8;
 constexpr int kGroups = 2, kGroupWarps = kConvWarps / kGroups;
+// The groups take blocks in turn, so a stage is always the same group's.  It
+// has to be: a group that met a stage's barrier at every other phase only
+// could not tell by the parity which of the two it sees.
+static_assert(kStages % kGroups == 0 && kCodeStages % kGroups == 0, "a stage has one group");
 constexpr int kDyWarp = kReadWarps + kConvWarps, kIssuerWarp = kDyWarp + 1,
               kCodeWarp = kDyWarp + 2;
 constexpr int kThreads = 640;        // 5 warpgroups
@@ -117,7 +122,8 @@ struct Smem {
 };
 
 constexpr size_t kSmemBytes =
-    1024 + (size_t)kStages * (2 * kOpBytes + kCodeBytes + kScaleBytes) + 8 * (4 * kStages + 5) + 16;
+    1024 + (size_t)kStages * 2 * kOpBytes + (size_t)kCodeStages * (kCodeBytes + kScaleBytes) +
+    8 * (2 * kStages + 2 * kCodeStages + 5) + 16;
 
 __device__ __forceinline__ Smem carve(unsigned char* base) {
   Smem s;
@@ -126,27 +132,27 @@ __device__ __forceinline__ Smem carve(unsigned char* base) {
   s.a = at;
   s.b = s.a + kStages * kOpBytes;
   s.codes = s.b + kStages * kOpBytes;
-  s.scales = s.codes + kStages * kCodeBytes;
-  uint64_t* bar =
-      reinterpret_cast<uint64_t*>(p + kStages * (2 * kOpBytes + kCodeBytes + kScaleBytes));
+  s.scales = s.codes + kCodeStages * kCodeBytes;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(p + (s.scales - at) + kCodeStages * kScaleBytes);
   s.full = bar;
   s.empty = s.full + kStages;
   s.cfull = s.empty + kStages;
-  s.cempty = s.cfull + kStages;
-  s.acc_full = s.cempty + kStages;
+  s.cempty = s.cfull + kCodeStages;
+  s.acc_full = s.cempty + kCodeStages;
   s.acc_empty = s.acc_full + 2;
   s.drain = s.acc_empty + 2;
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
   return s;
 }
 
+template <int N>
 struct Ring {
   int st = 0;
   uint32_t ph = 0;
   __device__ __forceinline__ void next(int by = 1) {
     st += by;
-    if (st >= kStages) {
-      st -= kStages;
+    if (st >= N) {
+      st -= N;
       ph ^= 1u;
     }
   }
@@ -235,6 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 2 * kGroupWarps + 1);
       mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < kCodeStages; ++i) {
       mbar_init(&s.cfull[i], 1);
       mbar_init(&s.cempty[i], kGroupWarps);
     }
@@ -263,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // These three warps run their loops as whole warps (uniform registers);
     // one elected lane issues.
     if (warp == kCodeWarp) {
-      Ring ring;
+      Ring<kCodeStages> ring;
       uint32_t loads = 0;
       while (ok && work.next(u)) {
         int64_t it, ot;
@@ -273,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         TokCursor cur(u.k0, a.plan.tok_blocks);
         for (int32_t n = (int32_t)(u.k1 - u.k0); n > 0; --n, ring.next(), cur.next()) {
           const int st = ring.st;
-          if (loads >= kStages) {
+          if (loads >= kCodeStages) {
             if (!mbar_wait(&s.cempty[st], ring.ph ^ 1u, kWaitCycles)) ok = false;
             if (__any_sync(0xffffffffu, !ok)) {
               ok = false;
@@ -295,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kDyWarp) {
       const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
-      Ring ring;
+      Ring<kStages> ring;
       uint32_t loads = 0;
       while (ok && work.next(u)) {
         int64_t it, ot;
@@ -340,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t db = smem_desc_sw128(s.b, kOpBytes / 2, 1024);
       const uint32_t hi = (uint32_t)(da >> 32);
       const uint32_t a0 = (uint32_t)da, b0 = (uint32_t)db;
-      Ring ring;
+      Ring<kStages> ring;
       uint32_t seg = 0;
       while (ok && work.next(u)) {
         int in_seg = 0;
@@ -386,8 +394,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int unit = lane & 7, row0 = (cw % kGroupWarps) * 16 + (lane >> 3);
     const uint32_t half = (uint32_t)(unit >> 2);
     const uint32_t full0 = map_to_rank(smem_u32(s.full), 0);
-    Ring ring;
+    Ring<kStages> ring;
+    Ring<kCodeStages> cring;
     ring.next(group);
+    cring.next(group);
     int64_t done = group, skip = group;  // block of this CTA, blocks to pass over
     while (ok && work.next(u)) {
       int64_t it, ot;
@@ -395,9 +405,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t sat =
           (uint32_t)(((it * kTile + rank * kHalf) / kActGroup & 15) + (unit >> 1));
       int64_t k = u.k0 + skip;
-      for (; k < u.k1; k += kGroups, done += kGroups, ring.next(kGroups)) {
-        const int st = ring.st;
-        bool got = mbar_wait(&s.cfull[st], ring.ph, kWaitCycles);
+      for (; k < u.k1;
+           k += kGroups, done += kGroups, ring.next(kGroups), cring.next(kGroups)) {
+        const int st = ring.st, cs = cring.st;
+        bool got = mbar_wait(&s.cfull[cs], cring.ph, kWaitCycles);
         if (got && done >= kStages) got = mbar_wait_cluster(&s.empty[st], ring.ph ^ 1u, kWaitCycles);
         if (__any_sync(0xffffffffu, !got)) {
           ok = false;
@@ -408,8 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const uint32_t r = (uint32_t)(row0 + p * 4);
-          c[p] = lds_u4(s.codes + st * kCodeBytes + r * kHalf + unit * 16);
-          b[p] = lds_u8(s.scales + st * kScaleBytes + r * 16 + sat);
+          c[p] = lds_u4(s.codes + cs * kCodeBytes + r * kHalf + unit * 16);
+          b[p] = lds_u8(s.scales + cs * kScaleBytes + r * 16 + sat);
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -428,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&s.cempty[st]);
+          mbar_arrive(&s.cempty[cs]);
           mbar_arrive_cluster(full0 + st * 8);
         }
         __syncwarp();

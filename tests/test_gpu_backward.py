@@ -504,6 +504,33 @@ def test_linear_wgrad_without_rows(gc, ctx):
     assert bool((dw == 0).all()) and bool((db == 0).all())
 
 
+@pytest.mark.parametrize("dtype,rows,cols,out", [("f32", 2501, 1001, 2051), ("bf16", 4096, 2048, 5504)])
+def test_linear_wgrad_back_to_back(gc, ctx, dtype, rows, cols, out):
+    """Hundreds of calls in a row on rotating inputs (codes and dy come from
+    memory in any order): every result keeps its bits, no wait runs out."""
+    import torch
+    r = np.random.default_rng(rows)
+    sets = []
+    for _ in range(3):
+        x = torch.randn(rows, cols, device="cuda") + float(r.standard_normal())
+        codes, scales = ckpt(rows, cols)
+        gc.ckpt_save(ctx, x, codes, scales)
+        sets.append((torch.randn(rows, out, device="cuda").to(_dt(torch, dtype)), codes, scales,
+                     torch.empty(out, cols, device="cuda"), torch.empty(out, device="cuda")))
+    with gc.Context(0) as own:
+        own.reserve_scratch(gc.linear_wgrad_scratch_bytes(rows, out, cols, dtype))
+        first = []
+        for dy, codes, scales, dw, db in sets:
+            gc.linear_wgrad(own, dy, codes, scales, dw, db)
+            first.append((dw.clone(), db.clone()))
+        for i in range(1500):
+            dy, codes, scales, dw, db = sets[i % 3]
+            gc.linear_wgrad(own, dy, codes, scales, dw, db if i % 2 else None)
+        own.check()
+        for (dw0, db0), (_, _, _, dw, db) in zip(first, sets):
+            assert bool((dw == dw0).all()) and bool((db == db0).all())
+
+
 # --- all together --------------------------------------------------------------------------------
 
 def test_another_stream_and_capture(gc):
