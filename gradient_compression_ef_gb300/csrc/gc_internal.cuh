@@ -497,6 +497,36 @@ bool allow_smem(const gc_ctx* ctx, Kernel* kernel, int bytes, uint64_t& devices)
   return true;
 }
 
+// Launches a kernel that may begin while the kernel before it on the stream
+// still runs (programmatic dependent launch).  Such a kernel calls
+// after_previous() in every block, before it touches what the kernel before
+// wrote, or, where it needs nothing of it, before it ends: the kernels after
+// it then find both done.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<Params>(args)...);
+}
+
+// In the kernel before: the next one may begin once every block is here.
+__device__ __forceinline__ void let_next_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// All work of the kernel before is done and visible from here on.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Launchers implemented in the .cu files (return GC_OK or GC_ERR_CUDA).
 gc_status launch_ef_topk(gc_ctx* ctx, const float* grad, float* err, int64_t n,
                          int64_t k, int32_t* idx_out, float* val_out);

@@ -1054,10 +1054,14 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, in
                                                           float* dbeta, int accumulate) {
   __shared__ float s[32][33];
   float* out = blockIdx.y ? dbeta : dgamma;
-  if (!out) return;
+  if (!out) {
+    after_previous();
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.0f;
+  after_previous();
   if (c < cols) {
     const float* p = part + (int64_t)blockIdx.y * cols + c;
     const int64_t pitch = 2 * cols;
@@ -1264,8 +1268,10 @@ gc_status backward_all(gc_ctx* ctx, NormArgs& a, bool aligned) {
     parts = a.codes ? backward_dt<DT, true>(ctx, a, aligned) : backward_dt<DT, false>(ctx, a, aligned);
   if ((a.dgamma || a.dbeta) && parts != 1) {
     LaunchScope L(ctx, GC_PHASE_NORM_REDUCE);
-    norm_reduce_kernel<<<dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0, ctx->stream>>>(
-        a.part, parts, a.cols, a.dgamma, a.dbeta, a.accumulate);
+    if (launch_early(norm_reduce_kernel, dim3((unsigned)ceil_div(a.cols, 32), 2), 1024, 0,
+                     ctx->stream, a.part, parts, a.cols, a.dgamma, a.dbeta,
+                     a.accumulate) != cudaSuccess)
+      return GC_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }

@@ -511,6 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
+  after_previous();  // db's sums, which this kernel may not have waited for
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -532,6 +533,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__
     __shared__ float s[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t o = (int64_t)blockIdx.x * 32 + lane;
+    after_previous();
     float v = 0.0f;
     if (o < a.out) {
 #pragma unroll 8
@@ -550,14 +552,14 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__
   const int n0 = (int)(b - t * (kTile / kJoinRows)) * kJoinRows;
   const int64_t b0 = t * p.blocks, b1 = b0 + p.blocks;
   const int64_t g0 = b0 / p.len, g1 = (b1 - 1) / p.len;
-  if (g0 == g1) return;  // one range held it all and stored it
   int64_t it, ot;
   tile_place(p, p.full + t, it, ot);
   const int64_t i = it * kTile + threadIdx.x;
   // the tile is the second one of its first range if that range begins with
   // another tile, the first one of every other
   const int64_t second = t - p.len * g0 / p.blocks;
-  if (i >= a.in) return;
+  after_previous();
+  if (g0 == g1 || i >= a.in) return;  // one range held it all and stored it
   for (int n = n0; n < n0 + kJoinRows; n += 4) {
     const float* src = a.part + n * kTile + threadIdx.x;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -623,6 +625,7 @@ __global__ void __launch_bounds__(256) wgrad_split_kernel(const char* dy, const 
       *reinterpret_cast<uint4*>(dst) = raw;
     }
   }
+  after_previous();  // db's sums, which this kernel did not wait for
 }
 
 // Column sums of dy: block (x, y) adds rows y * rows_per .. of 32 units (256
@@ -635,6 +638,7 @@ __global__ void __launch_bounds__(256) bias_kernel(const char* dy, const char* e
                                                    int accumulate) {
   constexpr int V = Elem<DT>::V, W = 32 * V;
   __shared__ float s[8][W];
+  let_next_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t off = ((int64_t)blockIdx.x * 32 + lane) * 16;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(rows, r0 + rows_per);
@@ -768,9 +772,11 @@ int launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t 
   return by > 1 ? (int)by : 0;
 }
 
+// early: the kernel before on the stream is db's, of which this one needs
+// nothing.
 template <int DT>
-void launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
-                  uint16_t* planes, int64_t plane_rows, int64_t pitch) {
+gc_status launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
+                       uint16_t* planes, int64_t plane_rows, int64_t pitch, bool early) {
   constexpr int kSize = elem_size(DT);
   const int64_t total = plane_rows * ceil_div(pitch, 32 * Elem<DT>::V);
   const unsigned g = (unsigned)std::min<int64_t>(ceil_div(total, 8), (int64_t)ctx->num_sms * 8);
@@ -779,18 +785,29 @@ void launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_
   const auto kernel =
       row_aligned(lddy, DT) ? wgrad_split_kernel<DT, true> : wgrad_split_kernel<DT, false>;
   LaunchScope L(ctx, GC_PHASE_WGRAD_SPLIT);
+  if (early)
+    return launch_early(kernel, dim3(g), 256, 0, ctx->stream, p, end, rows, out * kSize,
+                        lddy * kSize, planes, plane_rows, pitch) == cudaSuccess
+               ? GC_OK
+               : GC_ERR_CUDA;
   kernel<<<g, 256, 0, ctx->stream>>>(p, end, rows, out * kSize, lddy * kSize, planes, plane_rows,
                                      pitch);
+  return GC_OK;
 }
 
 template <bool F16>
 gc_status launch_tiles(gc_ctx* ctx, const CUtensorMap& md, const CUtensorMap& mc,
-                       const CUtensorMap& ms, const WgradArgs& a) {
+                       const CUtensorMap& ms, const WgradArgs& a, bool early) {
   static uint64_t devices = 0;
   if (!allow_smem(ctx, wgrad_kernel<F16>, (int)kSmemBytes, devices)) return GC_ERR_CUDA;
   const int64_t pairs =
       a.plan.full ? a.plan.pairs : std::min<int64_t>(a.plan.pairs, a.plan.ranges);
   LaunchScope L(ctx, GC_PHASE_WGRAD);
+  if (early)
+    return launch_early(wgrad_kernel<F16>, dim3((unsigned)(2 * pairs)), kThreads, kSmemBytes,
+                        ctx->stream, md, mc, ms, a) == cudaSuccess
+               ? GC_OK
+               : GC_ERR_CUDA;
   wgrad_kernel<F16><<<(unsigned)(2 * pairs), kThreads, kSmemBytes, ctx->stream>>>(md, mc, ms, a);
   return GC_OK;
 }
@@ -847,6 +864,8 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
       a.bias_parts = launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
   }
 
+  bool early = db != nullptr;
+
   // the tensor map takes dy as it lies when its rows start on 16-byte
   // boundaries
   const void* d16 = dy;
@@ -856,10 +875,12 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
     d_pitch = d_cols * 2;
     d_rows = np * a.plane_rows;
     d16 = planes;
-    if (dtype == GC_F32)
-      launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols);
-    else
-      launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols);
+    const gc_status st =
+        dtype == GC_F32
+            ? launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols, early)
+            : launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols, early);
+    if (st != GC_OK) return st;
+    early = false;  // the tiles need the planes
   } else if (rows == 1) {
     d_pitch = round_up(out * 2, 16);
   }
@@ -872,15 +893,17 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
       !make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, rows, sp, sp, 16, false))
     return GC_ERR_CUDA;
   const gc_status st =
-      f16 ? launch_tiles<true>(ctx, md, mc, ms, a) : launch_tiles<false>(ctx, md, mc, ms, a);
+      f16 ? launch_tiles<true>(ctx, md, mc, ms, a, early)
+          : launch_tiles<false>(ctx, md, mc, ms, a, early);
   if (st != GC_OK) return st;
   const int64_t tile_blocks =
       a.plan.ranges > a.plan.rest ? a.plan.rest * (kTile / kJoinRows) : 0;
   const int64_t bias_blocks = a.bias_parts ? ceil_div(out, 32) : 0;
   if (tile_blocks + bias_blocks > 0) {
     LaunchScope L(ctx, GC_PHASE_WGRAD_JOIN);
-    wgrad_join_kernel<<<(unsigned)(tile_blocks + bias_blocks), 256, 0, ctx->stream>>>(
-        a, (int)bias_blocks);
+    if (launch_early(wgrad_join_kernel, dim3((unsigned)(tile_blocks + bias_blocks)), 256, 0,
+                     ctx->stream, a, (int)bias_blocks) != cudaSuccess)
+      return GC_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
