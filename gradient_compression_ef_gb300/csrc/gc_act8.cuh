@@ -327,7 +327,7 @@ __device__ __forceinline__ void store_run(char* row, uint32_t at, bool inner, in
     const bool upper = lane >= 16u;
     // its place in the row
     const int64_t c = (int64_t)at - mis + (upper ? U * 512 : 0) + k * E;
-    if ((upper ? k * E < mis : k * E >= mis) && c < bytes) {
+    if (upper == ((int)(k * E) < (int)mis) && c < bytes) {
       if (DT == GC_F32) *reinterpret_cast<uint32_t*>(row + c) = word;
       else *reinterpret_cast<uint16_t*>(row + c) = (uint16_t)(k & 1u ? word >> 16 : word);
     }

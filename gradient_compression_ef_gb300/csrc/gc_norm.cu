@@ -658,10 +658,20 @@ __device__ __forceinline__ void ring_end(bool ok, uint32_t* status) {
 // units l, l + 32, ... of them.
 // Registers decide how many warps an SM holds, and these kernels live from
 // that: gamma and beta (read by each thread at its own place) are kept in
-// shared memory, a row between its passes packed as it came.  The limits give
-// 8 and 5 warps per scheduler.
-constexpr int kForwardRegs = 64, kBackwardRegs = 96;
-constexpr int kForwardWarps = 32, kBackwardWarps = 20;  // per SM
+// shared memory, a row between its passes packed as it came.  64, 80
+// and 96 registers give 8, 6 and 5 warps per scheduler.
+constexpr int kBackwardRegs = 96;
+constexpr int kBackwardWarps = 20;  // per SM
+constexpr int forward_regs(int rows) { return rows == 2 ? 80 : 64; }
+constexpr int forward_warps(int rows) { return rows == 2 ? 24 : 32; }  // per SM
+// Rows that a block of the forward kernel has in hand at once: 16-bit rows go
+// two at a time where one block's registers hold two.  The sums over its warps
+// (about 1000 cycles each, most of it waiting for the slowest warp) are then
+// paid once for both: 6000 x 11008 bf16 took 111 us by one row at a time, 96
+// by two; 16384 x 4096 without a checkpoint 66 and 54.
+int forward_rows(int64_t codes_pitch, int dtype) {
+  return dtype != GC_F32 && codes_pitch <= forward_warps(2) * 32 * kCols ? 2 : 1;
+}
 
 template <int V>
 __device__ __forceinline__ void sts_params(uint32_t at, const void* p, int ptype, int64_t c,
@@ -673,17 +683,17 @@ __device__ __forceinline__ void sts_params(uint32_t at, const void* p, int ptype
     sm100::sts128(at + j * 4, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
 }
 
-template <int DT, int ROWS>
-__global__ void __maxnreg__(kForwardRegs)
+template <int DT, int R, int ROWS>
+__global__ void __maxnreg__(forward_regs(R))
     norm_forward_ring_kernel(const __grid_constant__ NormArgs a) {
   using namespace sm100;
   using L = Elem<DT>;
   constexpr int V = L::V, K = kCols / V, H = V / 2;
   extern __shared__ __align__(128) char stages[];
-  __shared__ __align__(16) float slot[2][36 * 1];
+  __shared__ __align__(16) float slot[2][36 * R];
   __shared__ __align__(8) uint64_t full[kMaxStages];
   const int t = threadIdx.x, nt = blockDim.x;
-  for (int i = t; i < 72; i += nt) slot[i / 36][i % 36] = 0.0f;
+  for (int i = t; i < 72 * R; i += nt) slot[i / (36 * R)][i % (36 * R)] = 0.0f;
   int64_t fetch = blockIdx.x;  // next row to copy (thread 0)
   if (t == 0) {
     for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
@@ -692,7 +702,7 @@ __global__ void __maxnreg__(kForwardRegs)
       fill_stage<DT, false, false>(a, fetch, stages + i * a.stage_bytes, &full[i]);
   }
   __syncthreads();
-  RowsSum<1> sum{slot, nt};
+  RowsSum<R> sum{slot, nt};
   const uint32_t u0 = (t & ~31) * K, u1 = u0 + (t & 31);  // the warp's and the thread's first unit
   const uint32_t base = smem_u32(stages) + u1 * 16;
   const float inv_n = 1.0f / (float)a.cols;
@@ -709,90 +719,110 @@ __global__ void __maxnreg__(kForwardRegs)
   }
   bool ok = true;
   RingPos ring;
-  const char* x = a.x + blockIdx.x * a.xpitch;
-  char* out = a.out + blockIdx.x * a.outpitch;
-  uint8_t* codes = a.codes + blockIdx.x * a.codes_pitch;
-  uint8_t* scales = a.scales + blockIdx.x * a.scales_pitch;
   const int64_t hop = gridDim.x;
-  for (int64_t row = blockIdx.x; row < a.rows;
-       row += hop, x += hop * a.xpitch, out += hop * a.outpitch, codes += hop * a.codes_pitch,
-               scales += hop * a.scales_pitch) {
-    ok = mbar_wait(&full[ring.st], ring.ph, kWaitCycles);
-    const uint32_t stage = base + ring.st * a.stage_bytes;
-    const uint32_t mis = ROWS == kAnywhere ? (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15u) : 0u;
-    uint4 raw[K];
-    float2 c = both(0.0f);
+  for (int64_t row = blockIdx.x; row < a.rows; row += R * hop) {
+    uint4 raw[R][K];
+    float s[R];
+    RingPos next = ring;
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (ROWS == kFull || left[i] > 0)
-        raw[i] = staged_unit<DT, ROWS>(stage + i * 512, mis, left[i]);
-      float2 v[H];
-      unpack2<DT>(raw[i], v);
+    for (int r = 0; r < R; ++r) {
+      const bool here = r == 0 || row + r * hop < a.rows;
+      float2 c = both(0.0f);
+      if (here && !mbar_wait(&full[next.st], next.ph, kWaitCycles)) ok = false;
+      const uint32_t stage = base + next.st * a.stage_bytes;
+      const uint32_t mis =
+          ROWS == kAnywhere
+              ? (uint32_t)(reinterpret_cast<uintptr_t>(a.x + (row + r * hop) * a.xpitch) & 15u)
+              : 0u;
 #pragma unroll
-      for (int j = 0; j < H; ++j) c = __fadd2_rn(c, v[j]);
+      for (int i = 0; i < K; ++i) {
+        raw[r][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (here && (ROWS == kFull || left[i] > 0))
+          raw[r][i] = staged_unit<DT, ROWS>(stage + i * 512, mis, left[i]);
+        float2 v[H];
+        unpack2<DT>(raw[r][i], v);
+#pragma unroll
+        for (int j = 0; j < H; ++j) c = __fadd2_rn(c, v[j]);
+      }
+      s[r] = c.x + c.y;
+      if (here) next.next(a.stages);
     }
-    float s[1] = {c.x + c.y};
     sum(s, ok);
     if (!ok) break;
-    // every thread holds its part of the row: the stage takes a later one
-    if (t == 0 && fetch < a.rows) {
-      fence_proxy_async_smem();
-      fill_stage<DT, false, false>(a, fetch, stages + ring.st * a.stage_bytes, &full[ring.st]);
-      fetch += hop;
-    }
-    ring.next(a.stages);
-    const float mean = s[0] * inv_n;
-    const float2 m = both(-mean);
-    c = both(0.0f);
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      keep_packed(raw[i]);
-      float2 v[H];
-      unpack2<DT>(raw[i], v);
-#pragma unroll
-      for (int j = 0; j < H; ++j) v[j] = __fadd2_rn(v[j], m);
-      if (ROWS != kFull && left[i] < 16) {
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-          if (2 * j * elem_size(DT) >= left[i]) v[j].x = 0.0f;
-          if ((2 * j + 1) * elem_size(DT) >= left[i]) v[j].y = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < H; ++j) c = __ffma2_rn(v[j], v[j], c);
-    }
-    s[0] = c.x + c.y;
-    sum(s, ok);
-    const float rstd = rsqrtf(s[0] * inv_n + a.eps);
+    // every thread holds its part of the rows: their stages take later ones
     if (t == 0) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
-    const float2 rs = both(rstd);
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      keep_packed(raw[i]);
-      const uint32_t u = u1 + i * 32;
-      if (a.codes) {
-        float f[V];
-        L::unpack(raw[i], f);
-        const uint32_t sb = scale_byte(group_max_bits<DT>(raw[i]));
-        if (ROWS == kFull || u * V < a.codes_pitch) {
-          store_codes<DT>(codes + u * V, raw[i], f, sb);
-          if (t % (kActGroup / V) == 0) scales[u * V / kActGroup] = (uint8_t)sb;
-        }
+      for (int r = 0; r < R; ++r) {
+        if (fetch >= a.rows) break;
+        fence_proxy_async_smem();
+        fill_stage<DT, false, false>(a, fetch, stages + ring.st * a.stage_bytes, &full[ring.st]);
+        fetch += hop;
+        ring.next(a.stages);
       }
-      float2 v[H], g[H], b[H];
-      unpack2<DT>(raw[i], v);
-      lds_params<V>(g, gam + i * 32 * (V * 4));
-      lds_params<V>(b, bet + i * 32 * (V * 4));
-#pragma unroll
-      for (int j = 0; j < H; ++j)
-        v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j], m), rs), g[j], b[j]);
-      raw[i] = pack2<DT>(v);
     }
-    put_units<DT, ROWS>(out, u0, a.row_bytes, raw);
+    ring = next;
+    float mean[R], q[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = s[r] * inv_n;
+      const float2 m = both(-mean[r]);
+      float2 c = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        keep_packed(raw[r][i]);
+        float2 v[H];
+        unpack2<DT>(raw[r][i], v);
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[j] = __fadd2_rn(v[j], m);
+        if (ROWS != kFull && left[i] < 16) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            if (2 * j * elem_size(DT) >= left[i]) v[j].x = 0.0f;
+            if ((2 * j + 1) * elem_size(DT) >= left[i]) v[j].y = 0.0f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) c = __ffma2_rn(v[j], v[j], c);
+      }
+      q[r] = c.x + c.y;
+    }
+    sum(q, ok);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t at = row + r * hop;
+      if (r > 0 && at >= a.rows) break;
+      const float rstd = rsqrtf(q[r] * inv_n + a.eps);
+      if (t == 0) {
+        a.mean[at] = mean[r];
+        a.rstd[at] = rstd;
+      }
+      const float2 m = both(-mean[r]), rs = both(rstd);
+      uint8_t* codes = a.codes + at * a.codes_pitch;
+      uint8_t* scales = a.scales + at * a.scales_pitch;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        keep_packed(raw[r][i]);
+        const uint32_t u = u1 + i * 32;
+        if (a.codes) {
+          float f[V];
+          L::unpack(raw[r][i], f);
+          const uint32_t sb = scale_byte(group_max_bits<DT>(raw[r][i]));
+          if (ROWS == kFull || u * V < a.codes_pitch) {
+            store_codes<DT>(codes + u * V, raw[r][i], f, sb);
+            if (t % (kActGroup / V) == 0) scales[u * V / kActGroup] = (uint8_t)sb;
+          }
+        }
+        float2 v[H], g[H], b[H];
+        unpack2<DT>(raw[r][i], v);
+        lds_params<V>(g, gam + i * 32 * (V * 4));
+        lds_params<V>(b, bet + i * 32 * (V * 4));
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+          v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j], m), rs), g[j], b[j]);
+        raw[r][i] = pack2<DT>(v);
+      }
+      put_units<DT, ROWS>(a.out + at * a.outpitch, u0, a.row_bytes, raw[r]);
+    }
   }
   ring_end(ok, a.status);
 }
@@ -1087,15 +1117,13 @@ constexpr int kMaxSms = 160;  // the scratch is sized for at most so many
 struct RingPlan {
   int threads;  // of the rows; 0: not this way
   uint32_t second_at, scales_at, stage_bytes, smem;
-  int stages, per_sm;
+  int stages, per_sm, rows;  // rows: of a forward block at once
 };
 
-// Shared memory that each of n blocks of an SM may use (228 KB, of which the
-// system takes 1 KB a block, and the kernels' static part; one block at most
-// 227 KB).
-int64_t block_smem(int n) {
-  return std::min<int64_t>(228 * 1024 / n - 1024, 226 * 1024) - 512;
-}
+// Dynamic shared memory that each of n blocks of an SM may use: 228 KB less
+// the system's 1 KB a block and the kernels' static part (624 bytes: two turns
+// of 2 x 36 sums, the barriers).
+int64_t block_smem(int n) { return 228 * 1024 / n - 1024 - 768; }
 
 // Threads of a row; 0 where rows are too narrow or too wide.  (A wider row's
 // threads would leave an SM a single block of more registers: 11008 columns
@@ -1103,13 +1131,12 @@ int64_t block_smem(int n) {
 // a row twice.)
 int ring_threads(int64_t cols, bool back) {
   const int64_t c = ckpt_codes_pitch(cols);
-  return c <= 512 || c > (back ? 512 : 1024) * kCols ? 0 : (int)round_up(ceil_div(c, kCols), 32);
+  const int threads = back ? 512 : forward_warps(1) * 32;
+  return c <= 512 || c > threads * kCols ? 0 : (int)round_up(ceil_div(c, kCols), 32);
 }
 
-// Blocks per SM by registers, the backward kernel's producer warp counted.
-int ring_blocks(int threads, bool back) {
-  return back ? kBackwardWarps / (threads / 32 + 1) : kForwardWarps / (threads / 32);
-}
+// Blocks of the backward kernel per SM by registers, the producer warp counted.
+int backward_blocks(int threads) { return std::max(1, kBackwardWarps / (threads / 32 + 1)); }
 
 RingPlan ring_plan(int64_t cols, int dtype, bool back, bool ckpt) {
   RingPlan p{};
@@ -1125,11 +1152,12 @@ RingPlan ring_plan(int64_t cols, int dtype, bool back, bool ckpt) {
   p.stage_bytes = (uint32_t)round_up(bytes, 128);
   const int64_t params = (int64_t)p.threads * kCols * (back ? 4 : 8);
   // as many blocks as registers allow, fewer where two stages do not fit
-  p.per_sm = ring_blocks(p.threads, back);
+  p.rows = forward_rows(c, dtype);
+  p.per_sm = back ? backward_blocks(p.threads) : forward_warps(p.rows) / (p.threads / 32);
   while (p.per_sm > 1 && params + 2 * (int64_t)p.stage_bytes > block_smem(p.per_sm)) --p.per_sm;
   p.stages =
       (int)std::min<int64_t>(kMaxStages, (block_smem(p.per_sm) - params) / p.stage_bytes);
-  if (p.stages < 2) return RingPlan{};
+  if (p.stages < 2) return RingPlan{};  // two rows at once need two
   p.smem = (uint32_t)(p.stages * (int64_t)p.stage_bytes + params);
   return p;
 }
@@ -1145,7 +1173,7 @@ void apply(NormArgs& a, const RingPlan& p, const gc_ctx* ctx) {
 template <auto Kernel>
 void launch_ring(gc_ctx* ctx, const NormArgs& a, const RingPlan& p, unsigned grid, int threads) {
   static uint64_t devices = 0;
-  if (!allow_smem(ctx, Kernel, 226 * 1024, devices)) return;  // the launch's error says so
+  if (!allow_smem(ctx, Kernel, (int)block_smem(1), devices)) return;  // the launch's error says so
   Kernel<<<grid, threads, p.smem, ctx->stream>>>(a);
 }
 
@@ -1168,13 +1196,13 @@ void forward_warp(gc_ctx* ctx, const NormArgs& a, bool aligned) {
     norm_forward_warp_kernel<DT, K, false><<<g, 256, smem, ctx->stream>>>(a);
 }
 
-template <int DT>
+template <int DT, int R>
 void forward_ring(gc_ctx* ctx, const NormArgs& a, const RingPlan& p, bool aligned) {
   const unsigned g = (unsigned)std::min<int64_t>(a.rows, (int64_t)ctx->num_sms * p.per_sm);
-  if (!aligned) launch_ring<norm_forward_ring_kernel<DT, kAnywhere>>(ctx, a, p, g, p.threads);
+  if (!aligned) launch_ring<norm_forward_ring_kernel<DT, R, kAnywhere>>(ctx, a, p, g, p.threads);
   else if (a.cols == (int64_t)p.threads * kCols)
-    launch_ring<norm_forward_ring_kernel<DT, kFull>>(ctx, a, p, g, p.threads);
-  else launch_ring<norm_forward_ring_kernel<DT, kEnds>>(ctx, a, p, g, p.threads);
+    launch_ring<norm_forward_ring_kernel<DT, R, kFull>>(ctx, a, p, g, p.threads);
+  else launch_ring<norm_forward_ring_kernel<DT, R, kEnds>>(ctx, a, p, g, p.threads);
 }
 
 template <int DT>
@@ -1191,7 +1219,8 @@ void forward_dt(gc_ctx* ctx, NormArgs& a, bool aligned) {
     const RingPlan p = ring_plan(a.cols, DT, false, false);
     if (p.threads) {
       apply(a, p, ctx);
-      forward_ring<DT>(ctx, a, p, aligned);
+      if (DT != GC_F32 && p.rows == 2) forward_ring<DT, DT == GC_F32 ? 1 : 2>(ctx, a, p, aligned);
+      else forward_ring<DT, 1>(ctx, a, p, aligned);
     } else {
       forward_block<DT, 0>(ctx, a, 1024, aligned);
     }
@@ -1201,7 +1230,7 @@ void forward_dt(gc_ctx* ctx, NormArgs& a, bool aligned) {
 // Partial rows of the column sums that a call may leave.
 int64_t max_parts(int64_t cols) {
   const int threads = ring_threads(cols, true);
-  return (int64_t)kMaxSms * (threads ? ring_blocks(threads, true) : 2);
+  return (int64_t)kMaxSms * (threads ? backward_blocks(threads) : 2);
 }
 
 template <int DT, bool CKPT>
