@@ -821,7 +821,7 @@ gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
   if (db) GC_TRY(check_buf(db, out > 0));
   // tensor-map coordinates are 32 bits; fp32 takes three planes of rows
   if (dtype == GC_F32 && rows > ((int64_t)1 << 29)) return GC_ERR_UNSUPPORTED;
-  if (used && ctx->scratch_bytes < gc::wgrad_scratch_bytes(rows, out, in, dtype))
+  if ((used || db) && ctx->scratch_bytes < gc::wgrad_scratch_bytes(rows, out, in, dtype))
     return GC_ERR_WORKSPACE;
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return GC_ERR_CUDA;

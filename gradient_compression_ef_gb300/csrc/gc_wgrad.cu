@@ -812,60 +812,13 @@ gc_status launch_tiles(gc_ctx* ctx, const CUtensorMap& md, const CUtensorMap& mc
   return GC_OK;
 }
 
-}  // namespace
-
-int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype) {
-  if (rows == 0 || out == 0 || in == 0) return 0;
-  // partials of at most two slots per range, never more than one range per
-  // pair; a plane of 16-bit dy in case its rows are not 16-byte aligned
-  const Plan p = make_plan(rows, out, in, plane_count(dtype), kMaxPairs);
-  const int64_t tiles = p.in_tiles * p.out_tiles;
-  const int64_t slots = std::min<int64_t>(2 * kMaxPairs, tiles * p.blocks);
-  return planes_bytes(rows, out, dtype) + slots * kSlotBytes +
-         up256((int64_t)kMaxBiasParts * out * 4);
-}
-
-gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, const uint8_t* codes,
-                       const uint8_t* scales, int64_t rows, int64_t out, int64_t in, float* dw,
-                       int64_t lddw, float* db, int accumulate, void* scratch) {
-  if (out == 0 || in == 0) return GC_OK;
-  if (rows == 0) {
-    if (accumulate) return GC_OK;
-    if (cudaMemset2DAsync(dw, lddw * 4, 0, in * 4, out, ctx->stream) != cudaSuccess ||
-        (db && cudaMemsetAsync(db, 0, out * 4, ctx->stream) != cudaSuccess))
-      return GC_ERR_CUDA;
-    return GC_OK;
-  }
-  char* at = static_cast<char*>(scratch);
-  uint16_t* planes = reinterpret_cast<uint16_t*>(at);
-  at += planes_bytes(rows, out, dtype);
-  float* bias_part = reinterpret_cast<float*>(at);
-  at += up256((int64_t)kMaxBiasParts * out * 4);
-
-  WgradArgs a{};
+// The tiles, with dy's planes where they are needed.  early: the kernel before
+// on the stream is db's, of which these need nothing.
+gc_status launch_product(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
+                         const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                         uint16_t* planes, const WgradArgs& a, bool early) {
+  const int64_t out = a.out, in = a.in;
   const int np = plane_count(dtype);
-  a.plan = make_plan(rows, out, in, np, ctx->num_sms / 2);
-  a.dw = dw;
-  a.db = db;
-  a.part = reinterpret_cast<float*>(at);
-  a.bias_part = bias_part;
-  a.status = ctx->ws.status;
-  a.out = out;
-  a.in = in;
-  a.lddw = lddw;
-  a.plane_rows = a.plan.tok_blocks * kTok;
-  a.accumulate = accumulate;
-  if (db) {
-    if (dtype == GC_F32)
-      a.bias_parts = launch_bias<GC_F32>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-    else if (dtype == GC_BF16)
-      a.bias_parts = launch_bias<GC_BF16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-    else
-      a.bias_parts = launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-  }
-
-  bool early = db != nullptr;
-
   // the tensor map takes dy as it lies when its rows start on 16-byte
   // boundaries
   const void* d16 = dy;
@@ -892,10 +845,68 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
       !make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, rows, cp, cp, kHalf, false) ||
       !make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, rows, sp, sp, 16, false))
     return GC_ERR_CUDA;
-  const gc_status st =
-      f16 ? launch_tiles<true>(ctx, md, mc, ms, a, early)
-          : launch_tiles<false>(ctx, md, mc, ms, a, early);
-  if (st != GC_OK) return st;
+  return f16 ? launch_tiles<true>(ctx, md, mc, ms, a, early)
+             : launch_tiles<false>(ctx, md, mc, ms, a, early);
+}
+
+}  // namespace
+
+int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype) {
+  if (rows == 0 || out == 0) return 0;
+  const int64_t bias = up256((int64_t)kMaxBiasParts * out * 4);
+  if (in == 0) return bias;
+  // partials of at most two slots per range, never more than one range per
+  // pair; a plane of 16-bit dy in case its rows are not 16-byte aligned
+  const Plan p = make_plan(rows, out, in, plane_count(dtype), kMaxPairs);
+  const int64_t tiles = p.in_tiles * p.out_tiles;
+  const int64_t slots = std::min<int64_t>(2 * kMaxPairs, tiles * p.blocks);
+  return planes_bytes(rows, out, dtype) + slots * kSlotBytes + bias;
+}
+
+gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, const uint8_t* codes,
+                       const uint8_t* scales, int64_t rows, int64_t out, int64_t in, float* dw,
+                       int64_t lddw, float* db, int accumulate, void* scratch) {
+  if (out == 0) return GC_OK;
+  if (rows == 0) {
+    if (accumulate) return GC_OK;
+    if ((in && cudaMemset2DAsync(dw, lddw * 4, 0, in * 4, out, ctx->stream) != cudaSuccess) ||
+        (db && cudaMemsetAsync(db, 0, out * 4, ctx->stream) != cudaSuccess))
+      return GC_ERR_CUDA;
+    return GC_OK;
+  }
+  char* at = static_cast<char*>(scratch);
+  float* bias_part = reinterpret_cast<float*>(at);
+  at += up256((int64_t)kMaxBiasParts * out * 4);
+  uint16_t* planes = reinterpret_cast<uint16_t*>(at);
+  at += planes_bytes(rows, out, dtype);
+
+  WgradArgs a{};
+  const int np = plane_count(dtype);
+  if (in) a.plan = make_plan(rows, out, in, np, ctx->num_sms / 2);
+  a.dw = dw;
+  a.db = db;
+  a.part = reinterpret_cast<float*>(at);
+  a.bias_part = bias_part;
+  a.status = ctx->ws.status;
+  a.out = out;
+  a.in = in;
+  a.lddw = lddw;
+  a.plane_rows = a.plan.tok_blocks * kTok;
+  a.accumulate = accumulate;
+  if (db) {
+    if (dtype == GC_F32)
+      a.bias_parts = launch_bias<GC_F32>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    else if (dtype == GC_BF16)
+      a.bias_parts = launch_bias<GC_BF16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    else
+      a.bias_parts = launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+  }
+
+  if (in) {
+    const gc_status st =
+        launch_product(ctx, dy, dtype, lddy, codes, scales, rows, planes, a, db != nullptr);
+    if (st != GC_OK) return st;
+  }
   const int64_t tile_blocks =
       a.plan.ranges > a.plan.rest ? a.plan.rest * (kTile / kJoinRows) : 0;
   const int64_t bias_blocks = a.bias_parts ? ceil_div(out, 32) : 0;

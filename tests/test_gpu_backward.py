@@ -504,6 +504,23 @@ def test_linear_wgrad_without_rows(gc, ctx):
     assert bool((dw == 0).all()) and bool((db == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [0, 3, 1000])
+def test_linear_wgrad_without_input_features(gc, ctx, rows, dtype):
+    """A layer that is only a bias: db is written all the same."""
+    import torch
+    out = 40
+    r = np.random.default_rng(rows)
+    dy, dyv, _ = matrix(r.standard_normal((rows, out)), dtype)
+    codes, scales = ckpt(rows, 0)
+    dw, db = torch.empty(out, 0, device="cuda"), torch.full((out,), 2.0, device="cuda")
+    tol = (rows / 8 + 64) * 2.0 ** -23 * np.abs(dyv).sum(axis=0)
+    gc.linear_wgrad(ctx, dy, codes, scales, dw, db, accumulate=True)
+    close(f64(db), 2 + dyv.sum(axis=0), tol + 2.0 ** -20, "db on top")
+    gc.linear_wgrad(ctx, dy, codes, scales, dw, db)
+    close(f64(db), dyv.sum(axis=0), tol, "db")
+
+
 @pytest.mark.parametrize("dtype,rows,cols,out", [("f32", 2501, 1001, 2051), ("bf16", 4096, 2048, 5504)])
 def test_linear_wgrad_back_to_back(gc, ctx, dtype, rows, cols, out):
     """Hundreds of calls in a row on rotating inputs (codes and dy come from
