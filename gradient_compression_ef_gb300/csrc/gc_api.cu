@@ -199,8 +199,7 @@ const char* gc_phase_name(int phase) {
       "refine", "bk_hist", "bk_collect", "bk_refine", "bk_write", "bk_quant", "agg_bounds",
       "agg_accumulate", "randk_mark", "randk_write", "bk_diag", "bk_flush", "psgd_thin",
       "ckpt_save", "ckpt_restore", "act_forward", "act_backward", "norm_forward",
-      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join",
-      "wgrad_bias"};
+      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join"};
   return (phase >= 0 && phase < GC_PHASE_COUNT) ? names[phase] : "?";
 }
 

@@ -15,6 +15,7 @@
 // inputs x 256 outputs; each CTA holds 128 input columns of x^ and 128
 // output columns of dy per block of 64 tokens.
 //   producers two threads: TMA of dy (128-byte swizzle); of codes and scale bytes
+//   db        one warp: column sums of dy, through a ring of boxes of its own
 //   converter two groups of 4 warps, every second block each: codes -> bf16
 //             (or fp16) operand in shared memory
 //   issuer    one thread of the leader CTA: the MMAs of the pair
@@ -45,8 +46,10 @@ constexpr int kGroups = 2, kGroupWarps = kConvWarps / kGroups;
 // could not tell by the parity which of the two it sees.
 static_assert(kStages % kGroups == 0 && kCodeStages % kGroups == 0, "a stage has one group");
 constexpr int kDyWarp = kReadWarps + kConvWarps, kIssuerWarp = kDyWarp + 1,
-              kCodeWarp = kDyWarp + 2;
+              kCodeWarp = kDyWarp + 2, kBiasWarp = kDyWarp + 3;
 constexpr int kThreads = 640;        // 5 warpgroups
+constexpr int kBiasStages = 4;       // boxes of 64 tokens x 64 outputs
+constexpr uint32_t kBiasBytes = kTok * 64 * 2;
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
 constexpr int kSegBlocks = 8;        // token blocks per accumulator
 constexpr int kMaxPairs = 96;
@@ -67,11 +70,12 @@ struct WgradArgs {
   Plan plan;
   float *dw, *db;
   float* part;        // [2 * ranges][256 outputs][256 inputs]
-  float* bias_part;   // [bias_parts][out]
-  int bias_parts;     // 0: db is done, or not asked for
+  // db: bias_len token blocks of 64 outputs at a time are one of bias_items
+  float* bias_part;    // [bias_parts][out], where there are several
+  uint32_t bias_items;  // 0: no db asked for
+  uint32_t bias_len, bias_parts, strips;
   uint32_t* status;
   int64_t out, in, lddw;
-  int64_t plane_rows;  // rows from one plane of dy to the next
   int accumulate;
 };
 
@@ -116,14 +120,15 @@ __host__ __device__ inline void tile_place(const Plan& p, int64_t t, int64_t& it
 }
 
 struct Smem {
-  uint32_t a, b, codes, scales;  // shared addresses
-  uint64_t *full, *empty, *cfull, *cempty, *acc_full, *acc_empty, *drain;
+  uint32_t a, b, bias, codes, scales;  // shared addresses
+  uint64_t *full, *empty, *cfull, *cempty, *acc_full, *acc_empty, *bfull, *drain;
   uint32_t* tmem_slot;
 };
 
 constexpr size_t kSmemBytes =
-    1024 + (size_t)kStages * 2 * kOpBytes + (size_t)kCodeStages * (kCodeBytes + kScaleBytes) +
-    8 * (2 * kStages + 2 * kCodeStages + 5) + 16;
+    1024 + (size_t)kStages * 2 * kOpBytes + (size_t)kBiasStages * kBiasBytes +
+    (size_t)kCodeStages * (kCodeBytes + kScaleBytes) +
+    8 * (2 * kStages + 2 * kCodeStages + kBiasStages + 5) + 16;
 
 __device__ __forceinline__ Smem carve(unsigned char* base) {
   Smem s;
@@ -131,7 +136,8 @@ __device__ __forceinline__ Smem carve(unsigned char* base) {
   unsigned char* p = base + (at - sm100::smem_u32(base));
   s.a = at;
   s.b = s.a + kStages * kOpBytes;
-  s.codes = s.b + kStages * kOpBytes;
+  s.bias = s.b + kStages * kOpBytes;
+  s.codes = s.bias + kBiasStages * kBiasBytes;
   s.scales = s.codes + kCodeStages * kCodeBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(p + (s.scales - at) + kCodeStages * kScaleBytes);
   s.full = bar;
@@ -140,7 +146,8 @@ __device__ __forceinline__ Smem carve(unsigned char* base) {
   s.cempty = s.cfull + kCodeStages;
   s.acc_full = s.cempty + kCodeStages;
   s.acc_empty = s.acc_full + 2;
-  s.drain = s.acc_empty + 2;
+  s.bfull = s.acc_empty + 2;
+  s.drain = s.bfull + kBiasStages;
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
   return s;
 }
@@ -158,18 +165,14 @@ struct Ring {
   }
 };
 
-// A block's plane of dy and place in it, counted up without divisions.
+// A block's place in its plane of dy, counted up without divisions.
 struct TokCursor {
-  int32_t tb, per, plane;
+  int32_t tb, per;
   __device__ __forceinline__ TokCursor(int64_t k, int64_t tok_blocks) : per((int32_t)tok_blocks) {
-    plane = (int32_t)((uint32_t)k / (uint32_t)per);
-    tb = (int32_t)k - plane * per;
+    tb = (int32_t)((uint32_t)k % (uint32_t)per);
   }
-  __device__ __forceinline__ bool next() {  // true at the end of a plane
-    if (++tb < per) return false;
-    tb = 0;
-    ++plane;
-    return true;
+  __device__ __forceinline__ void next() {
+    if (++tb == per) tb = 0;
   }
 };
 
@@ -250,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&s.acc_full[i], 1);
       mbar_init(&s.acc_empty[i], 2 * kReadWarps);
     }
+    for (int i = 0; i < kBiasStages; ++i) mbar_init(&s.bfull[i], 1);
     mbar_init(s.drain, 1);
     mbar_fence_init();
   }
@@ -267,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Unit u;
 
   if (warp >= kDyWarp) {
-    reg_dec<40>();
+    reg_dec<64>();
     // These three warps run their loops as whole warps (uniform registers);
     // one elected lane issues.
     if (warp == kCodeWarp) {
@@ -303,15 +307,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kDyWarp) {
       const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
+      after_previous();  // dy's planes
       Ring<kStages> ring;
       uint32_t loads = 0;
       while (ok && work.next(u)) {
         int64_t it, ot;
         tile_place(a.plan, u.tile, it, ot);
         const int32_t x = (int32_t)(ot * kTile) + (int32_t)rank * kHalf;
-        TokCursor cur(u.k0, a.plan.tok_blocks);
-        int32_t row0 = (int32_t)(cur.plane * a.plane_rows);
-        for (int32_t n = (int32_t)(u.k1 - u.k0); n > 0; --n, ring.next()) {
+        int32_t y = (int32_t)u.k0 * kTok;  // planes follow one another without a gap
+        for (int32_t n = (int32_t)(u.k1 - u.k0); n > 0; --n, ring.next(), y += kTok) {
           const int st = ring.st;
           if (loads >= kStages) {
             // free once the pair's MMAs read it
@@ -325,12 +329,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kOpBytes);
-            const int32_t y = row0 + cur.tb * kTok;
             const uint32_t dst = s.b + st * kOpBytes;
             tma_load_2d_pair(dst, &map_dy, x, y, bar0 + st * 8);
             tma_load_2d_pair(dst + kOpBytes / 2, &map_dy, x + 64, y, bar0 + st * 8);
           }
-          if (cur.next()) row0 += (int32_t)a.plane_rows;
         }
       }
       // the arrivals of the last MMAs on this CTA's barriers: none may be
@@ -380,6 +382,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             in_seg = 0;
           }
         }
+      }
+    }
+    // Column sums of dy, beside the product and out of its way: a box is added
+    // up by itself (16 additions), then to the item's sum.
+    if (warp == kBiasWarp && a.bias_items > 0) {
+      after_previous();
+      const int c = lane & 7, r = lane >> 3;  // 16-byte chunk, first row
+      const uint32_t off0 = (uint32_t)(r * 128 + ((c ^ r) << 4));
+      const uint32_t off1 = (uint32_t)(r * 128 + ((c ^ (r + 4)) << 4));
+      // every gridDim.x-th item; box k .. k1 of `item` is the next to load,
+      // `left` boxes of `use` are to be added up
+      const uint32_t blocks = (uint32_t)a.plan.blocks;
+      uint32_t item = blockIdx.x, use = item, k = 0, k1 = 0, left = 0, x = 0;
+      int32_t y = 0;
+      auto more = [&] { return k < k1 || item < a.bias_items; };
+      auto load = [&](int st) {
+        if (k >= k1) {
+          const uint32_t part = item / a.strips;
+          x = (item - part * a.strips) * 64;
+          k = part * a.bias_len;
+          k1 = min(blocks, k + a.bias_len);
+          item += gridDim.x;
+          y = (int32_t)(k * kTok);
+        }
+        if (elect_one()) {
+          fence_proxy_async_smem();  // the warp read the stage through the generic proxy
+          mbar_arrive_expect_tx(&s.bfull[st], kBiasBytes);
+          tma_load_2d(s.bias + st * kBiasBytes, &map_dy, (int32_t)x, y, &s.bfull[st]);
+        }
+        ++k;
+        y += kTok;
+      };
+      for (int i = 0; i < kBiasStages && more(); ++i) load(i);
+      float2 sum[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
+      Ring<kBiasStages> ring;
+      for (; use < a.bias_items; ring.next()) {
+        const uint32_t part = use / a.strips;
+        if (left == 0) left = min(blocks - part * a.bias_len, a.bias_len);
+        const bool got = mbar_wait(&s.bfull[ring.st], ring.ph, kWaitCycles);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t at = s.bias + ring.st * kBiasBytes;
+        float2 box[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+          uint4 raw[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) raw[e] = lds_u4(at + (e & 1 ? off1 : off0) + (i + e) * 512);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float2 v[4];
+            unpack2<F16 ? GC_F16 : GC_BF16>(raw[e], v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) box[j] = __fadd2_rn(box[j], v[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = __fadd2_rn(sum[j], box[j]);
+        __syncwarp();
+        if (more()) load(ring.st);
+        if (--left) continue;
+        const int64_t o = (int64_t)(use - part * a.strips) * 64 + c * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float t = j & 1 ? sum[j / 2].y : sum[j / 2].x;
+          t += __shfl_xor_sync(0xffffffffu, t, 8);
+          t += __shfl_xor_sync(0xffffffffu, t, 16);
+          if (r == 0 && o + j < a.out) {
+            if (a.bias_parts > 1) a.bias_part[part * a.out + o + j] = t;
+            else a.db[o + j] = a.accumulate ? a.db[o + j] + t : t;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = both(0.0f);
+        use += gridDim.x;
       }
     }
     // MMAs still in flight read both CTAs' shared memory: wait for them (the
@@ -447,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       skip = k - u.k1;
     }
   } else {
-    reg_inc<168>();
+    reg_inc<160>();
     // warp w reads lanes 32 (w % 4) .. + 31 (inputs) of columns 128 (w / 4)
     // .. + 127 (outputs) of every accumulator
     const uint32_t q = (uint32_t)warp & 3u, ch = (uint32_t)warp >> 2;
@@ -511,7 +590,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  after_previous();  // db's sums, which this kernel may not have waited for
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -537,7 +615,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__
     float v = 0.0f;
     if (o < a.out) {
 #pragma unroll 8
-      for (int i = warp; i < a.bias_parts; i += 8) v += a.bias_part[i * a.out + o];
+      for (int i = warp; i < (int)a.bias_parts; i += 8) v += a.bias_part[i * a.out + o];
     }
     s[warp][lane] = v;
     __syncthreads();
@@ -600,6 +678,7 @@ __global__ void __launch_bounds__(256) wgrad_split_kernel(const char* dy, const 
                                                           int64_t plane_rows, int64_t pitch) {
   using E = Elem<DT>;
   constexpr int V = E::V;
+  let_next_begin();
   const int64_t segs = (pitch + 32 * V - 1) / (32 * V), total = plane_rows * segs;
   for (int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); at < total;
        at += (int64_t)gridDim.x * 8) {
@@ -625,70 +704,9 @@ __global__ void __launch_bounds__(256) wgrad_split_kernel(const char* dy, const 
       *reinterpret_cast<uint4*>(dst) = raw;
     }
   }
-  after_previous();  // db's sums, which this kernel did not wait for
-}
-
-// Column sums of dy: block (x, y) adds rows y * rows_per .. of 32 units (256
-// columns, 128 of fp32), eight warps taking every eighth row, into
-// part[y][out], or into db when there is one row range.
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(256) bias_kernel(const char* dy, const char* end, int64_t rows,
-                                                   int64_t out, int64_t dy_pitch,
-                                                   int64_t rows_per, float* part, float* db,
-                                                   int accumulate) {
-  constexpr int V = Elem<DT>::V, W = 32 * V;
-  __shared__ float s[8][W];
-  let_next_begin();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t off = ((int64_t)blockIdx.x * 32 + lane) * 16;
-  const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(rows, r0 + rows_per);
-  const int64_t bytes = out * elem_size(DT);
-  float2 v2[V / 2];
-#pragma unroll
-  for (int j = 0; j < V / 2; ++j) v2[j] = both(0.0f);
-  auto add = [&](const uint4& raw) {
-    float2 d[V / 2];
-    unpack2<DT>(raw, d);
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) v2[j] = __fadd2_rn(v2[j], d[j]);
-  };
-  if (ALIGNED && off + 16 <= bytes) {  // plain loads, eight at a time
-    const char* p = dy + (r0 + warp) * dy_pitch + off;
-    int64_t r = r0 + warp;
-    for (; r + 56 < r1; r += 64, p += 64 * dy_pitch) {
-      uint4 raw[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        raw[k] = __ldg(reinterpret_cast<const uint4*>(p + k * 8 * dy_pitch));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) add(raw[k]);
-    }
-    for (; r < r1; r += 8, p += 8 * dy_pitch) add(__ldg(reinterpret_cast<const uint4*>(p)));
-  } else {
-    for (int64_t r = r0 + warp; r < r1; r += 8)
-      add(load_unit<DT, ALIGNED>(dy + r * dy_pitch, off, bytes, end));
-  }
-  float v[V];
-#pragma unroll
-  for (int j = 0; j < V / 2; ++j) {
-    v[2 * j] = v2[j].x;
-    v[2 * j + 1] = v2[j].y;
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) s[warp][lane * V + j] = v[j];
-  __syncthreads();
-  const int64_t o = (int64_t)blockIdx.x * W + threadIdx.x;
-  if ((int)threadIdx.x >= W || o >= out) return;
-  float t = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
-  if (gridDim.y > 1) part[(int64_t)blockIdx.y * out + o] = t;
-  else db[o] = accumulate ? db[o] + t : t;
 }
 
 // --- host ----------------------------------------------------------------------------------------
-
-constexpr int kMaxBiasParts = 304;
 
 int plane_count(int dtype) { return dtype == GC_F32 ? 3 : 1; }
 
@@ -716,6 +734,17 @@ int64_t planes_bytes(int64_t rows, int64_t out, int dtype) {
   return up256((int64_t)plane_count(dtype) * round_up(rows, kTok) * round_up(out, 8) * 2);
 }
 constexpr int64_t kSlotBytes = (int64_t)kTile * kTile * 4;
+
+// Token blocks of one partial row of db: 8 (512 tokens), more where the
+// partial rows would be over kMaxBiasParts.
+constexpr int kMaxBiasParts = 127;
+int64_t bias_len(int64_t blocks) {
+  return std::max<int64_t>(kSegBlocks, ceil_div(blocks, (int64_t)kMaxBiasParts));
+}
+int64_t bias_bytes(int64_t blocks, int64_t out) {
+  const int64_t parts = ceil_div(blocks, bias_len(blocks));
+  return parts > 1 ? up256(parts * out * 4) : 0;
+}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -749,34 +778,9 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int6
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launches db's sums; returns the partial rows that are left to add.
 template <int DT>
-int launch_bias(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy, float* db,
-                int accumulate, float* part) {
-  constexpr int kSize = elem_size(DT);
-  const int64_t bx = ceil_div(out, 32 * Elem<DT>::V);
-  const int64_t want = std::min<int64_t>({ceil_div((int64_t)ctx->num_sms * 8, bx),
-                                          ceil_div(rows, 64), (int64_t)kMaxBiasParts});
-  const int64_t rows_per = ceil_div(rows, std::max<int64_t>(want, 1));
-  const int64_t by = ceil_div(rows, rows_per);
-  const dim3 g((unsigned)bx, (unsigned)by);
-  const char* p = static_cast<const char*>(dy);
-  const char* end = p + ((rows - 1) * lddy + out) * kSize;
-  LaunchScope L(ctx, GC_PHASE_WGRAD_BIAS);
-  if (row_aligned(lddy, DT))
-    bias_kernel<DT, true><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize, rows_per,
-                                                      part, db, accumulate);
-  else
-    bias_kernel<DT, false><<<g, 256, 0, ctx->stream>>>(p, end, rows, out, lddy * kSize, rows_per,
-                                                       part, db, accumulate);
-  return by > 1 ? (int)by : 0;
-}
-
-// early: the kernel before on the stream is db's, of which this one needs
-// nothing.
-template <int DT>
-gc_status launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
-                       uint16_t* planes, int64_t plane_rows, int64_t pitch, bool early) {
+void launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, int64_t lddy,
+                       uint16_t* planes, int64_t plane_rows, int64_t pitch) {
   constexpr int kSize = elem_size(DT);
   const int64_t total = plane_rows * ceil_div(pitch, 32 * Elem<DT>::V);
   const unsigned g = (unsigned)std::min<int64_t>(ceil_div(total, 8), (int64_t)ctx->num_sms * 8);
@@ -785,14 +789,8 @@ gc_status launch_split(gc_ctx* ctx, const void* dy, int64_t rows, int64_t out, i
   const auto kernel =
       row_aligned(lddy, DT) ? wgrad_split_kernel<DT, true> : wgrad_split_kernel<DT, false>;
   LaunchScope L(ctx, GC_PHASE_WGRAD_SPLIT);
-  if (early)
-    return launch_early(kernel, dim3(g), 256, 0, ctx->stream, p, end, rows, out * kSize,
-                        lddy * kSize, planes, plane_rows, pitch) == cudaSuccess
-               ? GC_OK
-               : GC_ERR_CUDA;
   kernel<<<g, 256, 0, ctx->stream>>>(p, end, rows, out * kSize, lddy * kSize, planes, plane_rows,
                                      pitch);
-  return GC_OK;
 }
 
 template <bool F16>
@@ -801,7 +799,9 @@ gc_status launch_tiles(gc_ctx* ctx, const CUtensorMap& md, const CUtensorMap& mc
   static uint64_t devices = 0;
   if (!allow_smem(ctx, wgrad_kernel<F16>, (int)kSmemBytes, devices)) return GC_ERR_CUDA;
   const int64_t pairs =
-      a.plan.full ? a.plan.pairs : std::min<int64_t>(a.plan.pairs, a.plan.ranges);
+      a.plan.full ? a.plan.pairs
+                  : std::min<int64_t>(a.plan.pairs,
+                                      std::max(a.plan.ranges, ceil_div((int64_t)a.bias_items, 2)));
   LaunchScope L(ctx, GC_PHASE_WGRAD);
   if (early)
     return launch_early(wgrad_kernel<F16>, dim3((unsigned)(2 * pairs)), kThreads, kSmemBytes,
@@ -812,28 +812,24 @@ gc_status launch_tiles(gc_ctx* ctx, const CUtensorMap& md, const CUtensorMap& mc
   return GC_OK;
 }
 
-// The tiles, with dy's planes where they are needed.  early: the kernel before
-// on the stream is db's, of which these need nothing.
+// The tiles and db, with dy's planes where they are needed.
 gc_status launch_product(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
                          const uint8_t* codes, const uint8_t* scales, int64_t rows,
-                         uint16_t* planes, const WgradArgs& a, bool early) {
+                         uint16_t* planes, const WgradArgs& a) {
   const int64_t out = a.out, in = a.in;
-  const int np = plane_count(dtype);
   // the tensor map takes dy as it lies when its rows start on 16-byte
   // boundaries
   const void* d16 = dy;
   int64_t d_rows = rows, d_cols = out, d_pitch = lddy * 2;
-  if (dtype == GC_F32 || (rows > 1 && lddy * 2 % 16 != 0)) {
+  const bool split = dtype == GC_F32 || (rows > 1 && lddy * 2 % 16 != 0);
+  if (split) {
     d_cols = round_up(out, 8);
     d_pitch = d_cols * 2;
-    d_rows = np * a.plane_rows;
+    d_rows = a.plan.blocks * kTok;
     d16 = planes;
-    const gc_status st =
-        dtype == GC_F32
-            ? launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols, early)
-            : launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plane_rows, d_cols, early);
-    if (st != GC_OK) return st;
-    early = false;  // the tiles need the planes
+    if (dtype == GC_F32)
+      launch_split<GC_F32>(ctx, dy, rows, out, lddy, planes, a.plan.tok_blocks * kTok, d_cols);
+    else launch_split<GC_BF16>(ctx, dy, rows, out, lddy, planes, a.plan.tok_blocks * kTok, d_cols);
   } else if (rows == 1) {
     d_pitch = round_up(out * 2, 16);
   }
@@ -841,26 +837,27 @@ gc_status launch_product(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
   CUtensorMap md, mc, ms;
   const int64_t cp = ckpt_codes_pitch(in), sp = ckpt_scales_pitch(in);
   if (!make_map(&md, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d16,
-                d_rows, d_cols, d_pitch, 64, true) ||
-      !make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, rows, cp, cp, kHalf, false) ||
-      !make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, rows, sp, sp, 16, false))
+                d_rows, d_cols, d_pitch, 64, true))
     return GC_ERR_CUDA;
-  return f16 ? launch_tiles<true>(ctx, md, mc, ms, a, early)
-             : launch_tiles<false>(ctx, md, mc, ms, a, early);
+  mc = ms = md;  // without inputs there are no tiles to read codes for
+  if (in && (!make_map(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, rows, cp, cp, kHalf, false) ||
+             !make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, rows, sp, sp, 16, false)))
+    return GC_ERR_CUDA;
+  // behind the split the kernel may begin early: only dy waits for the planes
+  return f16 ? launch_tiles<true>(ctx, md, mc, ms, a, split)
+             : launch_tiles<false>(ctx, md, mc, ms, a, split);
 }
 
 }  // namespace
 
 int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype) {
   if (rows == 0 || out == 0) return 0;
-  const int64_t bias = up256((int64_t)kMaxBiasParts * out * 4);
-  if (in == 0) return bias;
   // partials of at most two slots per range, never more than one range per
   // pair; a plane of 16-bit dy in case its rows are not 16-byte aligned
   const Plan p = make_plan(rows, out, in, plane_count(dtype), kMaxPairs);
   const int64_t tiles = p.in_tiles * p.out_tiles;
   const int64_t slots = std::min<int64_t>(2 * kMaxPairs, tiles * p.blocks);
-  return planes_bytes(rows, out, dtype) + slots * kSlotBytes + bias;
+  return planes_bytes(rows, out, dtype) + slots * kSlotBytes + bias_bytes(p.blocks, out);
 }
 
 gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, const uint8_t* codes,
@@ -874,42 +871,33 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
       return GC_ERR_CUDA;
     return GC_OK;
   }
+  if (in == 0 && !db) return GC_OK;
+  WgradArgs a{};
+  a.plan = make_plan(rows, out, in, plane_count(dtype), ctx->num_sms / 2);
   char* at = static_cast<char*>(scratch);
-  float* bias_part = reinterpret_cast<float*>(at);
-  at += up256((int64_t)kMaxBiasParts * out * 4);
+  a.bias_part = reinterpret_cast<float*>(at);
+  at += bias_bytes(a.plan.blocks, out);
   uint16_t* planes = reinterpret_cast<uint16_t*>(at);
   at += planes_bytes(rows, out, dtype);
-
-  WgradArgs a{};
-  const int np = plane_count(dtype);
-  if (in) a.plan = make_plan(rows, out, in, np, ctx->num_sms / 2);
+  a.part = reinterpret_cast<float*>(at);
   a.dw = dw;
   a.db = db;
-  a.part = reinterpret_cast<float*>(at);
-  a.bias_part = bias_part;
   a.status = ctx->ws.status;
   a.out = out;
   a.in = in;
   a.lddw = lddw;
-  a.plane_rows = a.plan.tok_blocks * kTok;
   a.accumulate = accumulate;
   if (db) {
-    if (dtype == GC_F32)
-      a.bias_parts = launch_bias<GC_F32>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-    else if (dtype == GC_BF16)
-      a.bias_parts = launch_bias<GC_BF16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
-    else
-      a.bias_parts = launch_bias<GC_F16>(ctx, dy, rows, out, lddy, db, accumulate, bias_part);
+    a.strips = (uint32_t)ceil_div(out, 64);
+    a.bias_len = (uint32_t)bias_len(a.plan.blocks);
+    a.bias_parts = (uint32_t)ceil_div(a.plan.blocks, a.bias_len);
+    a.bias_items = a.bias_parts * a.strips;  // at most 2^7 parts, 2^24 strips
   }
-
-  if (in) {
-    const gc_status st =
-        launch_product(ctx, dy, dtype, lddy, codes, scales, rows, planes, a, db != nullptr);
-    if (st != GC_OK) return st;
-  }
+  const gc_status st = launch_product(ctx, dy, dtype, lddy, codes, scales, rows, planes, a);
+  if (st != GC_OK) return st;
   const int64_t tile_blocks =
       a.plan.ranges > a.plan.rest ? a.plan.rest * (kTile / kJoinRows) : 0;
-  const int64_t bias_blocks = a.bias_parts ? ceil_div(out, 32) : 0;
+  const int64_t bias_blocks = a.bias_parts > 1 ? ceil_div(out, 32) : 0;
   if (tile_blocks + bias_blocks > 0) {
     LaunchScope L(ctx, GC_PHASE_WGRAD_JOIN);
     if (launch_early(wgrad_join_kernel, dim3((unsigned)(tile_blocks + bias_blocks)), 256, 0,

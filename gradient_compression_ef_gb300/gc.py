@@ -25,7 +25,7 @@ DTYPES = {"f32": F32, "bf16": BF16, "f16": F16}
 GELU, SILU = 0, 1
 ACTS = {"gelu": GELU, "silu": SILU}
 
-PHASE_COUNT = 36
+PHASE_COUNT = 35
 
 OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE = -1, -2, -3, -4

@@ -177,8 +177,7 @@ typedef enum gc_phase {
   GC_PHASE_WGRAD = 32,       /* linear layer: dw from dy and the checkpoint */
   GC_PHASE_WGRAD_SPLIT = 33, /* linear layer: dy as bf16 planes */
   GC_PHASE_WGRAD_JOIN = 34,  /* linear layer: sum of the token ranges' partials */
-  GC_PHASE_WGRAD_BIAS = 35,  /* linear layer: db, column sums of dy */
-  GC_PHASE_COUNT = 36
+  GC_PHASE_COUNT = 35
 } gc_phase;
 
 /* Name of a phase ("ef_hist", ...); "?" when out of range. */
