@@ -600,12 +600,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Adds the ranges' partials of a cut tile in the order of their tokens and
-// stores it (16 outputs of a rest tile per block), and the partial rows of db
-// (32 columns per block; the first blocks).
-constexpr int kJoinRows = 16;
-
+// stores it (join_rows outputs of a rest tile per block), and the partial rows
+// of db (32 columns per block; the first blocks).  A block's time is one trip
+// to L2 per four outputs and four partials.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__ WgradArgs a,
-                                                         int bias_blocks) {
+                                                         int bias_blocks, int join_rows) {
   const Plan& p = a.plan;
   if ((int)blockIdx.x < bias_blocks) {
     __shared__ float s[8][32];
@@ -626,8 +625,8 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__
     }
     return;
   }
-  const int64_t b = blockIdx.x - bias_blocks, t = b / (kTile / kJoinRows);
-  const int n0 = (int)(b - t * (kTile / kJoinRows)) * kJoinRows;
+  const int64_t b = blockIdx.x - bias_blocks, t = b / (kTile / join_rows);
+  const int n0 = (int)(b - t * (kTile / join_rows)) * join_rows;
   const int64_t b0 = t * p.blocks, b1 = b0 + p.blocks;
   const int64_t g0 = b0 / p.len, g1 = (b1 - 1) / p.len;
   int64_t it, ot;
@@ -638,7 +637,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const __grid_constant__
   const int64_t second = t - p.len * g0 / p.blocks;
   after_previous();
   if (g0 == g1 || i >= a.in) return;  // one range held it all and stored it
-  for (int n = n0; n < n0 + kJoinRows; n += 4) {
+  for (int n = n0; n < n0 + join_rows; n += 4) {
     const float* src = a.part + n * kTile + threadIdx.x;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int64_t g = g0; g <= g1; g += 4) {
@@ -895,13 +894,17 @@ gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, con
   }
   const gc_status st = launch_product(ctx, dy, dtype, lddy, codes, scales, rows, planes, a);
   if (st != GC_OK) return st;
+  // Tiles in many parts are few, and have blocks of fewer outputs.  The whole
+  // call, by 16 and by 4 outputs: 41.3 and 37.2 us for 6 tiles in 76 parts
+  // (32768 x 768 -> 512 fp16), 53.7 and 55.3 for 36 (2501 x 1001 -> 2051 fp32).
+  const int join_rows = a.plan.ranges >= 4 * a.plan.rest ? 4 : 16;
   const int64_t tile_blocks =
-      a.plan.ranges > a.plan.rest ? a.plan.rest * (kTile / kJoinRows) : 0;
+      a.plan.ranges > a.plan.rest ? a.plan.rest * (kTile / join_rows) : 0;
   const int64_t bias_blocks = a.bias_parts > 1 ? ceil_div(out, 32) : 0;
   if (tile_blocks + bias_blocks > 0) {
     LaunchScope L(ctx, GC_PHASE_WGRAD_JOIN);
     if (launch_early(wgrad_join_kernel, dim3((unsigned)(tile_blocks + bias_blocks)), 256, 0,
-                     ctx->stream, a, (int)bias_blocks) != cudaSuccess)
+                     ctx->stream, a, (int)bias_blocks, join_rows) != cudaSuccess)
       return GC_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
