@@ -14,14 +14,26 @@
 // Both passes are bound by memory; what they need is loads in flight and few
 // instructions per element:
 //   cols <= 512         a warp per row, up to 4 units of 16 bytes per lane;
-//   wider, while two    a block walks over rows that its producer warp copies
-//   rows fit in shared  into a ring of stages in shared memory (bulk copies,
-//   memory              several rows ahead); a thread owns 16 columns of all
-//                       rows, the column sums stay in its registers, and
-//                       nothing but the stage changes from row to row;
+//   up to 16384 columns a block walks over rows that bulk copies bring into a
+//   (backward 8192),    ring of stages in shared memory, several rows ahead; a
+//   while two rows fit  thread owns 16 columns of all rows, the column sums
+//   in shared memory    stay in its registers, and nothing but the stage
+//                       changes from row to row;
 //   wider still         the row is read again from L2 for each of its passes.
 // The backward pass leaves one partial row of column sums per block; a second
 // small grid adds the partials in block order.
+//
+// Measured, bytes read and written once over the time (a plain copy: 6.77
+// TB/s), forward and backward with a checkpoint: 16384 x 4096 bf16 74 us (4.5
+// TB/s) and 84 (4.0), fp32 104 (5.8) and 111 (5.5); without one bf16
+// 55 (4.9) and 82 (4.9), fp32 92 (5.8) and 130 (6.2).  fp32 is near the memory
+// rate; 16-bit rows have twice the elements per byte, and are held up by instruction issue (25
+// per element and lane forward) and shared-memory latency at the 20 to 24
+// warps per SM that registers allow.  Rows on odd boundaries: 16001 x 4099 fp32
+// without a checkpoint 119 us (4.4) and 196 (4.0), bf16 with one 140 and 137
+// (2.4).  Narrow rows: 65536 x 500 bf16 57 (2.9) and 116 (1.4).  Wider than the
+// ring: 4096 x 20000 bf16 210 (2.0) and 136 (3.0).  The column sums' second grid
+// 8 us at 4096 columns.
 #include <algorithm>
 
 #include "gc_act8.cuh"

@@ -681,7 +681,7 @@ GC_API int64_t gc_linear_wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t 
  * dw: fp32, row stride lddw >= in elements; db: fp32[out] or NULL.
  * Products are exact: a restored value is exact in bf16, a bf16 dy is taken
  * as it is, an fp32 dy as the three bf16 values it is the sum of (three times
- * the work).  With dtype GC_F16 the checkpoint must be one of fp16 values,
+ * the work; an infinite fp32 dy gives NaN in its row of dw and in db).  With dtype GC_F16 the checkpoint must be one of fp16 values,
  * exact in fp16: groups whose largest magnitude is above fp16's range count
  * as NaN, below it as 0.  Sums run on the tensor cores over 512 tokens, those
  * sums in fp32 rounded to nearest.  fp32 dy: rows <= 2^29
