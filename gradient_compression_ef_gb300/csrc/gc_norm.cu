@@ -27,9 +27,9 @@
 // TB/s), forward and backward with a checkpoint: 16384 x 4096 bf16 74 us (4.5
 // TB/s) and 84 (4.0), fp32 104 (5.8) and 111 (5.5); without one bf16
 // 55 (4.9) and 82 (4.9), fp32 92 (5.8) and 130 (6.2).  fp32 is near the memory
-// rate; 16-bit rows have twice the elements per byte, and are held up by instruction issue (25
-// per element and lane forward) and shared-memory latency at the 20 to 24
-// warps per SM that registers allow.  Rows on odd boundaries: 16001 x 4099 fp32
+// rate; 16-bit rows have twice the elements per byte, and are held up by
+// instruction issue (25 per element and lane forward) and shared-memory latency
+// at the 20 to 24 warps per SM that registers allow.  Rows on odd boundaries: 16001 x 4099 fp32
 // without a checkpoint 119 us (4.4) and 196 (4.0), bf16 with one 140 and 137
 // (2.4).  Narrow rows: 65536 x 500 bf16 57 (2.9) and 116 (1.4).  Wider than the
 // ring: 4096 x 20000 bf16 210 (2.0) and 136 (3.0).  The column sums' second grid
@@ -1249,10 +1249,11 @@ template <int DT, bool CKPT>
 int backward_ring(gc_ctx* ctx, const NormArgs& a, const RingPlan& p, bool aligned) {
   const unsigned g =
       (unsigned)std::min<int64_t>(a.rows, (int64_t)std::min(ctx->num_sms, kMaxSms) * p.per_sm);
-  if (!aligned) launch_ring<norm_backward_ring_kernel<DT, CKPT, kAnywhere>>(ctx, a, p, g, p.threads + 32);
+  const int threads = p.threads + 32;
+  if (!aligned) launch_ring<norm_backward_ring_kernel<DT, CKPT, kAnywhere>>(ctx, a, p, g, threads);
   else if (a.cols == (int64_t)p.threads * kCols)
-    launch_ring<norm_backward_ring_kernel<DT, CKPT, kFull>>(ctx, a, p, g, p.threads + 32);
-  else launch_ring<norm_backward_ring_kernel<DT, CKPT, kEnds>>(ctx, a, p, g, p.threads + 32);
+    launch_ring<norm_backward_ring_kernel<DT, CKPT, kFull>>(ctx, a, p, g, threads);
+  else launch_ring<norm_backward_ring_kernel<DT, CKPT, kEnds>>(ctx, a, p, g, threads);
   return (int)g;
 }
 

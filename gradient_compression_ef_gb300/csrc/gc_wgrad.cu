@@ -28,9 +28,9 @@
 // waits for its warp, which takes about 0.5 us for a box of 64 x 64.  (By a
 // kernel of its own before the product db cost 25 us, and a launch: 100 x 512
 // -> 512 bf16 12.4 us, now 10.4.  Only where a layer has hardly any inputs is
-// one warp too few: 8192 x 64 -> 11008 bf16 78 us by the kernel, 88 now.)  Small products are latency: 32768 x 768 -> 512 fp16 36 us and
-// the join; 2501 x 1001 -> 2051 fp32 (three planes) 35 us beside the split, 17,
-// and the join.
+// one warp too few: 8192 x 64 -> 11008 bf16 78 us by the kernel, 88 now.)
+// Small products are latency: 32768 x 768 -> 512 fp16 36 us and the join; 2501
+// x 1001 -> 2051 fp32 (three planes) 35 us beside the split, 17, and the join.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
