@@ -206,14 +206,15 @@ __device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
                : "memory");
 }
 
-// decode2 in fp16: +-(1 + m / 128) * 2 less +-2 is +-m * 2^-6; times
+// decode2 in fp16: +-(16 + m * 2^-6) less +-16 is +-m * 2^-6; times
 // 2^(B - 128), a power of two that fp16 holds for every B an fp16 value can
-// have (104 .. 143), subnormals included.
-__device__ __forceinline__ uint32_t two_f16(uint32_t w, uint32_t sel, uint32_t scale) {
-  const uint32_t v = __byte_perm(w, 0u, sel);  // code in the high byte of each half
-  const uint32_t c = (v & 0x80008000u) | 0x40004000u;
-  const uint32_t x = ((v >> 5) & 0x03F803F8u) | c;
-  uint32_t d;
+// have (104 .. 143), subnormals included.  SEL: a code in the low byte of each
+// half, its sign spread over the high byte.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t two_f16(uint32_t w, uint32_t scale) {
+  uint32_t v, d;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(v) : "r"(w), "n"(SEL));
+  const uint32_t x = (v & 0x807F807Fu) | 0x4C004C00u, c = (v & 0x80008000u) | 0x4C004C00u;
   asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
       : "=r"(d)
       : "r"(x), "r"(c), "r"(scale));
@@ -222,19 +223,17 @@ __device__ __forceinline__ uint32_t two_f16(uint32_t w, uint32_t sel, uint32_t s
 
 // 2^(B - 128) in both halves; 0 below fp16's range, NaN above it.
 __device__ __forceinline__ uint32_t f16_scale(uint32_t b) {
+  const float f = __uint_as_float((max(b, 1u) - 1u) << 23);
   uint32_t h;
-  if (b > 143u) h = 0x7E00u;
-  else if (b >= 114u) h = (b - 113u) << 10;
-  else if (b >= 104u) h = 1u << (b - 104u);
-  else h = 0u;
-  return h | (h << 16);
+  asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(f));
+  return b > 143u ? 0x7E007E00u : h;
 }
 
 template <bool F16>
 __device__ __forceinline__ uint4 eight(uint32_t w0, uint32_t w1, uint32_t s) {
   if (F16)
-    return make_uint4(two_f16(w0, 0x1404u, s), two_f16(w0, 0x3424u, s), two_f16(w1, 0x1404u, s),
-                      two_f16(w1, 0x3424u, s));
+    return make_uint4(two_f16<0x9180>(w0, s), two_f16<0xB3A2>(w0, s), two_f16<0x9180>(w1, s),
+                      two_f16<0xB3A2>(w1, s));
   return make_uint4(decode2(w0, 0x1100u, s), decode2(w0, 0x3322u, s), decode2(w1, 0x1100u, s),
                     decode2(w1, 0x3322u, s));
 }
@@ -516,15 +515,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int p = 0; p < 4; ++p) {
           const uint32_t r = (uint32_t)(row0 + p * 4);
           const uint32_t sc = F16 ? f16_scale(b[p]) : b[p] * 0x00800080u;
-          const uint4 lo = eight<F16>(c[p].x, c[p].y, sc), hi = eight<F16>(c[p].z, c[p].w, sc);
+          // the codes that are stored first and second: lower and upper
+          // eight, in the upper half's threads the other way round
+          const uint4 one = eight<F16>(half ? c[p].z : c[p].x, half ? c[p].w : c[p].y, sc);
+          const uint4 two = eight<F16>(half ? c[p].x : c[p].z, half ? c[p].y : c[p].w, sc);
           // 16-byte chunks 2 (unit % 4) and + 1 of the half's 128-byte row r,
           // swizzled; the upper half's threads store theirs in the other
           // order, so that eight threads cover all banks at each store
           const uint32_t row = s.a + st * kOpBytes + half * (kOpBytes / 2) + r * 128;
           const uint32_t ch = (uint32_t)(unit & 3) * 2;
           const uint32_t first = ((ch + half) ^ (r & 7u)) << 4;
-          sts_u4(row + first, half ? hi : lo);
-          sts_u4(row + (first ^ 16u), half ? lo : hi);
+          sts_u4(row + first, one);
+          sts_u4(row + (first ^ 16u), two);
         }
         fence_proxy_async_smem();
         __syncwarp();
