@@ -22,14 +22,14 @@
 //   read-out  8 warps: tensor memory -> running sums in registers -> dw
 //
 // Bound by the tensor cores where there are tiles for every pair: 8192 x 4096
-// -> 11008 bf16 with db takes 416 us, 1775 Tflop/s (cuBLAS reaches 1874 on this
-// GPU in a burst); fp16 511 us, 1447: its conversion takes two
-// instructions more for every two values.  db costs 2 to 7 us of that; nobody
+// -> 11008 bf16 with db takes 414 us, 1784 Tflop/s (cuBLAS reaches 1874 on this
+// GPU in a burst); fp16 478 us, 1546: its conversion takes an instruction more
+// for every two values and holds the tensor cores up.  db costs 2 to 7 us of that; nobody
 // waits for its warp, which takes about 0.5 us for a box of 64 x 64.  (By a
 // kernel of its own before the product db cost 25 us, and a launch: 100 x 512
 // -> 512 bf16 12.4 us, now 10.4.  Only where a layer has hardly any inputs is
 // one warp too few: 8192 x 64 -> 11008 bf16 78 us by the kernel, 88 now.)
-// Small products are latency: 32768 x 768 -> 512 fp16 36 us and the join; 2501
+// Small products are latency: 32768 x 768 -> 512 fp16 34 us and the join; 2501
 // x 1001 -> 2051 fp32 (three planes) 35 us beside the split, 17, and the join.
 #include <cudaTypedefs.h>
 
