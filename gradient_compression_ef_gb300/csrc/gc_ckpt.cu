@@ -48,22 +48,33 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // rate, and the packed fp32 instructions take half the slots.
 //
 // GELU: with a = |x|, Phi(-a) = exp(-a^2 / 2) R(a), where R(a) =
-// exp(a^2 / 2) Phi(-a) is smooth; R is a polynomial of degree 5 in
-// t = 1 / (1 + 0.32 a), fitted to R on [0, 14] so that the largest error of
-// Phi(-a) max(1, a) is least (3.1e-8; iteratively reweighted least squares).
+// exp(a^2 / 2) Phi(-a) is smooth; R is a polynomial of degree 7 in
+// t = 1 / (1 + 0.34 a), fitted on [0, 13.4] (iteratively reweighted least
+// squares) so that Phi(-a) is off by at most 3.3e-8 / max(1, a) and by at most
+// 7.3e-7 of itself: the negative tail, where the function is Phi(-a) alone, keeps
+// its digits down to where it leaves binary32's normal range (x = -13.1).
+// (A polynomial of degree 5 that held the absolute error alone was off by
+// 1e-4 of the value at -5 and by 1e-2 at -12, more than a bf16 rounding.)
+// What is added in fp32: the exponent's rounding, x^2 2^-23 of the tail.
 // x Phi(x) = (x + |x|) / 2 - a Phi(-a) for either sign; a is limited to 14
 // as a factor, where Phi(-a) is 0 in fp32, so that +inf gives +inf.
+//
+// SiLU: s(x) = 2^-8 / (2^-8 + 2^-8 exp(-x)).  The factor keeps the reciprocal
+// in the normal range as far down as x s(x) is in it (x = -91.8): the
+// approximate instructions give 0 for what lies below.
 template <int KIND, bool DERIV>
 __device__ __forceinline__ void act(const float2& x, float2& f, float2& d) {
   if (KIND == GC_GELU) {
     const float2 a = make_float2(fabsf(x.x), fabsf(x.y));
-    const float2 u = __ffma2_rn(a, both(0.32f), both(1.0f));
+    const float2 u = __ffma2_rn(a, both(0.34f), both(1.0f));
     const float2 t = make_float2(rcp_approx(u.x), rcp_approx(u.y));
-    float2 r = __ffma2_rn(t, both(-0.128873349f), both(0.491905883f));
-    r = __ffma2_rn(r, t, both(-0.259480187f));
-    r = __ffma2_rn(r, t, both(0.310232595f));
-    r = __ffma2_rn(r, t, both(0.0814068223f));
-    r = __ffma2_rn(r, t, both(0.00480820835f));
+    float2 r = __ffma2_rn(t, both(0.0472440794f), both(-0.211599767f));
+    r = __ffma2_rn(r, t, both(0.285200179f));
+    r = __ffma2_rn(r, t, both(-0.0523733199f));
+    r = __ffma2_rn(r, t, both(0.169367765f));
+    r = __ffma2_rn(r, t, both(0.125428692f));
+    r = __ffma2_rn(r, t, both(0.136785954f));
+    r = __ffma2_rn(r, t, both(-5.35652689e-05f));
     const float2 v = __fmul2_rn(__fmul2_rn(a, a), both(-0.72134752f));
     const float2 e = make_float2(exp2_approx(v.x), exp2_approx(v.y));  // exp(-a^2 / 2)
     const float2 q = __fmul2_rn(r, e);                                 // Phi(-a)
@@ -76,9 +87,11 @@ __device__ __forceinline__ void act(const float2& x, float2& f, float2& d) {
       d = __ffma2_rn(__fmul2_rn(x, both(0.39894228f)), e, p);
     }
   } else {
-    const float2 v = __fmul2_rn(x, both(-1.44269504f));
-    const float2 u = __fadd2_rn(make_float2(exp2_approx(v.x), exp2_approx(v.y)), both(1.0f));
-    const float2 s = make_float2(rcp_approx(u.x), rcp_approx(u.y));
+    const float2 v = __ffma2_rn(x, both(-1.44269504f), both(-8.0f));
+    const float2 u =
+        __fadd2_rn(make_float2(exp2_approx(v.x), exp2_approx(v.y)), both(0.00390625f));
+    const float2 s =
+        __fmul2_rn(make_float2(rcp_approx(u.x), rcp_approx(u.y)), both(0.00390625f));
     f = __fmul2_rn(x, s);
     if (DERIV) d = __ffma2_rn(f, __ffma2_rn(s, both(-1.0f), both(1.0f)), s);
   }

@@ -1,0 +1,110 @@
+"""The calls that fill the flat gradient where the tests of
+test_gpu_backward.py do not reach: the negative tails of the activation
+functions, kernels that only large matrices are given to, long-running calls,
+parameter gradients that start anywhere, the scratch's growth.
+
+Tolerances are bounds on rounding, as there: U is half an ulp of the output
+type, relative; the rest is stated where it is used.
+"""
+import numpy as np
+import pytest
+
+from oracle import backward as ref
+from tests.gpu_helpers import torch_cuda
+from tests.test_gpu_backward import U, close, f64, matrix, out_matrix
+
+pytestmark = pytest.mark.gpu
+
+SMALLEST = {"f32": 2.0 ** -126, "bf16": 2.0 ** -126, "f16": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def gc():
+    torch_cuda()
+    from gradient_compression_ef_gb300 import gc as binding
+    return binding
+
+
+@pytest.fixture(scope="module")
+def ctx(gc):
+    with gc.Context(0) as c:
+        c.reserve_scratch(256 << 20)
+        yield c
+
+
+# --- the negative tails of the activation functions ----------------------------------------------
+#
+# GELU there is x times exp(-x^2 / 2) R: three roundings of the exponent, each
+# 2^-24 of x^2 / 2 at most, are x^2 2^-23 of the value, and 2^-18 covers the
+# rest (the fit of R 7.3e-7 = 2^-20.4, eight steps of Horner's rule at 2^-24,
+# exponential and reciprocal 2^-22 each).  SiLU's exponent has two roundings of
+# 2^-24 |x|, the rest is below 2^-20.
+
+TAIL = {"gelu": -13.1, "silu": -91.0}
+
+
+def _part(kind, x):
+    """The part of itself that f may be off by at x < 0."""
+    return 2.0 ** -18 + x * x * 2.0 ** -23 if kind == "gelu" else 2.0 ** -20 - x * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["gelu", "silu"])
+def test_negative_tail_forward(gc, ctx, kind, dtype):
+    x = np.concatenate([np.linspace(TAIL[kind], -1e-3, 20000 - 2048), -np.geomspace(1e-6, 1, 2048)])
+    d, xv, _ = matrix(np.maximum(x, TAIL[kind]).reshape(-1, 32), dtype)
+    y, _ = out_matrix(*d.shape, dtype)
+    gc.act_forward(ctx, kind, d, y)
+    f, _ = ref.act(kind, xv)
+    tol = (U[dtype] + _part(kind, xv)) * np.abs(f)
+    if dtype == "f16":
+        tol += SMALLEST["f16"] / 2  # subnormal outputs
+    close(f64(y), f, tol, "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["gelu", "silu"])
+def test_negative_tail_backward(gc, ctx, kind, dtype):
+    """Columns hold one value each that the checkpoint keeps as it is: 64 to
+    127 times a power of two."""
+    import torch
+    x = np.concatenate([-np.arange(64, 128) * 2.0 ** -k for k in range(0, 12)])
+    x = x[x >= TAIL[kind]]
+    x = np.repeat(x[:, None], 32, axis=1)
+    d, xv, _ = matrix(x, "f32")
+    rows, cols = x.shape
+    codes, scales = (torch.zeros(n, dtype=torch.uint8, device="cuda")
+                     for n in (gc.ckpt_codes_bytes(rows, cols), gc.ckpt_scales_bytes(rows, cols)))
+    gc.ckpt_save(ctx, d, codes, scales)
+    assert np.array_equal(ref.restored(xv), xv)
+    dy, dyv, _ = matrix(np.full(x.shape, 1.5), dtype)
+    dx, _ = out_matrix(rows, cols, dtype)
+    dgate, _ = out_matrix(rows, cols, dtype)
+    gc.act_backward(ctx, kind, dy, dx, codes, scales, dgate, codes, scales)
+    f, df = ref.act(kind, xv)
+    if kind == "gelu":
+        terms = f / xv + np.abs(xv) * np.exp(-xv * xv / 2) / np.sqrt(2 * np.pi)
+    else:
+        terms = f / xv * (1 + np.abs(xv))
+    small = SMALLEST["f16"] / 2 if dtype == "f16" else 0.0
+    part = _part(kind, xv)
+    # where Phi(x) or s(x) itself is subnormal it has a spacing of 2^-149
+    close(f64(dx), dyv * xv * df, U[dtype] * np.abs(dyv * xv * df)
+          + np.abs(dyv * xv) * (2 * part * terms + np.abs(xv) * 2.0 ** -148) + small, "dx")
+    close(f64(dgate), dyv * f,
+          (U[dtype] + part) * np.abs(dyv * f) + np.abs(xv) * 2.0 ** -148 + small, "dgate")
+
+
+@pytest.mark.parametrize("kind", ["gelu", "silu"])
+def test_ends_of_the_range(gc, ctx, kind):
+    """Largest and smallest magnitudes, fp32: the identity on the right, half
+    of it near zero, nothing on the left."""
+    x = np.array([[3.4e38, 1e30, 200.0, 2.0 ** -126, -2.0 ** -126, 1e-30, -1e-30, 0.0, -0.0,
+                   -100.0, -1e10, -3.4e38]], np.float32)
+    d, xv, _ = matrix(x, "f32")
+    y, _ = out_matrix(1, x.shape[1], "f32")
+    gc.act_forward(ctx, kind, d, y)
+    got = f64(y)[0]
+    assert np.array_equal(got[:3], xv[0, :3])
+    assert np.abs(got[3:7] - xv[0, 3:7] / 2).max() <= 2.0 ** -149 + 2.0 ** -21 * 1e-30
+    assert (got[7:] == 0).all()
