@@ -48,50 +48,60 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // rate, and the packed fp32 instructions take half the slots.
 //
 // GELU: with a = |x|, Phi(-a) = exp(-a^2 / 2) R(a), where R(a) =
-// exp(a^2 / 2) Phi(-a) is smooth; R is a polynomial of degree 7 in
-// t = 1 / (1 + 0.34 a), fitted on [0, 13.4] (iteratively reweighted least
-// squares) so that Phi(-a) is off by at most 3.3e-8 / max(1, a) and by at most
-// 7.3e-7 of itself: the negative tail, where the function is Phi(-a) alone, keeps
-// its digits down to where it leaves binary32's normal range (x = -13.1).
-// (A polynomial of degree 5 that held the absolute error alone was off by
-// 1e-4 of the value at -5 and by 1e-2 at -12, more than a bf16 rounding.)
-// What is added in fp32: the exponent's rounding, x^2 2^-23 of the tail.
-// x Phi(x) = (x + |x|) / 2 - a Phi(-a) for either sign; a is limited to 14
-// as a factor, where Phi(-a) is 0 in fp32, so that +inf gives +inf.
+// exp(a^2 / 2) Phi(-a) is smooth: a polynomial in t = 1 / (1 + c a), fitted on
+// [0, 13.4] by iteratively reweighted least squares, so that Phi(-a) is off by
+// little absolutely and as a part of itself.  The negative tail, where the
+// function is x Phi(-a) alone, then keeps its digits down to where it leaves
+// binary32's normal range (x = -13.1).  fp32: degree 7, 3.3e-8 / max(1, a) and
+// 7.3e-7 of itself.  16-bit types: degree 6, 3.5e-8 / max(1, a) and 2^-14 of
+// itself (an eighth of a half's rounding; a degree less is a packed instruction
+// for two values, of about 46).  (Degree 5 for all, with the absolute error
+// alone in the fit, was off by 1e-4 of the value at -5 and by 1e-2 at -12,
+// more than a bf16 rounding.)  fp32 arithmetic adds the exponent's rounding,
+// x^2 2^-23 of the tail.
 //
 // SiLU: s(x) = 2^-8 / (2^-8 + 2^-8 exp(-x)).  The factor keeps the reciprocal
 // in the normal range as far down as x s(x) is in it (x = -91.8): the
-// approximate instructions give 0 for what lies below.
-template <int KIND, bool DERIV>
+// approximate instructions give 0 for what lies below.  fp16 has no such
+// values (its least is 2^-24) and goes without.
+template <int DT, int KIND, bool DERIV>
 __device__ __forceinline__ void act(const float2& x, float2& f, float2& d) {
   if (KIND == GC_GELU) {
     const float2 a = make_float2(fabsf(x.x), fabsf(x.y));
-    const float2 u = __ffma2_rn(a, both(0.34f), both(1.0f));
+    const float2 u = __ffma2_rn(a, both(DT == GC_F32 ? 0.34f : 0.28f), both(1.0f));
     const float2 t = make_float2(rcp_approx(u.x), rcp_approx(u.y));
-    float2 r = __ffma2_rn(t, both(0.0472440794f), both(-0.211599767f));
-    r = __ffma2_rn(r, t, both(0.285200179f));
-    r = __ffma2_rn(r, t, both(-0.0523733199f));
-    r = __ffma2_rn(r, t, both(0.169367765f));
-    r = __ffma2_rn(r, t, both(0.125428692f));
-    r = __ffma2_rn(r, t, both(0.136785954f));
-    r = __ffma2_rn(r, t, both(-5.35652689e-05f));
+    float2 r;
+    if (DT == GC_F32) {
+      r = __ffma2_rn(t, both(0.0472440794f), both(-0.211599767f));
+      r = __ffma2_rn(r, t, both(0.285200179f));
+      r = __ffma2_rn(r, t, both(-0.0523733199f));
+      r = __ffma2_rn(r, t, both(0.169367765f));
+      r = __ffma2_rn(r, t, both(0.125428692f));
+      r = __ffma2_rn(r, t, both(0.136785954f));
+      r = __ffma2_rn(r, t, both(-5.35652689e-05f));
+    } else {
+      r = __ffma2_rn(t, both(-0.108482867f), both(0.403031647f));
+      r = __ffma2_rn(r, t, both(-0.263652384f));
+      r = __ffma2_rn(r, t, both(0.297365874f));
+      r = __ffma2_rn(r, t, both(0.0506336838f));
+      r = __ffma2_rn(r, t, both(0.121776283f));
+      r = __ffma2_rn(r, t, both(-0.000672220427f));
+    }
     const float2 v = __fmul2_rn(__fmul2_rn(a, a), both(-0.72134752f));
     const float2 e = make_float2(exp2_approx(v.x), exp2_approx(v.y));  // exp(-a^2 / 2)
     const float2 q = __fmul2_rn(r, e);                                 // Phi(-a)
-    const float2 l = make_float2(fminf(a.x, 14.0f), fminf(a.y, 14.0f));
-    f = __ffma2_rn(__fmul2_rn(l, both(-1.0f)), q,
-                   __ffma2_rn(x, both(0.5f), __fmul2_rn(a, both(0.5f))));
-    if (DERIV) {
-      const float2 c = __ffma2_rn(q, both(-1.0f), both(1.0f));
-      const float2 p = make_float2(x.x < 0.0f ? q.x : c.x, x.y < 0.0f ? q.y : c.y);
-      d = __ffma2_rn(__fmul2_rn(x, both(0.39894228f)), e, p);
-    }
+    const float2 c = __ffma2_rn(q, both(-1.0f), both(1.0f));
+    const float2 p = make_float2(x.x < 0.0f ? q.x : c.x, x.y < 0.0f ? q.y : c.y);
+    f = __fmul2_rn(x, p);
+    if (DERIV) d = __ffma2_rn(__fmul2_rn(x, both(0.39894228f)), e, p);
   } else {
-    const float2 v = __ffma2_rn(x, both(-1.44269504f), both(-8.0f));
-    const float2 u =
-        __fadd2_rn(make_float2(exp2_approx(v.x), exp2_approx(v.y)), both(0.00390625f));
-    const float2 s =
-        __fmul2_rn(make_float2(rcp_approx(u.x), rcp_approx(u.y)), both(0.00390625f));
+    constexpr bool kScaled = DT != GC_F16;
+    const float2 v = kScaled ? __ffma2_rn(x, both(-1.44269504f), both(-8.0f))
+                             : __fmul2_rn(x, both(-1.44269504f));
+    const float2 u = __fadd2_rn(make_float2(exp2_approx(v.x), exp2_approx(v.y)),
+                                both(kScaled ? 0.00390625f : 1.0f));
+    float2 s = make_float2(rcp_approx(u.x), rcp_approx(u.y));
+    if (kScaled) s = __fmul2_rn(s, both(0.00390625f));
     f = __fmul2_rn(x, s);
     if (DERIV) d = __ffma2_rn(f, __ffma2_rn(s, both(-1.0f), both(1.0f)), s);
   }
@@ -184,7 +194,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         float2 f;
-        act<KIND, false>(v[j], f, d);
+        act<DT, KIND, false>(v[j], f, d);
         v[j] = GATED ? __fmul2_rn(f, w[j]) : f;
       }
       x[i] = pack2<DT>(v);
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 5)
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         float2 f, d;
-        act<KIND, true>(x[j], f, d);
+        act<DT, KIND, true>(x[j], f, d);
         if (GATED) dg[j] = __fmul2_rn(dy[j], f);
         x[j] = __fmul2_rn(GATED ? __fmul2_rn(dy[j], g[j]) : dy[j], d);
       }

@@ -623,9 +623,10 @@ GC_API gc_status gc_ckpt_restore(gc_ctx* ctx, const uint8_t* codes, const uint8_
  * pass.  codes / scales may both be NULL (no checkpoint); with a gate,
  * gate_codes / gate_scales go with them.
  * f and f' are evaluated in fp32: f within 2^-21 |x|, and on the negative
- * side, where f tends to zero, within a part 2^-18 + x^2 2^-23 (GELU) or
- * 2^-20 + |x| 2^-23 (SiLU) of itself as long as it is a normal binary32
- * number (x >= -13.1 and x >= -91.8); below that it may be zero.
+ * side, where f tends to zero, within a part 2^-18 + x^2 2^-23 (GELU; 2^-14 +
+ * x^2 2^-23 for 16-bit types) or 2^-20 + |x| 2^-23 (SiLU) of itself as long as
+ * that is a normal number (binary32: x >= -13.1, x >= -91.8); below it may be
+ * zero.
  */
 GC_API gc_status gc_act_forward(gc_ctx* ctx, int act, const void* x, int64_t ldx,
                                 const void* gate, int64_t ldgate, int dtype, int64_t rows,
