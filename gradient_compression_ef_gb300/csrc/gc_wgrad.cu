@@ -472,11 +472,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     // MMAs still in flight read both CTAs' shared memory: wait for them (the
-    // commit of the lane that issued them)
-    if (warp == kIssuerWarp) {
-      if (rank == 0 && elect_one()) mma_commit_pair(s.drain);
-      if (!mbar_wait_cluster(s.drain, 0, kWaitCycles)) ok = false;
-    }
+    // commit of the lane that issued them).  In each CTA it is the dy producer
+    // that waits, having kept step with the MMAs as far as here: a warp that
+    // had nothing else to do would wait for the whole kernel, and a kernel of
+    // more than kWaitCycles would look like one that hangs.
+    if (warp == kIssuerWarp && rank == 0 && elect_one()) mma_commit_pair(s.drain);
+    if (warp == kDyWarp && !mbar_wait_cluster(s.drain, 0, kWaitCycles)) ok = false;
   } else if (warp >= kReadWarps) {
     reg_dec<48>();
     const int cw = warp - kReadWarps, group = cw / kGroupWarps;

@@ -111,3 +111,31 @@ def test_ends_of_the_range(gc, ctx, kind):
     assert np.array_equal(got[:3], xv[0, :3])
     assert np.abs(got[3:7] - xv[0, 3:7] / 2).max() <= 2.0 ** -149 + 2.0 ** -21 * 1e-30
     assert (got[7:] == 0).all()
+
+
+# --- calls that run long -------------------------------------------------------------------------
+
+def test_linear_wgrad_of_seconds(gc):
+    """A product of 4.2e15 operations runs for more cycles than any single wait
+    in it may take (4e9): no wait may be one for the whole kernel.  Operands of
+    two values each (dy and the codes lie in one buffer, both only read), so
+    that every sum is exact."""
+    import torch
+    rows, cols, out = 163840, 131072, 98304
+    torch.cuda.empty_cache()
+    scratch = gc.linear_wgrad_scratch_bytes(rows, out, cols, "f16")
+    need = 2 * rows * out + 4 * out * cols + gc.ckpt_scales_bytes(rows, cols) + scratch
+    if torch.cuda.mem_get_info()[0] < need + (16 << 30):
+        pytest.skip("needs %d GB of device memory" % (need >> 30))
+    dy = torch.ones(rows, out, dtype=torch.float16, device="cuda")  # bytes 0x00, 0x3C
+    codes = dy.view(torch.uint8).view(-1)[:gc.ckpt_codes_bytes(rows, cols)]  # 0, 60, 0, 60, ...
+    scales = torch.full((gc.ckpt_scales_bytes(rows, cols),), 134, dtype=torch.uint8, device="cuda")
+    dw = torch.full((out, cols), 7.0, device="cuda")
+    with gc.Context(0) as own:
+        own.reserve_scratch(scratch)
+        gc.linear_wgrad(own, dy, codes, scales, dw)
+        own.check()
+    for part in dw.split(8192):
+        assert bool((part[:, 0::2] == 0).all()) and bool((part[:, 1::2] == 60.0 * rows).all())
+    del dy, codes, scales, dw, part
+    torch.cuda.empty_cache()
