@@ -35,6 +35,15 @@ gc_status check_buf(const void* p, bool used) {
   return GC_OK;
 }
 
+// A buffer that is only ever touched float by float, so that it may lie at any
+// place of a larger one (a parameter's gradient in the flat gradient).
+gc_status check_floats(const float* p, bool used) {
+  if (!used) return GC_OK;
+  if (!p) return GC_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return GC_ERR_ALIGNMENT;
+  return GC_OK;
+}
+
 #define GC_TRY(expr)                    \
   do {                                  \
     const gc_status _st = (expr);       \
@@ -753,8 +762,8 @@ gc_status gc_layernorm_forward(gc_ctx* ctx, const void* x, int64_t ldx, int dtyp
   const bool used = rows > 0 && cols > 0;
   GC_TRY(check_buf(x, used));
   GC_TRY(check_buf(y, used));
-  GC_TRY(check_buf(mean, used));
-  GC_TRY(check_buf(rstd, used));
+  GC_TRY(check_floats(mean, used));
+  GC_TRY(check_floats(rstd, used));
   if (gamma) GC_TRY(check_buf(gamma, used));
   if (beta) GC_TRY(check_buf(beta, used));
   GC_TRY(check_ckpt(codes, scales, used, true));
@@ -780,8 +789,8 @@ gc_status gc_layernorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const
   const bool used = rows > 0 && cols > 0;
   GC_TRY(check_buf(dy, used));
   GC_TRY(check_buf(dx, used));
-  GC_TRY(check_buf(mean, used));
-  GC_TRY(check_buf(rstd, used));
+  GC_TRY(check_floats(mean, used));
+  GC_TRY(check_floats(rstd, used));
   if (gamma) GC_TRY(check_buf(gamma, used));
   // the input, or its checkpoint
   if (x) {
@@ -791,8 +800,8 @@ gc_status gc_layernorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const
   } else {
     GC_TRY(check_ckpt(codes, scales, used, false));
   }
-  if (dgamma) GC_TRY(check_buf(dgamma, cols > 0));
-  if (dbeta) GC_TRY(check_buf(dbeta, cols > 0));
+  if (dgamma) GC_TRY(check_floats(dgamma, cols > 0));
+  if (dbeta) GC_TRY(check_floats(dbeta, cols > 0));
   if ((dgamma || dbeta) && used && ctx->scratch_bytes < gc::norm_scratch_bytes(rows, cols))
     return GC_ERR_WORKSPACE;
   DeviceGuard guard(ctx->device);
@@ -816,8 +825,8 @@ gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
   const bool used = rows > 0 && out > 0 && in > 0;
   GC_TRY(check_buf(dy, rows > 0 && out > 0));
   GC_TRY(check_ckpt(codes, scales, used, false));
-  GC_TRY(check_buf(dw, out > 0 && in > 0));
-  if (db) GC_TRY(check_buf(db, out > 0));
+  GC_TRY(check_floats(dw, out > 0 && in > 0));
+  if (db) GC_TRY(check_floats(db, out > 0));
   // tensor-map coordinates are 32 bits; fp32 takes three planes of rows
   if (dtype == GC_F32 && rows > ((int64_t)1 << 29)) return GC_ERR_UNSUPPORTED;
   if ((used || db) && ctx->scratch_bytes < gc::wgrad_scratch_bytes(rows, out, in, dtype))

@@ -12,8 +12,9 @@
  * --------------------------------
  *  - Buffers are DEVICE pointers owned by the caller (plain C types, no
  *    framework types).  Every buffer must start on a 16-byte boundary
- *    (GC_ERR_ALIGNMENT otherwise); a pointer may be NULL only when the call
- *    touches no element of it (n == 0, k == 0).
+ *    (GC_ERR_ALIGNMENT otherwise) unless a call's comment says that it need
+ *    not; a pointer may be NULL only when the call touches no element of it
+ *    (n == 0, k == 0).
  *  - Calls are asynchronous: they validate arguments on the host, enqueue
  *    kernels on the context's CUDA stream and return.  The return value
  *    reports host-side validation and launch errors only (a launch error is
@@ -571,9 +572,10 @@ GC_API gc_status gc_bucket_flush(gc_ctx* ctx);
  * produce it: activations are kept in 8 bits between the forward and the
  * backward pass, and the backward calls read those checkpoints and write the
  * parameters' gradients, in fp32, at their places of the flat gradient
- * (dw, db, dgamma and dbeta may point anywhere into it at a 16-byte
- * boundary; accumulate != 0 adds to what is there, for gradient
- * accumulation over micro-batches).
+ * (dw, db, dgamma and dbeta may point at any float of it, as mean and rstd
+ * may at any of theirs: unlike the other buffers they need no 16-byte
+ * boundary; accumulate != 0 adds to what is there, for gradient accumulation
+ * over micro-batches).
  *
  * Matrices are [rows, cols] of one element type (gc_dtype), columns
  * contiguous, with a row stride ld >= cols in elements; rows need no

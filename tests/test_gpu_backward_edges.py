@@ -11,7 +11,7 @@ import pytest
 
 from oracle import backward as ref
 from tests.gpu_helpers import torch_cuda
-from tests.test_gpu_backward import U, close, f64, matrix, out_matrix
+from tests.test_gpu_backward import EPS, U, acts, ckpt, close, device_ckpt, f64, matrix, out_matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,88 @@ def test_linear_wgrad_of_seconds(gc):
         assert bool((part[:, 0::2] == 0).all()) and bool((part[:, 1::2] == 60.0 * rows).all())
     del dy, codes, scales, dw, part
     torch.cuda.empty_cache()
+
+
+# --- parameter gradients that start anywhere -----------------------------------------------------
+
+def _flat(sizes, at):
+    """A buffer of sevens, and views of the given sizes back to back from
+    float `at` on."""
+    import torch
+    buf = torch.full((at + sum(sizes) + 9,), 7.0, device="cuda")
+    views = []
+    for n in sizes:
+        views.append(buf[at:at + n])
+        at += n
+    return buf, views
+
+
+@pytest.mark.parametrize("at", [1, 2, 3])
+@pytest.mark.parametrize("rows,cols", [(1, 4097), (50, 99), (400, 701), (20, 9001)])
+def test_norm_gradients_at_any_float(gc, ctx, rows, cols, at):
+    """dgamma, dbeta, mean and rstd off 16-byte boundaries: the bits that they
+    have on one, and nothing beside them."""
+    import torch
+    r = np.random.default_rng(cols)
+    x, _, _ = matrix(acts(r, rows, cols), "bf16")
+    dy, _, _ = matrix(r.standard_normal((rows, cols)), "bf16")
+    y, dx = (torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    got = []
+    for place in (0, at):
+        sbuf, (mean, rstd) = _flat((rows, rows), place) if place else _flat((rows + -rows % 4, rows),
+                                                                            0)
+        gbuf, (dg, db) = _flat((cols, cols), place) if place else _flat((cols + -cols % 4, cols), 0)
+        mean, rstd, dg, db = mean[:rows], rstd[:rows], dg[:cols], db[:cols]
+        gc.layernorm_forward(ctx, x, None, None, EPS, y, mean, rstd)
+        gc.layernorm_backward(ctx, dy, x, None, mean, rstd, dx, dg, db)
+        gc.layernorm_backward(ctx, dy, x, None, mean, rstd, dx, dg, db, accumulate=True)
+        got.append([t.clone() for t in (y, dx, mean, rstd, dg, db)])
+        if place:
+            for buf, n in ((sbuf, 2 * rows), (gbuf, 2 * cols)):
+                assert bool((buf[:at] == 7).all()) and bool((buf[at + n:] == 7).all())
+    for a, b in zip(*got):
+        assert bool((a == b).all())
+
+
+@pytest.mark.parametrize("at", [1, 2, 3])
+@pytest.mark.parametrize("rows,cols,out", [(0, 35, 21), (3, 33, 35), (1000, 257, 511)])
+def test_linear_gradients_at_any_float(gc, ctx, rows, cols, out, at):
+    """The same for dw and db, back to back: a layer with an odd number of
+    outputs leaves the next parameter's gradient off every boundary."""
+    import torch
+    r = np.random.default_rng(rows)
+    codes, scales = device_ckpt(*ref.encode(acts(r, rows, cols)))
+    dy, _, _ = matrix(r.standard_normal((rows, out)), "bf16")
+    dw0, db0 = torch.empty(out, cols, device="cuda"), torch.empty(out, device="cuda")
+    gc.linear_wgrad(ctx, dy, codes, scales, dw0, db0)
+    buf, (db, dw) = _flat((out, out * cols), at)
+    dw = dw.view(out, cols)
+    gc.linear_wgrad(ctx, dy, codes, scales, dw, db)
+    assert bool((dw == dw0).all()) and bool((db == db0).all())
+    gc.linear_wgrad(ctx, dy, codes, scales, dw, db, accumulate=True)
+    assert bool((dw == 2 * dw0).all()) and bool((db == 2 * db0).all())
+    assert bool((buf[:at] == 7).all()) and bool((buf[-9:] == 7).all())
+
+
+def test_addresses_between_floats_are_refused(gc, ctx):
+    import torch
+    rows, cols = 4, 64
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    codes, scales = ckpt(rows, cols)
+    f = torch.zeros(cols * cols, device="cuda").data_ptr()
+    L, h, p = gc.lib, ctx.handle, x.data_ptr()
+    c, s = codes.data_ptr(), scales.data_ptr()
+    bad = gc.ERR_ALIGNMENT
+    for off in (1, 2, 6):
+        assert L.gc_layernorm_forward(h, p, cols, gc.BF16, rows, cols, None, None, 0, EPS,
+                                      y.data_ptr(), cols, f + off, f, None, None) == bad
+        assert L.gc_layernorm_forward(h, p, cols, gc.BF16, rows, cols, None, None, 0, EPS,
+                                      y.data_ptr(), cols, f, f + off, None, None) == bad
+        for dg, db in ((f + off, f), (f, f + off)):
+            assert L.gc_layernorm_backward(h, p, cols, p, cols, None, None, gc.BF16, rows, cols,
+                                           None, 0, f, f, y.data_ptr(), cols, dg, db, 0) == bad
+        for dw, db in ((f + off, f), (f, f + off)):
+            assert L.gc_linear_wgrad(h, p, gc.BF16, cols, c, s, rows, cols, cols, dw, cols, db,
+                                     0) == bad
+    torch.cuda.synchronize()
