@@ -266,6 +266,11 @@ gc_status gc_ctx_destroy(gc_ctx* ctx) {
   if (ctx->ws_base) cudaFree(ctx->ws_base);
   if (ctx->psgd_base) cudaFree(ctx->psgd_base);
   if (ctx->scratch) cudaFree(ctx->scratch);
+  while (gc::OldScratch* old = ctx->old_scratch) {
+    ctx->old_scratch = old->next;
+    cudaFree(old->base);
+    free(old);
+  }
   gc::free_buckets(ctx);
   free(ctx);
   return st;
@@ -665,15 +670,21 @@ gc_status gc_ctx_reserve_scratch(gc_ctx* ctx, int64_t bytes) {
   if (bytes <= ctx->scratch_bytes) return GC_OK;
   DeviceGuard guard(ctx->device);
   if (!guard.ok) return GC_ERR_CUDA;
-  if (cudaStreamSynchronize(ctx->stream) != cudaSuccess) return GC_ERR_CUDA;
-  if (ctx->scratch) cudaFree(ctx->scratch);
-  ctx->scratch = nullptr;
-  ctx->scratch_bytes = 0;
+  gc::OldScratch* old = nullptr;
+  if (ctx->scratch) {
+    old = static_cast<gc::OldScratch*>(malloc(sizeof(gc::OldScratch)));
+    if (!old) return GC_ERR_NO_MEMORY;
+  }
   void* base = nullptr;
   const cudaError_t e = cudaMalloc(&base, (size_t)bytes);
-  if (e != cudaSuccess) {
+  if (e != cudaSuccess) {  // what was there stays
     cudaGetLastError();
+    free(old);
     return e == cudaErrorMemoryAllocation ? GC_ERR_NO_MEMORY : GC_ERR_CUDA;
+  }
+  if (old) {
+    *old = {ctx->scratch, ctx->old_scratch};
+    ctx->old_scratch = old;
   }
   ctx->scratch = base;
   ctx->scratch_bytes = bytes;

@@ -174,6 +174,11 @@ struct PsgdWorkspace {
   int64_t bytes;
 };
 
+struct OldScratch {
+  void* base;
+  OldScratch* next;
+};
+
 }  // namespace gc
 
 struct gc_ctx {
@@ -196,9 +201,12 @@ struct gc_ctx {
   gc::BucketWs bk;
   int bk_defer;             // deferred residual write-back of the bucketed hybrid
   float* bk_pending;        // error buffer whose kept-entry residuals are pending
-  // scratch of the backward-pass calls (gc_ctx_reserve_scratch)
+  // scratch of the backward-pass calls (gc_ctx_reserve_scratch), and what it
+  // has grown out of: captured graphs and calls in flight, on whatever stream,
+  // may still use that, so it stays until the context goes
   void* scratch;
   int64_t scratch_bytes;
+  gc::OldScratch* old_scratch;
 };
 
 namespace gc {

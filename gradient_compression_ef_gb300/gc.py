@@ -185,7 +185,8 @@ class Context:
 
     def reserve_scratch(self, nbytes):
         """At least nbytes of scratch for layernorm_backward and linear_wgrad
-        (their *_scratch_bytes); synchronises when it grows."""
+        (their *_scratch_bytes).  What it grows out of stays allocated (captured
+        graphs may use it): reserve the largest size first."""
         _check(lib.gc_ctx_reserve_scratch(self.handle, nbytes), "gc_ctx_reserve_scratch")
 
     def check(self):

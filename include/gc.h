@@ -21,9 +21,9 @@
  *    GC_ERR_CUDA).  Device-side self checks set a status word in the
  *    context; gc_ctx_check() synchronises the stream and reports it.
  *  - No call allocates memory.  Scratch space lives in the context and is
- *    reserved by gc_ctx_create / gc_ctx_reserve_powersgd.  Consecutive calls
- *    on one context are ordered by its stream; calls that overlap in time
- *    need one context each.
+ *    reserved by gc_ctx_create / gc_ctx_reserve_powersgd /
+ *    gc_ctx_reserve_scratch.  Consecutive calls on one context are ordered by
+ *    its stream; calls that overlap in time need one context each.
  *  - n <= 2^31 - 1 (indices are int32) and, for calls that use the context's
  *    scratch (Top-K, hybrid, quantisation with groups that do not fit the
  *    single-pass kernel), n <= the context's max_n (GC_ERR_WORKSPACE).
@@ -607,7 +607,11 @@ GC_API int64_t gc_ckpt_scales_bytes(int64_t rows, int64_t cols);
 
 /*
  * Reserves (or grows to) `bytes` of scratch for the calls below that state
- * one; synchronises the stream when it grows, so not during capture.
+ * one.  Growing allocates, so not during capture.  The scratch that was there
+ * stays allocated until the context is destroyed, for graphs captured with it
+ * and for calls in flight: a program with several sizes reserves the largest
+ * first.  Where the allocation fails (GC_ERR_NO_MEMORY) the context keeps what
+ * it had.
  */
 GC_API gc_status gc_ctx_reserve_scratch(gc_ctx* ctx, int64_t bytes);
 

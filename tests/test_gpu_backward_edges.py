@@ -224,3 +224,113 @@ def test_addresses_between_floats_are_refused(gc, ctx):
             assert L.gc_linear_wgrad(h, p, gc.BF16, cols, c, s, rows, cols, cols, dw, cols, db,
                                      0) == bad
     torch.cuda.synchronize()
+
+
+# --- the scratch's growth ------------------------------------------------------------------------
+
+class _Step:
+    """A weight gradient of cut tiles (partials in the scratch) and a norm's
+    column sums, on one context."""
+
+    rows, cols, out = 1000, 640, 130
+
+    def __init__(self, gc, c, seed):
+        import torch
+        r = np.random.default_rng(seed)
+        rows, cols, out = self.rows, self.cols, self.out
+        self.gc, self.c = gc, c
+        self.codes, self.scales = device_ckpt(*ref.encode(acts(r, rows, cols)))
+        self.dy = matrix(r.standard_normal((rows, out)), "f32")[0]
+        self.dn = matrix(r.standard_normal((rows, cols)), "f32")[0]
+        self.mean, self.rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+        self.dx = torch.empty(rows, cols, device="cuda")
+        self.outs = [torch.empty(out, cols, device="cuda")] + [
+            torch.empty(n, device="cuda") for n in (out, cols, cols)]
+
+    @classmethod
+    def need(cls, gc):
+        return max(gc.layernorm_scratch_bytes(cls.rows, cls.cols),
+                   gc.linear_wgrad_scratch_bytes(cls.rows, cls.out, cls.cols, "f32"))
+
+    def run(self):
+        dw, db, dg, dbt = self.outs
+        self.gc.linear_wgrad(self.c, self.dy, self.codes, self.scales, dw, db)
+        self.gc.layernorm_backward(self.c, self.dn, None, None, self.mean, self.rstd, self.dx, dg,
+                                   dbt, self.codes, self.scales)
+
+    def results(self):
+        return [t.clone() for t in self.outs]
+
+
+def test_scratch_that_cannot_grow_stays(gc):
+    with gc.Context(0) as c:
+        c.reserve_scratch(_Step.need(gc))
+        step = _Step(gc, c, 1)
+        step.run()
+        first = step.results()
+        with pytest.raises(gc.GCError) as e:
+            c.reserve_scratch(1 << 56)
+        assert e.value.status == gc.ERR_NO_MEMORY
+        step.run()
+        for a, b in zip(first, step.results()):
+            assert bool((a == b).all())
+        c.check()
+
+
+def test_scratch_growth_leaves_captured_graphs_valid(gc):
+    """A graph holds the address that the scratch had: after a growth it still
+    writes to memory of the context, and to no one else's."""
+    import torch
+    stream = torch.cuda.Stream()
+    with gc.Context(0, stream) as c:
+        c.reserve_scratch(_Step.need(gc))
+        step = _Step(gc, c, 2)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            step.run()
+        stream.synchronize()
+        first = step.results()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step.run()
+        c.reserve_scratch(2 * _Step.need(gc))
+        others = [torch.full((_Step.need(gc) // 4,), 3.0, device="cuda") for _ in range(4)]
+        for t in step.outs:
+            t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(first, step.results()):
+            assert bool((a == b).all())
+        assert all(bool((t == 3).all()) for t in others)
+        c.check()
+
+
+def test_scratch_growth_while_calls_are_under_way(gc):
+    import torch
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    with gc.Context(0, one) as c:
+        c.reserve_scratch(_Step.need(gc))
+        a, b = _Step(gc, c, 3), _Step(gc, c, 4)
+        torch.cuda.synchronize()
+        want = []
+        for s in (a, b):
+            s.run()
+            one.synchronize()
+            want.append(s.results())
+            for t in s.outs:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            a.run()
+        c.set_stream(two)
+        c.reserve_scratch(3 * _Step.need(gc))  # the first stream's calls are under way
+        two.wait_stream(one)
+        for _ in range(20):
+            b.run()
+        torch.cuda.synchronize()
+        for s, w in zip((a, b), want):
+            for x, y in zip(s.results(), w):
+                assert bool((x == y).all())
+        c.check()
