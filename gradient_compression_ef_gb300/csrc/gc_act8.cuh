@@ -1,5 +1,5 @@
 // gc_act8.cuh -- the 8-bit checkpoint format of an activation, and typed loads
-// and stores of eight consecutive columns, shared by the kernels of the
+// and stores of 16 consecutive bytes of a row, shared by the kernels of the
 // backward pass (gc_ckpt.cu, gc_norm.cu, gc_wgrad.cu).
 //
 // Format (include/gc.h): groups of 32 consecutive columns of a row share one
@@ -49,7 +49,6 @@ struct Elem<GC_F32> {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                       __float_as_uint(v[3]));
   }
-  static __device__ __forceinline__ float to_float(T x) { return x; }
 };
 
 template <>
@@ -73,7 +72,6 @@ struct Elem<GC_BF16> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  static __device__ __forceinline__ float to_float(T x) { return __bfloat162float(x); }
 };
 
 template <>
@@ -98,7 +96,6 @@ struct Elem<GC_F16> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  static __device__ __forceinline__ float to_float(T x) { return __half2float(x); }
 };
 
 // A unit as pairs, for the packed fp32 instructions.

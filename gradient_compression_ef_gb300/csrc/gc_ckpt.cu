@@ -118,8 +118,8 @@ struct Args {
   Mat x, gate, y;  // forward: inputs, output; backward: dy in x, dgate in gate, dx in y
   uint8_t *codes, *scales, *gate_codes, *gate_scales;
   int64_t row_bytes, codes_pitch, scales_pitch;
-  int64_t total;  // runs of all rows
-  uint32_t runs;  // of one row
+  uint32_t total;  // runs of all rows
+  uint32_t runs;   // of one row
 };
 
 // The warp's run: its row, first byte in the row, whether it lies inside.
@@ -130,16 +130,10 @@ struct Run {
   bool any, inner;
   __device__ __forceinline__ Run(const Args& a) {
     const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const uint32_t id = blockIdx.x * (kThreads / 32) + warp;
     any = id < a.total;
-    uint32_t run;
-    if (a.total <= 0xFFFFFFFFll) {
-      row = (uint32_t)id / a.runs;
-      run = (uint32_t)id - (uint32_t)row * a.runs;
-    } else {
-      row = id / a.runs;
-      run = (uint32_t)(id - row * a.runs);
-    }
+    row = id / a.runs;
+    const uint32_t run = id - (uint32_t)row * a.runs;
     at = run * (U * 512u);
     inner = (int64_t)at + U * 512 + (ALIGNED ? 0 : 16) <= a.row_bytes;
   }
@@ -270,15 +264,17 @@ __global__ void __launch_bounds__(kThreads, 5)
 constexpr int kUnroll = 4;
 
 template <int DT, int KIND, bool GATED, bool BACK, bool ALIGNED>
-void launch_sized(gc_ctx* ctx, Args a, int64_t rows) {
+gc_status launch_sized(gc_ctx* ctx, Args a, int64_t rows) {
   const int64_t segs = ceil_div(a.codes_pitch / Elem<DT>::V, 32);  // of 32 units, per row
   // long runs where a row has one and every SM gets at least two blocks of
   // them; else a unit per lane (17 x 4096 bf16: 34 blocks instead of 9)
   const int64_t runs = ceil_div(segs, kUnroll);
   const bool large = segs >= kUnroll && rows * runs >= (int64_t)ctx->num_sms * 16;
   a.runs = (uint32_t)(large ? runs : segs);
-  a.total = rows * a.runs;
-  const unsigned g = (unsigned)ceil_div(a.total, kThreads / 32);
+  // (a matrix of as many runs would take 2 TB)
+  if (rows * a.runs > UINT32_MAX - kThreads / 32) return GC_ERR_UNSUPPORTED;
+  a.total = (uint32_t)(rows * a.runs);
+  const unsigned g = (unsigned)ceil_div(rows * a.runs, (int64_t)(kThreads / 32));
   if (BACK) {
     if (large)
       act_backward_kernel<DT, KIND, GATED, ALIGNED, kUnroll><<<g, kThreads, 0, ctx->stream>>>(a);
@@ -290,21 +286,19 @@ void launch_sized(gc_ctx* ctx, Args a, int64_t rows) {
     else
       act_forward_kernel<DT, KIND, GATED, ALIGNED, 1><<<g, kThreads, 0, ctx->stream>>>(a);
   }
+  return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
 template <int KIND, bool GATED, bool BACK>
 gc_status launch_typed(gc_ctx* ctx, const Args& a, int64_t rows, int dtype, bool aligned) {
-  if (dtype == GC_F32) {
-    if (aligned) launch_sized<GC_F32, KIND, GATED, BACK, true>(ctx, a, rows);
-    else launch_sized<GC_F32, KIND, GATED, BACK, false>(ctx, a, rows);
-  } else if (dtype == GC_BF16) {
-    if (aligned) launch_sized<GC_BF16, KIND, GATED, BACK, true>(ctx, a, rows);
-    else launch_sized<GC_BF16, KIND, GATED, BACK, false>(ctx, a, rows);
-  } else {
-    if (aligned) launch_sized<GC_F16, KIND, GATED, BACK, true>(ctx, a, rows);
-    else launch_sized<GC_F16, KIND, GATED, BACK, false>(ctx, a, rows);
-  }
-  return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+  if (dtype == GC_F32)
+    return aligned ? launch_sized<GC_F32, KIND, GATED, BACK, true>(ctx, a, rows)
+                   : launch_sized<GC_F32, KIND, GATED, BACK, false>(ctx, a, rows);
+  if (dtype == GC_BF16)
+    return aligned ? launch_sized<GC_BF16, KIND, GATED, BACK, true>(ctx, a, rows)
+                   : launch_sized<GC_BF16, KIND, GATED, BACK, false>(ctx, a, rows);
+  return aligned ? launch_sized<GC_F16, KIND, GATED, BACK, true>(ctx, a, rows)
+                 : launch_sized<GC_F16, KIND, GATED, BACK, false>(ctx, a, rows);
 }
 
 Mat mat(const void* p, int64_t ld, int dtype, int64_t rows, int64_t cols) {

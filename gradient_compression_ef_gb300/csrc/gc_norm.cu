@@ -500,20 +500,6 @@ __device__ __forceinline__ void fill_stage(const NormArgs& a, int64_t row, char*
   }
 }
 
-__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds_u128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-
 // How the rows lie: every thread's units inside rows on 16-byte boundaries;
 // rows on such boundaries with a ragged end; rows that start anywhere.
 enum Rows { kFull, kEnds, kAnywhere };
@@ -524,14 +510,14 @@ template <int DT, int ROWS>
 __device__ __forceinline__ uint4 staged_unit(uint32_t at, uint32_t mis, int left) {
   uint4 r;
   if (ROWS != kAnywhere) {
-    r = lds_u128(at);
+    r = sm100::lds_u128(at);
   } else {
     const uint32_t p = at + (mis & ~3u);
     uint32_t w[5];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = lds_u32(p + 4 * i);
+    for (int i = 0; i < 4; ++i) w[i] = sm100::lds_u32(p + 4 * i);
     if (elem_size(DT) == 2 && (mis & 2u)) {
-      w[4] = lds_u32(p + 16);
+      w[4] = sm100::lds_u32(p + 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
     }
@@ -942,12 +928,7 @@ __global__ void __maxnreg__(kBackwardRegs)
       in[i].dy = staged_unit<DT, ROWS>(stage + u * 16, mis0, left[i]);
       if constexpr (CKPT) {
         const uint32_t at = stage + a.second_at + u * V;
-        uint32_t b;
-        asm volatile("ld.shared.u8 %0, [%1];"
-                     : "=r"(b)
-                     : "r"(stage + a.scales_at + u / (kActGroup / V))
-                     : "memory");
-        b *= 0x00800080u;
+        const uint32_t b = lds_u8(stage + a.scales_at + u / (kActGroup / V)) * 0x00800080u;
         const uint32_t c0 = lds_u32(at);
         in[i].x.x = decode2(c0, 0x1100u, b);
         in[i].x.y = decode2(c0, 0x3322u, b);
@@ -1133,9 +1114,11 @@ struct RingPlan {
 };
 
 // Dynamic shared memory that each of n blocks of an SM may use: 228 KB less
-// the system's 1 KB a block and the kernels' static part (624 bytes: two turns
-// of 2 x 36 sums, the barriers).
-int64_t block_smem(int n) { return 228 * 1024 / n - 1024 - 768; }
+// the system's 1 KB a block and the kernels' static part (two turns of 2 x 36
+// sums, a full and, backward, an empty barrier per stage).
+constexpr int64_t kStaticSmem =
+    (2 * 36 * 2 * sizeof(float) + 2 * kMaxStages * sizeof(uint64_t) + 127) / 128 * 128;
+int64_t block_smem(int n) { return 228 * 1024 / n - 1024 - kStaticSmem; }
 
 // Threads of a row; 0 where rows are too narrow or too wide.  (A wider row's
 // threads would leave an SM a single block of more registers: 11008 columns
@@ -1225,8 +1208,8 @@ void forward_dt(gc_ctx* ctx, NormArgs& a, bool aligned) {
     forward_block<DT, 1>(ctx, a, (int)round_up(units, 32), aligned);
   } else if (a.codes_pitch <= 512) {
     if (units <= 32) forward_warp<DT, 1>(ctx, a, aligned);
-    else if (units <= 64) forward_warp<DT, 2>(ctx, a, aligned);
-    else forward_warp<DT, 4>(ctx, a, aligned);
+    else if (DT != GC_F32 || units <= 64) forward_warp<DT, 2>(ctx, a, aligned);
+    else forward_warp<DT, DT == GC_F32 ? 4 : 2>(ctx, a, aligned);  // fp32: 4 columns a unit
   } else {
     const RingPlan p = ring_plan(a.cols, DT, false, false);
     if (p.threads) {

@@ -152,6 +152,24 @@ __device__ __forceinline__ float4 lds128(uint32_t a) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 lds_u128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ float lds32(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
@@ -329,9 +347,10 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 
 // Arrival on a barrier given by its cluster-space address.  What the arrival
 // announces are shared-memory writes for the tensor core, which a proxy fence
-// of the writing thread has already ordered, or finished tensor-memory loads;
-// a release at cluster scope would wait for every earlier memory operation
-// of the thread as well (about 1300 cycles per arrival, measured).
+// of each writing thread has completed before it and no thread of the other
+// CTA reads, or finished tensor-memory loads.  A release at cluster scope
+// would order the writes for those threads as well, at about 1000 cycles an
+// arrival (weight gradient 8192 x 4096 -> 11008 bf16 426 -> 802 us).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }

@@ -187,19 +187,6 @@ struct TokCursor {
   }
 };
 
-__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -441,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 16; i += 8) {
           uint4 raw[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) raw[e] = lds_u4(at + (e & 1 ? off1 : off0) + (i + e) * 512);
+          for (int e = 0; e < 8; ++e) raw[e] = lds_u128(at + (e & 1 ? off1 : off0) + (i + e) * 512);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float2 v[4];
@@ -509,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const uint32_t r = (uint32_t)(row0 + p * 4);
-          c[p] = lds_u4(s.codes + cs * kCodeBytes + r * kHalf + unit * 16);
+          c[p] = lds_u128(s.codes + cs * kCodeBytes + r * kHalf + unit * 16);
           b[p] = lds_u8(s.scales + cs * kScaleBytes + r * 16 + sat);
         }
 #pragma unroll
