@@ -11,7 +11,8 @@ import pytest
 
 from oracle import backward as ref
 from tests.gpu_helpers import torch_cuda
-from tests.test_gpu_backward import EPS, U, acts, ckpt, close, device_ckpt, f64, matrix, out_matrix
+from tests.test_gpu_backward import (CHAIN, EPS, TINY, U, _dt, acts, ckpt, close, device_ckpt, f64,
+                                     matrix, out_matrix, pad_untouched)
 
 pytestmark = pytest.mark.gpu
 
@@ -334,3 +335,242 @@ def test_scratch_growth_while_calls_are_under_way(gc):
             for x, y in zip(s.results(), w):
                 assert bool((x == y).all())
         c.check()
+
+
+# --- kernels that only large matrices are given to -----------------------------------------------
+#
+# Rows well above what the blocks of a launch have at a time and not a multiple
+# of it; the references in 64 bits by torch on the GPU, written from the
+# formulas.
+
+def _encode64(x):
+    """Codes [rows, pitch] and scale bytes [rows, groups] of x (float64)."""
+    import torch
+    rows, cols = x.shape
+    groups = -(-cols // 32)
+    g = torch.zeros(rows, groups * 32, dtype=torch.float64, device="cuda")
+    g[:, :cols] = x
+    g = g.view(rows, groups, 32)
+    top = g.abs().amax(dim=2)
+    e = torch.frexp(top).exponent
+    small = top < 2.0 ** -120
+    m = torch.clamp(torch.round(g.abs() * torch.exp2(7.0 - e.double())[..., None]), max=127)
+    m = torch.where(small[..., None], torch.zeros_like(m), m).long()
+    codes = m + 128 * ((g < 0) & (m > 0))
+    return (codes.to(torch.uint8).view(rows, groups * 32),
+            torch.where(small, torch.zeros_like(e), e + 127).to(torch.uint8))
+
+
+def _decode64(codes, b, cols):
+    import torch
+    rows, groups = b.shape
+    c = codes.view(rows, groups, 32).long()
+    v = (c & 127).double() * torch.exp2(b.double() - 134.0)[..., None]
+    return torch.where(c > 127, -v, v).view(rows, groups * 32)[:, :cols]
+
+
+def _random(rows, cols, dtype, pad, seed, scale=1.0):
+    """A device matrix of activations with a few empty rows, its pad NaN, and
+    its values in float64."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    x = torch.randn(rows, cols, generator=gen, device="cuda")
+    x *= torch.exp(torch.randn(1, cols, generator=gen, device="cuda")) * scale
+    x *= torch.rand(rows, 1, generator=gen, device="cuda") > 0.05
+    buf = torch.full((rows, cols + pad), float("nan"), dtype=_dt(torch, dtype), device="cuda")
+    buf[:, :cols] = x
+    return buf[:, :cols], buf[:, :cols].double()
+
+
+def _near(got, want, tol, what):
+    bad = (got.double() - want).abs() > tol
+    bad |= got.isnan()
+    n = int(bad.sum())
+    assert n == 0, "%s: %d outside, first at %s" % (what, n, bad.nonzero()[0].tolist())
+
+
+def _same_codes(codes, scales, want, b):
+    assert bool((codes == want).all()), "codes"
+    assert bool((scales[:, :b.shape[1]] == b).all()), "scale bytes"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols,pad", [(2500, 1024, 0), (2500, 1025, 1), (700, 4100, 3),
+                                           (900, 4097, 0), (801, 6016, 8)])
+def test_checkpoint_of_many_rows(gc, ctx, dtype, rows, cols, pad):
+    x, xv = _random(rows, cols, dtype, pad, cols)
+    codes, scales = ckpt(rows, cols)
+    gc.ckpt_save(ctx, x, codes, scales)
+    want, b = _encode64(xv)
+    _same_codes(codes, scales, want, b)
+    out, buf = out_matrix(rows, cols, dtype, pad)
+    gc.ckpt_restore(ctx, codes, scales, out)
+    assert bool((out.double() == _decode64(want, b, cols)).all())
+    pad_untouched(buf, cols)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["gelu", "silu"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,cols,pad", [(2500, 1024, 0), (2500, 1025, 1), (700, 4100, 3)])
+def test_activation_of_many_rows(gc, ctx, dtype, kind, gated, rows, cols, pad):
+    import torch
+
+    def act(v):
+        if kind == "gelu":
+            p = torch.special.ndtr(v)
+            return v * p, p + v * torch.exp(-v * v / 2) / np.sqrt(2 * np.pi)
+        p = torch.sigmoid(v)
+        return v * p, p * (1 + v * torch.sigmoid(-v))
+
+    x, xv = _random(rows, cols, dtype, pad, cols)
+    y, ybuf = out_matrix(rows, cols, dtype, pad)
+    codes, scales = ckpt(rows, cols)
+    gate = gcodes = gscales = None
+    gv = torch.ones_like(xv)
+    if gated:
+        gate, gv = _random(rows, cols, dtype, pad, cols + 1)
+        gcodes, gscales = ckpt(rows, cols)
+    gc.act_forward(ctx, kind, x, y, codes, scales, gate, gcodes, gscales)
+    f = act(xv)[0]
+    # bounds as for the small shapes
+    _near(y, f * gv, U[dtype] * (f * gv).abs() + 2.0 ** -21 * (xv * gv).abs() + TINY[dtype], "y")
+    pad_untouched(ybuf, cols)
+    want, b = _encode64(xv)
+    _same_codes(codes, scales, want, b)
+    xs, gs = _decode64(want, b, cols), gv
+    if gated:
+        want, b = _encode64(gv)
+        _same_codes(gcodes, gscales, want, b)
+        gs = _decode64(want, b, cols)
+
+    dy, dyv = _random(rows, cols, dtype, pad, cols + 2, 0.1)
+    dx, dxbuf = out_matrix(rows, cols, dtype, pad)
+    dgate, dgbuf = out_matrix(rows, cols, dtype, pad) if gated else (None, None)
+    gc.act_backward(ctx, kind, dy, dx, codes, scales, dgate, gcodes, gscales)
+    fs, ds = act(xs)
+    full = dyv * gs * ds
+    _near(dx, full, U[dtype] * full.abs() + 2.0 ** -19 * (dyv * gs).abs() + TINY[dtype], "dx")
+    pad_untouched(dxbuf, cols)
+    if gated:
+        _near(dgate, dyv * fs,
+              U[dtype] * (dyv * fs).abs() + 2.0 ** -21 * (dyv * xs).abs() + TINY[dtype], "dgate")
+        pad_untouched(dgbuf, cols)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("keep", [True, False])
+@pytest.mark.parametrize("rows,cols,pad", [(20001, 100, 0), (12001, 333, 1), (9001, 640, 0),
+                                           (9001, 1025, 3), (6001, 4096, 0), (5001, 4099, 2),
+                                           (3001, 8192, 0), (2003, 16384, 0)])
+def test_layernorm_of_many_rows(gc, ctx, dtype, keep, rows, cols, pad):
+    """Rows per block far above the ring's stages: every stage is filled
+    again, several times; the warp kernels take row after row."""
+    import torch
+    x, xv = _random(rows, cols, dtype, pad, cols)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    gamma = 1 + 0.2 * torch.randn(cols, generator=gen, device="cuda")
+    beta = 0.2 * torch.randn(cols, generator=gen, device="cuda")
+    g64, b64 = gamma.double(), beta.double()
+    y, ybuf = out_matrix(rows, cols, dtype, pad)
+    mean, rstd = (torch.empty(rows, device="cuda") for _ in range(2))
+    codes, scales = ckpt(rows, cols) if keep else (None, None)
+    gc.layernorm_forward(ctx, x, gamma, beta, EPS, y, mean, rstd, codes, scales)
+    m = xv.mean(dim=1, keepdim=True)
+    s = 1 / torch.sqrt((xv - m).square().mean(dim=1, keepdim=True) + EPS)
+    want = (xv - m) * s * g64 + b64
+    # bounds as for the small shapes
+    a = xv.abs().mean(dim=1, keepdim=True)
+    _near(mean[:, None], m, CHAIN * a + 1e-30, "mean")
+    _near(rstd[:, None], s, CHAIN * s * (1 + (a * s) ** 2 * CHAIN), "rstd")
+    n = ((xv - m) * s).abs()
+    _near(y, want, U[dtype] * want.abs() + CHAIN * (g64.abs() * (s * (a + xv.abs()) + n) + 1e-3)
+          + TINY[dtype], "y")
+    pad_untouched(ybuf, cols)
+    xs = xv
+    if keep:
+        wc, wb = _encode64(xv)
+        _same_codes(codes, scales, wc, wb)
+        xs = _decode64(wc, wb, cols)
+
+    dy, dyv = _random(rows, cols, dtype, pad, cols + 1, 0.01)
+    dx, dxbuf = out_matrix(rows, cols, dtype, pad)
+    dg, db = (torch.full((cols,), 5.0, device="cuda") for _ in range(2))
+    args = (dy, None if keep else x, gamma, mean, rstd)
+    gc.layernorm_backward(ctx, *args, dx, dg, db, codes, scales)
+    m, s = mean.double()[:, None], rstd.double()[:, None]
+    n, d = (xs - m) * s, dyv * g64
+    full = s * (d - d.mean(dim=1, keepdim=True) - n * (d * n).mean(dim=1, keepdim=True))
+    big = s * (xs.abs() + m.abs())
+    tol = s * (d.abs() + d.abs().mean(dim=1, keepdim=True)
+               + big * (d.abs() * big).mean(dim=1, keepdim=True))
+    _near(dx, full, U[dtype] * full.abs() + CHAIN * tol + TINY[dtype], "dx")
+    pad_untouched(dxbuf, cols)
+    _near(dg, (dyv * n).sum(dim=0), CHAIN * (dyv.abs() * big).sum(dim=0), "dgamma")
+    _near(db, dyv.sum(dim=0), CHAIN * dyv.abs().sum(dim=0), "dbeta")
+    dg2, db2, dx2 = torch.empty_like(dg), torch.empty_like(db), torch.empty_like(dx)
+    gc.layernorm_backward(ctx, *args, dx2, dg2, db2, codes, scales)
+    assert bool((dg2 == dg).all()) and bool((db2 == db).all()) and bool((dx2 == dx).all())
+    ctx.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols,out", [(600, 2100, 2300), (600, 2100, 5000), (70, 4100, 9000)])
+def test_linear_wgrad_of_whole_rounds_of_tiles(gc, ctx, dtype, rows, cols, out):
+    """81, 180 and 612 tiles: rounds of whole tiles for every pair of SMs, then
+    cut ones.  Whole numbers, so that every sum is exact."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(out)
+
+    def whole(top, *shape):
+        return torch.randint(-top, top + 1, shape, generator=gen, device="cuda").float()
+
+    x = whole(8, rows, cols)
+    x[:, ::32] = 64.0  # the step is 1 everywhere
+    codes, scales = ckpt(rows, cols)
+    gc.ckpt_save(ctx, x, codes, scales)
+    _same_codes(codes, scales, *_encode64(x.double()))
+    dy = whole(4, rows, out).to(_dt(torch, dtype))
+    dw, db = torch.empty(out, cols, device="cuda"), torch.empty(out, device="cuda")
+    with gc.Context(0) as own:
+        own.reserve_scratch(gc.linear_wgrad_scratch_bytes(rows, out, cols, dtype))
+        gc.linear_wgrad(own, dy, codes, scales, dw, db)
+        want, wantb = dy.double().t() @ x.double(), dy.double().sum(dim=0)
+        assert bool((dw == want).all()) and bool((db == wantb).all())
+        gc.linear_wgrad(own, dy, codes, scales, dw, db, accumulate=True)
+        assert bool((dw == 2 * want).all()) and bool((db == 2 * wantb).all())
+        # not whole numbers
+        codes2, scales2 = ckpt(rows, cols)
+        x2, x2v = _random(rows, cols, "f16" if dtype == "f16" else "f32", 0, rows)
+        gc.ckpt_save(own, x2, codes2, scales2)
+        xs = _decode64(*_encode64(x2v), cols)
+        dy2, dy2v = _random(rows, out, dtype, 0, cols)
+        gc.linear_wgrad(own, dy2, codes2, scales2, dw, db)
+        _near(dw, dy2v.t() @ xs, (rows / 8 + 64) * 2.0 ** -23 * (dy2v.abs().t() @ xs.abs()), "dw")
+        _near(db, dy2v.sum(dim=0), (rows / 8 + 64) * 2.0 ** -23 * dy2v.abs().sum(dim=0), "db")
+        own.check()
+
+
+def test_linear_wgrad_of_the_smallest_values(gc, ctx):
+    """fp16 operands in the subnormal range, bf16 ones at the end of the normal
+    range: whole multiples of the smallest, every sum exact."""
+    import torch
+    rows, cols, out = 130, 64, 40
+    r = np.random.default_rng(11)
+    x = r.integers(-127, 128, (rows, cols)).astype(np.float64)
+    x[:, ::32] = 127.0
+    d = r.integers(-4, 5, (rows, out)).astype(np.float64)
+    for dtype, unit, dunit in (("f16", 2.0 ** -24, 2.0 ** -24), ("f16", 2.0 ** -24, 1.0),
+                               ("bf16", 2.0 ** -126, 1.0), ("f32", 2.0 ** -126, 1.0)):
+        xm, xv, _ = matrix(x * unit, "f16" if dtype == "f16" else "f32")
+        assert np.array_equal(xv, x * unit)
+        codes, scales = ckpt(rows, cols)
+        gc.ckpt_save(ctx, xm, codes, scales)
+        dy, dyv, _ = matrix(d * dunit, dtype)
+        dw, db = torch.empty(out, cols, device="cuda"), torch.empty(out, device="cuda")
+        gc.linear_wgrad(ctx, dy, codes, scales, dw, db)
+        assert np.array_equal(f64(dw), dyv.T @ xv)
+        assert np.array_equal(f64(db), dyv.sum(axis=0))
