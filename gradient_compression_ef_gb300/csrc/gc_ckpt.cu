@@ -164,10 +164,14 @@ __device__ __forceinline__ void save_run(const uint4 (&r)[U], uint8_t* codes, ui
   }
 }
 
-// Blocks per SM: 64 registers hold two tensors' units, 48 one's.  (Left to the
-// compiler, GELU's gated form took 70: 8192 x 11008 bf16 131 us instead of 121.)
+// Blocks per SM: 64 registers hold two tensors' units, 48 one's, 40 those of a
+// save alone.  (Left to the compiler, GELU's gated form took 70: 8192 x 11008
+// bf16 131 us instead of 121; with 42, a save of 8192 x 4096 fp32 36 instead
+// of 34.)
+constexpr int forward_blocks(int kind, bool gated) { return kind == kKindNone ? 6 : gated ? 4 : 5; }
+
 template <int DT, int KIND, bool GATED, bool ALIGNED, int U>
-__global__ void __launch_bounds__(kThreads, GATED ? 4 : 5)
+__global__ void __launch_bounds__(kThreads, forward_blocks(KIND, GATED))
     act_forward_kernel(const __grid_constant__ Args a) {
   constexpr int V = Elem<DT>::V;
   const Run<U, ALIGNED> run(a);
