@@ -4,8 +4,8 @@ compressed gradients, all through the library's calls.
     x -> layer norm -> up, gate (linear) -> silu(up) * gate -> down (linear) -> + x
 
 Forward, per step: the norm's input, the linear layers' inputs and the gated
-activation's inputs are saved as 8-bit checkpoints (1 1/32 bytes per value
-instead of 2 in bf16).  Backward: every call reads those checkpoints and writes
+activation's inputs are saved as 8-bit checkpoints (1 1/32 bytes per value of a
+row of 512 columns, instead of 2 in bf16).  Backward: every call reads those checkpoints and writes
 its parameters' gradients in fp32 at their places of one flat gradient, which
 the bucketed compressor (error feedback, Top-K 1 %, 8-bit QSGD) takes as it
 lies.  The plain matrix products of the forward pass and of the input gradients

@@ -18,11 +18,12 @@
 // aligned pieces that cover the run, shifted into place between lanes.
 //
 // Measured, bytes read and written once over the time (a plain copy: 6.77
-// TB/s): gated SiLU 8192 x 11008 bf16 forward 116 us (6.3 TB/s), backward 131
-// (5.6); save and restore 8192 x 4096 fp32 59 us one after the
-// other (5.7); GELU 8192 x 4096 fp16 34 and 43.  Unaligned rows spend the
-// instructions: GELU 4093 x 4097 fp16 32 and 29 us (2.6 and 2.9 TB/s) at 75%
-// of the issue slots.
+// TB/s): gated SiLU 8192 x 11008 bf16 forward 113 us (6.4 TB/s), backward 131
+// (5.5); save and restore 8192 x 4096 fp32 58 us one after the other (5.8),
+// 16384 x 4096 bf16 34 and 35 (6.0, 5.8); GELU 8192 x 4096 fp16 33 and 40,
+// fp32 47 and 58.  Unaligned rows spend instructions on the shifting of every
+// unit: GELU 4093 x 4097 fp16 27 and 27 us (3.1 and 3.2 TB/s) at 81% and 73%
+// of the issue slots, SiLU 23 and 22.
 #include <algorithm>
 
 #include "gc_act8.cuh"

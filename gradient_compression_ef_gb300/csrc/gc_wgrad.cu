@@ -23,8 +23,9 @@
 //
 // Bound by the tensor cores where there are tiles for every pair: 8192 x 4096
 // -> 11008 bf16 with db takes 414 us, 1784 Tflop/s (cuBLAS reaches 1874 on this
-// GPU in a burst); fp16 478 us, 1546: its conversion takes an instruction more
-// for every two values and holds the tensor cores up.  db costs 2 to 7 us of that; nobody
+// GPU in a burst), and 486 us, 1519, back to back for seconds, when the power
+// limit lowers the clock (cuBLAS then 1728); fp16 478 us, 1546: its conversion
+// takes an instruction more for every two values and holds the tensor cores up.  db costs 2 to 7 us of that; nobody
 // waits for its warp, which takes about 0.5 us for a box of 64 x 64.  (By a
 // kernel of its own before the product db cost 25 us, and a launch: 100 x 512
 // -> 512 bf16 12.4 us, now 10.4.  Only where a layer has hardly any inputs is

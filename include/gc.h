@@ -578,13 +578,13 @@ GC_API gc_status gc_bucket_flush(gc_ctx* ctx);
  * over micro-batches).
  *
  * Matrices are [rows, cols] of one element type (gc_dtype), columns
- * contiguous, with a row stride ld >= cols in elements; rows need no
- * alignment (rows that start on 16-byte boundaries run faster).  Unlike the
- * compressing calls, infinities and NaN are allowed and carry through: a
- * loss-scaling step must see them.  Products and sums are fp32 (fused
- * multiply-adds allowed), outputs are rounded once to their type, and every
- * sum is added in an order that depends on sizes alone, so equal inputs on
- * one GPU give equal bits.  rows <= 2^31 - 1, cols <= 2^30.
+ * contiguous, with a row stride cols <= ld <= 2^30 in elements; rows after
+ * the first need no alignment (rows that start on 16-byte boundaries run
+ * faster).  Unlike the compressing calls, infinities and NaN are allowed and
+ * carry through: a loss-scaling step must see them.  Products and sums are
+ * fp32 (fused multiply-adds allowed), outputs are rounded once to their type,
+ * and every sum is added in an order that depends on sizes alone, so equal
+ * inputs on one GPU give equal bits.  rows <= 2^31 - 1, cols <= 2^30.
  *
  * Checkpoint format: groups of 32 consecutive columns of a row (the last may
  * be partial) share one scale byte B: the biased binary32 exponent of the
@@ -597,7 +597,8 @@ GC_API gc_status gc_bucket_flush(gc_ctx* ctx);
  * in fp16, and off by at most half a step, max / 128 (a whole step where m
  * was clamped).  Row r's codes start at r * round_up(cols, 32) bytes, its
  * scale bytes at r * round_up(ceil(cols / 32), 16); codes past cols within
- * the last group are 0.
+ * the last group are 0.  (A row of 512 columns takes 1 1/32 bytes per value,
+ * one of 64 1.25, one of 33 2.4.)
  */
 
 /* Bytes of a [rows, cols] checkpoint's codes / scale bytes; -1 for invalid
@@ -692,12 +693,13 @@ GC_API int64_t gc_linear_wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t 
  * dw: fp32, row stride lddw >= in elements; db: fp32[out] or NULL.
  * Products are exact: a restored value is exact in bf16, a bf16 dy is taken
  * as it is, an fp32 dy as the three bf16 values it is the sum of (three times
- * the work; an infinite fp32 dy gives NaN in its row of dw and in db).  With dtype GC_F16 the checkpoint must be one of fp16 values,
- * exact in fp16: groups whose largest magnitude is above fp16's range count
- * as NaN, below it as 0.  Sums run on the tensor cores over 512 tokens, those
- * sums in fp32 rounded to nearest.  fp32 dy: rows <= 2^29
+ * the work; an infinite fp32 dy gives NaN in its row of dw and in db).  With
+ * dtype GC_F16 the checkpoint must be one of fp16 values, exact in fp16: groups
+ * whose largest magnitude is above fp16's range count as NaN, below it as 0.
+ * Sums run on the tensor cores over 512 tokens, where they are rounded towards
+ * zero, and those sums in fp32 rounded to nearest.  fp32 dy: rows <= 2^29
  * (GC_ERR_UNSUPPORTED above).  The scratch size covers a copy of a dy whose
- * rows do not start on 16-byte boundaries.
+ * rows do not start on 16-byte boundaries, whatever the stride will be.
  * rows == 0 writes zeros (or leaves what is there, with accumulate).
  * GC_ERR_WORKSPACE when less than gc_linear_wgrad_scratch_bytes is reserved.
  */
