@@ -516,6 +516,32 @@ def test_layernorm_of_many_rows(gc, ctx, dtype, keep, rows, cols, pad):
     ctx.check()
 
 
+@pytest.mark.parametrize("ptype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", [(900, 64), (900, 500), (400, 777), (400, 4096), (100, 4099),
+                                       (200, 9001), (200, 17000)])
+def test_layernorm_with_16_bit_parameters(gc, ctx, ptype, rows, cols):
+    """gamma and beta of the 16-bit types through every kernel: the bits that
+    the same values in fp32 give."""
+    import torch
+    x, _ = _random(rows, cols, "bf16", 0, cols)
+    dy, _ = _random(rows, cols, "bf16", 0, cols + 1, 0.01)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    gamma = (1 + 0.2 * torch.randn(cols, generator=gen, device="cuda")).to(_dt(torch, ptype))
+    beta = torch.randn(cols, generator=gen, device="cuda").to(_dt(torch, ptype))
+    ctx.reserve_scratch(gc.layernorm_scratch_bytes(rows, cols))
+    got = []
+    for g, b in ((gamma, beta), (gamma.float(), beta.float())):
+        y, dx = (torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        mean, rstd = (torch.empty(rows, device="cuda") for _ in range(2))
+        dg, db = (torch.empty(cols, device="cuda") for _ in range(2))
+        gc.layernorm_forward(ctx, x, g, b, EPS, y, mean, rstd)
+        gc.layernorm_backward(ctx, dy, x, g, mean, rstd, dx, dg, db)
+        got.append((y, mean, rstd, dx, dg, db))
+    for a, b in zip(*got):
+        assert bool((a == b).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols,out", [(600, 2100, 2300), (600, 2100, 5000), (70, 4100, 9000)])
 def test_linear_wgrad_of_whole_rounds_of_tiles(gc, ctx, dtype, rows, cols, out):
