@@ -208,7 +208,8 @@ const char* gc_phase_name(int phase) {
       "refine", "bk_hist", "bk_collect", "bk_refine", "bk_write", "bk_quant", "agg_bounds",
       "agg_accumulate", "randk_mark", "randk_write", "bk_diag", "bk_flush", "psgd_thin",
       "ckpt_save", "ckpt_restore", "act_forward", "act_backward", "norm_forward",
-      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join"};
+      "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join", "rms_forward",
+      "rms_backward", "rms_reduce", "embed_forward", "embed_sort", "embed_sum", "embed_join"};
   return (phase >= 0 && phase < GC_PHASE_COUNT) ? names[phase] : "?";
 }
 
@@ -846,6 +847,133 @@ gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy,
   if (!guard.ok) return GC_ERR_CUDA;
   return gc::launch_wgrad(ctx, dy, dtype, lddy, codes, scales, rows, out, in, dw, lddw, db,
                           accumulate, ctx->scratch);
+}
+
+gc_status gc_rmsnorm_forward(gc_ctx* ctx, const void* x, int64_t ldx, const void* res,
+                             int64_t ldres, int dtype, int64_t rows, int64_t cols,
+                             const void* gamma, int ptype, float eps, void* h, int64_t ldh,
+                             void* y, int64_t ldy, float* rstd, uint8_t* codes, uint8_t* scales,
+                             uint8_t* y_codes, uint8_t* y_scales) {
+  if (!ctx || !valid_dtype(ptype) || !(eps >= 0.0f)) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, ldx));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(x, used));
+  if (res) {
+    GC_TRY(check_matrix(rows, cols, dtype, ldres));
+    GC_TRY(check_buf(res, used));
+  }
+  if (h) {
+    GC_TRY(check_matrix(rows, cols, dtype, ldh));
+    GC_TRY(check_buf(h, used));
+  }
+  if (y) {
+    GC_TRY(check_matrix(rows, cols, dtype, ldy));
+    GC_TRY(check_buf(y, used));
+  } else if (used && !y_codes) {
+    return GC_ERR_INVALID_ARG;
+  }
+  GC_TRY(check_floats(rstd, used));
+  if (gamma) GC_TRY(check_buf(gamma, used));
+  GC_TRY(check_ckpt(codes, scales, used, true));
+  GC_TRY(check_ckpt(y_codes, y_scales, used, true));
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_rms_forward(ctx, x, ldx, res, ldres, dtype, rows, cols, gamma, ptype, eps, h,
+                                ldh, y, ldy, rstd, codes, scales, y_codes, y_scales);
+}
+
+int64_t gc_rmsnorm_scratch_bytes(int64_t rows, int64_t cols) {
+  if (!valid_sizes(rows, cols)) return -1;
+  return gc::rms_scratch_bytes(rows, cols);
+}
+
+gc_status gc_rmsnorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* dres,
+                              int64_t lddres, const void* h, int64_t ldh, const uint8_t* codes,
+                              const uint8_t* scales, int dtype, int64_t rows, int64_t cols,
+                              const void* gamma, int ptype, const float* rstd, void* dx,
+                              int64_t lddx, float* dgamma, int accumulate) {
+  if (!ctx || !valid_dtype(ptype)) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(rows, cols, dtype, lddy));
+  GC_TRY(check_matrix(rows, cols, dtype, lddx));
+  const bool used = rows > 0 && cols > 0;
+  GC_TRY(check_buf(dy, used));
+  GC_TRY(check_buf(dx, used));
+  if (dres) {
+    GC_TRY(check_matrix(rows, cols, dtype, lddres));
+    GC_TRY(check_buf(dres, used));
+  }
+  GC_TRY(check_floats(rstd, used));
+  if (gamma) GC_TRY(check_buf(gamma, used));
+  // the input, or its checkpoint
+  if (h) {
+    if (codes || scales) return GC_ERR_INVALID_ARG;
+    GC_TRY(check_matrix(rows, cols, dtype, ldh));
+    GC_TRY(check_buf(h, used));
+  } else {
+    GC_TRY(check_ckpt(codes, scales, used, false));
+  }
+  if (dgamma) GC_TRY(check_floats(dgamma, cols > 0));
+  if (dgamma && used && ctx->scratch_bytes < gc::rms_scratch_bytes(rows, cols))
+    return GC_ERR_WORKSPACE;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_rms_backward(ctx, dy, lddy, dres, lddres, h, ldh, codes, scales, dtype, rows,
+                                 cols, gamma, ptype, rstd, dx, lddx, dgamma, accumulate,
+                                 static_cast<float*>(ctx->scratch));
+}
+
+namespace {
+// Token ids: any element of an array of theirs.
+gc_status check_ids(const void* ids, int itype, int64_t tokens, int64_t vocab) {
+  if ((itype != GC_I32 && itype != GC_I64) || tokens < 0 || tokens > INT32_MAX || vocab < 0 ||
+      vocab > INT32_MAX)
+    return GC_ERR_INVALID_ARG;
+  if (tokens == 0) return GC_OK;
+  if (!ids) return GC_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ids) & (itype == GC_I64 ? 7u : 3u)) return GC_ERR_ALIGNMENT;
+  return GC_OK;
+}
+}  // namespace
+
+gc_status gc_embedding_forward(gc_ctx* ctx, const void* ids, int itype, int64_t tokens,
+                               int64_t pad, const void* table, int64_t ldtable, int ptype,
+                               int64_t vocab, int64_t cols, float scale, void* y, int64_t ldy,
+                               int dtype) {
+  if (!ctx) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_ids(ids, itype, tokens, vocab));
+  GC_TRY(check_matrix(vocab, cols, ptype, ldtable));
+  GC_TRY(check_matrix(tokens, cols, dtype, ldy));
+  const bool used = tokens > 0 && cols > 0;
+  GC_TRY(check_buf(table, used && vocab > 0));
+  GC_TRY(check_buf(y, used));
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_embed_forward(ctx, ids, itype, tokens, pad, table, ldtable, ptype, vocab, cols,
+                                  scale, y, ldy, dtype);
+}
+
+int64_t gc_embedding_scratch_bytes(int64_t tokens, int64_t vocab, int64_t cols) {
+  if (!valid_sizes(tokens, cols) || !valid_sizes(vocab, cols)) return -1;
+  return gc::embed_scratch_bytes(tokens, vocab, cols);
+}
+
+gc_status gc_embedding_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtype,
+                             const void* ids, int itype, int64_t tokens, int64_t pad,
+                             int64_t vocab, int64_t cols, float scale, float* dtable, int64_t ldd,
+                             int accumulate) {
+  if (!ctx) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_ids(ids, itype, tokens, vocab));
+  GC_TRY(check_matrix(tokens, cols, dtype, lddy));
+  GC_TRY(check_matrix(vocab, cols, GC_F32, ldd));
+  const bool used = tokens > 0 && cols > 0 && vocab > 0;
+  GC_TRY(check_buf(dy, used));
+  GC_TRY(check_floats(dtable, cols > 0 && vocab > 0));
+  if (used && ctx->scratch_bytes < gc::embed_scratch_bytes(tokens, vocab, cols))
+    return GC_ERR_WORKSPACE;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_embed_wgrad(ctx, dy, lddy, dtype, ids, itype, tokens, pad, vocab, cols, scale,
+                                dtable, ldd, accumulate, ctx->scratch);
 }
 
 }  // extern "C"

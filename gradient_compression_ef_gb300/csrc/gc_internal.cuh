@@ -33,6 +33,7 @@ constexpr uint32_t kStatusTopkSelect = 1u << 1;  // threshold search failed
 constexpr uint32_t kStatusTopkOverflow = 1u << 2;  // more than k entries kept
 constexpr uint32_t kStatusScatterIndex = 1u << 3;  // residual index out of range
 constexpr uint32_t kStatusWaitTimeout = 1u << 4;   // a bounded wait on an mbarrier ran out
+constexpr uint32_t kStatusTokenId = 1u << 5;       // a token's id outside the embedding table
 
 // Per-context Top-K selection state in device memory.
 struct TopkSel {
@@ -477,9 +478,9 @@ struct LaunchScope {
   }
 };
 
-// Host helpers.
-inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Sizes.
+__host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Resident blocks per SM of a kernel at `threads` threads (at least 1).
 template <class K>
@@ -640,6 +641,29 @@ int64_t wgrad_scratch_bytes(int64_t rows, int64_t out, int64_t in, int dtype);
 gc_status launch_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t lddy, const uint8_t* codes,
                        const uint8_t* scales, int64_t rows, int64_t out, int64_t in, float* dw,
                        int64_t lddw, float* db, int accumulate, void* scratch);
+
+// RMS norm behind the residual's addition (gc_rms.cu).
+int64_t rms_scratch_bytes(int64_t rows, int64_t cols);
+gc_status launch_rms_forward(gc_ctx* ctx, const void* x, int64_t ldx, const void* res,
+                             int64_t ldres, int dtype, int64_t rows, int64_t cols,
+                             const void* gamma, int ptype, float eps, void* h, int64_t ldh,
+                             void* y, int64_t ldy, float* rstd, uint8_t* codes, uint8_t* scales,
+                             uint8_t* y_codes, uint8_t* y_scales);
+gc_status launch_rms_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* dres,
+                              int64_t lddres, const void* h, int64_t ldh, const uint8_t* codes,
+                              const uint8_t* scales, int dtype, int64_t rows, int64_t cols,
+                              const void* gamma, int ptype, const float* rstd, void* dx,
+                              int64_t lddx, float* dgamma, int accumulate, float* part);
+// Embedding lookup and the table's gradient (gc_embed.cu).
+int64_t embed_scratch_bytes(int64_t tokens, int64_t vocab, int64_t cols);
+gc_status launch_embed_forward(gc_ctx* ctx, const void* ids, int itype, int64_t tokens,
+                               int64_t pad, const void* table, int64_t ldtable, int ptype,
+                               int64_t vocab, int64_t cols, float scale, void* y, int64_t ldy,
+                               int dtype);
+gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtype, const void* ids,
+                             int itype, int64_t tokens, int64_t pad, int64_t vocab, int64_t cols,
+                             float scale, float* dtable, int64_t ldd, int accumulate,
+                             void* scratch);
 
 // Builds the device plan of nb buckets (synchronous; frees the previous).
 gc_status plan_buckets(gc_ctx* ctx, int nb, const int64_t* bucket_n, const int64_t* bucket_k);

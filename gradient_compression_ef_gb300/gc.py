@@ -24,8 +24,10 @@ F32, BF16, F16 = 0, 1, 2
 DTYPES = {"f32": F32, "bf16": BF16, "f16": F16}
 GELU, SILU = 0, 1
 ACTS = {"gelu": GELU, "silu": SILU}
+I32, I64 = 0, 1
+NO_PAD = -1 << 63  # no id is padding (INT64_MIN)
 
-PHASE_COUNT = 35
+PHASE_COUNT = 42
 
 OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE = -1, -2, -3, -4
@@ -93,6 +95,16 @@ SIGNATURES = [
     ("gc_linear_wgrad_scratch_bytes", _i64, [_i64, _i64, _i64, _int]),
     ("gc_linear_wgrad", _int, [_vp, _vp, _int, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
                                _int]),
+    ("gc_rmsnorm_forward", _int, [_vp, _vp, _i64, _vp, _i64, _int, _i64, _i64, _vp, _int,
+                                  ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    ("gc_rmsnorm_scratch_bytes", _i64, [_i64, _i64]),
+    ("gc_rmsnorm_backward", _int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _int, _i64,
+                                   _i64, _vp, _int, _vp, _vp, _i64, _vp, _int]),
+    ("gc_embedding_forward", _int, [_vp, _vp, _int, _i64, _i64, _vp, _i64, _int, _i64, _i64,
+                                    ctypes.c_float, _vp, _i64, _int]),
+    ("gc_embedding_scratch_bytes", _i64, [_i64, _i64, _i64]),
+    ("gc_embedding_wgrad", _int, [_vp, _vp, _i64, _int, _vp, _int, _i64, _i64, _i64, _i64,
+                                  ctypes.c_float, _vp, _i64, _int]),
 ]
 
 # largest n of gc_ef_topk_noalloc (GC_NOALLOC_MAX_N in include/gc.h)
@@ -571,3 +583,89 @@ def linear_wgrad(ctx, dy, codes, scales, dw, db=None, accumulate=False):
                                in_features, dw.data_ptr(), lddw,
                                _floats(db, out, "db"), 1 if accumulate else 0),
            "gc_linear_wgrad")
+
+
+# --- the residual stream: RMS norm behind the residual's addition, embedding ---
+
+
+def rmsnorm_scratch_bytes(rows, cols):
+    return int(lib.gc_rmsnorm_scratch_bytes(rows, cols))
+
+
+def rmsnorm_forward(ctx, x, res, gamma, eps, h, y, rstd, codes=None, scales=None, y_codes=None,
+                    y_scales=None):
+    """h = x + res (res may be None: h = x) and y = h * rstd * gamma over the
+    columns.  h and y may be None; codes / scales receive the checkpoint of h,
+    y_codes / y_scales that of y; gamma may be None."""
+    rows, cols, ldx = _matrix(x, "x")
+    ldr = _matrix(res, "res", x)[2] if res is not None else 0
+    ldh = _matrix(h, "h", x)[2] if h is not None else 0
+    ldy = _matrix(y, "y", x)[2] if y is not None else 0
+    c, s = _ckpt(codes, scales, rows, cols)
+    yc, ys = _ckpt(y_codes, y_scales, rows, cols)
+    _check(lib.gc_rmsnorm_forward(
+        ctx.handle, x.data_ptr(), ldx, None if res is None else res.data_ptr(), ldr, _dtype(x),
+        rows, cols, _param(gamma, cols, "gamma"), F32 if gamma is None else _dtype(gamma), eps,
+        None if h is None else h.data_ptr(), ldh, None if y is None else y.data_ptr(), ldy,
+        _floats(rstd, rows, "rstd"), c, s, yc, ys), "gc_rmsnorm_forward")
+
+
+def rmsnorm_backward(ctx, dy, dres, h, gamma, rstd, dx, dgamma=None, codes=None, scales=None,
+                     accumulate=False):
+    """RMS norm backward from h, or (h None) from its checkpoint; dres: the
+    gradient that arrives at h along the residual stream, or None; dgamma: an
+    fp32 tensor of cols elements (a slice of the flat gradient), or None."""
+    rows, cols, lddy = _matrix(dy, "dy")
+    _, _, lddx = _matrix(dx, "dx", dy)
+    ldr = _matrix(dres, "dres", dy)[2] if dres is not None else 0
+    ldh = _matrix(h, "h", dy)[2] if h is not None else 0
+    c, s = _ckpt(codes, scales, rows, cols)
+    _check(lib.gc_rmsnorm_backward(
+        ctx.handle, dy.data_ptr(), lddy, None if dres is None else dres.data_ptr(), ldr,
+        None if h is None else h.data_ptr(), ldh, c, s, _dtype(dy), rows, cols,
+        _param(gamma, cols, "gamma"), F32 if gamma is None else _dtype(gamma),
+        _floats(rstd, rows, "rstd"), dx.data_ptr(), lddx, _floats(dgamma, cols, "dgamma"),
+        1 if accumulate else 0), "gc_rmsnorm_backward")
+
+
+def _ids(ids, tokens):
+    """(address, type) of a contiguous int32 or int64 tensor of `tokens` ids."""
+    import torch
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids: unsupported element type %s (int32 or int64)" % ids.dtype)
+    if ids.numel() != tokens or not ids.is_contiguous():
+        raise ValueError("ids: needs %d contiguous ids" % tokens)
+    return ids.data_ptr(), I64 if ids.dtype == torch.int64 else I32
+
+
+def embedding_forward(ctx, ids, table, scale, y, pad=None):
+    """y[t] = scale * table[ids[t]]; zeros where the id is `pad`.  table and y
+    may differ in type.  An id outside the table gives zeros and a failed
+    ctx.check()."""
+    vocab, cols, ldt = _matrix(table, "table")
+    tokens, ycols, ldy = _matrix(y, "y")
+    if ycols != cols:
+        raise ValueError("y: %d columns, the table has %d" % (ycols, cols))
+    p, itype = _ids(ids, tokens)
+    _check(lib.gc_embedding_forward(
+        ctx.handle, p, itype, tokens, NO_PAD if pad is None else pad, table.data_ptr(), ldt,
+        _dtype(table), vocab, cols, scale, y.data_ptr(), ldy, _dtype(y)), "gc_embedding_forward")
+
+
+def embedding_scratch_bytes(tokens, vocab, cols):
+    return int(lib.gc_embedding_scratch_bytes(tokens, vocab, cols))
+
+
+def embedding_wgrad(ctx, dy, ids, scale, dtable, pad=None, accumulate=False):
+    """dtable [vocab, cols], fp32 (a slice of the flat gradient), of
+    embedding_forward: scale times the sum of dy's rows of each id."""
+    tokens, cols, lddy = _matrix(dy, "dy")
+    vocab, tcols, ldd = _matrix(dtable, "dtable")
+    if tcols != cols or _dtype(dtable) != F32:
+        raise ValueError("dtable: %s %s, expected fp32 with %d columns" % (
+            tuple(dtable.shape), dtable.dtype, cols))
+    p, itype = _ids(ids, tokens)
+    _check(lib.gc_embedding_wgrad(
+        ctx.handle, dy.data_ptr(), lddy, _dtype(dy), p, itype, tokens,
+        NO_PAD if pad is None else pad, vocab, cols, scale, dtable.data_ptr(), ldd,
+        1 if accumulate else 0), "gc_embedding_wgrad")

@@ -99,6 +99,9 @@ typedef enum gc_dtype { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;
 /* Activation function: x Phi(x) (exact GELU), or x / (1 + exp(-x)). */
 typedef enum gc_act { GC_GELU = 0, GC_SILU = 1 } gc_act;
 
+/* Type of token ids. */
+typedef enum gc_itype { GC_I32 = 0, GC_I64 = 1 } gc_itype;
+
 typedef struct gc_ctx gc_ctx;
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -178,7 +181,14 @@ typedef enum gc_phase {
   GC_PHASE_WGRAD = 32,       /* linear layer: dw from dy and the checkpoint */
   GC_PHASE_WGRAD_SPLIT = 33, /* linear layer: dy as bf16 planes */
   GC_PHASE_WGRAD_JOIN = 34,  /* linear layer: sum of the token ranges' partials */
-  GC_PHASE_COUNT = 35
+  GC_PHASE_RMS_FORWARD = 35, /* residual's addition and RMS norm */
+  GC_PHASE_RMS_BACKWARD = 36,
+  GC_PHASE_RMS_REDUCE = 37,  /* RMS norm: column sums of the blocks' partials */
+  GC_PHASE_EMBED_FORWARD = 38, /* embedding lookup */
+  GC_PHASE_EMBED_SORT = 39,  /* embedding gradient: tokens by their ids */
+  GC_PHASE_EMBED_SUM = 40,   /* embedding gradient: sums of runs, empty rows */
+  GC_PHASE_EMBED_JOIN = 41,  /* embedding gradient: runs that cross chunks */
+  GC_PHASE_COUNT = 42
 } gc_phase;
 
 /* Name of a phase ("ef_hist", ...); "?" when out of range. */
@@ -707,6 +717,76 @@ GC_API gc_status gc_linear_wgrad(gc_ctx* ctx, const void* dy, int dtype, int64_t
                                  const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                  int64_t out, int64_t in, float* dw, int64_t lddw, float* db,
                                  int accumulate);
+
+/*
+ * Root-mean-square norm behind the residual's addition: per row
+ *   h = x + res (one rounding to dtype; h = x when res is NULL),
+ *   rstd = 1 / sqrt(sum(h^2) / cols + eps),  y = h * rstd * gamma,
+ * the norm being that of h as it is stored.  gamma: [cols] of type ptype, or
+ * NULL (1).  rstd: fp32[rows].  Outputs, each optional (NULL): h and y whole;
+ * codes / scales, the checkpoint of h (what gc_rmsnorm_backward reads);
+ * y_codes / y_scales, y in 8 bits with scales: the checkpoint of y rounded to
+ * dtype, the same bytes as gc_ckpt_save(y) (what gc_linear_wgrad of the layer
+ * behind the norm reads).  At least one output of y is asked for.  eps >= 0.
+ * No output may alias an input.
+ */
+GC_API gc_status gc_rmsnorm_forward(gc_ctx* ctx, const void* x, int64_t ldx, const void* res,
+                                    int64_t ldres, int dtype, int64_t rows, int64_t cols,
+                                    const void* gamma, int ptype, float eps, void* h,
+                                    int64_t ldh, void* y, int64_t ldy, float* rstd,
+                                    uint8_t* codes, uint8_t* scales, uint8_t* y_codes,
+                                    uint8_t* y_scales);
+
+/* Scratch bytes of gc_rmsnorm_backward; -1 for invalid arguments. */
+GC_API int64_t gc_rmsnorm_scratch_bytes(int64_t rows, int64_t cols);
+
+/*
+ * RMS norm backward from h, or (h NULL) from its checkpoint: with n = h * rstd
+ * and d = dy * gamma,
+ *   dx = rstd * (d - n * sum(d * n) / cols) + dres   (the gradient of x and of
+ *   res), dgamma (+)= sum over rows of dy * n.
+ * dres: the gradient that arrives at h along the residual stream, or NULL (0).
+ * rstd: the forward call's.  dgamma: fp32[cols] or NULL.  GC_ERR_WORKSPACE when
+ * less than gc_rmsnorm_scratch_bytes is reserved (and dgamma is asked for).
+ */
+GC_API gc_status gc_rmsnorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* dres,
+                                     int64_t lddres, const void* h, int64_t ldh,
+                                     const uint8_t* codes, const uint8_t* scales, int dtype,
+                                     int64_t rows, int64_t cols, const void* gamma, int ptype,
+                                     const float* rstd, void* dx, int64_t lddx, float* dgamma,
+                                     int accumulate);
+
+/*
+ * Embedding lookup with a scale: y[t] = scale * table[ids[t]], the product in
+ * fp32 and rounded once to dtype.  ids: [tokens] of type itype (gc_itype);
+ * table: [vocab, cols] of type ptype; y: [tokens, cols] of type dtype.  A token
+ * whose id equals `pad` (any number; INT64_MIN: none) gives a row of zeros, and
+ * so does one whose id is outside the table, which also sets the device status
+ * (GC_ERR_DEVICE_CHECK from gc_ctx_check).  tokens, vocab <= 2^31 - 1.
+ */
+GC_API gc_status gc_embedding_forward(gc_ctx* ctx, const void* ids, int itype, int64_t tokens,
+                                      int64_t pad, const void* table, int64_t ldtable, int ptype,
+                                      int64_t vocab, int64_t cols, float scale, void* y,
+                                      int64_t ldy, int dtype);
+
+/* Scratch bytes of gc_embedding_wgrad; -1 for invalid arguments. */
+GC_API int64_t gc_embedding_scratch_bytes(int64_t tokens, int64_t vocab, int64_t cols);
+
+/*
+ * The table's gradient: dtable[v] (+)= scale * sum of dy[t] over the tokens t
+ * whose id is v.  dtable: fp32 [vocab, cols], row stride ldd, at any float of
+ * the flat gradient; without accumulate the rows of ids that do not occur are
+ * set to zero, with it they are not touched.  Tokens whose id is `pad` add
+ * nothing, nor do those outside the table, which set the device status as
+ * above.  The tokens are sorted by id (stable) and added in an order that the
+ * ids alone decide: the same bits on every call.  GC_ERR_WORKSPACE when less
+ * than gc_embedding_scratch_bytes is reserved; GC_ERR_UNSUPPORTED above 2^31
+ * blocks of 64 tokens x 4096 bytes.
+ */
+GC_API gc_status gc_embedding_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtype,
+                                    const void* ids, int itype, int64_t tokens, int64_t pad,
+                                    int64_t vocab, int64_t cols, float scale, float* dtable,
+                                    int64_t ldd, int accumulate);
 
 /*
  * Largest n accepted by gc_ef_topk_noalloc: its scratch is a fixed device
