@@ -209,7 +209,8 @@ const char* gc_phase_name(int phase) {
       "agg_accumulate", "randk_mark", "randk_write", "bk_diag", "bk_flush", "psgd_thin",
       "ckpt_save", "ckpt_restore", "act_forward", "act_backward", "norm_forward",
       "norm_backward", "norm_reduce", "wgrad", "wgrad_split", "wgrad_join", "rms_forward",
-      "rms_backward", "rms_reduce", "embed_forward", "embed_sort", "embed_sum", "embed_join"};
+      "rms_backward", "rms_reduce", "embed_forward", "embed_sort", "embed_sum", "embed_join",
+      "orth_input", "orth_product"};
   return (phase >= 0 && phase < GC_PHASE_COUNT) ? names[phase] : "?";
 }
 
@@ -974,6 +975,28 @@ gc_status gc_embedding_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
   if (!guard.ok) return GC_ERR_CUDA;
   return gc::launch_embed_wgrad(ctx, dy, lddy, dtype, ids, itype, tokens, pad, vocab, cols, scale,
                                 dtable, ldd, accumulate, ctx->scratch);
+}
+
+int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n) {
+  if (m < 0 || n < 0 || m > kMaxCols || n > kMaxCols) return -1;
+  return gc::orth_scratch_bytes(m, n);
+}
+
+gc_status gc_orthogonalize(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n,
+                           int64_t ldg, int steps, const float* coefs, float eps, float scale,
+                           void* out, int odtype, int64_t ldo) {
+  if (!ctx || steps < 1 || !coefs || !(eps >= 0.0f) || m > kMaxCols) return GC_ERR_INVALID_ARG;
+  GC_TRY(check_matrix(m, n, dtype, ldg));
+  GC_TRY(check_matrix(m, n, odtype, ldo));
+  if (m == 0 || n == 0) return GC_OK;
+  if (!g || !out) return GC_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(g) & (dtype == GC_F32 ? 3u : 1u)) return GC_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(out) & (odtype == GC_F32 ? 3u : 1u)) return GC_ERR_ALIGNMENT;
+  if (ctx->scratch_bytes < gc::orth_scratch_bytes(m, n)) return GC_ERR_WORKSPACE;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok) return GC_ERR_CUDA;
+  return gc::launch_orth(ctx, g, dtype, m, n, ldg, steps, coefs, eps, scale, out, odtype, ldo,
+                         ctx->scratch);
 }
 
 }  // extern "C"

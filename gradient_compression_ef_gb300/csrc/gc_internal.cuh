@@ -664,6 +664,11 @@ gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
                              int itype, int64_t tokens, int64_t pad, int64_t vocab, int64_t cols,
                              float scale, float* dtable, int64_t ldd, int accumulate,
                              void* scratch);
+// Newton-Schulz orthogonalisation (gc_orth.cu); coefs: [steps][3] on the host.
+int64_t orth_scratch_bytes(int64_t m, int64_t n);
+gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n, int64_t ldg,
+                      int steps, const float* coefs, float eps, float scale, void* out,
+                      int odtype, int64_t ldo, void* scratch);
 
 // Builds the device plan of nb buckets (synchronous; frees the previous).
 gc_status plan_buckets(gc_ctx* ctx, int nb, const int64_t* bucket_n, const int64_t* bucket_k);

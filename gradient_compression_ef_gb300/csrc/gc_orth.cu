@@ -1,0 +1,761 @@
+// gc_orth.cu -- an update orthogonalised by Newton-Schulz products.
+//
+//   X = g / (|g|_F + eps), on its narrow side: [s, l], s = min, l = max of m, n;
+//   per step   A = X X^T,  B = a I + b A + c A A,  X <- B X;
+//   out = scale X
+//
+// Every singular value x of X goes to x (a + b x^2 + c x^4) in each step and
+// the singular vectors stay.  Directions far below the largest one grow by a
+// factor of a each step, and so do errors in them, so that the iterates carry
+// 22 bits: each is held as two fp16 planes, v 2^12 = hi + lo, and a product is
+// hi hi + hi lo + lo hi on the tensor cores (tcgen05, exact products, fp32
+// accumulation; lo lo is below 2^-22 and left out).  Magnitudes: X, A and B
+// of a converging polynomial stay below 16, and an entry below 2^-15 loses
+// bits only against 2^-37.
+//
+// A and B are symmetric: tiles below the diagonal are not computed, every
+// tile above it is stored twice, mirrored.  a is put on B's diagonal, so that
+// a step's last product needs no epilogue.
+//
+// A product: one persistent CTA pair per two SMs (cta_group::2) owns tiles of
+// 256 x TN.  Blocks of 64 of the sum's axis come by TMA (128-byte swizzle),
+// both planes of both operands; each block is 12 MMAs.
+//   producer   one warp: TMA
+//   issuer     one warp of the leader CTA: the MMAs of the pair
+//   read-out   8 warps: tensor memory -> running sums in registers -> planes
+// The tensor cores round their running sums towards zero; read-out takes them
+// over every kSegBlocks blocks and adds in registers, rounded to nearest.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "gc_act8.cuh"
+#include "gc_sm100.cuh"
+
+namespace gc {
+namespace {
+
+constexpr int kTM = 256;             // rows of a pair's tile
+constexpr int kBK = 64;              // of the sum's axis, per block
+constexpr uint32_t kABytes = 128 * kBK * 2;  // one plane, one CTA
+constexpr int kSegBlocks = 2;        // blocks per accumulator
+constexpr int kReadWarps = 8, kProducerWarp = 8, kIssuerWarp = 9;
+constexpr int kThreads = 384;
+constexpr long long kWaitCycles = 4000000000ll;  // bound on each wait: ~2 s
+constexpr float kUnit = 4096.0f;     // planes hold v * kUnit
+
+enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
+
+template <int TN>
+struct Shape {
+  static constexpr int kBN = TN / 2;                       // second operand, one CTA
+  static constexpr uint32_t kBBytes = kBN * kBK * 2;       // one plane
+  static constexpr uint32_t kStage = 2 * (kABytes + kBBytes);
+  static constexpr int kStages = TN == 256 ? 3 : 4;
+  static constexpr uint32_t kCols = 2 * TN;                // tensor memory: two accumulators
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 8 * (2 * kStages + 5) + 16;
+};
+
+struct ProductArgs {
+  int64_t rows, cols;      // of the result
+  int64_t sum;             // length of the sum
+  int64_t row_tiles, col_tiles, tiles;
+  uint16_t* dst;           // planes of the result, plane_size apart
+  const uint16_t* prev;    // kPoly: A's planes
+  int64_t pitch, plane_size;  // elements
+  float a, b, c;
+  void* out;               // kLast
+  int64_t ldo;
+  float scale;
+  int odtype, transposed;
+  uint32_t* status;
+};
+
+struct Smem {
+  uint32_t stage0;
+  uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+  uint32_t* tmem_slot;
+};
+template <int TN>
+__device__ __forceinline__ Smem carve(unsigned char* base) {
+  using S = Shape<TN>;
+  Smem s;
+  const uint32_t at = (sm100::smem_u32(base) + 1023u) & ~1023u;
+  unsigned char* p = base + (at - sm100::smem_u32(base));
+  s.stage0 = at;
+  s.full = reinterpret_cast<uint64_t*>(p + S::kStages * S::kStage);
+  s.empty = s.full + S::kStages;
+  s.acc_full = s.empty + S::kStages;
+  s.acc_empty = s.acc_full + 2;
+  s.drain = s.acc_empty + 2;
+  s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
+  return s;
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                                 int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// v = hi + lo as two fp16 values each, of a pair: hi the nearest, lo the rest.
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(v0, v1);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(__fsub_rn(v0, f.x), __fsub_rn(v1, f.y));
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ float2 join2(uint32_t hi, uint32_t lo) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  return make_float2(h.x + l.x, h.y + l.y);
+}
+
+// Tiles by rows of tiles, outputs of neighbouring columns next to one another;
+// of a symmetric result those on and above the diagonal.
+template <int TN, bool SYM>
+__device__ __forceinline__ void tile_place(const ProductArgs& a, int64_t t, int64_t& i, int64_t& j) {
+  if (!SYM) {
+    // bands of 8 row tiles, rows fastest: the tiles that pairs work on at the
+    // same time share their operands in L2
+    const int64_t per = 8 * a.col_tiles, band = t / per, r = t - band * per;
+    const int64_t w = min((int64_t)8, a.row_tiles - band * 8);
+    j = r / w;
+    i = band * 8 + r - j * w;
+    return;
+  }
+  for (i = 0;; ++i) {
+    const int64_t first = i * kTM / TN, n = a.col_tiles - first;
+    if (t < n) {
+      j = first + t;
+      return;
+    }
+    t -= n;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void put(void* out, int64_t at, float v) {
+  if (DT == GC_F32) static_cast<float*>(out)[at] = v;
+  else if (DT == GC_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(out)[at] = __float2half_rn(v);
+}
+
+// N columns of one row of the result.
+template <int DT, int N>
+__device__ __forceinline__ void put_out(const ProductArgs& a, int64_t i, int64_t j,
+                                        const float* v) {
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    if (j + c < a.cols)
+      put<DT>(a.out, a.transposed ? (j + c) * a.ldo + i : i * a.ldo + j + c,
+              __fmul_rn(v[c], a.scale));
+}
+
+// A thread's N columns from j0 on of row i, from their sums.
+template <int MODE, int TN>
+__device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[TN / 2], int64_t i,
+                                           int64_t j0) {
+  constexpr int N = TN / 2;
+  constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  if (i >= a.rows) return;
+#pragma unroll
+  for (int c = 0; c < N; ++c) sum[c] *= MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
+  if (MODE == kLast) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+      if (a.odtype == GC_F32) put_out<GC_F32, 16>(a, i, j0 + c, sum + c);
+      else if (a.odtype == GC_BF16) put_out<GC_BF16, 16>(a, i, j0 + c, sum + c);
+      else put_out<GC_F16, 16>(a, i, j0 + c, sum + c);
+    }
+    return;
+  }
+  uint16_t* hi_row = a.dst + i * a.pitch;
+#pragma unroll
+  for (int c = 0; c < N; c += 8) {
+    const int64_t j = j0 + c;
+    if (j >= a.cols || (kSym && j + 7 < i)) continue;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = sum[c + e];
+    if (MODE == kPoly) {
+      const uint16_t* src = a.prev + i * a.pitch + j;
+      const uint4 h = *reinterpret_cast<const uint4*>(src);
+      const uint4 l = *reinterpret_cast<const uint4*>(src + a.plane_size);
+      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = join2(hw[e], lw[e]);
+        v[2 * e] = fmaf(a.c, v[2 * e], a.b * p.x);
+        v[2 * e + 1] = fmaf(a.c, v[2 * e + 1], a.b * p.y);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e == i) v[e] += a.a * kUnit;
+    }
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(v[2 * e], v[2 * e + 1], hw[e], lw[e]);
+    // rows of planes are padded to whole groups of 8
+    if (!kSym || j >= i) {
+      *reinterpret_cast<uint4*>(hi_row + j) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      *reinterpret_cast<uint4*>(hi_row + a.plane_size + j) =
+          make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    }
+    if (kSym) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t h = (uint16_t)(hw[e / 2] >> (16 * (e & 1)));
+        const uint16_t l = (uint16_t)(lw[e / 2] >> (16 * (e & 1)));
+        if (j < i && j + e >= i) {  // the group that the diagonal cuts
+          hi_row[j + e] = h;
+          hi_row[a.plane_size + j + e] = l;
+        }
+        if (j + e > i && j + e < a.cols) {
+          uint16_t* m = a.dst + (j + e) * a.pitch + i;
+          m[0] = h;
+          m[a.plane_size] = l;
+        }
+      }
+    }
+  }
+}
+
+template <int MODE, int TN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    orth_product_kernel(const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ ProductArgs a) {
+  using namespace sm100;
+  using S = Shape<TN>;
+  constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  constexpr bool kBMN = !kSym;  // the second operand's columns lie contiguous
+  extern __shared__ unsigned char orth_smem[];
+  const Smem s = carve<TN>(orth_smem);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int32_t blocks = (int32_t)((a.sum + kBK - 1) / kBK);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 2 * kReadWarps);
+    }
+    mbar_init(s.drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == kIssuerWarp) {
+    tmem_alloc_pair(s.tmem_slot, S::kCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers exist before either CTA arrives on one
+  tc_fence_after_sync();
+  const uint32_t tmem = *s.tmem_slot;
+  bool ok = true;
+  let_next_begin();
+
+  if (warp == kProducerWarp) {
+    const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
+    after_previous();
+    int st = 0;
+    uint32_t ph = 0, loads = 0;
+    for (int64_t t = pair; ok && t < a.tiles; t += pairs) {
+      int64_t ti, tj;
+      tile_place<TN, kSym>(a, t, ti, tj);
+      const int32_t r0 = (int32_t)(ti * kTM) + (int32_t)rank * 128;
+      const int32_t c0 = (int32_t)(tj * TN) + (int32_t)rank * S::kBN;
+      for (int32_t k = 0; k < blocks; ++k) {
+        if (loads >= S::kStages) {
+          // free once the pair's MMAs read it
+          if (!mbar_wait_cluster(&s.empty[st], ph ^ 1u, kWaitCycles)) ok = false;
+          if (__any_sync(0xffffffffu, !ok)) {
+            ok = false;
+            break;
+          }
+        } else {
+          ++loads;
+        }
+        if (elect_one()) {
+          const uint32_t bar = bar0 + st * 8, at = s.stage0 + st * S::kStage;
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * S::kStage);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            tma_load_3d_pair(at + p * kABytes, &map_a, k * kBK, r0, p, bar);
+            const uint32_t b = at + 2 * kABytes + p * S::kBBytes;
+            if (!kBMN) {
+              tma_load_3d_pair(b, &map_b, k * kBK, c0, p, bar);
+            } else {
+#pragma unroll
+              for (int h = 0; h < S::kBN / 64; ++h)
+                tma_load_3d_pair(b + h * 8192, &map_b, c0 + h * 64, k * kBK, p, bar);
+            }
+          }
+        }
+        if (++st == S::kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // the arrivals of the last MMAs on this CTA's barriers: none may be under
+    // way when the CTA ends
+    for (int i = 0; ok && i < S::kStages; ++i) {
+      if (loads >= S::kStages || (uint32_t)st < loads)
+        if (!mbar_wait_cluster(&s.empty[st], ph ^ 1u, kWaitCycles)) ok = false;
+      if (++st == S::kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  } else if (warp == kIssuerWarp) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = (1u << 4) | ((kBMN ? 1u : 0u) << 16) |
+                                 ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24);
+      // K-major: 128-byte rows of 64, 8 rows per 1024-byte group; 16 of the sum
+      // are 32 bytes.  MN-major: 128-byte rows of 64 columns, 8 of the sum per
+      // group, blocks of 64 columns 8 KB apart; 16 of the sum are 2048 bytes.
+      const uint64_t da = smem_desc_sw128(s.stage0, 16, 1024);
+      const uint64_t db = smem_desc_sw128(s.stage0 + 2 * kABytes, kBMN ? 8192 : 16, 1024);
+      const uint32_t hi = (uint32_t)(da >> 32), a0 = (uint32_t)da, b0 = (uint32_t)db;
+      constexpr uint32_t kAStep = 32 >> 4, kBStep = (kBMN ? 2048 : 32) >> 4;
+      constexpr uint32_t kALo = kABytes >> 4, kBLo = S::kBBytes >> 4;
+      int st = 0;
+      uint32_t ph = 0, seg = 0;
+      for (int64_t t = pair; ok && t < a.tiles; t += pairs) {
+        int in_seg = 0;
+        for (int32_t k = 0; k < blocks; ++k) {
+          const uint32_t buf = seg & 1u;
+          if (in_seg == 0 && seg >= 2 &&
+              !mbar_wait_cluster(&s.acc_empty[buf], ((seg >> 1) - 1u) & 1u, kWaitCycles))
+            ok = false;
+          if (ok && !mbar_wait_cluster(&s.full[st], ph, kWaitCycles)) ok = false;
+          if (__any_sync(0xffffffffu, !ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const bool last = in_seg == kSegBlocks - 1 || k + 1 == blocks;
+          if (elect_one()) {
+            const uint32_t off = (uint32_t)st * (S::kStage >> 4), d = tmem + buf * TN;
+            // the small products first: the sum is large only once hi hi is in it
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_f16_pair(d, a0 + off + kALo + kk * kAStep, b0 + off + kk * kBStep, hi, idesc,
+                           (in_seg | kk) ? 1u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kBLo + kk * kBStep, hi, idesc, 1u);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kk * kBStep, hi, idesc, 1u);
+            mma_commit_pair(&s.empty[st]);
+            if (last) mma_commit_pair(&s.acc_full[buf]);
+          }
+          ++in_seg;
+          if (last) {
+            ++seg;
+            in_seg = 0;
+          }
+          if (++st == S::kStages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (elect_one()) mma_commit_pair(s.drain);
+    }
+  } else if (warp < kReadWarps) {
+    // warp w reads lanes 32 (w % 4) .. + 31 (rows) of columns N (w / 4) .. of
+    // every accumulator
+    constexpr int N = TN / 2;
+    const uint32_t q = (uint32_t)warp & 3u, ch = (uint32_t)warp >> 2;
+    const uint32_t acc_empty0 = map_to_rank(smem_u32(s.acc_empty), 0);
+    after_previous();
+    uint32_t seg = 0;
+    for (int64_t t = pair; ok && t < a.tiles; t += pairs) {
+      float sum[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) sum[c] = 0.0f;
+      for (int32_t k = 0; k < blocks; k += kSegBlocks, ++seg) {
+        const uint32_t buf = seg & 1u;
+        const bool got = mbar_wait_cluster(&s.acc_full[buf], (seg >> 1) & 1u, kWaitCycles);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t at = tmem + ((q * 32) << 16) + buf * TN + ch * N;
+#pragma unroll
+        for (int j = 0; j < N / 16; ++j) {
+          float v[16];
+          tmem_ld16(at + j * 16, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sum[j * 16 + c] += v[c];
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0 + buf * 8);
+      }
+      if (!ok) break;
+      int64_t ti, tj;
+      tile_place<TN, kSym>(a, t, ti, tj);
+      store_tile<MODE, TN>(a, sum, ti * kTM + rank * 128 + q * 32 + lane, tj * TN + ch * N);
+      __syncwarp();
+    }
+  }
+  // MMAs still in flight read both CTAs' shared memory: the producers, which
+  // have kept step with them as far as here, wait for the issuer's last commit
+  if (warp == kProducerWarp && ok && !mbar_wait_cluster(s.drain, 0, kWaitCycles)) ok = false;
+  if (!ok) {
+    atomicOr(a.status, kStatusWaitTimeout);
+    // a wait ran out: let copies in flight land before the CTA's memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000ll) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == kIssuerWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, S::kCols);
+  }
+}
+
+// --- norm and planes of g ------------------------------------------------------------------------
+
+struct InputArgs {
+  const void* g;
+  int64_t m, n, ld;      // as given
+  int64_t pitch, plane_size;
+  double* part;          // sums of squares, one per block
+  int parts;
+  float eps;
+  uint16_t* dst;
+};
+
+template <int DT>
+__device__ __forceinline__ float get(const void* g, int64_t at) {
+  if (DT == GC_F32) return __ldg(static_cast<const float*>(g) + at);
+  if (DT == GC_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(g)[at]);
+  return __half2float(static_cast<const __half*>(g)[at]);
+}
+
+// Eight consecutive elements of a row, zero from column n on.  VEC: rows start
+// on 16-byte boundaries.
+template <int DT, bool VEC>
+__device__ __forceinline__ void get8(float (&v)[8], const InputArgs& a, int64_t r, int64_t c) {
+  if (VEC && c + 8 <= a.n) {
+    const char* p = static_cast<const char*>(a.g) + (r * a.ld + c) * elem_size(DT);
+    if constexpr (DT == GC_F32) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+      Elem<DT>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? get<DT>(a.g, r * a.ld + c + e) : 0.0f;
+}
+
+// Sum of squares, a double per block: eight squares in fp32 where they keep
+// clear of its range's ends, in binary64 where not.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ InputArgs a) {
+  __shared__ double s[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
+  double sum = 0.0;
+  let_next_begin();
+  for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < total; w += (int64_t)gridDim.x * 8) {
+    const int64_t r = w / segs;
+    float v[8];
+    get8<DT, VEC>(v, a, r, (w - r * segs) * 256 + lane * 8);
+    float top = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      top = fmaxf(top, fabsf(v[e]));
+      q = fmaf(v[e], v[e], q);
+    }
+    if (top == 0.0f || (top > 0x1p-50f && top < 0x1p60f)) {
+      sum += (double)q;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += (double)v[e] * (double)v[e];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int w = 0; w < 8; ++w) t += s[w];
+    a.part[blockIdx.x] = t;
+  }
+}
+
+// kUnit / (|g| + eps) as two factors, each inside binary32's range whatever
+// the norm; NaN where g is not finite.
+__device__ __forceinline__ float2 unit_factors(const InputArgs& a) {
+  __shared__ float2 f;
+  if (threadIdx.x < 32) {
+    double t = 0.0;
+    for (int p = threadIdx.x; p < a.parts; p += 32) t += a.part[p];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const double d = sqrt(t) + (double)a.eps;
+    if (threadIdx.x == 0) {
+      if (d == 0.0) {
+        f = make_float2(0.0f, 0.0f);
+      } else if (!(d <= 1.0e300)) {
+        f = make_float2(NAN, NAN);
+      } else {
+        const int e = ilogb(d) / 2;
+        f = make_float2((float)ldexp(1.0, -e), (float)((double)kUnit / d * ldexp(1.0, e)));
+      }
+    }
+  }
+  __syncthreads();
+  return f;
+}
+
+// A zero times NaN is NaN: not finite anywhere makes NaN everywhere.
+__device__ __forceinline__ float in_units(float v, float2 f) {
+  return __fmul_rn(__fmul_rn(v, f.x), f.y);
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) orth_split_kernel(const __grid_constant__ InputArgs a) {
+  after_previous();
+  let_next_begin();
+  const float2 f = unit_factors(a);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < total; w += (int64_t)gridDim.x * 8) {
+    const int64_t r = w / segs, c = (w - r * segs) * 256 + lane * 8;
+    if (c >= a.n) continue;
+    float v[8];
+    get8<DT, VEC>(v, a, r, c);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      split2(in_units(v[2 * e], f), in_units(v[2 * e + 1], f), h[e], l[e]);
+    uint16_t* dst = a.dst + r * a.pitch + c;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+// The same for m > n, transposed: tiles of 64 x 64 through shared memory.
+template <int DT>
+__global__ void __launch_bounds__(256) orth_turn_kernel(const __grid_constant__ InputArgs a) {
+  __shared__ float t[64][65];
+  after_previous();
+  let_next_begin();
+  const float2 f = unit_factors(a);
+  const int64_t ct = ceil_div(a.n, (int64_t)64), total = ceil_div(a.m, (int64_t)64) * ct;
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const int64_t r0 = w / ct * 64, c0 = (w % ct) * 64;
+    __syncthreads();
+#pragma unroll 4
+    for (int k = threadIdx.x; k < 64 * 64; k += 256) {
+      const int64_t r = r0 + (k >> 6), c = c0 + (k & 63);
+      t[k >> 6][k & 63] = r < a.m && c < a.n ? in_units(get<DT>(a.g, r * a.ld + c), f) : 0.0f;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < 64 * 8; k += 256) {
+      const int c = k >> 3, r = (k & 7) * 8;
+      if (c0 + c >= a.n || r0 + r >= a.m) continue;
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2(t[r + 2 * e][c], t[r + 2 * e + 1][c], h[e], l[e]);
+      uint16_t* dst = a.dst + (c0 + c) * a.pitch + r0 + r;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+}
+
+// --- host ----------------------------------------------------------------------------------------
+
+constexpr int kMaxParts = 608;
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+// A matrix as two fp16 planes in the scratch.
+struct Planes {
+  uint16_t* at;
+  int64_t rows, cols, pitch, size;  // size: elements of a plane
+};
+int64_t plane_pitch(int64_t cols) { return round_up(cols, 64); }
+int64_t planes_bytes(int64_t rows, int64_t cols) { return 2 * rows * plane_pitch(cols) * 2; }
+
+bool make_map(CUtensorMap* map, const Planes& p, uint32_t box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.cols, (cuuint64_t)p.rows, 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)(p.pitch * 2), (cuuint64_t)(p.size * 2)};
+  const cuuint32_t boxes[3] = {kBK, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p.at, dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int TN>
+gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d, ProductArgs a) {
+  static uint64_t devices = 0;
+  constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  if (!allow_smem(ctx, orth_product_kernel<MODE, TN>, (int)Shape<TN>::kSmem, devices))
+    return GC_ERR_CUDA;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, x, 128) || !make_map(&mb, y, kSym ? TN / 2 : kBK)) return GC_ERR_CUDA;
+  a.rows = d.rows;
+  a.cols = d.cols;
+  a.sum = x.cols;
+  a.row_tiles = ceil_div(d.rows, (int64_t)kTM);
+  a.col_tiles = ceil_div(d.cols, (int64_t)TN);
+  a.tiles = 0;
+  if (kSym)
+    for (int64_t i = 0; i < a.row_tiles; ++i) a.tiles += a.col_tiles - i * kTM / TN;
+  else
+    a.tiles = a.row_tiles * a.col_tiles;
+  a.dst = d.at;
+  a.pitch = d.pitch;
+  a.plane_size = d.size;
+  a.status = ctx->ws.status;
+  const int64_t pairs = std::min<int64_t>(a.tiles, ctx->num_sms / 2);
+  LaunchScope L(ctx, GC_PHASE_ORTH_PRODUCT);
+  return launch_early(orth_product_kernel<MODE, TN>, dim3((unsigned)(2 * pairs)), kThreads,
+                      Shape<TN>::kSmem, ctx->stream, ma, mb, a) == cudaSuccess
+             ? GC_OK
+             : GC_ERR_CUDA;
+}
+
+template <int MODE>
+gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d,
+                  const ProductArgs& a) {
+  return product<MODE, 256>(ctx, x, y, d, a);
+}
+
+template <int DT>
+gc_status input(gc_ctx* ctx, const InputArgs& a) {
+  const bool vec = (reinterpret_cast<uintptr_t>(a.g) & 15u) == 0 && (a.m == 1 || row_aligned(a.ld, DT));
+  {
+    LaunchScope L(ctx, GC_PHASE_ORTH_INPUT);
+    const auto k = vec ? orth_norm_kernel<DT, true> : orth_norm_kernel<DT, false>;
+    k<<<a.parts, 256, 0, ctx->stream>>>(a);
+  }
+  LaunchScope L(ctx, GC_PHASE_ORTH_INPUT);
+  cudaError_t e;
+  if (a.m > a.n) {
+    const int64_t tiles = ceil_div(a.m, (int64_t)64) * ceil_div(a.n, (int64_t)64);
+    e = launch_early(orth_turn_kernel<DT>,
+                     dim3((unsigned)std::min<int64_t>(tiles, (int64_t)ctx->num_sms * 8)), 256, 0,
+                     ctx->stream, a);
+  } else {
+    const int64_t warps = a.m * ceil_div(a.n, (int64_t)256);
+    const dim3 g((unsigned)std::min<int64_t>(ceil_div(warps, (int64_t)8), (int64_t)ctx->num_sms * 8));
+    e = vec ? launch_early(orth_split_kernel<DT, true>, g, 256, 0, ctx->stream, a)
+            : launch_early(orth_split_kernel<DT, false>, g, 256, 0, ctx->stream, a);
+  }
+  return e == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}
+
+}  // namespace
+
+int64_t orth_scratch_bytes(int64_t m, int64_t n) {
+  if (m == 0 || n == 0) return 0;
+  const int64_t s = std::min(m, n), l = std::max(m, n);
+  return kMaxParts * 8 + 2 * planes_bytes(s, l) + 2 * planes_bytes(s, s);
+}
+
+gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n, int64_t ldg,
+                      int steps, const float* coefs, float eps, float scale, void* out,
+                      int odtype, int64_t ldo, void* scratch) {
+  if (m == 0 || n == 0) return GC_OK;
+  const int64_t s = std::min(m, n), l = std::max(m, n);
+  char* at = static_cast<char*>(scratch);
+  InputArgs in{};
+  in.part = reinterpret_cast<double*>(at);
+  at += kMaxParts * 8;
+  auto planes = [&](int64_t rows, int64_t cols) {
+    Planes p{reinterpret_cast<uint16_t*>(at), rows, cols, plane_pitch(cols), 0};
+    p.size = rows * p.pitch;
+    at += planes_bytes(rows, cols);
+    return p;
+  };
+  Planes x = planes(s, l), next = planes(s, l);
+  const Planes gram = planes(s, s), poly = planes(s, s);
+  in.g = g;
+  in.m = m;
+  in.n = n;
+  in.ld = ldg;
+  in.pitch = x.pitch;
+  in.plane_size = x.size;
+  in.dst = x.at;
+  in.eps = eps;
+  in.parts = (int)std::min<int64_t>(ceil_div(m * ceil_div(n, (int64_t)256), (int64_t)8),
+                                    std::min(kMaxParts, ctx->num_sms * 4));
+  gc_status st = dtype == GC_F32    ? input<GC_F32>(ctx, in)
+                 : dtype == GC_BF16 ? input<GC_BF16>(ctx, in)
+                                    : input<GC_F16>(ctx, in);
+  for (int k = 0; st == GC_OK && k < steps; ++k) {
+    ProductArgs a{};
+    st = product<kGram>(ctx, x, x, gram, a);
+    if (st != GC_OK) break;
+    a.a = coefs[3 * k];
+    a.b = coefs[3 * k + 1];
+    a.c = coefs[3 * k + 2];
+    a.prev = gram.at;
+    st = product<kPoly>(ctx, gram, gram, poly, a);
+    if (st != GC_OK) break;
+    if (k + 1 < steps) {
+      st = product<kApply>(ctx, poly, x, next, a);
+      std::swap(x, next);
+    } else {
+      a.out = out;
+      a.odtype = odtype;
+      a.ldo = ldo;
+      a.scale = scale;
+      a.transposed = m > n;
+      st = product<kLast>(ctx, poly, x, next, a);
+    }
+  }
+  if (st != GC_OK) return st;
+  return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}
+
+}  // namespace gc

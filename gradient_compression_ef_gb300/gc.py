@@ -27,7 +27,7 @@ ACTS = {"gelu": GELU, "silu": SILU}
 I32, I64 = 0, 1
 NO_PAD = -1 << 63  # no id is padding (INT64_MIN)
 
-PHASE_COUNT = 42
+PHASE_COUNT = 44
 
 OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE = -1, -2, -3, -4
@@ -105,6 +105,10 @@ SIGNATURES = [
     ("gc_embedding_scratch_bytes", _i64, [_i64, _i64, _i64]),
     ("gc_embedding_wgrad", _int, [_vp, _vp, _i64, _int, _vp, _int, _i64, _i64, _i64, _i64,
                                   ctypes.c_float, _vp, _i64, _int]),
+    ("gc_orthogonalize_scratch_bytes", _i64, [_i64, _i64]),
+    ("gc_orthogonalize", _int, [_vp, _vp, _int, _i64, _i64, _i64, _int,
+                                ctypes.POINTER(ctypes.c_float), ctypes.c_float, ctypes.c_float,
+                                _vp, _int, _i64]),
 ]
 
 # largest n of gc_ef_topk_noalloc (GC_NOALLOC_MAX_N in include/gc.h)
@@ -669,3 +673,33 @@ def embedding_wgrad(ctx, dy, ids, scale, dtable, pad=None, accumulate=False):
         ctx.handle, dy.data_ptr(), lddy, _dtype(dy), p, itype, tokens,
         NO_PAD if pad is None else pad, vocab, cols, scale, dtable.data_ptr(), ldd,
         1 if accumulate else 0), "gc_embedding_wgrad")
+
+
+# --- the update ------------------------------------------------------------------
+
+# A quintic that takes singular values from 1e-2 .. 1 near 1 in five steps.
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_scratch_bytes(m, n):
+    return int(lib.gc_orthogonalize_scratch_bytes(m, n))
+
+
+def orthogonalize(ctx, g, out, steps=5, coefs=QUINTIC, eps=1e-7, scale=1.0):
+    """out = scale * g / (|g|_F + eps) after `steps` Newton-Schulz steps X <- a X
+    + (b A + c A A) X, A = X X^T, with coefs = (a, b, c), or one such triple for
+    each step.  g and out: 2-D, types of their own, at any element of a larger
+    tensor; out may be g."""
+    m, n, ldg = _matrix(g, "g")
+    om, on, ldo = _matrix(out, "out")
+    if (om, on) != (m, n):
+        raise ValueError("out: %d x %d, expected %d x %d" % (om, on, m, n))
+    flat = [float(v) for c in coefs for v in (c if isinstance(c, (tuple, list)) else (c,))]
+    if len(flat) == 3:
+        flat = flat * max(0, steps)
+    elif len(flat) != 3 * steps:
+        raise ValueError("coefs: needs 3 numbers, or 3 for each of %d steps" % steps)
+    _check(lib.gc_orthogonalize(
+        ctx.handle, g.data_ptr(), _dtype(g), m, n, ldg, steps,
+        (ctypes.c_float * max(1, len(flat)))(*flat), eps, scale, out.data_ptr(), _dtype(out),
+        ldo), "gc_orthogonalize")

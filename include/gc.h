@@ -188,7 +188,9 @@ typedef enum gc_phase {
   GC_PHASE_EMBED_SORT = 39,  /* embedding gradient: tokens by their ids */
   GC_PHASE_EMBED_SUM = 40,   /* embedding gradient: sums of runs, empty rows */
   GC_PHASE_EMBED_JOIN = 41,  /* embedding gradient: runs that cross chunks */
-  GC_PHASE_COUNT = 42
+  GC_PHASE_ORTH_INPUT = 42,  /* orthogonalisation: norm, planes of g */
+  GC_PHASE_ORTH_PRODUCT = 43,
+  GC_PHASE_COUNT = 44
 } gc_phase;
 
 /* Name of a phase ("ef_hist", ...); "?" when out of range. */
@@ -787,6 +789,32 @@ GC_API gc_status gc_embedding_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, i
                                     const void* ids, int itype, int64_t tokens, int64_t pad,
                                     int64_t vocab, int64_t cols, float scale, float* dtable,
                                     int64_t ldd, int accumulate);
+
+/* Scratch bytes of gc_orthogonalize; -1 for invalid arguments. */
+GC_API int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n);
+
+/*
+ * An update orthogonalised by Newton-Schulz products (what a step with the
+ * aggregated gradient or its momentum applies to a weight matrix): with
+ * X_0 = g / (|g|_F + eps) and, for each step k of `steps`,
+ *   A = X X^T (X^T X when m > n),  X <- a X + (b A + c A A) X (X (b A + c A A)),
+ *   (a, b, c) = coefs[3 k ..],
+ *   out = scale * X, rounded once to odtype.
+ * Each singular value x of X becomes x (a + b x^2 + c x^4), its singular
+ * vectors stay.  coefs: HOST array of 3 * steps floats, read during the call;
+ * steps >= 1.  g: [m, n] of type dtype; out: [m, n] of type odtype; either may
+ * start at any element (a slice of the flat gradient), and out may be g itself.
+ * The iterates are held in 22 bits and products are added in fp32: the error is
+ * that of fp32 products, as long as no element of X, A = X X^T or
+ * a I + b A + c A A reaches 16 in magnitude (it comes out as infinity and then
+ * NaN); with |X_0| <= 1 a polynomial that keeps singular values below 2 stays
+ * far from it.  A g of zeros gives zeros; one with an infinity or NaN gives NaN
+ * everywhere.  m, n <= 2^30.  GC_ERR_WORKSPACE when less than
+ * gc_orthogonalize_scratch_bytes is reserved.
+ */
+GC_API gc_status gc_orthogonalize(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n,
+                                  int64_t ldg, int steps, const float* coefs, float eps,
+                                  float scale, void* out, int odtype, int64_t ldo);
 
 /*
  * Largest n accepted by gc_ef_topk_noalloc: its scratch is a fixed device

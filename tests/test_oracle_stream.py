@@ -93,7 +93,41 @@ def test_refusals_before_any_device_work(gc):
         assert L.gc_embedding_wgrad(*call) == want, (at, value)
 
 
+def test_orthogonalize_maps_singular_values():
+    r = np.random.default_rng(2)
+    for m, n in ((6, 9), (9, 6)):
+        g = r.standard_normal((m, n))
+        coefs = [(3.4445, -4.775, 2.0315)] * 2 + [(1.5, -0.5, 0.0)] * 12
+        u, s, vt = np.linalg.svd(g, full_matrices=False)
+        x = s / np.sqrt((s ** 2).sum())
+        for a, b, c in coefs:
+            x = a * x + b * x ** 3 + c * x ** 5
+        got = ref.orthogonalize(g, coefs, 0.0, 2.0)
+        assert np.allclose(got, 2.0 * (u * x) @ vt, atol=1e-12)
+        assert np.allclose(np.linalg.svd(got)[1], 2.0, atol=1e-6)
+
+
+def test_orthogonalize_refusals_before_any_device_work(gc):
+    L, c = gc.lib, fake(gc)
+    buf = ctypes.create_string_buffer(4096)
+    p = (ctypes.addressof(buf) + 255) // 256 * 256
+    bad = gc.ERR_INVALID_ARG
+    coefs = (ctypes.c_float * 3)(1.5, -0.5, 0.0)
+    good = [c, p, 0, 4, 8, 8, 1, coefs, 1e-7, 1.0, p, 1, 8]
+    for at, value, want in ((0, None, bad), (1, None, bad), (1, p + 2, gc.ERR_ALIGNMENT), (2, 3, bad),
+                            (3, -1, bad), (3, 2 ** 30 + 1, bad), (4, -1, bad), (5, 7, bad), (6, 0, bad),
+                            (7, None, bad), (8, -1.0, bad), (10, None, bad),
+                            (10, p + 1, gc.ERR_ALIGNMENT), (11, 5, bad), (12, 7, bad),
+                            (6, 1, gc.ERR_WORKSPACE)):
+        call = list(good)
+        call[at] = value
+        assert L.gc_orthogonalize(*call) == want, (at, value)
+
+
 def test_scratch_sizes(gc):
+    assert gc.orthogonalize_scratch_bytes(-1, 4) == -1
+    assert gc.orthogonalize_scratch_bytes(0, 4) == 0
+    assert gc.orthogonalize_scratch_bytes(64, 128) == gc.orthogonalize_scratch_bytes(128, 64) > 0
     assert gc.rmsnorm_scratch_bytes(-1, 4) == -1 and gc.rmsnorm_scratch_bytes(4, -1) == -1
     assert gc.rmsnorm_scratch_bytes(0, 4096) == 0
     assert gc.rmsnorm_scratch_bytes(10 ** 6, 4096) < 16 << 20  # partial rows, whatever the rows
