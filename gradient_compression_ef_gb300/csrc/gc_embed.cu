@@ -21,9 +21,10 @@
 namespace gc {
 namespace {
 
-constexpr int kChunk = 64;       // sorted tokens of one unit of work
-constexpr int kCountMax = 8192;  // tokens that are sorted by counting
-constexpr int kTile = 4096;      // tokens of a block of a radix pass
+constexpr int kMaxChunk = 64;    // sorted tokens of one unit of work, at most
+constexpr int kCountMax = 2048;  // tokens that are sorted by counting
+constexpr int kSortBlocks = 128; // blocks of a radix pass, at most
+constexpr int kBins = 512;       // digits of up to 9 bits
 
 struct EmbedArgs {
   const void* ids;
@@ -37,8 +38,18 @@ struct EmbedArgs {
   int64_t row_bytes;                        // of a row of the table, or of dy
   int64_t zero_blocks;
   float scale;
-  int wide_ids, accumulate;
+  int wide_ids, accumulate, chunk;
 };
+
+// Radix passes over (key, token) pairs; block b of a pass has the pairs from b
+// * tile on.
+struct SortArgs {
+  const uint32_t *key, *tok;  // NULL: the ids as they come
+  uint32_t *key_out, *tok_out;
+  uint32_t* count;            // [passes][kCounts]: of this pass, then of those behind it
+  int shift, bits, blocks, tile, more;  // more: passes behind this one
+};
+constexpr int kCounts = kSortBlocks * kBins;
 
 __device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t t) {
   return wide ? __ldg(static_cast<const long long*>(ids) + t)
@@ -163,6 +174,7 @@ __global__ void __launch_bounds__(1024) embed_count_kernel(const __grid_constant
   extern __shared__ __align__(16) uint32_t keys[];  // all keys, then the warps' counts
   const int n = (int)a.tokens, padded = (int)round_up(n, 128);
   __shared__ uint32_t before[32][33];
+  let_next_begin();
   for (int t = threadIdx.x; t < padded; t += 1024)
     keys[t] = t < n ? key_of(a, t) : 0xFFFFFFFFu;
   __syncthreads();
@@ -193,40 +205,23 @@ __global__ void __launch_bounds__(1024) embed_count_kernel(const __grid_constant
   }
 }
 
-// Radix pass, counts: cnt[digit][block] of the blocks' tokens.
-__global__ void __launch_bounds__(256)
-    embed_digit_kernel(const __grid_constant__ EmbedArgs a, const uint32_t* key, uint32_t* cnt,
-                       int64_t blocks, int shift) {
-  __shared__ uint32_t hist[256];
+// Counts of the first pass's digits; those of the passes behind it are set to zero.
+__global__ void __launch_bounds__(kBins)
+    embed_digit_kernel(const __grid_constant__ EmbedArgs a, const __grid_constant__ SortArgs s) {
+  __shared__ uint32_t hist[kBins];
   hist[threadIdx.x] = 0u;
   __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * kTile;
-  for (int64_t t = t0 + threadIdx.x; t < min(t0 + kTile, a.tokens); t += 256) {
-    const uint32_t k = key ? key[t] : key_of(a, t);
-    atomicAdd(&hist[(k >> shift) & 255u], 1u);
-  }
+  let_next_begin();
+  const int64_t t0 = (int64_t)blockIdx.x * s.tile, t1 = min(t0 + s.tile, a.tokens);
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += kBins)
+    atomicAdd(&hist[(key_of(a, t) >> s.shift) & ((1u << s.bits) - 1u)], 1u);
   __syncthreads();
-  cnt[threadIdx.x * blocks + blockIdx.x] = hist[threadIdx.x];
+  s.count[blockIdx.x * kBins + threadIdx.x] = hist[threadIdx.x];
+  for (int p = 1; p <= s.more; ++p) s.count[p * kCounts + blockIdx.x * kBins + threadIdx.x] = 0u;
 }
 
-// Exclusive sums of cnt: one block per digit sums its row, then places it
-// behind the digits before (their totals are counted again: 256 rows).
-__global__ void __launch_bounds__(256)
-    embed_total_kernel(const uint32_t* cnt, uint32_t* total, int64_t blocks) {
-  __shared__ uint32_t s[8];
-  uint32_t t = 0;
-  for (int64_t b = threadIdx.x; b < blocks; b += 256) t += cnt[blockIdx.x * blocks + b];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = t;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    t = 0;
-    for (int w = 0; w < 8; ++w) t += s[w];
-    total[blockIdx.x] = t;
-  }
-}
-__device__ __forceinline__ uint32_t block_scan256(uint32_t v, uint32_t* warps, uint32_t& all) {
+// Sum of v over the threads before this one, and over all (kBins threads).
+__device__ __forceinline__ uint32_t scan_bins(uint32_t v, uint32_t* warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x = v;
 #pragma unroll
@@ -234,54 +229,48 @@ __device__ __forceinline__ uint32_t block_scan256(uint32_t v, uint32_t* warps, u
     const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
   if (lane == 31) warps[warp] = x;
   __syncthreads();
   uint32_t before = 0;
-  all = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    before += w < warp ? warps[w] : 0u;
-    all += warps[w];
-  }
+  for (int w = 0; w < kBins / 32; ++w) before += w < warp ? warps[w] : 0u;
   return before + x - v;
 }
-__global__ void __launch_bounds__(256)
-    embed_scan_kernel(uint32_t* cnt, const uint32_t* total, int64_t blocks) {
-  __shared__ uint32_t warps[8];
-  uint32_t all;
-  block_scan256(threadIdx.x < blockIdx.x ? total[threadIdx.x] : 0u, warps, all);
-  uint32_t base = all;
-  for (int64_t b0 = 0; b0 < blocks; b0 += 256) {
-    const int64_t b = b0 + threadIdx.x;
-    const uint32_t v = b < blocks ? cnt[blockIdx.x * blocks + b] : 0u;
-    const uint32_t e = block_scan256(v, warps, all);
-    if (b < blocks) cnt[blockIdx.x * blocks + b] = base + e;
-    base += all;
-  }
-}
 
-// Radix pass, places: a block moves its tokens in their order, 256 at a time;
-// inside a warp equal digits are ranked by lane, warps by their order.
-__global__ void __launch_bounds__(256)
-    embed_place_kernel(const __grid_constant__ EmbedArgs a, const uint32_t* key,
-                       const uint32_t* tok, const uint32_t* cnt, int64_t blocks, int shift,
-                       uint32_t* key_out, uint32_t* tok_out) {
-  __shared__ uint32_t next[256], wcount[8][256];
+// A pass: a block finds where its pairs of each digit begin (all blocks'
+// smaller digits, earlier blocks' same digits), then moves its pairs in their
+// order, kBins at a time; inside a warp equal digits are ranked by lane, warps
+// by their order.  The next pass's counts are made on the way (whole numbers:
+// their order does not matter).
+__global__ void __launch_bounds__(kBins)
+    embed_place_kernel(const __grid_constant__ EmbedArgs a, const __grid_constant__ SortArgs s) {
+  constexpr int kWarps = kBins / 32;
+  __shared__ uint32_t next[kBins], warps[kWarps];
+  __shared__ uint16_t wcount[kWarps][kBins];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  next[threadIdx.x] = cnt[threadIdx.x * blocks + blockIdx.x];
-  const int64_t t0 = (int64_t)blockIdx.x * kTile, t1 = min(t0 + kTile, a.tokens);
-  for (int64_t b = t0; b < t1; b += 256) {
+  const uint32_t mask = (1u << s.bits) - 1u;
+  after_previous();
+  let_next_begin();
+  uint32_t before = 0, total = 0;
+#pragma unroll 8
+  for (int b = 0; b < s.blocks; ++b) {
+    const uint32_t c = __ldcg(s.count + b * kBins + threadIdx.x);
+    if (b < (int)blockIdx.x) before += c;
+    total += c;
+  }
+  next[threadIdx.x] = scan_bins(total, warps) + before;
+  const int64_t t0 = (int64_t)blockIdx.x * s.tile, t1 = min(t0 + s.tile, a.tokens);
+  for (int64_t b = t0; b < t1; b += kBins) {
 #pragma unroll
-    for (int w = 0; w < 8; ++w) wcount[w][threadIdx.x] = 0u;
+    for (int w = 0; w < kWarps; ++w) wcount[w][threadIdx.x] = 0;
     __syncthreads();
     const int64_t t = b + threadIdx.x;
     const bool in = t < t1;
-    const uint32_t k = in ? (key ? key[t] : key_of(a, t)) : 0u;
-    const uint32_t d = in ? (k >> shift) & 255u : 256u;
+    const uint32_t k = in ? (s.key ? __ldcg(s.key + t) : key_of(a, t)) : 0u;
+    const uint32_t d = in ? (k >> s.shift) & mask : kBins;
     const uint32_t same = __match_any_sync(0xffffffffu, d);
     const uint32_t rank = __popc(same & ((1u << lane) - 1u));
-    if (in && rank == 0) wcount[warp][d] = __popc(same);
+    if (in && rank == 0) wcount[warp][d] = (uint16_t)__popc(same);
     __syncthreads();
     uint32_t at = 0;
     if (in) {
@@ -291,11 +280,15 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     uint32_t sum = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) sum += wcount[w][threadIdx.x];
+    for (int w = 0; w < kWarps; ++w) sum += wcount[w][threadIdx.x];
     next[threadIdx.x] += sum;
     if (in) {
-      key_out[at] = k;
-      tok_out[at] = tok ? tok[t] : (uint32_t)t;
+      s.key_out[at] = k;
+      s.tok_out[at] = s.tok ? __ldcg(s.tok + t) : (uint32_t)t;
+      if (s.more)
+        atomicAdd(s.count + kCounts + (at / (uint32_t)s.tile) * kBins +
+                      ((k >> (s.shift + s.bits)) & mask),
+                  1u);
     }
     __syncthreads();
   }
@@ -303,22 +296,43 @@ __global__ void __launch_bounds__(256)
 
 // --- sums ----------------------------------------------------------------------------------------
 
-// A lane's sum of a run to columns c .. of a row.
+// A lane's sum of a run to columns c .. of a row (c a multiple of 4).  Added by
+// a reduction in L2, which nothing waits for: every place is written once in a
+// call, so there is no order to depend on.
 template <int V>
 __device__ __forceinline__ void put_row(float* row, const float2 (&s)[V / 2], float scale,
                                         int64_t c, int64_t cols, bool add) {
+  float v[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = __fmul_rn(j & 1 ? s[j / 2].y : s[j / 2].x, scale);
+  row += c;
+  if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0 && c + V <= cols) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      if (add)
+        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(row + j),
+                     "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3])
+                     : "memory");
+      else
+        *reinterpret_cast<float4*>(row + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const float v = __fmul_rn(j & 1 ? s[j / 2].y : s[j / 2].x, scale);
-    if (c + j < cols) row[c + j] = add ? row[c + j] + v : v;
+    if (c + j >= cols) continue;
+    if (add) atomicAdd(row + j, v[j]);
+    else row[j] = v[j];
   }
 }
 
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ EmbedArgs a) {
   constexpr int V = Elem<DT>::V, H = V / 2, kDeep = 8;
+  after_previous();
+  let_next_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t chunks = ceil_div(a.tokens, (int64_t)kChunk);
+  const int64_t chunks = ceil_div(a.tokens, (int64_t)a.chunk);
   const int64_t segs = ceil_div(a.row_bytes, (int64_t)512), seg_blocks = ceil_div(segs, (int64_t)8);
   const int64_t sum_blocks = chunks * seg_blocks;
   if (blockIdx.x >= sum_blocks) {
@@ -353,8 +367,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
   const int64_t chunk = blockIdx.x / seg_blocks;
   const int64_t seg = (blockIdx.x - chunk * seg_blocks) * 8 + warp;
   if (seg >= segs) return;
-  const int64_t p0 = chunk * kChunk;
-  const int n = (int)min((int64_t)kChunk, a.tokens - p0);
+  const int64_t p0 = chunk * a.chunk;
+  const int n = (int)min((int64_t)a.chunk, a.tokens - p0);
   const int64_t off = seg * 512 + lane * 16, c = off / elem_size(DT);
   // a token's pair per lane, two rounds
   uint32_t key[2], tok[2];
@@ -412,30 +426,46 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
 // columns.
 __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__ EmbedArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t chunks = ceil_div(a.tokens, (int64_t)kChunk);
+  const int64_t chunks = ceil_div(a.tokens, (int64_t)a.chunk);
   const int64_t segs = ceil_div(a.cols, (int64_t)128);
   after_previous();
   const int64_t total = (chunks - 1) * segs, step = (int64_t)gridDim.x * 8;
   const uint32_t none = (uint32_t)a.vocab;
   for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += step) {
     const int64_t chunk = w / segs;
-    const int64_t p0 = chunk * kChunk, p1 = p0 + kChunk;
+    const int64_t p0 = chunk * a.chunk, p1 = p0 + a.chunk;
     const uint32_t key = __ldg(a.key + p1 - 1);
     if (key == none || __ldg(a.key + p1) != key) continue;
     if (p0 > 0 && __ldg(a.key + p0 - 1) == key) continue;  // an earlier chunk's run
     const int64_t c = (w - chunk * segs) * 128 + lane * 4;
+    // a lane looks at each of the next 32 chunks' first key
     const float* src = a.part + (chunk * 2 + 1) * a.part_pitch + c;
-    if (c >= a.part_pitch) continue;
-    float4 s = *reinterpret_cast<const float4*>(src);
-    for (int64_t k = chunk + 1; k < chunks; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part + k * 2 * a.part_pitch + c);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-      const int64_t q = (k + 1) * kChunk;
-      if (q >= a.tokens || __ldg(a.key + q) != key) break;
+    const bool in = c < a.part_pitch;
+    float4 s = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    src += a.part_pitch;
+    for (int64_t k = chunk + 1;; k += 32) {
+      const int64_t q = (k + lane) * a.chunk;
+      const uint32_t on = __ballot_sync(0xffffffffu, q < a.tokens && __ldg(a.key + q) == key);
+      const int n = on == 0xffffffffu ? 32 : __ffs(~on) - 1;
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = in && i0 + i < n
+                     ? *reinterpret_cast<const float4*>(src + (i0 + i) * 2 * a.part_pitch)
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s.x += v[i].x;
+          s.y += v[i].y;
+          s.z += v[i].z;
+          s.w += v[i].w;
+        }
+      }
+      if (n < 32) break;
+      src += 64 * a.part_pitch;
     }
+    if (!in) continue;
     const float2 t[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
     put_row<4>(a.dtable + (int64_t)key * a.ldd, t, a.scale, c, a.cols, a.accumulate);
   }
@@ -446,27 +476,32 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
 int64_t up256(int64_t b) { return round_up(b, 256); }
 int64_t part_pitch(int64_t cols) { return round_up(cols, 4); }
 
+// Sorted tokens per unit of work: fewer where there would be fewer warps than
+// the GPU takes at once.
+int chunk_of(int64_t tokens, int64_t cols) {
+  int chunk = kMaxChunk;
+  while (chunk > 8 && ceil_div(tokens, (int64_t)chunk) * ceil_div(cols, (int64_t)256) < 2432) chunk /= 2;
+  return chunk;
+}
+
 struct Scratch {
-  int64_t key[2], tok[2], cnt, total, part, bytes;
+  int64_t key[2], tok[2], count, part, bytes;
 };
 Scratch lay_out(int64_t tokens, int64_t cols) {
   Scratch s{};
-  const int buffers = tokens > kCountMax ? 2 : 1;
-  for (int i = 0; i < buffers; ++i) {
+  const bool radix = tokens > kCountMax;
+  for (int i = 0; i < (radix ? 2 : 1); ++i) {
     s.key[i] = s.bytes;
     s.bytes += up256(tokens * 4);
     s.tok[i] = s.bytes;
     s.bytes += up256(tokens * 4);
   }
-  if (buffers > 1) {
-    s.cnt = s.bytes;
-    s.bytes += up256(ceil_div(tokens, (int64_t)kTile) * 256 * 4);
-    s.total = s.bytes;
-    s.bytes += 1024;
-  }
+  s.count = s.bytes;
+  if (radix) s.bytes += 4 * kCounts * 4;
   s.part = s.bytes;
   // one chunk has no run that crosses
-  if (tokens > kChunk) s.bytes += ceil_div(tokens, (int64_t)kChunk) * 2 * part_pitch(cols) * 4;
+  const int64_t chunks = ceil_div(tokens, (int64_t)chunk_of(tokens, cols));
+  if (chunks > 1) s.bytes += chunks * 2 * part_pitch(cols) * 4;
   return s;
 }
 
@@ -491,7 +526,7 @@ void lookup_cast(gc_ctx* ctx, const EmbedArgs& a, bool aligned) {
   else embed_cast_kernel<P, T, false><<<g, 256, 0, ctx->stream>>>(a);
 }
 
-void sort_tokens(gc_ctx* ctx, EmbedArgs& a, char* scratch) {
+gc_status sort_tokens(gc_ctx* ctx, EmbedArgs& a, char* scratch) {
   const Scratch s = lay_out(a.tokens, a.cols);
   auto at = [&](int64_t o) { return reinterpret_cast<uint32_t*>(scratch + o); };
   if (a.tokens <= kCountMax) {
@@ -500,35 +535,38 @@ void sort_tokens(gc_ctx* ctx, EmbedArgs& a, char* scratch) {
     LaunchScope L(ctx, GC_PHASE_EMBED_SORT);
     embed_count_kernel<<<(unsigned)ceil_div(a.tokens, (int64_t)32), 1024,
                          (size_t)round_up(a.tokens, 128) * 4, ctx->stream>>>(a);
-    return;
+    return GC_OK;
   }
-  const int64_t blocks = ceil_div(a.tokens, (int64_t)kTile);
-  const uint32_t *key = nullptr, *tok = nullptr;
-  int to = 0;
-  for (int shift = 0; shift == 0 || (a.vocab >> shift) != 0; shift += 8, to ^= 1) {
+  int bits = 1;
+  while (a.vocab >> bits) ++bits;  // keys 0 .. vocab
+  const int passes = (bits + 8) / 9;
+  SortArgs r{};
+  r.bits = (bits + passes - 1) / passes;
+  r.tile = (int)round_up(ceil_div(a.tokens, (int64_t)kSortBlocks), kBins);
+  r.blocks = (int)ceil_div(a.tokens, (int64_t)r.tile);
+  for (int p = 0; p < passes; ++p) {
+    const int to = p & 1;
+    r.count = at(s.count) + p * kCounts;
+    r.shift = p * r.bits;
+    r.more = passes - 1 - p;
+    if (p == 0) {
+      LaunchScope L(ctx, GC_PHASE_EMBED_SORT);
+      embed_digit_kernel<<<r.blocks, kBins, 0, ctx->stream>>>(a, r);
+    }
+    r.key_out = at(s.key[to]);
+    r.tok_out = at(s.tok[to]);
     {
       LaunchScope L(ctx, GC_PHASE_EMBED_SORT);
-      embed_digit_kernel<<<(unsigned)blocks, 256, 0, ctx->stream>>>(a, key, at(s.cnt), blocks,
-                                                                    shift);
+      if (launch_early(embed_place_kernel, dim3(r.blocks), kBins, 0, ctx->stream, a, r) !=
+          cudaSuccess)
+        return GC_ERR_CUDA;
     }
-    {
-      LaunchScope L(ctx, GC_PHASE_EMBED_SORT);
-      embed_total_kernel<<<256, 256, 0, ctx->stream>>>(at(s.cnt), at(s.total), blocks);
-    }
-    {
-      LaunchScope L(ctx, GC_PHASE_EMBED_SORT);
-      embed_scan_kernel<<<256, 256, 0, ctx->stream>>>(at(s.cnt), at(s.total), blocks);
-    }
-    {
-      LaunchScope L(ctx, GC_PHASE_EMBED_SORT);
-      embed_place_kernel<<<(unsigned)blocks, 256, 0, ctx->stream>>>(
-          a, key, tok, at(s.cnt), blocks, shift, at(s.key[to]), at(s.tok[to]));
-    }
-    key = at(s.key[to]);
-    tok = at(s.tok[to]);
+    r.key = r.key_out;
+    r.tok = r.tok_out;
   }
-  a.key = const_cast<uint32_t*>(key);
-  a.tok = const_cast<uint32_t*>(tok);
+  a.key = r.key_out;
+  a.tok = r.tok_out;
+  return GC_OK;
 }
 
 }  // namespace
@@ -603,13 +641,15 @@ gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
   a.status = ctx->ws.status;
   a.part_pitch = part_pitch(cols);
   a.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + lay_out(tokens, cols).part);
-  const int64_t chunks = ceil_div(tokens, (int64_t)kChunk);
+  a.chunk = chunk_of(tokens, cols);
+  const int64_t chunks = ceil_div(tokens, (int64_t)a.chunk);
   const int64_t sum_blocks = chunks * ceil_div(ceil_div(a.row_bytes, (int64_t)512), (int64_t)8);
   a.zero_blocks =
       accumulate ? 0
                  : std::min<int64_t>(ceil_div(vocab, (int64_t)64), (int64_t)ctx->num_sms * 8);
   if (sum_blocks + a.zero_blocks > INT32_MAX) return GC_ERR_UNSUPPORTED;
-  sort_tokens(ctx, a, static_cast<char*>(scratch));
+  const gc_status st = sort_tokens(ctx, a, static_cast<char*>(scratch));
+  if (st != GC_OK) return st;
   const bool al = tokens == 1 || row_aligned(lddy, dtype);
   {
     LaunchScope L(ctx, GC_PHASE_EMBED_SUM);
@@ -617,7 +657,9 @@ gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
         dtype == GC_F32    ? (al ? embed_sum_kernel<GC_F32, true> : embed_sum_kernel<GC_F32, false>)
         : dtype == GC_BF16 ? (al ? embed_sum_kernel<GC_BF16, true> : embed_sum_kernel<GC_BF16, false>)
                            : (al ? embed_sum_kernel<GC_F16, true> : embed_sum_kernel<GC_F16, false>);
-    kernel<<<(unsigned)(sum_blocks + a.zero_blocks), 256, 0, ctx->stream>>>(a);
+    if (launch_early(kernel, dim3((unsigned)(sum_blocks + a.zero_blocks)), 256, 0, ctx->stream,
+                     a) != cudaSuccess)
+      return GC_ERR_CUDA;
   }
   if (chunks > 1) {
     LaunchScope L(ctx, GC_PHASE_EMBED_JOIN);

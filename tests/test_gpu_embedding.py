@@ -268,3 +268,40 @@ def test_refusals(gc, ctx):
         call = list(args)
         call[at] = value
         assert L.gc_embedding_wgrad(*call) == want, (at, value)
+
+
+@pytest.mark.parametrize("vocab,tokens", [(2 ** 18, 3000), (2 ** 20 + 7, 70000), (511, 70000), (512, 2049)])
+def test_sorting_passes(gc, ctx, vocab, tokens):
+    """One to three radix passes, more than one round of tokens per block, digits of every width."""
+    import torch
+    r = np.random.default_rng(vocab)
+    cols = 8
+    ids = np.where(r.random(tokens) < 0.5, r.integers(0, vocab, tokens), r.integers(0, 40, tokens) * (vocab // 40))
+    ids[0], ids[1] = 0, vocab - 1
+    dy, dyv, _ = matrix(r.standard_normal((tokens, cols)), "f32")
+    want, size, n = ref.embedding_wgrad(dyv, ids, vocab, 1.0)
+    d, _ = out_matrix(vocab, cols, "f32")
+    gc.embedding_wgrad(ctx, dy, tensor_ids(ids, "i32"), 1.0, d)
+    close(f64(d), want, (n[:, None] + 2) * 2.0 ** -24 * size, "dtable")
+    ctx.check()
+
+
+@pytest.mark.parametrize("at", [0, 1, 2, 4])
+def test_accumulation_at_any_float(gc, ctx, at):
+    """Rows that start on and off 16-byte boundaries: the same bits."""
+    import torch
+    r = np.random.default_rng(at)
+    tokens, vocab, cols = 500, 60, 132
+    ids = tensor_ids(some_ids(r, tokens, vocab, "skew"), "i64")
+    dy, _, _ = matrix(r.standard_normal((tokens, cols)), "f16")
+    first = torch.empty(vocab, cols, device="cuda")
+    gc.embedding_wgrad(ctx, dy, ids, 1.25, first)
+    flat = torch.randn(vocab * cols + 8, device="cuda")
+    before = flat.clone()
+    view = flat[at:at + vocab * cols].view(vocab, cols)
+    gc.embedding_wgrad(ctx, dy, ids, 1.25, view, accumulate=True)
+    used = torch.zeros(vocab, 1, dtype=torch.bool, device="cuda")
+    used[ids] = True
+    old = before[at:at + vocab * cols].view(vocab, cols)
+    assert torch.equal(view, torch.where(used, old + first, old))
+    assert torch.equal(flat[:at], before[:at]) and torch.equal(flat[at + vocab * cols:], before[at + vocab * cols:])
