@@ -41,7 +41,7 @@ namespace {
 constexpr int kTM = 256;             // rows of a pair's tile
 constexpr int kBK = 64;              // of the sum's axis, per block
 constexpr uint32_t kABytes = 128 * kBK * 2;  // one plane, one CTA
-constexpr int kSegBlocks = 2;        // blocks per accumulator
+constexpr int kSegBlocks = 1;        // blocks per accumulator
 constexpr int kReadWarps = 8, kProducerWarp = 8, kIssuerWarp = 9;
 constexpr int kThreads = 384;
 constexpr long long kWaitCycles = 4000000000ll;  // bound on each wait: ~2 s
@@ -475,8 +475,33 @@ __device__ __forceinline__ void get8(float (&v)[8], const InputArgs& a, int64_t 
   for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? get<DT>(a.g, r * a.ld + c + e) : 0.0f;
 }
 
-// Sum of squares, a double per block: eight squares in fp32 where they keep
-// clear of its range's ends, in binary64 where not.
+// Sum of eight squares: in fp32 where they keep clear of its range's ends, in
+// binary64 where not.
+__device__ __forceinline__ double sum_squares(const float (&v)[8]) {
+  float top = 0.0f, q = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    top = fmaxf(top, fabsf(v[e]));
+    q = fmaf(v[e], v[e], q);
+  }
+  if (top == 0.0f || (top > 0x1p-50f && top < 0x1p60f)) return (double)q;
+  double t = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t += (double)v[e] * (double)v[e];
+  return t;
+}
+
+// kUnit / (|g| + eps) as two factors, each inside binary32's range whatever
+// the norm; NaN where g is not finite.
+__device__ __forceinline__ float2 unit_factors(double squares, float eps) {
+  const double d = sqrt(squares) + (double)eps;
+  if (d == 0.0) return make_float2(0.0f, 0.0f);
+  if (!(d <= 1.0e300)) return make_float2(NAN, NAN);
+  const int e = ilogb(d) / 2;
+  return make_float2((float)ldexp(1.0, -e), (float)((double)kUnit / d * ldexp(1.0, e)));
+}
+
+// Sums of squares, a double per block.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ InputArgs a) {
   __shared__ double s[8];
@@ -488,18 +513,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
     const int64_t r = w / segs;
     float v[8];
     get8<DT, VEC>(v, a, r, (w - r * segs) * 256 + lane * 8);
-    float top = 0.0f, q = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      top = fmaxf(top, fabsf(v[e]));
-      q = fmaf(v[e], v[e], q);
-    }
-    if (top == 0.0f || (top > 0x1p-50f && top < 0x1p60f)) {
-      sum += (double)q;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += (double)v[e] * (double)v[e];
-    }
+    sum += sum_squares(v);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -512,8 +526,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   }
 }
 
-// kUnit / (|g| + eps) as two factors, each inside binary32's range whatever
-// the norm; NaN where g is not finite.
+// The factors from the blocks' sums; the whole block calls it.
 __device__ __forceinline__ float2 unit_factors(const InputArgs& a) {
   __shared__ float2 f;
   if (threadIdx.x < 32) {
@@ -521,17 +534,7 @@ __device__ __forceinline__ float2 unit_factors(const InputArgs& a) {
     for (int p = threadIdx.x; p < a.parts; p += 32) t += a.part[p];
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const double d = sqrt(t) + (double)a.eps;
-    if (threadIdx.x == 0) {
-      if (d == 0.0) {
-        f = make_float2(0.0f, 0.0f);
-      } else if (!(d <= 1.0e300)) {
-        f = make_float2(NAN, NAN);
-      } else {
-        const int e = ilogb(d) / 2;
-        f = make_float2((float)ldexp(1.0, -e), (float)((double)kUnit / d * ldexp(1.0, e)));
-      }
-    }
+    if (threadIdx.x == 0) f = unit_factors(t, a.eps);
   }
   __syncthreads();
   return f;
@@ -591,6 +594,338 @@ __global__ void __launch_bounds__(256) orth_turn_kernel(const __grid_constant__ 
       *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
     }
+  }
+}
+
+// --- narrow matrices: every step in one kernel --------------------------------------------------
+//
+// s <= 128: a CTA keeps 256 columns of X in shared memory for the whole call
+// (both planes; the layout is the same whether the sum runs along a row, in X
+// X^T, or along a column, in B X), and A, then B, in one buffer.  Several CTAs
+// (a cooperative launch) add their parts of A through L2: each adds up its
+// share of the elements, then all read A.  A barrier takes about 1.5 us.
+
+constexpr int kSmallS = 128, kSmallCols = 256, kSmallSteps = 32;
+constexpr uint32_t kBlock = 128 * 128;  // 128 rows of 64 columns, one plane
+constexpr uint32_t kXPlane = (kSmallCols / 64) * kBlock, kAPlane = 2 * kBlock;
+constexpr size_t kSmallSmem = 1024 + 2 * kXPlane + 2 * kAPlane;
+
+struct SmallArgs {
+  const void* g;
+  void* out;
+  int64_t l, ldg, ldo;
+  int s, s16, tall, dtype, odtype, steps;
+  float eps, scale;
+  double* norms;     // [CTAs]
+  float* part;       // [CTAs][s16][s16]
+  uint32_t* gram;    // [s16][s16], hi | lo << 16
+  uint32_t* arrived;
+  uint32_t* status;
+  float coefs[kSmallSteps][3];
+};
+
+__device__ __forceinline__ float get_any(const SmallArgs& a, int64_t at) {
+  return a.dtype == GC_F32 ? get<GC_F32>(a.g, at)
+         : a.dtype == GC_BF16 ? get<GC_BF16>(a.g, at)
+                              : get<GC_F16>(a.g, at);
+}
+__device__ __forceinline__ void put_any(const SmallArgs& a, int64_t at, float v) {
+  if (a.odtype == GC_F32) put<GC_F32>(a.out, at, v);
+  else if (a.odtype == GC_BF16) put<GC_BF16>(a.out, at, v);
+  else put<GC_F16>(a.out, at, v);
+}
+
+// Elements (i, j .. j + 7) of X's slice, j a multiple of 8; zero outside.
+__device__ __forceinline__ void get_slice(float (&v)[8], const SmallArgs& a, int i, int64_t j) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t c = j + e;
+    v[e] = i < a.s && c < a.l ? get_any(a, a.tall ? c * a.ldg + i : i * a.ldg + c) : 0.0f;
+  }
+}
+
+// Place of 16 bytes (row i, columns 8 c ..) in a plane of blocks of 64 columns.
+__device__ __forceinline__ uint32_t chunk_at(int i, int c) {
+  return (uint32_t)(c >> 3) * kBlock + (uint32_t)i * 128u + (uint32_t)(((c ^ i) & 7) << 4);
+}
+__device__ __forceinline__ void put_planes(uint32_t at, uint32_t plane, const float (&v)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) split2(v[2 * e], v[2 * e + 1], h[e], l[e]);
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]),
+               "r"(h[2]), "r"(h[3])
+               : "memory");
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + plane), "r"(l[0]), "r"(l[1]),
+               "r"(l[2]), "r"(l[3])
+               : "memory");
+}
+
+// Every CTA of the grid is here, and what it wrote is visible; false when the
+// wait ran out.
+__device__ __forceinline__ bool grid_barrier(const SmallArgs& a, uint32_t& target) {
+  __shared__ uint32_t ok;
+  __syncthreads();
+  target += gridDim.x;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(a.arrived, 1u);
+    const long long t0 = clock64();
+    uint32_t n;
+    do {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(a.arrived) : "memory");
+    } while (n < target && clock64() - t0 < kWaitCycles);
+    ok = n >= target;
+  }
+  __syncthreads();
+  return ok != 0u;
+}
+
+// The MMAs of a product: `blocks` blocks of 64 of the sum (the last of `tail`
+// 16s), each into an accumulator of its own, 512 / accumulators columns apart.
+template <bool MN>
+__device__ __forceinline__ void small_product(uint32_t tmem, uint32_t cols, uint32_t a_at,
+                                              uint32_t a_plane, uint32_t b_at, uint32_t b_plane,
+                                              int sixteens, uint32_t idesc) {
+  using namespace sm100;
+  const uint64_t da = smem_desc_sw128(a_at, 16, 1024);
+  const uint64_t db = smem_desc_sw128(b_at, MN ? kBlock : 16, 1024);
+  const uint32_t hi = (uint32_t)(da >> 32), a0 = (uint32_t)da, b0 = (uint32_t)db;
+  // 16 of the sum: 32 bytes of a row, every 64 the next block; or 16 rows
+  auto a_step = [](int k) { return ((uint32_t)(k >> 2) * kBlock + (uint32_t)(k & 3) * 32u) >> 4; };
+  auto b_step = [&](int k) { return MN ? ((uint32_t)k * 2048u) >> 4 : a_step(k); };
+  for (int k0 = 0; k0 < sixteens; k0 += 4) {
+    const uint32_t d = tmem + (uint32_t)(k0 >> 2) * cols;
+    const int k1 = min(k0 + 4, sixteens);
+    for (int k = k0; k < k1; ++k)
+      mma_f16_one(d, a0 + (a_plane >> 4) + a_step(k), b0 + b_step(k), hi, idesc, k > k0);
+    for (int k = k0; k < k1; ++k)
+      mma_f16_one(d, a0 + a_step(k), b0 + (b_plane >> 4) + b_step(k), hi, idesc, 1u);
+    for (int k = k0; k < k1; ++k) mma_f16_one(d, a0 + a_step(k), b0 + b_step(k), hi, idesc, 1u);
+  }
+}
+
+__global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constant__ SmallArgs a) {
+  using namespace sm100;
+  extern __shared__ unsigned char small_smem[];
+  __shared__ uint64_t done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ double norm_part[8];
+  __shared__ float2 factors;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t xs = (smem_u32(small_smem) + 1023u) & ~1023u, as = xs + 2 * kXPlane;
+  const int64_t c0 = (int64_t)blockIdx.x * kSmallCols;
+  const int cols = (int)min((int64_t)kSmallCols, a.l - c0);
+  const int x16 = (cols + 15) / 16, xpad = x16 * 16;
+  const uint32_t row0 = (uint32_t)(warp & 3) * 32u;
+  const int i = (int)row0 + lane, half = warp >> 2;
+  const bool mine = i < a.s16;
+  uint32_t target = 0, phase = 0;
+  bool ok = true;
+  if (threadIdx.x == 0) {
+    mbar_init(&done, 1);
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // the slice's sum of squares
+  double sum = 0.0;
+  const int chunks = xpad / 8, rows16 = a.s16;
+  auto place = [&](int w, int& r, int& c) {
+    // neighbouring lanes along the axis that is contiguous in memory
+    if (a.tall) {
+      r = w % rows16;
+      c = w / rows16;
+    } else {
+      c = w % chunks;
+      r = w / chunks;
+    }
+  };
+  for (int w = threadIdx.x; w < rows16 * chunks; w += 256) {
+    int r, c;
+    place(w, r, c);
+    float v[8];
+    get_slice(v, a, r, c0 + c * 8);
+    sum += sum_squares(v);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) norm_part[warp] = sum;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      sum = 0.0;
+      for (int w = 0; w < 8; ++w) sum += norm_part[w];
+      a.norms[blockIdx.x] = sum;
+    }
+    ok = grid_barrier(a, target);
+  }
+  if (warp == 0) {
+    sum = 0.0;
+    if (gridDim.x > 1)
+      for (int p = lane; p < (int)gridDim.x; p += 32) sum += __ldcg(a.norms + p);
+    else if (lane < 8)
+      sum = norm_part[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) factors = unit_factors(sum, a.eps);
+  }
+  __syncthreads();
+  const float2 f = factors;
+  for (int w = threadIdx.x; w < rows16 * chunks; w += 256) {
+    int r, c;
+    place(w, r, c);
+    float v[8];
+    get_slice(v, a, r, c0 + c * 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = r < a.s && c0 + c * 8 + e < a.l ? in_units(v[e], f) : 0.0f;
+    put_planes(xs + chunk_at(r, c), kXPlane, v);
+  }
+
+  auto idesc = [](int n, bool mn) {
+    return (1u << 4) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+  };
+  // Operands are in place; issues a product and waits for it.
+  auto multiply = [&](int what) {
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0 && elect_one()) {
+      const int s = a.s16 / 16;
+      if (what == kGram)
+        small_product<false>(tmem, 128, xs, kXPlane, xs, kXPlane, x16, idesc(a.s16, false));
+      else if (what == kPoly)
+        small_product<false>(tmem, 128, as, kAPlane, as, kAPlane, s, idesc(a.s16, false));
+      else
+        small_product<true>(tmem, 256, as, kAPlane, xs, kXPlane, s, idesc(xpad, true));
+      mma_commit(&done);
+    }
+    __syncwarp();
+    if (!mbar_wait(&done, phase, kWaitCycles)) ok = false;
+    phase ^= 1u;
+    tc_fence_after_sync();
+  };
+  // 16 columns from c on of this thread's row, from `parts` accumulators.
+  auto take = [&](float (&v)[16], int c, int parts, uint32_t apart) {
+    tmem_ld16(tmem + (row0 << 16) + c, v);
+    for (int p = 1; p < parts; ++p) {
+      float w[16];
+      tmem_ld16(tmem + (row0 << 16) + p * apart + c, w);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] += w[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kUnit;
+  };
+  auto store16 = [&](uint32_t at, uint32_t plane, int c, const float (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = v[h * 8 + e];
+      put_planes(at + chunk_at(i, (c >> 3) + h), plane, u);
+    }
+  };
+
+  const int s_parts = (a.s16 + 63) / 64;
+  for (int step = 0; step < a.steps && ok; ++step) {
+    multiply(kGram);
+    for (int c = half * 16; c < a.s16; c += 32) {
+      float v[16];
+      take(v, c, (x16 + 3) / 4, 128);
+      if (!mine) continue;
+      if (gridDim.x == 1) {
+        store16(as, kAPlane, c, v);
+      } else {
+        float* p = a.part + ((int64_t)blockIdx.x * a.s16 + c) * a.s16 + i;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) __stcg(p + e * a.s16, v[e]);
+      }
+    }
+    if (gridDim.x > 1) {
+      const int all = a.s16 * a.s16;
+      if (!grid_barrier(a, target)) ok = false;
+      for (int e = blockIdx.x * 256 + threadIdx.x; e < all; e += gridDim.x * 256) {
+        float v = 0.0f;
+#pragma unroll 8
+        for (int p = 0; p < (int)gridDim.x; ++p) v += __ldcg(a.part + (int64_t)p * all + e);
+        uint32_t h, l;
+        split2(v, 0.0f, h, l);
+        __stcg(a.gram + e, (h & 0xFFFFu) | (l << 16));
+      }
+      if (!grid_barrier(a, target)) ok = false;
+      for (int q = threadIdx.x; q < all / 8; q += 256) {
+        const uint4 u = __ldcg(reinterpret_cast<const uint4*>(a.gram) + 2 * q);
+        const uint4 w = __ldcg(reinterpret_cast<const uint4*>(a.gram) + 2 * q + 1);
+        const int r = q * 8 / a.s16, c = q * 8 - r * a.s16;
+        const uint32_t at = as + chunk_at(r, c >> 3);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                     "r"(__byte_perm(u.x, u.y, 0x5410)), "r"(__byte_perm(u.z, u.w, 0x5410)),
+                     "r"(__byte_perm(w.x, w.y, 0x5410)), "r"(__byte_perm(w.z, w.w, 0x5410))
+                     : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + kAPlane),
+                     "r"(__byte_perm(u.x, u.y, 0x7632)), "r"(__byte_perm(u.z, u.w, 0x7632)),
+                     "r"(__byte_perm(w.x, w.y, 0x7632)), "r"(__byte_perm(w.z, w.w, 0x7632))
+                     : "memory");
+      }
+    }
+    multiply(kPoly);
+    const float ca = a.coefs[step][0] * kUnit, cb = a.coefs[step][1], cc = a.coefs[step][2];
+    for (int c = half * 16; c < a.s16; c += 32) {
+      float v[16];
+      take(v, c, s_parts, 128);
+      if (!mine) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = as + chunk_at(i, (c >> 3) + h);
+        const uint4 hi = lds_u128(at), lo = lds_u128(at + kAPlane);
+        const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 p = join2(hw[e], lw[e]);
+          const int k = h * 8 + 2 * e;
+          v[k] = fmaf(cc, v[k], cb * p.x);
+          v[k + 1] = fmaf(cc, v[k + 1], cb * p.y);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (c + e == i) v[e] += ca;
+      store16(as, kAPlane, c, v);
+    }
+    multiply(kApply);
+    const bool last = step + 1 == a.steps;
+    ok = !__syncthreads_or(!ok);  // a wait that ran out ends the call for every thread
+    for (int c = half * 16; c < xpad; c += 32) {
+      float v[16];
+      take(v, c, s_parts, 256);
+      if (!mine) continue;
+      if (!last) {
+        store16(xs, kXPlane, c, v);
+      } else if (i < a.s) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t j = c0 + c + e;
+          if (j < a.l)
+            put_any(a, a.tall ? j * a.ldo + i : i * a.ldo + j,
+                    __fmul_rn(v[e] * (1.0f / kUnit), a.scale));
+        }
+      }
+    }
+  }
+  if (!ok) atomicOr(a.status, kStatusWaitTimeout);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -694,12 +1029,45 @@ gc_status input(gc_ctx* ctx, const InputArgs& a) {
   return e == cudaSuccess ? GC_OK : GC_ERR_CUDA;
 }
 
+// Scratch of the narrow kernel: norms and the barrier's counter, A, its parts.
+int64_t small_bytes(int64_t s, int64_t l) {
+  const int64_t s16 = round_up(s, 16), ctas = ceil_div(l, (int64_t)kSmallCols);
+  return round_up(ctas * 8, 256) + 256 + (1 + ctas) * s16 * s16 * 4;
+}
+
+gc_status launch_small(gc_ctx* ctx, SmallArgs& a, char* at) {
+  static uint64_t devices = 0;
+  if (!allow_smem(ctx, orth_small_kernel, (int)kSmallSmem, devices)) return GC_ERR_CUDA;
+  const int64_t ctas = ceil_div(a.l, (int64_t)kSmallCols);
+  a.s16 = (int)round_up(a.s, 16);
+  a.status = ctx->ws.status;
+  a.norms = reinterpret_cast<double*>(at);
+  at += round_up(ctas * 8, 256);
+  a.arrived = reinterpret_cast<uint32_t*>(at);
+  at += 256;
+  a.gram = reinterpret_cast<uint32_t*>(at);
+  at += (int64_t)a.s16 * a.s16 * 4;
+  a.part = reinterpret_cast<float*>(at);
+  if (ctas > 1 && cudaMemsetAsync(a.arrived, 0, 4, ctx->stream) != cudaSuccess) return GC_ERR_CUDA;
+  LaunchScope L(ctx, GC_PHASE_ORTH_PRODUCT);
+  void* args[] = {&a};
+  const cudaError_t e =
+      ctas > 1 ? cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(orth_small_kernel),
+                                             dim3((unsigned)ctas), dim3(256), args, kSmallSmem,
+                                             ctx->stream)
+               : cudaLaunchKernel(reinterpret_cast<const void*>(orth_small_kernel), dim3(1),
+                                  dim3(256), args, kSmallSmem, ctx->stream);
+  return e == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+}
+
 }  // namespace
 
 int64_t orth_scratch_bytes(int64_t m, int64_t n) {
   if (m == 0 || n == 0) return 0;
   const int64_t s = std::min(m, n), l = std::max(m, n);
-  return kMaxParts * 8 + 2 * planes_bytes(s, l) + 2 * planes_bytes(s, s);
+  int64_t bytes = kMaxParts * 8 + 2 * planes_bytes(s, l) + 2 * planes_bytes(s, s);
+  if (s <= kSmallS) bytes = std::max(bytes, small_bytes(s, l));
+  return bytes;
 }
 
 gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n, int64_t ldg,
@@ -708,6 +1076,23 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
   if (m == 0 || n == 0) return GC_OK;
   const int64_t s = std::min(m, n), l = std::max(m, n);
   char* at = static_cast<char*>(scratch);
+  if (s <= kSmallS && ceil_div(l, (int64_t)kSmallCols) <= ctx->num_sms && steps <= kSmallSteps) {
+    SmallArgs a{};
+    a.g = g;
+    a.out = out;
+    a.l = l;
+    a.ldg = ldg;
+    a.ldo = ldo;
+    a.s = (int)s;
+    a.tall = m > n;
+    a.dtype = dtype;
+    a.odtype = odtype;
+    a.steps = steps;
+    a.eps = eps;
+    a.scale = scale;
+    for (int k = 0; k < 3 * steps; ++k) a.coefs[k / 3][k % 3] = coefs[k];
+    return launch_small(ctx, a, at);
+  }
   InputArgs in{};
   in.part = reinterpret_cast<double*>(at);
   at += kMaxParts * 8;

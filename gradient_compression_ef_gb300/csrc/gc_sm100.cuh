@@ -418,6 +418,20 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint32_t a_lo, uin
       : "memory");
 }
 
+// The same within one CTA: A's 128 rows, B and D its own.
+__device__ __forceinline__ void mma_f16_one(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                            uint32_t desc_hi, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrives once on the barrier at this offset in both CTAs when every pair
 // operation this thread issued before has completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {

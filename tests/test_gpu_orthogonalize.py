@@ -302,3 +302,19 @@ def test_refusals(gc, ctx):
         with pytest.raises(gc.GCError) as e:
             gc.orthogonalize(bare, g, g)
         assert e.value.status == gc.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("m,n,steps", [(128, 38912, 2), (128, 38913, 2), (129, 257, 2), (20, 90, 32), (20, 90, 33)])
+def test_both_sides_of_the_narrow_kernel(gc, m, n, steps):
+    """Narrow matrices run in one kernel up to a width, a length and a number of steps."""
+    import torch
+    coefs = [(1.5, -0.5, 0.0)] * steps
+    with gc.Context(0) as c:
+        c.reserve_scratch(gc.orthogonalize_scratch_bytes(m, n))
+        g = update(13, m, n)
+        for x in (g, g.t().contiguous()):
+            out = torch.empty_like(x)
+            gc.orthogonalize(c, x, out, steps=steps, coefs=coefs)
+            want, err = reference(x, coefs, 1e-7, 1.0)
+            check(out, want, err, "f32")
+        c.check()
