@@ -33,6 +33,10 @@ struct RmsArgs {
   int64_t codes_pitch, scales_pitch, part_pitch;
   float eps;
   int ptype, accumulate;
+  // ring of stages (set at launch)
+  uint32_t* status;
+  uint32_t second_at, third_at, scales_at, stage_bytes;  // places within a stage
+  int stages;
 };
 
 // A unit's part of a checkpoint, column c on; every lane of the warp calls it.
@@ -176,6 +180,170 @@ __global__ void __launch_bounds__(1024)
                       a.codes_pitch);
     }
   }
+}
+
+// --- rows through a ring of stages ---------------------------------------------------------------
+
+constexpr int kMaxStages = 6;
+constexpr int kCols = 16;          // columns per thread
+constexpr int kForwardRegs = 64;   // 32 warps per SM
+constexpr int kBackwardRegs = 72;  // 28 warps per SM
+
+// One thread's part: row `row` into a stage.  Forward: x, res.  BACK: dy,
+// dres, then h or its checkpoint.
+template <int DT, bool BACK, bool CKPT>
+__device__ __forceinline__ void fill_stage(const RmsArgs& a, int64_t row, char* stage,
+                                           uint64_t* full) {
+  using namespace sm100;
+  const char* r0 = BACK ? a.dy + row * a.dypitch : a.x + row * a.xpitch;
+  const char* r1 = BACK ? a.dres + row * a.drespitch : a.res + row * a.respitch;
+  const char* r2 = a.x + row * a.xpitch;
+  const bool second = BACK ? a.dres != nullptr : a.res != nullptr;
+  const uint32_t n0 = bulk_size<DT>(r0, a.row_bytes, BACK ? a.dyend : a.xend, stage);
+  uint32_t n1 = 0, n2 = 0, n3 = 0;
+  if (second)
+    n1 = bulk_size<DT>(r1, a.row_bytes, BACK ? a.dresend : a.resend, stage + a.second_at);
+  if (BACK && CKPT) {
+    n2 = (uint32_t)a.codes_pitch;
+    n3 = (uint32_t)a.scales_pitch;
+  } else if (BACK) {
+    n2 = bulk_size<DT>(r2, a.row_bytes, a.xend, stage + a.third_at);
+  }
+  mbar_arrive_expect_tx(full, n0 + n1 + n2 + n3);
+  auto from = [](const char* r) { return r - (reinterpret_cast<uintptr_t>(r) & 15u); };
+  if (n0) bulk_load(stage, from(r0), n0, full);
+  if (n1) bulk_load(stage + a.second_at, from(r1), n1, full);
+  if (BACK && CKPT) {
+    bulk_load(stage + a.third_at, a.codes + row * a.codes_pitch, n2, full);
+    bulk_load(stage + a.scales_at, a.scales + row * a.scales_pitch, n3, full);
+  } else if (n2) {
+    bulk_load(stage + a.third_at, from(r2), n2, full);
+  }
+}
+
+// The producer warp: copies the block's rows, stage after stage, as the row's
+// warps hand the stages back.
+template <int DT, bool BACK, bool CKPT>
+__device__ __forceinline__ bool produce(const RmsArgs& a, char* stages, uint64_t* full,
+                                        uint64_t* empty) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    RingPos ring;
+    int filled = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ring.next(a.stages)) {
+      if (filled < a.stages) {
+        ++filled;
+      } else {
+        if (!sm100::mbar_wait(&empty[ring.st], ring.ph ^ 1u, kWaitCycles)) {
+          ok = false;
+          break;
+        }
+        // the warps read the stage through the generic proxy, the copy
+        // refills it through the asynchronous one
+        sm100::fence_proxy_async_smem();
+      }
+      fill_stage<DT, BACK, CKPT>(a, row, stages + ring.st * a.stage_bytes, &full[ring.st]);
+    }
+  }
+  return ok;
+}
+
+// The ring's barriers and the sums' slots; the whole block calls it.
+__device__ __forceinline__ void ring_begin(const RmsArgs& a, float (&slot)[2][36], uint64_t* full,
+                                           uint64_t* empty) {
+  for (int i = threadIdx.x; i < 72; i += blockDim.x) slot[i / 36][i % 36] = 0.0f;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      sm100::mbar_init(&full[i], 1);
+      sm100::mbar_init(&empty[i], (blockDim.x - 32) / 32);
+    }
+    sm100::mbar_fence_init();
+  }
+  __syncthreads();
+}
+
+// Where in its 16 bytes a row begins.
+__device__ __forceinline__ uint32_t shift_of(const char* p, int64_t pitch, int64_t row) {
+  return ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)row * (uint32_t)pitch) & 15u;
+}
+
+template <int DT, int ROWS>
+__global__ void __maxnreg__(kForwardRegs)
+    rms_forward_ring_kernel(const __grid_constant__ RmsArgs a) {
+  using namespace sm100;
+  constexpr int V = Elem<DT>::V, K = kCols / V;
+  extern __shared__ __align__(128) char stages[];
+  __shared__ __align__(16) float slot[2][36];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  const int t = threadIdx.x, nt = blockDim.x - 32;  // the last warp is the producer
+  ring_begin(a, slot, full, empty);
+  if (t >= nt) {
+    ring_end(produce<DT, false, false>(a, stages, full, empty), a.status);
+    return;
+  }
+  RowsSum<1> sum{slot, nt};
+  const uint32_t u0 = (t & ~31) * K, u1 = u0 + (t & 31);  // the warp's and the thread's first unit
+  const uint32_t base = smem_u32(stages) + u1 * 16;
+  const float inv_n = 1.0f / (float)a.cols;
+  float g[K][V];
+  // bytes of the row from the first unit on
+  const int rest = (int)min((int64_t)(1 << 30), a.row_bytes - (int64_t)u1 * 16);
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int64_t u = u1 + i * 32;
+    load_params<V>(g[i], a.gamma, a.ptype, u * V, a.cols, 1.0f);
+  }
+  bool ok = true;
+  RingPos ring;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    ok = mbar_wait(&full[ring.st], ring.ph, kWaitCycles);
+    const uint32_t stage = base + ring.st * a.stage_bytes;
+    const uint32_t mis0 = ROWS == kAnywhere ? shift_of(a.x, a.xpitch, row) : 0u;
+    const uint32_t mis1 = ROWS == kAnywhere ? shift_of(a.res, a.respitch, row) : 0u;
+    uint4 h[K];
+    float2 q = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      h[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (ROWS == kFull || rest - i * 512 > 0) {
+        h[i] = staged_unit<DT, ROWS>(stage + i * 512, mis0, rest - i * 512);
+        if (a.res)
+          h[i] = add_units<DT>(
+              h[i], staged_unit<DT, ROWS>(stage + a.second_at + i * 512, mis1, rest - i * 512));
+      }
+      q = add_squares<DT>(h[i], q);
+      keep_packed(h[i]);
+    }
+    // the warp holds its part of the row
+    __syncwarp();
+    if ((t & 31) == 0) mbar_arrive(&empty[ring.st]);
+    ring.next(a.stages);
+    if (a.h) put_units<DT, ROWS>(a.h + row * a.hpitch, u0, a.row_bytes, h);
+    if (a.codes) {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        save_unit<DT>(a.codes + row * a.codes_pitch, a.scales + row * a.scales_pitch, h[i],
+                      (int64_t)(u1 + i * 32) * V, a.codes_pitch);
+    }
+    float s[1] = {q.x + q.y};
+    sum(s, ok);
+    if (!ok) break;
+    const float rstd = rsqrtf(s[0] * inv_n + a.eps);
+    if (t == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      keep_packed(h[i]);
+      h[i] = scale_unit<DT>(h[i], rstd, g[i]);
+    }
+    if (a.y) put_units<DT, ROWS>(a.y + row * a.ypitch, u0, a.row_bytes, h);
+    if (a.ycodes) {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        save_unit<DT>(a.ycodes + row * a.codes_pitch, a.yscales + row * a.scales_pitch, h[i],
+                      (int64_t)(u1 + i * 32) * V, a.codes_pitch);
+    }
+  }
+  ring_end(ok, a.status);
 }
 
 // --- backward ------------------------------------------------------------------------------------
@@ -355,6 +523,113 @@ __global__ void __launch_bounds__(WARP ? 256 : 512)
   }
 }
 
+// The same through the ring: dy and h are read from the stage in both passes,
+// so that a thread keeps gamma and the column sums alone.
+template <int DT, bool CKPT, int ROWS>
+__global__ void __maxnreg__(kBackwardRegs)
+    rms_backward_ring_kernel(const __grid_constant__ RmsArgs a) {
+  using namespace sm100;
+  constexpr int V = Elem<DT>::V, K = kCols / V, H = V / 2;
+  extern __shared__ __align__(128) char stages[];
+  __shared__ __align__(16) float slot[2][36];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  const int t = threadIdx.x, nt = blockDim.x - 32;  // the last warp is the producer
+  ring_begin(a, slot, full, empty);
+  if (t >= nt) {
+    ring_end(produce<DT, true, CKPT>(a, stages, full, empty), a.status);
+    return;
+  }
+  RowsSum<1> sum{slot, nt};
+  const uint32_t u0 = (t & ~31) * K, u1 = u0 + (t & 31);  // the warp's and the thread's first unit
+  const uint32_t base = smem_u32(stages);
+  const float inv_n = 1.0f / (float)a.cols;
+  float g[K][V];
+  float2 acc[K][H];
+  // bytes of the row from the first unit on
+  const int rest = (int)min((int64_t)(1 << 30), a.row_bytes - (int64_t)u1 * 16);
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int64_t u = u1 + i * 32;
+    load_params<V>(g[i], a.gamma, a.ptype, u * V, a.cols, 1.0f);
+#pragma unroll
+    for (int j = 0; j < H; ++j) acc[i][j] = both(0.0f);
+  }
+  float rstd = blockIdx.x < a.rows ? __ldg(a.rstd + blockIdx.x) : 0.0f;
+  bool ok = true;
+  RingPos ring;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float next = row + gridDim.x < a.rows ? __ldg(a.rstd + row + gridDim.x) : 0.0f;
+    ok = mbar_wait(&full[ring.st], ring.ph, kWaitCycles);
+    const uint32_t stage = base + ring.st * a.stage_bytes;
+    const uint32_t mis0 = ROWS == kAnywhere ? shift_of(a.dy, a.dypitch, row) : 0u;
+    const uint32_t mis1 = ROWS == kAnywhere ? shift_of(a.dres, a.drespitch, row) : 0u;
+    const uint32_t mis2 = ROWS == kAnywhere ? shift_of(a.x, a.xpitch, row) : 0u;
+    const float2 rs = both(rstd);
+    // dy and n = h rstd of a unit (past the last column dy is 0)
+    auto get = [&](int i, float2 (&d)[H], float2 (&n)[H]) {
+      const uint32_t u = u1 + i * 32;
+      unpack2<DT>(staged_unit<DT, ROWS>(stage + u * 16, mis0, rest - i * 512), d);
+      if constexpr (CKPT) {
+        Codes<V> c;
+#pragma unroll
+        for (int w = 0; w < V / 4; ++w) c.w[w] = lds_u32(stage + a.third_at + u * V + 4 * w);
+        decode<V>(n, c, lds_u8(stage + a.scales_at + u / (kActGroup / V)));
+      } else {
+        unpack2<DT>(staged_unit<DT, ROWS>(stage + a.third_at + u * 16, mis2, rest - i * 512), n);
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) n[j] = __fmul2_rn(n[j], rs);
+    };
+    float2 q = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if (ROWS != kFull && rest - i * 512 <= 0) continue;
+      float2 d[H], n[H];
+      get(i, d, n);
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        const float2 p = __fmul2_rn(d[j], n[j]);
+        acc[i][j] = __fadd2_rn(acc[i][j], p);
+        q = __ffma2_rn(p, make_float2(g[i][2 * j], g[i][2 * j + 1]), q);
+      }
+    }
+    float s[1] = {q.x + q.y};
+    sum(s, ok);
+    if (!ok) break;
+    const float2 m = both(-s[0] * inv_n);
+    uint4 res[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      res[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (ROWS != kFull && rest - i * 512 <= 0) continue;
+      float2 d[H], n[H], r[H];
+      get(i, d, n);
+      if (a.dres)
+        unpack2<DT>(
+            staged_unit<DT, ROWS>(stage + a.second_at + (u1 + i * 32) * 16, mis1, rest - i * 512), r);
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        d[j] = __fmul2_rn(d[j], make_float2(g[i][2 * j], g[i][2 * j + 1]));
+        d[j] = __ffma2_rn(n[j], m, d[j]);
+        d[j] = a.dres ? __ffma2_rn(d[j], rs, r[j]) : __fmul2_rn(d[j], rs);
+      }
+      res[i] = pack2<DT>(d);
+    }
+    __syncwarp();
+    if ((t & 31) == 0) mbar_arrive(&empty[ring.st]);
+    ring.next(a.stages);
+    put_units<DT, ROWS>(a.y + row * a.ypitch, u0, a.row_bytes, res);
+    rstd = next;
+  }
+  ring_end(ok, a.status);
+  if (!a.dgamma) return;
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      put_sum(a, (int64_t)(u1 + i * 32) * V + j, j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x);
+}
+
 // Wider rows: two passes over the inputs, the column sums in the block's
 // partial row (each place is one thread's).
 template <int DT, bool CKPT, bool ALIGNED>
@@ -462,8 +737,66 @@ Shape pick(int64_t units, int64_t rows, int sms, int most, int deep, int per_sm)
   return s;
 }
 
+// Rows that go through the ring: more of them than SMs (a row per block is
+// loaded sooner by its own threads), not narrower than a block of 160 threads
+// or so, not wider than a block's registers hold, two stages or more in shared
+// memory.
+struct RingPlan {
+  int threads, per_sm;  // threads of the rows; 0: not this way
+  unsigned smem;
+};
+
+// Dynamic shared memory that each of n blocks of an SM may use: 228 KB less
+// the system's 1 KB a block and the kernels' static part.
+constexpr int64_t kStaticSmem =
+    (2 * 36 * sizeof(float) + 2 * kMaxStages * sizeof(uint64_t) + 127) / 128 * 128;
+int64_t block_smem(int n) { return 228 * 1024 / n / 128 * 128 - 1024 - kStaticSmem; }
+
+RingPlan plan_ring(const gc_ctx* ctx, RmsArgs& a, int dtype, bool back) {
+  RingPlan p{};
+  const int warps = 65536 / (32 * (back ? kBackwardRegs : kForwardRegs));  // per SM
+  const int64_t c = ckpt_codes_pitch(a.cols);
+  if (a.rows <= ctx->num_sms || c * elem_size(dtype) <= 2048 ||
+      c > (std::min(warps, 32) - 1) * 32 * kCols)
+    return p;
+  const int64_t row = round_up(a.row_bytes + 30, 128);  // with a shifted start
+  int64_t bytes = row;
+  a.second_at = (uint32_t)bytes;
+  if (back ? a.dres != nullptr : a.res != nullptr) bytes += row;
+  a.third_at = (uint32_t)bytes;
+  if (back) bytes += a.codes ? round_up(c, 128) : row;
+  a.scales_at = (uint32_t)bytes;
+  if (back && a.codes) bytes += round_up(a.scales_pitch, 128);
+  a.stage_bytes = (uint32_t)bytes;
+  const int threads = (int)round_up(ceil_div(c, (int64_t)kCols), 32);
+  p.per_sm = warps / (threads / 32 + 1);
+  while (p.per_sm > 1 && 2 * bytes > block_smem(p.per_sm)) --p.per_sm;
+  a.stages = (int)std::min<int64_t>(kMaxStages, block_smem(p.per_sm) / bytes);
+  if (a.stages < 2) return p;
+  a.status = ctx->ws.status;
+  p.threads = threads;
+  p.smem = (unsigned)(a.stages * bytes);
+  return p;
+}
+
+template <auto Kernel>
+void launch_ring(gc_ctx* ctx, const RmsArgs& a, const RingPlan& p, unsigned grid) {
+  static uint64_t devices = 0;
+  if (!allow_smem(ctx, Kernel, (int)block_smem(1), devices)) return;  // the launch's error says so
+  Kernel<<<grid, p.threads + 32, p.smem, ctx->stream>>>(a);
+}
+
 template <int DT, bool ALIGNED>
-void forward(gc_ctx* ctx, const RmsArgs& a) {
+void forward(gc_ctx* ctx, RmsArgs& a) {
+  if (const RingPlan p = plan_ring(ctx, a, DT, false); p.threads) {
+    LaunchScope L(ctx, GC_PHASE_RMS_FORWARD);
+    const unsigned g = (unsigned)std::min<int64_t>(a.rows, (int64_t)ctx->num_sms * p.per_sm);
+    if (!ALIGNED) launch_ring<rms_forward_ring_kernel<DT, kAnywhere>>(ctx, a, p, g);
+    else if (a.cols == (int64_t)p.threads * kCols)
+      launch_ring<rms_forward_ring_kernel<DT, kFull>>(ctx, a, p, g);
+    else launch_ring<rms_forward_ring_kernel<DT, kEnds>>(ctx, a, p, g);
+    return;
+  }
   const Shape s = pick(ceil_div(a.row_bytes, (int64_t)16), a.rows, ctx->num_sms, 1024, 2, 1024);
   LaunchScope L(ctx, GC_PHASE_RMS_FORWARD);
   const auto kernel =
@@ -477,11 +810,20 @@ void forward(gc_ctx* ctx, const RmsArgs& a) {
 }
 
 template <int DT, bool CKPT, bool ALIGNED>
-gc_status backward(gc_ctx* ctx, const RmsArgs& a) {
+gc_status backward(gc_ctx* ctx, RmsArgs& a) {
   Shape s = pick(ceil_div(a.row_bytes, (int64_t)16), a.rows, ctx->num_sms, 512, 4, 512);
   s.grid = (unsigned)std::min<int64_t>(s.grid, kMaxParts);
   const size_t smem = s.warp ? (size_t)8 * s.u * 32 * Elem<DT>::V * 4 : 0;
-  {
+  if (const RingPlan p = plan_ring(ctx, a, DT, true); p.threads) {
+    LaunchScope L(ctx, GC_PHASE_RMS_BACKWARD);
+    s.wide = false;
+    s.grid = (unsigned)std::min<int64_t>(
+        {a.rows, (int64_t)ctx->num_sms * p.per_sm, kMaxParts});
+    if (!ALIGNED) launch_ring<rms_backward_ring_kernel<DT, CKPT, kAnywhere>>(ctx, a, p, s.grid);
+    else if (a.cols == (int64_t)p.threads * kCols)
+      launch_ring<rms_backward_ring_kernel<DT, CKPT, kFull>>(ctx, a, p, s.grid);
+    else launch_ring<rms_backward_ring_kernel<DT, CKPT, kEnds>>(ctx, a, p, s.grid);
+  } else {
     LaunchScope L(ctx, GC_PHASE_RMS_BACKWARD);
     const auto kernel =
         s.wide ? rms_backward_wide_kernel<DT, CKPT, ALIGNED>
