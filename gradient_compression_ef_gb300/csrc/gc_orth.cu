@@ -44,7 +44,13 @@ constexpr uint32_t kABytes = 128 * kBK * 2;  // one plane, one CTA
 constexpr int kSegBlocks = 1;        // blocks per accumulator
 constexpr int kReadWarps = 8, kProducerWarp = 8, kIssuerWarp = 9;
 constexpr int kThreads = 384;
+// Registers a thread: as launched, and (tiles of 256 columns) of the read-out
+// warps and of the other four; 8 * 232 + 4 * 40 = 12 * 168.
+constexpr int kLaunchRegs = 168, kReadRegs = 232, kOtherRegs = 40;
+static_assert(8 * kReadRegs + 4 * kOtherRegs <= 12 * kLaunchRegs);
 constexpr long long kWaitCycles = 4000000000ll;  // bound on each wait: ~2 s
+constexpr uint32_t kWarpStage = 4096;  // of a read-out warp, for its stores
+constexpr int kMaxPartsOfTile = 4, kMaxPairs = 80;
 constexpr float kUnit = 4096.0f;     // planes hold v * kUnit
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
@@ -56,13 +62,18 @@ struct Shape {
   static constexpr uint32_t kStage = 2 * (kABytes + kBBytes);
   static constexpr int kStages = TN == 256 ? 3 : 4;
   static constexpr uint32_t kCols = 2 * TN;                // tensor memory: two accumulators
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 8 * (2 * kStages + 5) + 16;
+  static constexpr size_t kSmem =
+      1024 + (size_t)kStages * kStage + kReadWarps * kWarpStage + 8 * (2 * kStages + 5) + 16;
 };
 
 struct ProductArgs {
   int64_t rows, cols;      // of the result
   int64_t sum;             // length of the sum
-  int64_t row_tiles, col_tiles, tiles;
+  int64_t row_tiles, col_tiles;
+  int64_t whole, items;    // tiles computed whole; all items of work
+  int parts;               // the tiles behind them are computed in so many parts
+  float* part;             // sums of the parts, [split tile][part][CTA of the pair][..]
+  uint32_t* arrived;       // [split tile][CTA of the pair][warp], zero before and after
   uint16_t* dst;           // planes of the result, plane_size apart
   const uint16_t* prev;    // kPoly: A's planes
   int64_t pitch, plane_size;  // elements
@@ -70,12 +81,12 @@ struct ProductArgs {
   void* out;               // kLast
   int64_t ldo;
   float scale;
-  int odtype, transposed;
+  int odtype, transposed, out_vec;
   uint32_t* status;
 };
 
 struct Smem {
-  uint32_t stage0;
+  uint32_t stage0, out0;
   uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
   uint32_t* tmem_slot;
 };
@@ -86,7 +97,8 @@ __device__ __forceinline__ Smem carve(unsigned char* base) {
   const uint32_t at = (sm100::smem_u32(base) + 1023u) & ~1023u;
   unsigned char* p = base + (at - sm100::smem_u32(base));
   s.stage0 = at;
-  s.full = reinterpret_cast<uint64_t*>(p + S::kStages * S::kStage);
+  s.out0 = at + S::kStages * S::kStage;
+  s.full = reinterpret_cast<uint64_t*>(p + S::kStages * S::kStage + kReadWarps * kWarpStage);
   s.empty = s.full + S::kStages;
   s.acc_full = s.empty + S::kStages;
   s.acc_empty = s.acc_full + 2;
@@ -148,84 +160,271 @@ __device__ __forceinline__ void put(void* out, int64_t at, float v) {
   else static_cast<__half*>(out)[at] = __float2half_rn(v);
 }
 
-// N columns of one row of the result.
-template <int DT, int N>
-__device__ __forceinline__ void put_out(const ProductArgs& a, int64_t i, int64_t j,
-                                        const float* v) {
-#pragma unroll
-  for (int c = 0; c < N; ++c)
-    if (j + c < a.cols)
-      put<DT>(a.out, a.transposed ? (j + c) * a.ldo + i : i * a.ldo + j + c,
-              __fmul_rn(v[c], a.scale));
+// Item t of the work: a tile and the blocks [k0, k1) of its sum.  Tiles go
+// round by round; those that would leave most pairs idle in a last round are
+// computed in parts of the sum.
+template <int TN, bool SYM>
+struct Item {
+  int64_t i, j, split;  // split: which of the tiles in parts, or -1
+  int32_t k0, k1;
+  int part;
+  __device__ __forceinline__ Item(const ProductArgs& a, int64_t t, int32_t blocks) {
+    split = -1;
+    part = 0;
+    k0 = 0;
+    k1 = blocks;
+    if (t >= a.whole) {
+      if (a.parts > 1) {
+        split = (t - a.whole) / a.parts;
+        part = (int)(t - a.whole - split * a.parts);
+        k0 = blocks * part / a.parts;
+        k1 = blocks * (part + 1) / a.parts;
+        t = a.whole + split;
+      }
+    }
+    tile_place<TN, SYM>(a, t, i, j);
+  }
+};
+
+// Where 16 bytes c of row r lie in a warp's stage of 32 rows of 128 bytes: no
+// bank is hit twice when lanes write a row each, when 8 lanes read a row, and
+// when rows 8 q + 2 m, 8 q + 2 m + 1 (q = 0 .. 3) are read as a matrix.
+__device__ __forceinline__ uint32_t staged(uint32_t stage, int r, int c) {
+  return stage + (uint32_t)r * 128u + (uint32_t)((c ^ (r & 7) ^ ((r >> 3) << 1)) << 4);
+}
+__device__ __forceinline__ void sts_u128(uint32_t at, uint32_t x, uint32_t y, uint32_t z,
+                                         uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+// Column lane / 4 of 8, rows 8 (lane % 4) .. + 7 of the stage's 32, of the
+// fp16 elements of 16 bytes c.
+__device__ __forceinline__ uint4 staged_column(uint32_t stage, int c) {
+  const int lane = threadIdx.x & 31;
+  // lane 8 m + k names row k of matrix m
+  const int m = lane >> 3, k = lane & 7;
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(staged(stage, (k >> 1) * 8 + 2 * m + (k & 1), c))
+               : "memory");
+  return v;
 }
 
-// A thread's N columns from j0 on of row i, from their sums.
-template <int MODE, int TN>
-__device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[TN / 2], int64_t i,
-                                           int64_t j0) {
-  constexpr int N = TN / 2;
+// Elements [lo, hi) of 8 fp16 ones.
+__device__ __forceinline__ void store_halves(uint16_t* p, const uint4& r, int lo, int hi) {
+  store_some<GC_F16>(reinterpret_cast<char*>(p), r, lo, hi);
+}
+
+// One plane of 64 columns from j on of the warp's 32 rows from i on, staged,
+// and of a symmetric result their mirror image.
+template <bool SYM>
+__device__ __forceinline__ void store_plane(const ProductArgs& a, uint16_t* dst, uint32_t stage,
+                                            int64_t i, int64_t j) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t r = i + k * 4 + (lane >> 3), c = j + (lane & 7) * 8;
+    if (r >= a.rows || c >= a.cols || (SYM && c + 7 < r)) continue;
+    const uint4 v = sm100::lds_u128(staged(stage, k * 4 + (lane >> 3), lane & 7));
+    uint16_t* p = dst + r * a.pitch + c;
+    // rows of planes are padded to whole groups of 8
+    if (!SYM || c >= r) *reinterpret_cast<uint4*>(p) = v;
+    else store_halves(p, v, (int)(r - c), 8);  // the group that the diagonal cuts
+  }
+  if (!SYM) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint4 v = staged_column(stage, k);
+    const int64_t c = j + k * 8 + (lane >> 2), r = i + (lane & 3) * 8;
+    if (c >= a.cols || r >= c) continue;
+    uint16_t* p = dst + c * a.pitch + r;
+    if (r + 7 < c) *reinterpret_cast<uint4*>(p) = v;
+    else store_halves(p, v, 0, (int)(c - r));
+  }
+}
+
+// A warp's part of an output of type DT, rows from i, columns from j on, by
+// rows: through the stage, 128 bytes of each row at a time.
+template <int DT, int N>
+__device__ __forceinline__ void store_rows(const ProductArgs& a, const float (&v)[N],
+                                           uint32_t stage, int64_t i, int64_t j) {
+  constexpr int E = elem_size(DT), C = 128 / E, V = Elem<DT>::V;
+  using T = typename Elem<DT>::T;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c0 = 0; c0 < N; c0 += C) {
+    if (j + c0 >= a.cols) break;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float u[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) u[e] = __fmul_rn(v[c0 + k * V + e], a.scale);
+      const uint4 r = Elem<DT>::pack(u);
+      sts_u128(staged(stage, lane, k), r.x, r.y, r.z, r.w);
+    }
+    __syncwarp();
+    if (a.out_vec) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t r = i + k * 4 + (lane >> 3), c = j + c0 + (lane & 7) * V;
+        if (r >= a.rows || c >= a.cols) continue;
+        const uint4 q = sm100::lds_u128(staged(stage, k * 4 + (lane >> 3), lane & 7));
+        char* p = reinterpret_cast<char*>(static_cast<T*>(a.out) + r * a.ldo + c);
+        if (c + V <= a.cols) *reinterpret_cast<uint4*>(p) = q;
+        else store_some<DT>(p, q, 0, (int)(a.cols - c));
+      }
+    } else {
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        if (i + r >= a.rows) break;
+        T* p = static_cast<T*>(a.out) + (i + r) * a.ldo + j + c0;
+#pragma unroll
+        for (int h = 0; h < C / 32; ++h) {
+          const int c = h * 32 + lane;
+          if (j + c0 + c >= a.cols) continue;
+          const uint32_t at = staged(stage, r, c / V) + (uint32_t)(c % V) * E;
+          if constexpr (E == 4) {
+            reinterpret_cast<uint32_t*>(p)[c] = sm100::lds_u32(at);
+          } else {
+            uint16_t q;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(q) : "r"(at) : "memory");
+            reinterpret_cast<uint16_t*>(p)[c] = q;
+          }
+        }
+      }
+    }
+  }
+}
+template <int DT, int N>
+__device__ __forceinline__ void store_result(const ProductArgs& a, const float (&v)[N],
+                                             uint32_t stage, int64_t i, int64_t j) {
+  if (!a.transposed) {
+    store_rows<DT, N>(a, v, stage, i, j);
+    return;
+  }
+  const int64_t r = i + (threadIdx.x & 31);
+  if (r >= a.rows) return;
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    if (j + c < a.cols) put<DT>(a.out, (j + c) * a.ldo + r, __fmul_rn(v[c], a.scale));
+}
+
+// A warp's part of a tile, 32 rows from i, N columns from j on, from the sums.
+template <int MODE, int N>
+__device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N], uint32_t stage,
+                                           int64_t i, int64_t j) {
   constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  const int lane = threadIdx.x & 31;
   if (i >= a.rows) return;
 #pragma unroll
   for (int c = 0; c < N; ++c) sum[c] *= MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
   if (MODE == kLast) {
-#pragma unroll
-    for (int c = 0; c < N; c += 16) {
-      if (a.odtype == GC_F32) put_out<GC_F32, 16>(a, i, j0 + c, sum + c);
-      else if (a.odtype == GC_BF16) put_out<GC_BF16, 16>(a, i, j0 + c, sum + c);
-      else put_out<GC_F16, 16>(a, i, j0 + c, sum + c);
-    }
+    if (a.odtype == GC_F32) store_result<GC_F32, N>(a, sum, stage, i, j);
+    else if (a.odtype == GC_BF16) store_result<GC_BF16, N>(a, sum, stage, i, j);
+    else store_result<GC_F16, N>(a, sum, stage, i, j);
     return;
   }
-  uint16_t* hi_row = a.dst + i * a.pitch;
 #pragma unroll
-  for (int c = 0; c < N; c += 8) {
-    const int64_t j = j0 + c;
-    if (j >= a.cols || (kSym && j + 7 < i)) continue;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = sum[c + e];
+  for (int c0 = 0; c0 < N; c0 += 64) {
+    const int64_t jc = j + c0;
+    if (jc >= a.cols || (kSym && jc + 63 < i)) continue;  // outside, or the mirror's
     if (MODE == kPoly) {
-      const uint16_t* src = a.prev + i * a.pitch + j;
-      const uint4 h = *reinterpret_cast<const uint4*>(src);
-      const uint4 l = *reinterpret_cast<const uint4*>(src + a.plane_size);
-      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 p = join2(hw[e], lw[e]);
-        v[2 * e] = fmaf(a.c, v[2 * e], a.b * p.x);
-        v[2 * e + 1] = fmaf(a.c, v[2 * e + 1], a.b * p.y);
+      for (int e = 0; e < 64; ++e) sum[c0 + e] *= a.c;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {  // plus b A, read by rows
+        uint4 q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int64_t r = i + k * 4 + (lane >> 3), c = jc + (lane & 7) * 8;
+          q[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < a.rows && c < a.cols)
+            q[k] = __ldcg(reinterpret_cast<const uint4*>(a.prev + p * a.plane_size + r * a.pitch + c));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          sts_u128(staged(stage, k * 4 + (lane >> 3), lane & 7), q[k].x, q[k].y, q[k].z, q[k].w);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float2 f[4];
+          unpack2<GC_F16>(sm100::lds_u128(staged(stage, lane, k)), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* t = sum + c0 + k * 8 + 2 * e;
+            t[0] = fmaf(a.b, f[e].x, t[0]);
+            t[1] = fmaf(a.b, f[e].y, t[1]);
+          }
+        }
       }
+      const int64_t d = i + lane - jc;  // the diagonal's column
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (j + e == i) v[e] += a.a * kUnit;
+      for (int e = 0; e < 64; ++e)
+        if (e == d) sum[c0 + e] += a.a * kUnit;
     }
-    uint32_t hw[4], lw[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2(v[2 * e], v[2 * e + 1], hw[e], lw[e]);
-    // rows of planes are padded to whole groups of 8
-    if (!kSym || j >= i) {
-      *reinterpret_cast<uint4*>(hi_row + j) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-      *reinterpret_cast<uint4*>(hi_row + a.plane_size + j) =
-          make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    for (int p = 0; p < 2; ++p) {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          split2(sum[c0 + k * 8 + 2 * e], sum[c0 + k * 8 + 2 * e + 1], h[e], l[e]);
+        if (p == 0) sts_u128(staged(stage, lane, k), h[0], h[1], h[2], h[3]);
+        else sts_u128(staged(stage, lane, k), l[0], l[1], l[2], l[3]);
+      }
+      __syncwarp();
+      store_plane<kSym>(a, a.dst + p * a.plane_size, stage, i, jc);
     }
-    if (kSym) {
+  }
+}
+
+// A part's sums go to the scratch; the warp that comes last adds all parts, in
+// their order, and has the tile.
+template <int N>
+__device__ __forceinline__ bool join_parts(const ProductArgs& a, float (&sum)[N], int64_t split,
+                                           int part, uint32_t rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto at = [&](int p) {
+    return reinterpret_cast<float4*>(a.part) +
+           (((split * a.parts + p) * 2 + rank) * kReadWarps + warp) * (N / 4 * 32) + lane;
+  };
+  float4* mine = at(part);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint16_t h = (uint16_t)(hw[e / 2] >> (16 * (e & 1)));
-        const uint16_t l = (uint16_t)(lw[e / 2] >> (16 * (e & 1)));
-        if (j < i && j + e >= i) {  // the group that the diagonal cuts
-          hi_row[j + e] = h;
-          hi_row[a.plane_size + j + e] = l;
-        }
-        if (j + e > i && j + e < a.cols) {
-          uint16_t* m = a.dst + (j + e) * a.pitch + i;
-          m[0] = h;
-          m[a.plane_size] = l;
-        }
+  for (int c = 0; c < N; c += 4)
+    __stcg(mine + c * 8, make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]));
+  __threadfence();
+  __syncwarp();
+  uint32_t* count = a.arrived + (split * 2 + rank) * kReadWarps + warp;
+  uint32_t before = 0;
+  if (lane == 0) before = atomicAdd(count, 1u);
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before != (uint32_t)a.parts - 1u) return false;
+  __threadfence();
+  if (lane == 0) *count = 0u;  // as it was, for the next product
+  constexpr int kBatch = 16;  // loads in flight
+  for (int p = 0; p < a.parts; ++p) {
+#pragma unroll
+    for (int c0 = 0; c0 < N; c0 += 4 * kBatch) {
+      float4 f[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) f[k] = __ldcg(at(p) + (c0 + 4 * k) * 8);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        float* t = sum + c0 + 4 * k;
+        t[0] = p ? t[0] + f[k].x : f[k].x;
+        t[1] = p ? t[1] + f[k].y : f[k].y;
+        t[2] = p ? t[2] + f[k].z : f[k].z;
+        t[3] = p ? t[3] + f[k].w : f[k].w;
       }
     }
   }
+  return true;
 }
 
 template <int MODE, int TN>
@@ -266,118 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s.tmem_slot;
   bool ok = true;
   let_next_begin();
-
-  if (warp == kProducerWarp) {
-    const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
-    after_previous();
-    int st = 0;
-    uint32_t ph = 0, loads = 0;
-    for (int64_t t = pair; ok && t < a.tiles; t += pairs) {
-      int64_t ti, tj;
-      tile_place<TN, kSym>(a, t, ti, tj);
-      const int32_t r0 = (int32_t)(ti * kTM) + (int32_t)rank * 128;
-      const int32_t c0 = (int32_t)(tj * TN) + (int32_t)rank * S::kBN;
-      for (int32_t k = 0; k < blocks; ++k) {
-        if (loads >= S::kStages) {
-          // free once the pair's MMAs read it
-          if (!mbar_wait_cluster(&s.empty[st], ph ^ 1u, kWaitCycles)) ok = false;
-          if (__any_sync(0xffffffffu, !ok)) {
-            ok = false;
-            break;
-          }
-        } else {
-          ++loads;
-        }
-        if (elect_one()) {
-          const uint32_t bar = bar0 + st * 8, at = s.stage0 + st * S::kStage;
-          if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * S::kStage);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            tma_load_3d_pair(at + p * kABytes, &map_a, k * kBK, r0, p, bar);
-            const uint32_t b = at + 2 * kABytes + p * S::kBBytes;
-            if (!kBMN) {
-              tma_load_3d_pair(b, &map_b, k * kBK, c0, p, bar);
-            } else {
-#pragma unroll
-              for (int h = 0; h < S::kBN / 64; ++h)
-                tma_load_3d_pair(b + h * 8192, &map_b, c0 + h * 64, k * kBK, p, bar);
-            }
-          }
-        }
-        if (++st == S::kStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-    // the arrivals of the last MMAs on this CTA's barriers: none may be under
-    // way when the CTA ends
-    for (int i = 0; ok && i < S::kStages; ++i) {
-      if (loads >= S::kStages || (uint32_t)st < loads)
-        if (!mbar_wait_cluster(&s.empty[st], ph ^ 1u, kWaitCycles)) ok = false;
-      if (++st == S::kStages) {
-        st = 0;
-        ph ^= 1u;
-      }
-    }
-  } else if (warp == kIssuerWarp) {
-    if (rank == 0) {
-      constexpr uint32_t idesc = (1u << 4) | ((kBMN ? 1u : 0u) << 16) |
-                                 ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24);
-      // K-major: 128-byte rows of 64, 8 rows per 1024-byte group; 16 of the sum
-      // are 32 bytes.  MN-major: 128-byte rows of 64 columns, 8 of the sum per
-      // group, blocks of 64 columns 8 KB apart; 16 of the sum are 2048 bytes.
-      const uint64_t da = smem_desc_sw128(s.stage0, 16, 1024);
-      const uint64_t db = smem_desc_sw128(s.stage0 + 2 * kABytes, kBMN ? 8192 : 16, 1024);
-      const uint32_t hi = (uint32_t)(da >> 32), a0 = (uint32_t)da, b0 = (uint32_t)db;
-      constexpr uint32_t kAStep = 32 >> 4, kBStep = (kBMN ? 2048 : 32) >> 4;
-      constexpr uint32_t kALo = kABytes >> 4, kBLo = S::kBBytes >> 4;
-      int st = 0;
-      uint32_t ph = 0, seg = 0;
-      for (int64_t t = pair; ok && t < a.tiles; t += pairs) {
-        int in_seg = 0;
-        for (int32_t k = 0; k < blocks; ++k) {
-          const uint32_t buf = seg & 1u;
-          if (in_seg == 0 && seg >= 2 &&
-              !mbar_wait_cluster(&s.acc_empty[buf], ((seg >> 1) - 1u) & 1u, kWaitCycles))
-            ok = false;
-          if (ok && !mbar_wait_cluster(&s.full[st], ph, kWaitCycles)) ok = false;
-          if (__any_sync(0xffffffffu, !ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const bool last = in_seg == kSegBlocks - 1 || k + 1 == blocks;
-          if (elect_one()) {
-            const uint32_t off = (uint32_t)st * (S::kStage >> 4), d = tmem + buf * TN;
-            // the small products first: the sum is large only once hi hi is in it
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_f16_pair(d, a0 + off + kALo + kk * kAStep, b0 + off + kk * kBStep, hi, idesc,
-                           (in_seg | kk) ? 1u : 0u);
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kBLo + kk * kBStep, hi, idesc, 1u);
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kk * kBStep, hi, idesc, 1u);
-            mma_commit_pair(&s.empty[st]);
-            if (last) mma_commit_pair(&s.acc_full[buf]);
-          }
-          ++in_seg;
-          if (last) {
-            ++seg;
-            in_seg = 0;
-          }
-          if (++st == S::kStages) {
-            st = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-      if (elect_one()) mma_commit_pair(s.drain);
-    }
-  } else if (warp < kReadWarps) {
+  if (warp < kReadWarps) {
+    if constexpr (TN == 256) reg_inc<kReadRegs>();
     // warp w reads lanes 32 (w % 4) .. + 31 (rows) of columns N (w / 4) .. of
     // every accumulator
     constexpr int N = TN / 2;
@@ -385,11 +474,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t acc_empty0 = map_to_rank(smem_u32(s.acc_empty), 0);
     after_previous();
     uint32_t seg = 0;
-    for (int64_t t = pair; ok && t < a.tiles; t += pairs) {
+    for (int64_t t = pair; ok && t < a.items; t += pairs) {
+      const Item<TN, kSym> item(a, t, blocks);
       float sum[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) sum[c] = 0.0f;
-      for (int32_t k = 0; k < blocks; k += kSegBlocks, ++seg) {
+      for (int32_t k = item.k0; k < item.k1; k += kSegBlocks, ++seg) {
         const uint32_t buf = seg & 1u;
         const bool got = mbar_wait_cluster(&s.acc_full[buf], (seg >> 1) & 1u, kWaitCycles);
         if (__any_sync(0xffffffffu, !got)) {
@@ -410,10 +500,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(acc_empty0 + buf * 8);
       }
       if (!ok) break;
-      int64_t ti, tj;
-      tile_place<TN, kSym>(a, t, ti, tj);
-      store_tile<MODE, TN>(a, sum, ti * kTM + rank * 128 + q * 32 + lane, tj * TN + ch * N);
+      if (item.split < 0 || join_parts<N>(a, sum, item.split, item.part, rank))
+        store_tile<MODE, N>(a, sum, s.out0 + warp * kWarpStage,
+                            item.i * kTM + rank * 128 + q * 32, item.j * TN + ch * N);
       __syncwarp();
+    }
+  } else {
+    if constexpr (TN == 256) reg_dec<kOtherRegs>();
+    if (warp == kProducerWarp) {
+      const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
+      after_previous();
+      int st = 0;
+      uint32_t ph = 0, loads = 0;
+      for (int64_t t = pair; ok && t < a.items; t += pairs) {
+        const Item<TN, kSym> item(a, t, blocks);
+        const int32_t r0 = (int32_t)(item.i * kTM) + (int32_t)rank * 128;
+        const int32_t c0 = (int32_t)(item.j * TN) + (int32_t)rank * S::kBN;
+        for (int32_t k = item.k0; k < item.k1; ++k) {
+          if (loads >= S::kStages) {
+            // free once the pair's MMAs read it
+            if (!mbar_wait_cluster(&s.empty[st], ph ^ 1u, kWaitCycles)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+          } else {
+            ++loads;
+          }
+          if (elect_one()) {
+            const uint32_t bar = bar0 + st * 8, at = s.stage0 + st * S::kStage;
+            if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * S::kStage);
+  #pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              tma_load_3d_pair(at + p * kABytes, &map_a, k * kBK, r0, p, bar);
+              const uint32_t b = at + 2 * kABytes + p * S::kBBytes;
+              if (!kBMN) {
+                tma_load_3d_pair(b, &map_b, k * kBK, c0, p, bar);
+              } else {
+  #pragma unroll
+                for (int h = 0; h < S::kBN / 64; ++h)
+                  tma_load_3d_pair(b + h * 8192, &map_b, c0 + h * 64, k * kBK, p, bar);
+              }
+            }
+          }
+          if (++st == S::kStages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // the arrivals of the last MMAs on this CTA's barriers: none may be under
+      // way when the CTA ends
+      for (int i = 0; ok && i < S::kStages; ++i) {
+        if (loads >= S::kStages || (uint32_t)st < loads)
+          if (!mbar_wait_cluster(&s.empty[st], ph ^ 1u, kWaitCycles)) ok = false;
+        if (++st == S::kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    } else if (warp == kIssuerWarp) {
+      if (rank == 0) {
+        constexpr uint32_t idesc = (1u << 4) | ((kBMN ? 1u : 0u) << 16) |
+                                   ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24);
+        // K-major: 128-byte rows of 64, 8 rows per 1024-byte group; 16 of the sum
+        // are 32 bytes.  MN-major: 128-byte rows of 64 columns, 8 of the sum per
+        // group, blocks of 64 columns 8 KB apart; 16 of the sum are 2048 bytes.
+        const uint64_t da = smem_desc_sw128(s.stage0, 16, 1024);
+        const uint64_t db = smem_desc_sw128(s.stage0 + 2 * kABytes, kBMN ? 8192 : 16, 1024);
+        const uint32_t hi = (uint32_t)(da >> 32), a0 = (uint32_t)da, b0 = (uint32_t)db;
+        constexpr uint32_t kAStep = 32 >> 4, kBStep = (kBMN ? 2048 : 32) >> 4;
+        constexpr uint32_t kALo = kABytes >> 4, kBLo = S::kBBytes >> 4;
+        int st = 0;
+        uint32_t ph = 0, seg = 0;
+        for (int64_t t = pair; ok && t < a.items; t += pairs) {
+          const Item<TN, kSym> item(a, t, blocks);
+          int in_seg = 0;
+          for (int32_t k = item.k0; k < item.k1; ++k) {
+            const uint32_t buf = seg & 1u;
+            if (in_seg == 0 && seg >= 2 &&
+                !mbar_wait_cluster(&s.acc_empty[buf], ((seg >> 1) - 1u) & 1u, kWaitCycles))
+              ok = false;
+            if (ok && !mbar_wait_cluster(&s.full[st], ph, kWaitCycles)) ok = false;
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const bool last = in_seg == kSegBlocks - 1 || k + 1 == item.k1;
+            if (elect_one()) {
+              const uint32_t off = (uint32_t)st * (S::kStage >> 4), d = tmem + buf * TN;
+              // the small products first: the sum is large only once hi hi is in it
+  #pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                mma_f16_pair(d, a0 + off + kALo + kk * kAStep, b0 + off + kk * kBStep, hi, idesc,
+                             (in_seg | kk) ? 1u : 0u);
+  #pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kBLo + kk * kBStep, hi, idesc, 1u);
+  #pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kk * kBStep, hi, idesc, 1u);
+              mma_commit_pair(&s.empty[st]);
+              if (last) mma_commit_pair(&s.acc_full[buf]);
+            }
+            ++in_seg;
+            if (last) {
+              ++seg;
+              in_seg = 0;
+            }
+            if (++st == S::kStages) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        if (elect_one()) mma_commit_pair(s.drain);
+      }
     }
   }
   // MMAs still in flight read both CTAs' shared memory: the producers, which
@@ -446,6 +649,7 @@ struct InputArgs {
   int parts;
   float eps;
   uint16_t* dst;
+  uint32_t* arrived;     // the products' counters, set to zero
 };
 
 template <int DT>
@@ -509,6 +713,8 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
   double sum = 0.0;
   let_next_begin();
+  if (blockIdx.x == 0)
+    for (int k = threadIdx.x; k < kMaxPairs * 2 * kReadWarps; k += 256) a.arrived[k] = 0u;
   for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < total; w += (int64_t)gridDim.x * 8) {
     const int64_t r = w / segs;
     float v[8];
@@ -933,6 +1139,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
 
 constexpr int kMaxParts = 608;
 
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -969,12 +1176,50 @@ bool make_map(CUtensorMap* map, const Planes& p, uint32_t box_rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How T tiles are dealt to the pairs, and what that costs in blocks of 256
+// columns (a block of 128 columns takes a bit more than half of it, storing a
+// tile about four, joining a part about one).
+struct Deal {
+  int64_t whole, items;
+  int parts;
+  double cost;
+};
+Deal deal(int64_t tiles, int64_t pairs, int64_t blocks, int tn) {
+  const double block = tn == 256 ? 1.0 : 0.55, store = tn / 64.0, join = tn / 256.0;
+  Deal d{};
+  const int64_t full = tiles / pairs * pairs, rem = tiles - full;
+  d.parts = rem ? (int)std::min<int64_t>({pairs / rem, kMaxPartsOfTile, blocks}) : 1;
+  d.whole = d.parts > 1 ? full : tiles;
+  d.items = d.whole + (d.parts > 1 ? rem * d.parts : 0);
+  d.cost = (double)(full / pairs) * ((double)blocks * block + store);
+  if (rem) d.cost += (double)ceil_div(blocks, (int64_t)d.parts) * block + store + d.parts * join;
+  return d;
+}
+
+// Tiles of a [rows, cols] result; of a symmetric one those on and above the
+// diagonal.
+int64_t count_tiles(int64_t rows, int64_t cols, int tn, bool sym) {
+  const int64_t r = ceil_div(rows, (int64_t)kTM), c = ceil_div(cols, (int64_t)tn);
+  if (!sym) return r * c;
+  int64_t n = 0;
+  for (int64_t i = 0; i < r; ++i) n += c - i * kTM / tn;
+  return n;
+}
+
 template <int MODE, int TN>
-gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d, ProductArgs a) {
+gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d, ProductArgs a,
+                  const Deal& deal) {
   static uint64_t devices = 0;
   constexpr bool kSym = MODE == kGram || MODE == kPoly;
   if (!allow_smem(ctx, orth_product_kernel<MODE, TN>, (int)Shape<TN>::kSmem, devices))
     return GC_ERR_CUDA;
+  // the registers that warps take over have to be there
+  static const bool regs = [] {
+    cudaFuncAttributes f{};
+    return TN != 256 || (cudaFuncGetAttributes(&f, orth_product_kernel<MODE, TN>) == cudaSuccess &&
+                         f.numRegs >= kLaunchRegs);
+  }();
+  if (!regs) return GC_ERR_CUDA;
   CUtensorMap ma, mb;
   if (!make_map(&ma, x, 128) || !make_map(&mb, y, kSym ? TN / 2 : kBK)) return GC_ERR_CUDA;
   a.rows = d.rows;
@@ -982,16 +1227,14 @@ gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d
   a.sum = x.cols;
   a.row_tiles = ceil_div(d.rows, (int64_t)kTM);
   a.col_tiles = ceil_div(d.cols, (int64_t)TN);
-  a.tiles = 0;
-  if (kSym)
-    for (int64_t i = 0; i < a.row_tiles; ++i) a.tiles += a.col_tiles - i * kTM / TN;
-  else
-    a.tiles = a.row_tiles * a.col_tiles;
+  a.whole = deal.whole;
+  a.items = deal.items;
+  a.parts = deal.parts;
   a.dst = d.at;
   a.pitch = d.pitch;
   a.plane_size = d.size;
   a.status = ctx->ws.status;
-  const int64_t pairs = std::min<int64_t>(a.tiles, ctx->num_sms / 2);
+  const int64_t pairs = std::min<int64_t>(a.items, ctx->num_sms / 2);
   LaunchScope L(ctx, GC_PHASE_ORTH_PRODUCT);
   return launch_early(orth_product_kernel<MODE, TN>, dim3((unsigned)(2 * pairs)), kThreads,
                       Shape<TN>::kSmem, ctx->stream, ma, mb, a) == cudaSuccess
@@ -1002,8 +1245,21 @@ gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d
 template <int MODE>
 gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d,
                   const ProductArgs& a) {
-  return product<MODE, 256>(ctx, x, y, d, a);
+  constexpr bool kSym = MODE == kGram || MODE == kPoly;
+  const int64_t pairs = std::min(ctx->num_sms / 2, kMaxPairs), blocks = ceil_div(x.cols, (int64_t)kBK);
+  const Deal wide = deal(count_tiles(d.rows, d.cols, 256, kSym), pairs, blocks, 256);
+  const Deal slim = deal(count_tiles(d.rows, d.cols, 128, kSym), pairs, blocks, 128);
+  return slim.cost < wide.cost ? product<MODE, 128>(ctx, x, y, d, a, slim)
+                               : product<MODE, 256>(ctx, x, y, d, a, wide);
 }
+
+// Scratch of the tiles in parts: at most kMaxPairs items of work, and no more
+// than kMaxPartsOfTile for each tile of 128 columns.
+int64_t parts_bytes(int64_t s, int64_t l) {
+  const int64_t tiles = count_tiles(s, l, 128, false);
+  return std::min<int64_t>(kMaxPairs * 2, kMaxPartsOfTile * tiles) * kTM * 128 * 4;
+}
+constexpr int64_t kArrivedBytes = kMaxPairs * 2 * kReadWarps * 4;
 
 template <int DT>
 gc_status input(gc_ctx* ctx, const InputArgs& a) {
@@ -1065,7 +1321,8 @@ gc_status launch_small(gc_ctx* ctx, SmallArgs& a, char* at) {
 int64_t orth_scratch_bytes(int64_t m, int64_t n) {
   if (m == 0 || n == 0) return 0;
   const int64_t s = std::min(m, n), l = std::max(m, n);
-  int64_t bytes = kMaxParts * 8 + 2 * planes_bytes(s, l) + 2 * planes_bytes(s, s);
+  int64_t bytes = kMaxParts * 8 + round_up(kArrivedBytes, 256) + 2 * planes_bytes(s, l) +
+                  2 * planes_bytes(s, s) + parts_bytes(s, l);
   if (s <= kSmallS) bytes = std::max(bytes, small_bytes(s, l));
   return bytes;
 }
@@ -1096,6 +1353,8 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
   InputArgs in{};
   in.part = reinterpret_cast<double*>(at);
   at += kMaxParts * 8;
+  in.arrived = reinterpret_cast<uint32_t*>(at);
+  at += round_up(kArrivedBytes, 256);
   auto planes = [&](int64_t rows, int64_t cols) {
     Planes p{reinterpret_cast<uint16_t*>(at), rows, cols, plane_pitch(cols), 0};
     p.size = rows * p.pitch;
@@ -1117,8 +1376,11 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
   gc_status st = dtype == GC_F32    ? input<GC_F32>(ctx, in)
                  : dtype == GC_BF16 ? input<GC_BF16>(ctx, in)
                                     : input<GC_F16>(ctx, in);
+  float* const part = reinterpret_cast<float*>(at);
   for (int k = 0; st == GC_OK && k < steps; ++k) {
     ProductArgs a{};
+    a.part = part;
+    a.arrived = in.arrived;
     st = product<kGram>(ctx, x, x, gram, a);
     if (st != GC_OK) break;
     a.a = coefs[3 * k];
@@ -1136,6 +1398,8 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
       a.ldo = ldo;
       a.scale = scale;
       a.transposed = m > n;
+      a.out_vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 &&
+                  (m == 1 || row_aligned(ldo, odtype));
       st = product<kLast>(ctx, poly, x, next, a);
     }
   }
