@@ -55,6 +55,16 @@ constexpr float kUnit = 4096.0f;     // planes hold v * kUnit
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
+// What a sum over a block of 16 k elements loses on average to the tensor
+// cores' roundings towards zero, as a share of its value: put back when it is
+// read.  Measured as the mean of sum(x^2) - 1 over unit vectors x; in B X,
+// whose sums have one large term (B is near a multiple of the identity), as
+// the shrinking of a step's result, about half of it in whole blocks.
+__host__ __device__ constexpr float lost(int k, int mode) {
+  return (k >= 4 ? 3.0f : k == 3 ? 2.2f : k == 2 ? 1.5f : 0.9f) *
+         (k >= 4 && (mode == kApply || mode == kLast) ? 0x1p-25f : 0x1p-24f);
+}
+
 template <int TN>
 struct Shape {
   static constexpr int kBN = TN / 2;                       // second operand, one CTA
@@ -320,7 +330,9 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N]
   const int lane = threadIdx.x & 31;
   if (i >= a.rows) return;
 #pragma unroll
-  for (int c = 0; c < N; ++c) sum[c] *= MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
+  for (int c = 0; c < N; ++c)
+    sum[c] = fmaf(sum[c], lost(kBK / 16, MODE), sum[c]) *
+             (MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit);
   if (MODE == kLast) {
     if (a.odtype == GC_F32) store_result<GC_F32, N>(a, sum, stage, i, j);
     else if (a.odtype == GC_BF16) store_result<GC_BF16, N>(a, sum, stage, i, j);
@@ -1019,7 +1031,9 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     tc_fence_after_sync();
   };
   // 16 columns from c on of this thread's row, from `parts` accumulators.
-  auto take = [&](float (&v)[16], int c, int parts, uint32_t apart) {
+  auto take = [&](float (&v)[16], int c, int mode, int sixteens, uint32_t apart) {
+    const int parts = (sixteens + 3) / 4;
+    const float back = lost(sixteens, mode);
     tmem_ld16(tmem + (row0 << 16) + c, v);
     for (int p = 1; p < parts; ++p) {
       float w[16];
@@ -1028,7 +1042,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
       for (int e = 0; e < 16; ++e) v[e] += w[e];
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kUnit;
+    for (int e = 0; e < 16; ++e) v[e] = fmaf(v[e], back, v[e]) * (1.0f / kUnit);
   };
   auto store16 = [&](uint32_t at, uint32_t plane, int c, const float (&v)[16]) {
 #pragma unroll
@@ -1040,12 +1054,11 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     }
   };
 
-  const int s_parts = (a.s16 + 63) / 64;
   for (int step = 0; step < a.steps && ok; ++step) {
     multiply(kGram);
     for (int c = half * 16; c < a.s16; c += 32) {
       float v[16];
-      take(v, c, (x16 + 3) / 4, 128);
+      take(v, c, kGram, x16, 128);
       if (!mine) continue;
       if (gridDim.x == 1) {
         store16(as, kAPlane, c, v);
@@ -1086,7 +1099,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     const float ca = a.coefs[step][0] * kUnit, cb = a.coefs[step][1], cc = a.coefs[step][2];
     for (int c = half * 16; c < a.s16; c += 32) {
       float v[16];
-      take(v, c, s_parts, 128);
+      take(v, c, kPoly, a.s16 / 16, 128);
       if (!mine) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1111,7 +1124,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     ok = !__syncthreads_or(!ok);  // a wait that ran out ends the call for every thread
     for (int c = half * 16; c < xpad; c += 32) {
       float v[16];
-      take(v, c, s_parts, 256);
+      take(v, c, kApply, a.s16 / 16, 256);
       if (!mine) continue;
       if (!last) {
         store16(xs, kXPlane, c, v);

@@ -14,6 +14,7 @@
 // memory: forward 2 inputs and up to 2 outputs with their codes, backward 3
 // inputs and one output, 10 to 20 instructions per element.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "gc_rows.cuh"
@@ -73,16 +74,39 @@ __device__ __forceinline__ float2 add_squares(const uint4& r, float2 s) {
   return s;
 }
 
-// y's unit from h's: (h rstd) gamma.
+// 1 / sqrt(sum / n + eps) as two terms, the second one what the first lacks:
+// y may lie next to a border of its rounding, or of its code.
+struct Rstd {
+  float hi, lo;
+};
+struct Count {  // 1 / n as two terms
+  float hi, lo;
+  __device__ __forceinline__ explicit Count(int64_t n)
+      : hi(1.0f / (float)n), lo(fmaf(-hi, (float)n, 1.0f) * hi) {}
+};
+__device__ __forceinline__ Rstd rstd_of(float sum, const Count& n, float eps) {
+  const float v = fmaf(sum, n.hi, (sum <= FLT_MAX ? sum * n.lo : 0.0f) + eps);
+  const float r = rsqrtf(v);
+  const float q = __fmul_rn(r, r);
+  const float e = fmaf(-v, fmaf(r, r, -q), fmaf(-v, q, 1.0f));  // 1 - v r^2
+  return {r, fabsf(e) < 1.0f ? 0.5f * r * e : 0.0f};  // not where r is 0 or infinite
+}
+
+// y's unit from h's: h rstd as two terms, times gamma, rounded once to fp32.
 template <int DT>
-__device__ __forceinline__ uint4 scale_unit(const uint4& r, float rstd,
+__device__ __forceinline__ uint4 scale_unit(const uint4& r, const Rstd& rstd,
                                             const float (&g)[Elem<DT>::V]) {
   constexpr int H = Elem<DT>::V / 2;
   float2 v[H];
   unpack2<DT>(r, v);
 #pragma unroll
-  for (int j = 0; j < H; ++j)
-    v[j] = __fmul2_rn(__fmul2_rn(v[j], both(rstd)), make_float2(g[2 * j], g[2 * j + 1]));
+  for (int j = 0; j < H; ++j) {
+    const float2 w = make_float2(g[2 * j], g[2 * j + 1]);
+    const float2 p = __fmul2_rn(v[j], both(rstd.hi));
+    const float2 minus = make_float2(-p.x, -p.y);
+    const float2 q = __ffma2_rn(v[j], both(rstd.lo), __ffma2_rn(v[j], both(rstd.hi), minus));
+    v[j] = __ffma2_rn(p, w, __fmul2_rn(q, w));
+  }
   return pack2<DT>(v);
 }
 
@@ -99,7 +123,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
   const int64_t c0 = at / elem_size(DT) + lane * V;
   const int64_t step = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
   int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
-  const float inv_n = 1.0f / (float)a.cols;
+  const Count n(a.cols);
   uint4 u[U], v[U];
   auto load = [&](int64_t r) {
     load_run<DT, ALIGNED>(u, a.x + r * a.xpitch, at, inner, a.row_bytes, a.xend);
@@ -121,8 +145,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
       s = add_squares<DT>(h[i], s);
       keep_packed(h[i]);
     }
-    const float rstd = rsqrtf(sum(s.x + s.y) * inv_n + a.eps);
-    if (WARP ? lane == 0 : threadIdx.x == 0) a.rstd[row] = rstd;
+    const Rstd rstd = rstd_of(sum(s.x + s.y), n, a.eps);
+    if (WARP ? lane == 0 : threadIdx.x == 0) a.rstd[row] = rstd.hi + rstd.lo;
     if (a.h) store_run<DT, ALIGNED>(a.h + row * a.hpitch, at, inner, a.row_bytes, h);
     if (a.codes) {
 #pragma unroll
@@ -151,7 +175,7 @@ __global__ void __launch_bounds__(1024)
   __shared__ float2 slot[2][32];
   RowSum<false> sum{slot};
   const int64_t round = (int64_t)blockDim.x * 16;
-  const float inv_n = 1.0f / (float)a.cols;
+  const Count n(a.cols);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const char *x = a.x + row * a.xpitch, *res = a.res + (a.res ? row * a.respitch : 0);
     auto get = [&](int64_t off) {
@@ -162,8 +186,8 @@ __global__ void __launch_bounds__(1024)
     float2 s = both(0.0f);
     for (int64_t b = 0; b < a.row_bytes; b += round)
       s = add_squares<DT>(get(b + threadIdx.x * 16), s);
-    const float rstd = rsqrtf(sum(s.x + s.y) * inv_n + a.eps);
-    if (threadIdx.x == 0) a.rstd[row] = rstd;
+    const Rstd rstd = rstd_of(sum(s.x + s.y), n, a.eps);
+    if (threadIdx.x == 0) a.rstd[row] = rstd.hi + rstd.lo;
     for (int64_t b = 0; b < a.row_bytes; b += round) {
       const int64_t off = b + threadIdx.x * 16, c = off / elem_size(DT);
       const uint4 h = get(off);
@@ -284,7 +308,7 @@ __global__ void __maxnreg__(kForwardRegs)
   RowsSum<1> sum{slot, nt};
   const uint32_t u0 = (t & ~31) * K, u1 = u0 + (t & 31);  // the warp's and the thread's first unit
   const uint32_t base = smem_u32(stages) + u1 * 16;
-  const float inv_n = 1.0f / (float)a.cols;
+  const Count n(a.cols);
   float g[K][V];
   // bytes of the row from the first unit on
   const int rest = (int)min((int64_t)(1 << 30), a.row_bytes - (int64_t)u1 * 16);
@@ -328,8 +352,8 @@ __global__ void __maxnreg__(kForwardRegs)
     float s[1] = {q.x + q.y};
     sum(s, ok);
     if (!ok) break;
-    const float rstd = rsqrtf(s[0] * inv_n + a.eps);
-    if (t == 0) a.rstd[row] = rstd;
+    const Rstd rstd = rstd_of(s[0], n, a.eps);
+    if (t == 0) a.rstd[row] = rstd.hi + rstd.lo;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       keep_packed(h[i]);
