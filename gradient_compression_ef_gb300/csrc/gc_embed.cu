@@ -22,7 +22,8 @@ namespace gc {
 namespace {
 
 constexpr int kMaxChunk = 64;    // sorted tokens of one unit of work, at most
-constexpr int kCountMax = 2048;  // tokens that are sorted by counting
+constexpr int kFew = 256;        // tokens that are not sorted
+constexpr int kCountMax = 8192;  // tokens that are sorted by counting
 constexpr int kSortBlocks = 128; // blocks of a radix pass, at most
 constexpr int kBins = 512;       // digits of up to 9 bits
 
@@ -91,13 +92,11 @@ __global__ void __launch_bounds__(256) embed_forward_kernel(const __grid_constan
     uint4 r[U];
     if (row >= 0) {
       load_run<DT, ALIGNED>(r, a.table + row * a.tpitch, at, inner, a.row_bytes, a.tend);
+#pragma unroll
+      for (int i = 0; i < U; ++i) r[i] = scale_unit<DT>(r[i], a.scale);
     } else {
 #pragma unroll
       for (int i = 0; i < U; ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (row >= 0) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) r[i] = scale_unit<DT>(r[i], a.scale);
     }
     store_run<DT, ALIGNED>(a.y + t * a.ypitch, at, inner, a.row_bytes, r);
   }
@@ -326,6 +325,86 @@ __device__ __forceinline__ void put_row(float* row, const float2 (&s)[V / 2], fl
   }
 }
 
+// Zeros to rows v0 + i of the table, i the bits of `todo`; a warp.
+__device__ __forceinline__ void zero_rows(const EmbedArgs& a, int64_t v0, uint32_t todo) {
+  const int lane = threadIdx.x & 31;
+  while (todo) {
+    const int r = __ffs(todo) - 1;
+    todo &= todo - 1;
+    float* row = a.dtable + (v0 + r) * a.ldd;
+    // up to a 16-byte boundary, by 16 bytes, the rest
+    const int64_t head =
+        min((int64_t)((0u - (uint32_t)(reinterpret_cast<uintptr_t>(row) >> 2)) & 3u), a.cols);
+    const int64_t quads = (a.cols - head) >> 2;
+    if (lane < head) row[lane] = 0.0f;
+    float4* q = reinterpret_cast<float4*>(row + head);
+    for (int64_t c = lane; c < quads; c += 32) q[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int64_t c = head + (quads << 2) + lane;
+    if (c < a.cols) row[c] = 0.0f;
+  }
+}
+
+// Few tokens, one launch: every block looks all ids up; a warp has a token and
+// 512 bytes of its row, and, where no earlier token has that id, sums the rows
+// of all that have it.  The blocks behind them write zeros, 8 rows per warp.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(256) embed_few_kernel(const __grid_constant__ EmbedArgs a) {
+  constexpr int V = Elem<DT>::V, H = V / 2, kDeep = 16;
+  __shared__ uint32_t keys[kFew];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)a.tokens;
+  const uint32_t none = (uint32_t)a.vocab;
+  keys[threadIdx.x] = (int)threadIdx.x < n ? key_of(a, threadIdx.x) : none;
+  __syncthreads();
+  const int64_t segs = ceil_div(a.row_bytes, (int64_t)512);
+  const int64_t sum_blocks = ceil_div(a.tokens * segs, (int64_t)8);
+  if (blockIdx.x >= sum_blocks) {
+    for (int64_t w = (blockIdx.x - sum_blocks) * 8 + warp; w * 8 < a.vocab;
+         w += a.zero_blocks * 8) {
+      uint32_t used = 0u;
+      for (int j = lane; j < n; j += 32) {
+        const uint32_t d = keys[j] - (uint32_t)(w * 8);
+        if (d < 8u) used |= 1u << d;
+      }
+      used = __reduce_or_sync(0xffffffffu, used);
+      const int rows = (int)min((int64_t)8, a.vocab - w * 8);
+      zero_rows(a, w * 8, ~used & ((1u << rows) - 1u));
+    }
+    return;
+  }
+  const int64_t w = (int64_t)blockIdx.x * 8 + warp, t = w / segs;
+  if (t >= n) return;
+  const uint32_t key = keys[t];
+  if (key == none) return;
+  for (int j = lane; j < (int)t + lane + 1; j += 32)
+    if (__any_sync(0xffffffffu, j < t && keys[j] == key)) return;
+  const int64_t off = (w - t * segs) * 512 + lane * 16, c = off / elem_size(DT);
+  float2 s[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) s[j] = both(0.0f);
+  for (int j0 = (int)t & ~31; j0 < n; j0 += 32) {
+    uint32_t m = __ballot_sync(0xffffffffu, j0 + lane < n && keys[j0 + lane] == key);
+    while (m) {
+      uint4 r[kDeep];
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        r[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (m)
+          r[i] = load_unit<DT, ALIGNED>(a.table + (int64_t)(j0 + __ffs(m) - 1) * a.tpitch, off,
+                                        a.row_bytes, a.tend);
+        m &= m - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        float2 v[H];
+        unpack2<DT>(r[i], v);
+#pragma unroll
+        for (int j = 0; j < H; ++j) s[j] = __fadd2_rn(s[j], v[j]);
+      }
+    }
+  }
+  put_row<V>(a.dtable + (int64_t)key * a.ldd, s, a.scale, c, a.cols, a.accumulate);
+}
+
 template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ EmbedArgs a) {
   constexpr int V = Elem<DT>::V, H = V / 2, kDeep = 8;
@@ -347,20 +426,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
         else hi = mid;
       }
       const bool empty = lane < 8 && v < a.vocab && (lo == a.tokens || __ldg(a.key + lo) != v);
-      uint32_t todo = __ballot_sync(0xffffffffu, empty);
-      while (todo) {
-        const int r = __ffs(todo) - 1;
-        todo &= todo - 1;
-        float* row = a.dtable + (w * 8 + r) * a.ldd;
-        // up to a 16-byte boundary, by 16 bytes, the rest
-        const int64_t head = min((int64_t)((0u - (uint32_t)(reinterpret_cast<uintptr_t>(row) >> 2)) & 3u), a.cols);
-        const int64_t quads = (a.cols - head) >> 2;
-        if (lane < head) row[lane] = 0.0f;
-        float4* q = reinterpret_cast<float4*>(row + head);
-        for (int64_t c = lane; c < quads; c += 32) q[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const int64_t c = head + (quads << 2) + lane;
-        if (c < a.cols) row[c] = 0.0f;
-      }
+      zero_rows(a, w * 8, __ballot_sync(0xffffffffu, empty));
     }
     return;
   }
@@ -478,9 +544,10 @@ int64_t part_pitch(int64_t cols) { return round_up(cols, 4); }
 
 // Sorted tokens per unit of work: fewer where there would be fewer warps than
 // the GPU takes at once.
-int chunk_of(int64_t tokens, int64_t cols) {
+int chunk_of(int64_t tokens, int64_t row_bytes) {
   int chunk = kMaxChunk;
-  while (chunk > 8 && ceil_div(tokens, (int64_t)chunk) * ceil_div(cols, (int64_t)256) < 2432) chunk /= 2;
+  while (chunk > 8 && ceil_div(tokens, (int64_t)chunk) * ceil_div(row_bytes, (int64_t)512) < 2432)
+    chunk /= 2;
   return chunk;
 }
 
@@ -500,7 +567,7 @@ Scratch lay_out(int64_t tokens, int64_t cols) {
   if (radix) s.bytes += 4 * kCounts * 4;
   s.part = s.bytes;
   // one chunk has no run that crosses
-  const int64_t chunks = ceil_div(tokens, (int64_t)chunk_of(tokens, cols));
+  const int64_t chunks = ceil_div(tokens, (int64_t)chunk_of(tokens, cols * 2));  // 16-bit rows: the most
   if (chunks > 1) s.bytes += chunks * 2 * part_pitch(cols) * 4;
   return s;
 }
@@ -641,16 +708,27 @@ gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
   a.status = ctx->ws.status;
   a.part_pitch = part_pitch(cols);
   a.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + lay_out(tokens, cols).part);
-  a.chunk = chunk_of(tokens, cols);
+  a.chunk = chunk_of(tokens, a.row_bytes);
   const int64_t chunks = ceil_div(tokens, (int64_t)a.chunk);
   const int64_t sum_blocks = chunks * ceil_div(ceil_div(a.row_bytes, (int64_t)512), (int64_t)8);
   a.zero_blocks =
       accumulate ? 0
                  : std::min<int64_t>(ceil_div(vocab, (int64_t)64), (int64_t)ctx->num_sms * 8);
   if (sum_blocks + a.zero_blocks > INT32_MAX) return GC_ERR_UNSUPPORTED;
+  const bool al = tokens == 1 || row_aligned(lddy, dtype);
+  if (tokens <= kFew) {
+    LaunchScope L(ctx, GC_PHASE_EMBED_SUM);
+    const auto kernel =
+        dtype == GC_F32    ? (al ? embed_few_kernel<GC_F32, true> : embed_few_kernel<GC_F32, false>)
+        : dtype == GC_BF16 ? (al ? embed_few_kernel<GC_BF16, true> : embed_few_kernel<GC_BF16, false>)
+                           : (al ? embed_few_kernel<GC_F16, true> : embed_few_kernel<GC_F16, false>);
+    const int64_t few = ceil_div(tokens * ceil_div(a.row_bytes, (int64_t)512), (int64_t)8);
+    if (few + a.zero_blocks > INT32_MAX) return GC_ERR_UNSUPPORTED;
+    kernel<<<(unsigned)(few + a.zero_blocks), 256, 0, ctx->stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? GC_OK : GC_ERR_CUDA;
+  }
   const gc_status st = sort_tokens(ctx, a, static_cast<char*>(scratch));
   if (st != GC_OK) return st;
-  const bool al = tokens == 1 || row_aligned(lddy, dtype);
   {
     LaunchScope L(ctx, GC_PHASE_EMBED_SUM);
     const auto kernel =

@@ -305,3 +305,24 @@ def test_accumulation_at_any_float(gc, ctx, at):
     old = before[at:at + vocab * cols].view(vocab, cols)
     assert torch.equal(view, torch.where(used, old + first, old))
     assert torch.equal(flat[:at], before[:at]) and torch.equal(flat[at + vocab * cols:], before[at + vocab * cols:])
+
+
+@pytest.mark.parametrize("tokens", [255, 256, 257])
+@pytest.mark.parametrize("kind,vocab", [("one", 3), ("any", 1000), ("skew", 77)])
+@pytest.mark.parametrize("dtype,pad", [("f32", 3), ("bf16", 0), ("f16", 1)])
+def test_with_and_without_sorting(gc, ctx, tokens, kind, vocab, dtype, pad):
+    """Both sides of the number of tokens from which they are sorted."""
+    r = np.random.default_rng(tokens)
+    cols = 391
+    ids = some_ids(r, tokens, vocab, kind)
+    ids[::17] = -1
+    dy, dyv, _ = matrix(r.standard_normal((tokens, cols)), dtype, pad)
+    want, size, n = ref.embedding_wgrad(dyv, ids, vocab, 0.5, -1)
+    d, buf = out_matrix(vocab, cols, "f32", pad)
+    gc.embedding_wgrad(ctx, dy, tensor_ids(ids, "i32"), 0.5, d, pad=-1)
+    close(f64(d), want, (n[:, None] + 2) * 2.0 ** -24 * size, "dtable")
+    pad_untouched(buf, cols)
+    gc.embedding_wgrad(ctx, dy, tensor_ids(ids, "i32"), 0.5, d, pad=-1, accumulate=True)
+    close(f64(d), 2.0 * want, (2 * n[:, None] + 6) * 2.0 ** -24 * size, "dtable, twice")
+    pad_untouched(buf, cols)
+    ctx.check()
