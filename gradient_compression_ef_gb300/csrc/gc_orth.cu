@@ -708,13 +708,17 @@ __device__ __forceinline__ double sum_squares(const float (&v)[8]) {
 }
 
 // kUnit / (|g| + eps) as two factors, each inside binary32's range whatever
-// the norm; NaN where g is not finite.
+// the norm; NaN where g is not finite.  The sum is m 4^k with 1 <= m < 4, so
+// that root and quotient are fp32 ones (binary64's take thousands of cycles).
 __device__ __forceinline__ float2 unit_factors(double squares, float eps) {
-  const double d = sqrt(squares) + (double)eps;
-  if (d == 0.0) return make_float2(0.0f, 0.0f);
-  if (!(d <= 1.0e300)) return make_float2(NAN, NAN);
-  const int e = ilogb(d) / 2;
-  return make_float2((float)ldexp(1.0, -e), (float)((double)kUnit / d * ldexp(1.0, e)));
+  if (squares == 0.0) return make_float2(0.0f, 0.0f);
+  if (!(squares <= 1.0e300)) return make_float2(NAN, NAN);
+  const long long bits = __double_as_longlong(squares);
+  const int e = (int)(bits >> 52) - 1023, k = e >> 1;
+  const float m = (float)__longlong_as_double((bits & 0xFFFFFFFFFFFFFll) |
+                                              ((long long)(1023 + e - 2 * k) << 52));
+  const float n = sqrtf(m) + ldexpf(eps, -k);
+  return make_float2(ldexpf(1.0f, -(k / 2)), ldexpf(kUnit / n, -(k - k / 2)));
 }
 
 // Sums of squares, a double per block.
@@ -842,23 +846,16 @@ struct SmallArgs {
   float coefs[kSmallSteps][3];
 };
 
-__device__ __forceinline__ float get_any(const SmallArgs& a, int64_t at) {
-  return a.dtype == GC_F32 ? get<GC_F32>(a.g, at)
-         : a.dtype == GC_BF16 ? get<GC_BF16>(a.g, at)
-                              : get<GC_F16>(a.g, at);
-}
-__device__ __forceinline__ void put_any(const SmallArgs& a, int64_t at, float v) {
-  if (a.odtype == GC_F32) put<GC_F32>(a.out, at, v);
-  else if (a.odtype == GC_BF16) put<GC_BF16>(a.out, at, v);
-  else put<GC_F16>(a.out, at, v);
-}
-
 // Elements (i, j .. j + 7) of X's slice, j a multiple of 8; zero outside.
+template <int DT>
 __device__ __forceinline__ void get_slice(float (&v)[8], const SmallArgs& a, int i, int64_t j) {
+  const int64_t at = a.tall ? j * a.ldg + i : i * a.ldg + j, step = a.tall ? a.ldg : 1;
+  if (i < a.s && j + 8 <= a.l) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int64_t c = j + e;
-    v[e] = i < a.s && c < a.l ? get_any(a, a.tall ? c * a.ldg + i : i * a.ldg + c) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = get<DT>(a.g, at + e * step);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = i < a.s && j + e < a.l ? get<DT>(a.g, at + e * step) : 0.0f;
   }
 }
 
@@ -876,6 +873,57 @@ __device__ __forceinline__ void put_planes(uint32_t at, uint32_t plane, const fl
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + plane), "r"(l[0]), "r"(l[1]),
                "r"(l[2]), "r"(l[3])
                : "memory");
+}
+
+// Row r and columns 8 c .. of the slice that a thread takes in its w-th turn:
+// neighbouring lanes along the axis that is contiguous in memory.
+__device__ __forceinline__ void slice_place(const SmallArgs& a, int chunks, int w, int& r, int& c) {
+  r = a.tall ? w % a.s16 : w / chunks;
+  c = a.tall ? w / a.s16 : w % chunks;
+}
+
+// The slice's sum of squares (a thread's part).  (Loops that are not unrolled:
+// in a kernel that runs once through its code, fetching the code counts.)
+template <int DT>
+__device__ __forceinline__ double slice_squares(const SmallArgs& a, int64_t c0, int chunks) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int w = threadIdx.x; w < a.s16 * chunks; w += 256) {
+    int r, c;
+    slice_place(a, chunks, w, r, c);
+    float v[8];
+    get_slice<DT>(v, a, r, c0 + c * 8);
+    sum += sum_squares(v);
+  }
+  return sum;
+}
+
+// The slice, in units, to its planes.
+template <int DT>
+__device__ __forceinline__ void slice_planes(const SmallArgs& a, int64_t c0, int chunks, float2 f,
+                                             uint32_t xs) {
+#pragma unroll 1
+  for (int w = threadIdx.x; w < a.s16 * chunks; w += 256) {
+    int r, c;
+    slice_place(a, chunks, w, r, c);
+    float v[8];
+    get_slice<DT>(v, a, r, c0 + c * 8);
+    const int64_t left = r < a.s ? a.l - c0 - c * 8 : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? in_units(v[e], f) : 0.0f;
+    put_planes(xs + chunk_at(r, c), kXPlane, v);
+  }
+}
+
+// 16 columns of a row of the result.
+template <int DT>
+__device__ __forceinline__ void put_slice(const SmallArgs& a, int i, int64_t j,
+                                          const float (&v)[16]) {
+  const int64_t at = a.tall ? j * a.ldo + i : i * a.ldo + j, step = a.tall ? a.ldo : 1;
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (j + e < a.l)
+      put<DT>(a.out, at + e * step, __fmul_rn(v[e] * (1.0f / kUnit), a.scale));
 }
 
 // Every CTA of the grid is here, and what it wrote is visible; false when the
@@ -949,25 +997,10 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
   }
 
   // the slice's sum of squares
-  double sum = 0.0;
-  const int chunks = xpad / 8, rows16 = a.s16;
-  auto place = [&](int w, int& r, int& c) {
-    // neighbouring lanes along the axis that is contiguous in memory
-    if (a.tall) {
-      r = w % rows16;
-      c = w / rows16;
-    } else {
-      c = w % chunks;
-      r = w / chunks;
-    }
-  };
-  for (int w = threadIdx.x; w < rows16 * chunks; w += 256) {
-    int r, c;
-    place(w, r, c);
-    float v[8];
-    get_slice(v, a, r, c0 + c * 8);
-    sum += sum_squares(v);
-  }
+  const int chunks = xpad / 8;
+  double sum = a.dtype == GC_F32    ? slice_squares<GC_F32>(a, c0, chunks)
+               : a.dtype == GC_BF16 ? slice_squares<GC_BF16>(a, c0, chunks)
+                                    : slice_squares<GC_F16>(a, c0, chunks);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) norm_part[warp] = sum;
@@ -995,16 +1028,9 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
   }
   __syncthreads();
   const float2 f = factors;
-  for (int w = threadIdx.x; w < rows16 * chunks; w += 256) {
-    int r, c;
-    place(w, r, c);
-    float v[8];
-    get_slice(v, a, r, c0 + c * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = r < a.s && c0 + c * 8 + e < a.l ? in_units(v[e], f) : 0.0f;
-    put_planes(xs + chunk_at(r, c), kXPlane, v);
-  }
+  if (a.dtype == GC_F32) slice_planes<GC_F32>(a, c0, chunks, f, xs);
+  else if (a.dtype == GC_BF16) slice_planes<GC_BF16>(a, c0, chunks, f, xs);
+  else slice_planes<GC_F16>(a, c0, chunks, f, xs);
 
   auto idesc = [](int n, bool mn) {
     return (1u << 4) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
@@ -1129,13 +1155,9 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
       if (!last) {
         store16(xs, kXPlane, c, v);
       } else if (i < a.s) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int64_t j = c0 + c + e;
-          if (j < a.l)
-            put_any(a, a.tall ? j * a.ldo + i : i * a.ldo + j,
-                    __fmul_rn(v[e] * (1.0f / kUnit), a.scale));
-        }
+        if (a.odtype == GC_F32) put_slice<GC_F32>(a, i, c0 + c, v);
+        else if (a.odtype == GC_BF16) put_slice<GC_BF16>(a, i, c0 + c, v);
+        else put_slice<GC_F16>(a, i, c0 + c, v);
       }
     }
   }
