@@ -13,6 +13,13 @@
 // of a converging polynomial stay below 16, and an entry below 2^-15 loses
 // bits only against 2^-37.
 //
+// An input in 16 bits is exact in one plane (times a power of two; what X_0 is
+// beyond that is one factor for the whole matrix, put in when the sums are
+// stored): the first step's A takes one product, its B X two.  A result in bf16
+// is rounded to 8 bits: the last step's A and B X use their operands' 11 bits
+// alone, 2^-12 of each entry, which leaves the result's error (0.0017 of its
+// norm) as it is to three digits.
+//
 // A and B are symmetric: tiles below the diagonal are not computed, every
 // tile above it is stored twice, mirrored.  a is put on B's diagonal, so that
 // a step's last product needs no epilogue.
@@ -87,6 +94,8 @@ struct ProductArgs {
   uint16_t* dst;           // planes of the result, plane_size apart
   const uint16_t* prev;    // kPoly: A's planes
   int64_t pitch, plane_size;  // elements
+  int a_planes, b_planes;  // of the operands: 2, or their first alone
+  const float* phi;        // X stands for phi times its planes, or NULL: 1
   float a, b, c;
   void* out;               // kLast
   int64_t ldo;
@@ -329,10 +338,13 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N]
   constexpr bool kSym = MODE == kGram || MODE == kPoly;
   const int lane = threadIdx.x & 31;
   if (i >= a.rows) return;
+  float unit = MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
+  if (MODE != kPoly && a.phi) {
+    const float phi = __ldcg(a.phi);
+    unit *= MODE == kGram ? phi * phi : phi;
+  }
 #pragma unroll
-  for (int c = 0; c < N; ++c)
-    sum[c] = fmaf(sum[c], lost(kBK / 16, MODE), sum[c]) *
-             (MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit);
+  for (int c = 0; c < N; ++c) sum[c] = fmaf(sum[c], lost(kBK / 16, MODE), sum[c]) * unit;
   if (MODE == kLast) {
     if (a.odtype == GC_F32) store_result<GC_F32, N>(a, sum, stage, i, j);
     else if (a.odtype == GC_BF16) store_result<GC_BF16, N>(a, sum, stage, i, j);
@@ -521,6 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if constexpr (TN == 256) reg_dec<kOtherRegs>();
     if (warp == kProducerWarp) {
       const uint32_t bar0 = map_to_rank(smem_u32(s.full), 0);  // the leader counts the bytes
+      const uint32_t stage_bytes = 2 * (a.a_planes * kABytes + a.b_planes * S::kBBytes);
       after_previous();
       int st = 0;
       uint32_t ph = 0, loads = 0;
@@ -541,15 +554,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (elect_one()) {
             const uint32_t bar = bar0 + st * 8, at = s.stage0 + st * S::kStage;
-            if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * S::kStage);
-  #pragma unroll
+            if (rank == 0) mbar_arrive_expect_tx(&s.full[st], stage_bytes);
+#pragma unroll
             for (int p = 0; p < 2; ++p) {
-              tma_load_3d_pair(at + p * kABytes, &map_a, k * kBK, r0, p, bar);
+              if (p < a.a_planes)
+                tma_load_3d_pair(at + p * kABytes, &map_a, k * kBK, r0, p, bar);
+              if (p >= a.b_planes) continue;
               const uint32_t b = at + 2 * kABytes + p * S::kBBytes;
               if (!kBMN) {
                 tma_load_3d_pair(b, &map_b, k * kBK, c0, p, bar);
               } else {
-  #pragma unroll
+#pragma unroll
                 for (int h = 0; h < S::kBN / 64; ++h)
                   tma_load_3d_pair(b + h * 8192, &map_b, c0 + h * 64, k * kBK, p, bar);
               }
@@ -603,16 +618,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (elect_one()) {
               const uint32_t off = (uint32_t)st * (S::kStage >> 4), d = tmem + buf * TN;
               // the small products first: the sum is large only once hi hi is in it
-  #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk)
-                mma_f16_pair(d, a0 + off + kALo + kk * kAStep, b0 + off + kk * kBStep, hi, idesc,
-                             (in_seg | kk) ? 1u : 0u);
-  #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk)
-                mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kBLo + kk * kBStep, hi, idesc, 1u);
-  #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk)
-                mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kk * kBStep, hi, idesc, 1u);
+              uint32_t more = in_seg ? 1u : 0u;
+              auto multiply = [&](uint32_t a_at, uint32_t b_at) {
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                  mma_f16_pair(d, a0 + off + a_at + kk * kAStep, b0 + off + b_at + kk * kBStep, hi,
+                               idesc, more);
+                  more = 1u;
+                }
+              };
+              if (a.a_planes == 2) multiply(kALo, 0u);
+              if (a.b_planes == 2) multiply(0u, kBLo);
+              multiply(0u, 0u);
               mma_commit_pair(&s.empty[st]);
               if (last) mma_commit_pair(&s.acc_full[buf]);
             }
@@ -661,6 +678,8 @@ struct InputArgs {
   int parts;
   float eps;
   uint16_t* dst;
+  uint32_t* top;         // the blocks' largest magnitudes, as bits (16-bit types)
+  float* phi;            // 16-bit types: X_0 is phi times its plane
   uint32_t* arrived;     // the products' counters, set to zero
 };
 
@@ -707,27 +726,40 @@ __device__ __forceinline__ double sum_squares(const float (&v)[8]) {
   return t;
 }
 
-// kUnit / (|g| + eps) as two factors, each inside binary32's range whatever
-// the norm; NaN where g is not finite.  The sum is m 4^k with 1 <= m < 4, so
-// that root and quotient are fp32 ones (binary64's take thousands of cycles).
-__device__ __forceinline__ float2 unit_factors(double squares, float eps) {
-  if (squares == 0.0) return make_float2(0.0f, 0.0f);
-  if (!(squares <= 1.0e300)) return make_float2(NAN, NAN);
-  const long long bits = __double_as_longlong(squares);
-  const int e = (int)(bits >> 52) - 1023, k = e >> 1;
-  const float m = (float)__longlong_as_double((bits & 0xFFFFFFFFFFFFFll) |
-                                              ((long long)(1023 + e - 2 * k) << 52));
-  const float n = sqrtf(m) + ldexpf(eps, -k);
-  return make_float2(ldexpf(1.0f, -(k / 2)), ldexpf(kUnit / n, -(k - k / 2)));
-}
+// kUnit / (|g| + eps) = n 2^-k: the sum of squares is m 4^k with 1 <= m < 4,
+// so that root and quotient are fp32 ones (binary64's take thousands of
+// cycles).  n = 0 where g is zero, NaN where it is not finite.
+struct Unit {
+  float n;
+  int k;
+  __device__ __forceinline__ Unit(double squares, float eps) : n(0.0f), k(0) {
+    if (squares == 0.0) return;
+    if (!(squares <= 1.0e300)) {
+      n = NAN;
+      return;
+    }
+    const long long bits = __double_as_longlong(squares);
+    const int e = (int)(bits >> 52) - 1023;
+    k = e >> 1;
+    const float m = (float)__longlong_as_double((bits & 0xFFFFFFFFFFFFFll) |
+                                                ((long long)(1023 + e - 2 * k) << 52));
+    n = kUnit / (sqrtf(m) + ldexpf(eps, -k));
+  }
+  // as two factors, each inside binary32's range whatever the norm
+  __device__ __forceinline__ float2 factors() const {
+    return make_float2(ldexpf(1.0f, -(k / 2)), ldexpf(n, -(k - k / 2)));
+  }
+};
 
 // Sums of squares, a double per block.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ InputArgs a) {
   __shared__ double s[8];
+  __shared__ uint32_t tops[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
   double sum = 0.0;
+  uint32_t top = 0u;
   let_next_begin();
   if (blockIdx.x == 0)
     for (int k = threadIdx.x; k < kMaxPairs * 2 * kReadWarps; k += 256) a.arrived[k] = 0u;
@@ -736,27 +768,58 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
     float v[8];
     get8<DT, VEC>(v, a, r, (w - r * segs) * 256 + lane * 8);
     sum += sum_squares(v);
+    if (DT != GC_F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s[warp] = sum;
+  if (DT != GC_F32) top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) {
+    s[warp] = sum;
+    tops[warp] = top;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     double t = 0.0;
-    for (int w = 0; w < 8; ++w) t += s[w];
+    for (int w = 0; w < 8; ++w) {
+      t += s[w];
+      top = max(top, tops[w]);
+    }
     a.part[blockIdx.x] = t;
+    if (DT != GC_F32) a.top[blockIdx.x] = top;
   }
 }
 
-// The factors from the blocks' sums; the whole block calls it.
-__device__ __forceinline__ float2 unit_factors(const InputArgs& a) {
+// What g's elements are multiplied by, from the blocks' sums; the whole block
+// calls it.  fp32: kUnit / (|g| + eps).  16-bit types: the power of two that
+// brings the largest magnitude to 2^14 .. 2^15 (elements below 2^-39 of it lose
+// bits), the rest of the factor being phi.
+template <int DT>
+__device__ __forceinline__ float2 plane_factors(const InputArgs& a) {
   __shared__ float2 f;
   if (threadIdx.x < 32) {
     double t = 0.0;
-    for (int p = threadIdx.x; p < a.parts; p += 32) t += a.part[p];
+    uint32_t top = 0u;
+    for (int p = threadIdx.x; p < a.parts; p += 32) {
+      t += a.part[p];
+      if (DT != GC_F32) top = max(top, a.top[p]);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (threadIdx.x == 0) f = unit_factors(t, a.eps);
+    if (DT != GC_F32) top = __reduce_max_sync(0xffffffffu, top);
+    if (threadIdx.x == 0) {
+      const Unit u(t, a.eps);
+      if (DT == GC_F32) {
+        f = u.factors();
+      } else {
+        const bool some = u.n > 0.0f;  // neither zero nor NaN
+        const int e = some ? 14 - ilogbf(__uint_as_float(top)) : 0;
+        f = make_float2(ldexpf(1.0f, e / 2), ldexpf(1.0f, e - e / 2));
+        if (blockIdx.x == 0) *a.phi = some ? ldexpf(u.n, -u.k - e) : u.n;
+      }
+    }
   }
   __syncthreads();
   return f;
@@ -771,7 +834,7 @@ template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) orth_split_kernel(const __grid_constant__ InputArgs a) {
   after_previous();
   let_next_begin();
-  const float2 f = unit_factors(a);
+  const float2 f = plane_factors<DT>(a);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
   for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < total; w += (int64_t)gridDim.x * 8) {
@@ -785,7 +848,8 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const __grid_constant__
       split2(in_units(v[2 * e], f), in_units(v[2 * e + 1], f), h[e], l[e]);
     uint16_t* dst = a.dst + r * a.pitch + c;
     *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
+    if (DT == GC_F32)
+      *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -795,7 +859,7 @@ __global__ void __launch_bounds__(256) orth_turn_kernel(const __grid_constant__ 
   __shared__ float t[64][65];
   after_previous();
   let_next_begin();
-  const float2 f = unit_factors(a);
+  const float2 f = plane_factors<DT>(a);
   const int64_t ct = ceil_div(a.n, (int64_t)64), total = ceil_div(a.m, (int64_t)64) * ct;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const int64_t r0 = w / ct * 64, c0 = (w % ct) * 64;
@@ -814,7 +878,8 @@ __global__ void __launch_bounds__(256) orth_turn_kernel(const __grid_constant__ 
       for (int e = 0; e < 4; ++e) split2(t[r + 2 * e][c], t[r + 2 * e + 1][c], h[e], l[e]);
       uint16_t* dst = a.dst + (c0 + c) * a.pitch + r0 + r;
       *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
+      if (DT == GC_F32)
+        *reinterpret_cast<uint4*>(dst + a.plane_size) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
@@ -1024,7 +1089,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
       sum = norm_part[lane];
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) factors = unit_factors(sum, a.eps);
+    if (lane == 0) factors = Unit(sum, a.eps).factors();
   }
   __syncthreads();
   const float2 f = factors;
@@ -1219,8 +1284,8 @@ struct Deal {
   int parts;
   double cost;
 };
-Deal deal(int64_t tiles, int64_t pairs, int64_t blocks, int tn) {
-  const double block = tn == 256 ? 1.0 : 0.55, store = tn / 64.0, join = tn / 256.0;
+Deal deal(int64_t tiles, int64_t pairs, int64_t blocks, int tn, int products) {
+  const double block = (tn == 256 ? 1.0 : 0.55) * products / 3.0, store = tn / 64.0, join = tn / 256.0;
   Deal d{};
   const int64_t full = tiles / pairs * pairs, rem = tiles - full;
   d.parts = rem ? (int)std::min<int64_t>({pairs / rem, kMaxPartsOfTile, blocks}) : 1;
@@ -1282,8 +1347,9 @@ gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d
                   const ProductArgs& a) {
   constexpr bool kSym = MODE == kGram || MODE == kPoly;
   const int64_t pairs = std::min(ctx->num_sms / 2, kMaxPairs), blocks = ceil_div(x.cols, (int64_t)kBK);
-  const Deal wide = deal(count_tiles(d.rows, d.cols, 256, kSym), pairs, blocks, 256);
-  const Deal slim = deal(count_tiles(d.rows, d.cols, 128, kSym), pairs, blocks, 128);
+  const int products = a.a_planes + a.b_planes - 1;
+  const Deal wide = deal(count_tiles(d.rows, d.cols, 256, kSym), pairs, blocks, 256, products);
+  const Deal slim = deal(count_tiles(d.rows, d.cols, 128, kSym), pairs, blocks, 128, products);
   return slim.cost < wide.cost ? product<MODE, 128>(ctx, x, y, d, a, slim)
                                : product<MODE, 256>(ctx, x, y, d, a, wide);
 }
@@ -1294,6 +1360,7 @@ int64_t parts_bytes(int64_t s, int64_t l) {
   const int64_t tiles = count_tiles(s, l, 128, false);
   return std::min<int64_t>(kMaxPairs * 2, kMaxPartsOfTile * tiles) * kTM * 128 * 4;
 }
+constexpr int64_t kTopBytes = kMaxParts * 4 + 256;  // and phi
 constexpr int64_t kArrivedBytes = kMaxPairs * 2 * kReadWarps * 4;
 
 template <int DT>
@@ -1356,7 +1423,7 @@ gc_status launch_small(gc_ctx* ctx, SmallArgs& a, char* at) {
 int64_t orth_scratch_bytes(int64_t m, int64_t n) {
   if (m == 0 || n == 0) return 0;
   const int64_t s = std::min(m, n), l = std::max(m, n);
-  int64_t bytes = kMaxParts * 8 + round_up(kArrivedBytes, 256) + 2 * planes_bytes(s, l) +
+  int64_t bytes = kMaxParts * 8 + kTopBytes + round_up(kArrivedBytes, 256) + 2 * planes_bytes(s, l) +
                   2 * planes_bytes(s, s) + parts_bytes(s, l);
   if (s <= kSmallS) bytes = std::max(bytes, small_bytes(s, l));
   return bytes;
@@ -1388,6 +1455,9 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
   InputArgs in{};
   in.part = reinterpret_cast<double*>(at);
   at += kMaxParts * 8;
+  in.top = reinterpret_cast<uint32_t*>(at);
+  in.phi = reinterpret_cast<float*>(in.top + kMaxParts);
+  at += kTopBytes;
   in.arrived = reinterpret_cast<uint32_t*>(at);
   at += round_up(kArrivedBytes, 256);
   auto planes = [&](int64_t rows, int64_t cols) {
@@ -1416,14 +1486,21 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
     ProductArgs a{};
     a.part = part;
     a.arrived = in.arrived;
+    const bool exact = k == 0 && dtype != GC_F32;             // X is one plane
+    const bool rough = k + 1 == steps && odtype == GC_BF16;  // X and B by one plane
+    a.phi = exact ? in.phi : nullptr;
+    a.a_planes = a.b_planes = exact || rough ? 1 : 2;
     st = product<kGram>(ctx, x, x, gram, a);
     if (st != GC_OK) break;
     a.a = coefs[3 * k];
     a.b = coefs[3 * k + 1];
     a.c = coefs[3 * k + 2];
     a.prev = gram.at;
+    a.a_planes = a.b_planes = 2;
     st = product<kPoly>(ctx, gram, gram, poly, a);
     if (st != GC_OK) break;
+    a.a_planes = rough ? 1 : 2;
+    a.b_planes = exact || rough ? 1 : 2;
     if (k + 1 < steps) {
       st = product<kApply>(ctx, poly, x, next, a);
       std::swap(x, next);

@@ -318,3 +318,43 @@ def test_both_sides_of_the_narrow_kernel(gc, m, n, steps):
             want, err = reference(x, coefs, 1e-7, 1.0)
             check(out, want, err, "f32")
         c.check()
+
+
+@pytest.mark.parametrize("m,n", [(150, 400), (400, 150), (700, 700)])
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e-38), ("bf16", 1e-20), ("bf16", 1e36), ("f16", 1e-5), ("f16", 1e4),
+                                        ("f32", 1e-38), ("f32", 1e36)])
+@pytest.mark.parametrize("steps", [1, 3])
+def test_magnitudes_of_wider_matrices(gc, ctx, m, n, dtype, size, steps):
+    """Two orders of magnitude between the elements, at the ends of the types' ranges."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(m)
+    spread = 10.0 ** (-2.0 * torch.rand(m, n, generator=gen, device="cuda"))
+    g = (torch.randn(m, n, generator=gen, device="cuda").clamp(-4, 4) * spread * size).to(dt(dtype))
+    for out in ("f32", "bf16"):
+        o = torch.empty(m, n, dtype=dt(out), device="cuda")
+        gc.orthogonalize(ctx, g, o, steps=steps, eps=0.0, scale=1.3)
+        want, err = reference(g, [F32_QUINTIC] * steps, 0.0, 1.3)
+        # a bf16 result's last step takes X and B with 11 bits: 2^-12 of each entry, grown by the largest slope of the
+        # polynomial or, from B, as it is; 2^-11 + 4 2^-12 = 2^-9.4 of the norm at most
+        check(o, want, err + (2.0 ** -9.4 * float(torch.linalg.norm(want)) if out == "bf16" else 0.0), out)
+    ctx.check()
+
+
+@pytest.mark.parametrize("m,n", [(150, 400), (400, 150)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_zeros_and_non_finite_of_wider_matrices(gc, ctx, m, n, dtype):
+    import torch
+    out = torch.full((m, n), 7.0, dtype=dt(dtype), device="cuda")
+    for eps in (0.0, 1e-7):
+        gc.orthogonalize(ctx, torch.zeros(m, n, dtype=dt(dtype), device="cuda"), out, eps=eps)
+        assert bool((out == 0).all())
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        g = update(2, m, n, dtype, 1.0)
+        g[m // 2, n // 3] = bad
+        gc.orthogonalize(ctx, g, out)
+        assert bool(out.isnan().all())
+    # far below eps: X_0 is 0 to all its bits
+    gc.orthogonalize(ctx, update(2, m, n, dtype, 1e-4 if dtype == "f16" else 1e-30), out, eps=1e30)
+    assert bool((out == 0).all())
+    ctx.check()
