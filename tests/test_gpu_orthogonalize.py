@@ -358,3 +358,57 @@ def test_zeros_and_non_finite_of_wider_matrices(gc, ctx, m, n, dtype):
     gc.orthogonalize(ctx, update(2, m, n, dtype, 1e-4 if dtype == "f16" else 1e-30), out, eps=1e30)
     assert bool((out == 0).all())
     ctx.check()
+
+
+@pytest.mark.parametrize("m,n,dtype", [(64, 3000, "f32"), (3000, 100, "bf16"), (700, 1300, "bf16"), (1300, 260, "f16")])
+def test_capture_of_every_kernel(gc, m, n, dtype):
+    """The kernels whose blocks wait for one another, and tiles in parts, captured and replayed."""
+    import torch
+    stream = torch.cuda.Stream()
+    g = update(4, m, n, dtype, 1.0)
+    with gc.Context(0, stream) as c:
+        c.reserve_scratch(gc.orthogonalize_scratch_bytes(m, n))
+        one, two = torch.empty_like(g), torch.empty_like(g)
+        stream.wait_stream(torch.cuda.current_stream())
+        gc.orthogonalize(c, g, one)
+        c.check()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            gc.orthogonalize(c, g, two)
+        for _ in range(3):
+            two.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(one, two)
+        c.check()
+
+
+def test_two_streams_at_once(gc):
+    """Contexts of their own on streams of their own, every kernel in flight next to another's."""
+    import torch
+    sizes = [(64, 6000), (128, 20000), (500, 900), (100, 9000)]
+    gs = [update(k, m, n) for k, (m, n) in enumerate(sizes)]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    ctxs = [gc.Context(0, s) for s in streams]
+    try:
+        for c, (m, n) in zip(ctxs, sizes):
+            c.reserve_scratch(gc.orthogonalize_scratch_bytes(m, n))
+        alone = []
+        torch.cuda.synchronize()
+        for c, g in zip(ctxs, gs):
+            o = torch.empty_like(g)
+            gc.orthogonalize(c, g, o)
+            c.check()
+            alone.append(o)
+        outs = [torch.empty_like(g) for g in gs]
+        torch.cuda.synchronize()
+        for _ in range(30):
+            for c, g, o in zip(ctxs, gs, outs):
+                gc.orthogonalize(c, g, o)
+        for c, o, a in zip(ctxs, outs, alone):
+            c.check()
+            assert torch.equal(o, a)
+    finally:
+        for c in ctxs:
+            c.close()

@@ -306,3 +306,45 @@ def test_refusals(gc, ctx):
         assert e.value.status == gc.ERR_WORKSPACE
         gc.rmsnorm_backward(bare, x, None, x, g, rstd, out_matrix(4, 64, "bf16")[0])  # no dgamma
         bare.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", [(200, 600), (153, 1056), (311, 4099), (460, 4096), (170, 11008), (155, 13800),
+                                       (155, 15800)])
+@pytest.mark.parametrize("pad,ptype,with_res", [(0, "f32", True), (3, "bf16", False), (1, None, True)])
+def test_more_rows_than_multiprocessors(gc, ctx, dtype, rows, cols, pad, ptype, with_res):
+    """Rows through the ring of stages: the same checks as above."""
+    test_forward_and_backward(gc, ctx, dtype, rows, cols, pad, ptype, with_res)
+
+
+@pytest.mark.parametrize("cols", [40, 700, 4100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_non_finite_rows_stay_alone(gc, ctx, cols, dtype):
+    """Among many rows: an infinity, a NaN and zeros change no other row."""
+    import torch
+    rows = 400
+    r = np.random.default_rng(cols)
+    x = r.standard_normal((rows, cols)).astype(np.float32)
+    clean, _, _ = matrix(x, dtype, 1)
+    x[7] = 0.0
+    x[190, 3], x[191, cols - 1], x[399, 0] = np.inf, np.nan, -np.inf
+    bad = [190, 191, 399]
+    m, _, _ = matrix(x, dtype, 1)
+    outs = [forward(gc, ctx, a, None, None, 1) for a in (clean, m)]
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[bad + [7]] = False
+    assert torch.equal(outs[0][1][keep], outs[1][1][keep])
+    assert bool((outs[1][1][7] == 0).all())
+    for b in bad:
+        assert bool(outs[1][1][b].isnan().any())
+    dy, _, _ = matrix(r.standard_normal((rows, cols)), dtype)
+    dxs = []
+    for h, _, rstd, hc, _ in outs:
+        for whole in (True, False):
+            dx, _ = out_matrix(rows, cols, dtype)
+            gc.rmsnorm_backward(ctx, dy, dy, h if whole else None, None, rstd, dx, None, *((None, None) if whole else hc))
+            dxs.append(dx)
+    for a, b in ((dxs[0], dxs[2]), (dxs[1], dxs[3])):
+        assert torch.equal(a[keep], b[keep])
+        assert bool(b[191].isnan().all()) and bool(torch.isfinite(b[7]).all())
+    ctx.check()
