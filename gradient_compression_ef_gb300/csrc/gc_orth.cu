@@ -20,8 +20,8 @@
 // alone, 2^-12 of each entry, which leaves the result's error (0.0017 of its
 // norm) as it is to three digits.
 //
-// A and B are symmetric: tiles below the diagonal are not computed, every
-// tile above it is stored twice, mirrored.  a is put on B's diagonal, so that
+// A and B are symmetric: tiles below the diagonal are not computed, what lies
+// above it is stored twice, mirrored.  a is put on B's diagonal, so that
 // a step's last product needs no epilogue.
 //
 // A product: one persistent CTA pair per two SMs (cta_group::2) owns tiles of
@@ -231,36 +231,33 @@ __device__ __forceinline__ uint4 staged_column(uint32_t stage, int c) {
   return v;
 }
 
-// Elements [lo, hi) of 8 fp16 ones.
-__device__ __forceinline__ void store_halves(uint16_t* p, const uint4& r, int lo, int hi) {
-  store_some<GC_F16>(reinterpret_cast<char*>(p), r, lo, hi);
-}
-
 // One plane of 64 columns from j on of the warp's 32 rows from i on, staged,
-// and of a symmetric result their mirror image.
+// and of a symmetric result their mirror image: a group of 8 columns of a row
+// that lies below the diagonal to its last element is the mirror's, every other
+// one the row's own, so that each element is written once.  (Short code: a
+// tile's epilogue runs once or a few times in a kernel, and fetching its
+// instructions was half of its time.)
 template <bool SYM>
 __device__ __forceinline__ void store_plane(const ProductArgs& a, uint16_t* dst, uint32_t stage,
                                             int64_t i, int64_t j) {
   const int lane = threadIdx.x & 31;
+  const int rows = (int)min((int64_t)32, a.rows - i), cols = (int)min((int64_t)64, a.cols - j);
+  const int d = (int)min((int64_t)64, j - i);  // >= -63
+  uint16_t* p = dst + (i + (lane >> 3)) * a.pitch + j + (lane & 7) * 8;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t r = i + k * 4 + (lane >> 3), c = j + (lane & 7) * 8;
-    if (r >= a.rows || c >= a.cols || (SYM && c + 7 < r)) continue;
-    const uint4 v = sm100::lds_u128(staged(stage, k * 4 + (lane >> 3), lane & 7));
-    uint16_t* p = dst + r * a.pitch + c;
+  for (int k = 0; k < 8; ++k, p += 4 * a.pitch) {
+    const int r = k * 4 + (lane >> 3), c = (lane & 7) * 8;
+    const uint4 v = sm100::lds_u128(staged(stage, r, lane & 7));
     // rows of planes are padded to whole groups of 8
-    if (!SYM || c >= r) *reinterpret_cast<uint4*>(p) = v;
-    else store_halves(p, v, (int)(r - c), 8);  // the group that the diagonal cuts
+    if (r < rows && c < cols && (!SYM || c + 7 + d >= r)) *reinterpret_cast<uint4*>(p) = v;
   }
   if (!SYM) return;
+  p = dst + (j + (lane >> 2)) * a.pitch + i + (lane & 3) * 8;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < 8; ++k, p += 8 * a.pitch) {
+    const int r = (lane & 3) * 8, c = k * 8 + (lane >> 2);
     const uint4 v = staged_column(stage, k);
-    const int64_t c = j + k * 8 + (lane >> 2), r = i + (lane & 3) * 8;
-    if (c >= a.cols || r >= c) continue;
-    uint16_t* p = dst + c * a.pitch + r;
-    if (r + 7 < c) *reinterpret_cast<uint4*>(p) = v;
-    else store_halves(p, v, 0, (int)(c - r));
+    if (c < cols && r + 7 < c + d) *reinterpret_cast<uint4*>(p) = v;
   }
 }
 
@@ -358,20 +355,25 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N]
     if (MODE == kPoly) {
 #pragma unroll
       for (int e = 0; e < 64; ++e) sum[c0 + e] *= a.c;
+      // plus b A, read by rows, both planes at once
+      const uint16_t* src = a.prev + (i + (lane >> 3)) * a.pitch + jc + (lane & 7) * 8;
+      const bool in = jc + (lane & 7) * 8 < a.cols;
+      uint4 q[2][8];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {  // plus b A, read by rows
-        uint4 q[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int64_t r = i + k * 4 + (lane >> 3), c = jc + (lane & 7) * 8;
-          q[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < a.rows && c < a.cols)
-            q[k] = __ldcg(reinterpret_cast<const uint4*>(a.prev + p * a.plane_size + r * a.pitch + c));
+      for (int k = 0; k < 8; ++k, src += 4 * a.pitch) {
+        q[0][k] = q[1][k] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && i + k * 4 + (lane >> 3) < a.rows) {
+          q[0][k] = __ldcg(reinterpret_cast<const uint4*>(src));
+          q[1][k] = __ldcg(reinterpret_cast<const uint4*>(src + a.plane_size));
         }
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          sts_u128(staged(stage, k * 4 + (lane >> 3), lane & 7), q[k].x, q[k].y, q[k].z, q[k].w);
+          sts_u128(staged(stage, k * 4 + (lane >> 3), lane & 7), q[p][k].x, q[p][k].y, q[p][k].z,
+                   q[p][k].w);
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -385,26 +387,45 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N]
           }
         }
       }
-      const int64_t d = i + lane - jc;  // the diagonal's column
+      if (jc < i + 32) {  // the diagonal comes through
+        const int64_t d = i + lane - jc;
 #pragma unroll
-      for (int e = 0; e < 64; ++e)
-        if (e == d) sum[c0 + e] += a.a * kUnit;
-    }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          split2(sum[c0 + k * 8 + 2 * e], sum[c0 + k * 8 + 2 * e + 1], h[e], l[e]);
-        if (p == 0) sts_u128(staged(stage, lane, k), h[0], h[1], h[2], h[3]);
-        else sts_u128(staged(stage, lane, k), l[0], l[1], l[2], l[3]);
+        for (int e = 0; e < 64; ++e)
+          if (e == d) sum[c0 + e] += a.a * kUnit;
       }
-      __syncwarp();
-      store_plane<kSym>(a, a.dst + p * a.plane_size, stage, i, jc);
     }
+    // the first planes; what is left of the values are the second ones
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float* t = sum + c0 + k * 8 + 2 * e;
+        const __half2 w = __floats2half2_rn(t[0], t[1]);
+        const float2 f = __half22float2(w);
+        t[0] = __fsub_rn(t[0], f.x);
+        t[1] = __fsub_rn(t[1], f.y);
+        h[e] = *reinterpret_cast<const uint32_t*>(&w);
+      }
+      sts_u128(staged(stage, lane, k), h[0], h[1], h[2], h[3]);
+    }
+    __syncwarp();
+    store_plane<kSym>(a, a.dst, stage, i, jc);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* t = sum + c0 + k * 8 + 2 * e;
+        const __half2 w = __floats2half2_rn(t[0], t[1]);
+        l[e] = *reinterpret_cast<const uint32_t*>(&w);
+      }
+      sts_u128(staged(stage, lane, k), l[0], l[1], l[2], l[3]);
+    }
+    __syncwarp();
+    store_plane<kSym>(a, a.dst + a.plane_size, stage, i, jc);
   }
 }
 
@@ -466,6 +487,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int32_t blocks = (int32_t)((a.sum + kBK - 1) / kBK);
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&s.full[i], 1);
