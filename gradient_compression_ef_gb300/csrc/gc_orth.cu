@@ -1301,23 +1301,25 @@ bool make_map(CUtensorMap* map, const Planes& p, uint32_t box_rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How T tiles are dealt to the pairs, and what that costs in blocks of 256
-// columns (a block of 128 columns takes a bit more than half of it, storing a
-// tile about four, joining a part about one).
+// How T tiles are dealt to the pairs, and what that costs in cycles, as measured:
+// a block of 64 of the sum, a tile's epilogue, a part's way through memory and
+// its share of the joining, for tiles of 256 and of 128 columns.
 struct Deal {
   int64_t whole, items;
   int parts;
   double cost;
 };
 Deal deal(int64_t tiles, int64_t pairs, int64_t blocks, int tn, int products) {
-  const double block = (tn == 256 ? 1.0 : 0.55) * products / 3.0, store = tn / 64.0, join = tn / 256.0;
-  Deal d{};
+  const double block = (tn == 256 ? 1540 : 820) * products / 3.0, store = tn == 256 ? 7000 : 4500;
+  const double leave = tn == 256 ? 5000 : 4000, join = tn == 256 ? 2200 : 1300;
   const int64_t full = tiles / pairs * pairs, rem = tiles - full;
-  d.parts = rem ? (int)std::min<int64_t>({pairs / rem, kMaxPartsOfTile, blocks}) : 1;
-  d.whole = d.parts > 1 ? full : tiles;
-  d.items = d.whole + (d.parts > 1 ? rem * d.parts : 0);
-  d.cost = (double)(full / pairs) * ((double)blocks * block + store);
-  if (rem) d.cost += (double)ceil_div(blocks, (int64_t)d.parts) * block + store + d.parts * join;
+  Deal d{tiles, tiles, 1, (double)ceil_div(tiles, pairs) * ((double)blocks * block + store)};
+  if (!rem) return d;
+  for (int p = 2; p <= std::min<int64_t>({pairs / rem, kMaxPartsOfTile, blocks}); ++p) {
+    const double cost = (double)(full / pairs) * ((double)blocks * block + store) +
+                        (double)ceil_div(blocks, (int64_t)p) * block + leave + p * join + store;
+    if (cost < d.cost) d = {full, full + rem * p, p, cost};
+  }
   return d;
 }
 
