@@ -210,8 +210,13 @@ __global__ void __launch_bounds__(1024)
 
 constexpr int kMaxStages = 6;
 constexpr int kCols = 16;          // columns per thread
-constexpr int kForwardRegs = 64;   // 32 warps per SM
-constexpr int kBackwardRegs = 72;  // 28 warps per SM
+// Registers a thread: the first where a block's warps fit with them, the second
+// for wider rows.  (A kernel that spills pays twice beside a ring: shared memory
+// leaves the L1 nothing to keep the spilled in.  Backward at 72 registers, three
+// blocks per SM, 3001 x 4099 fp32: 59 us, at 96, two blocks: 45.)
+constexpr int kForwardRegs[2] = {80, 64}, kBackwardRegs[2] = {96, 80};
+// warps that an SM's four register files hold
+constexpr int warps_at(int regs) { return 16384 / (32 * regs) * 4; }
 
 // One thread's part: row `row` into a stage.  Forward: x, res.  BACK: dy,
 // dres, then h or its checkpoint.
@@ -291,8 +296,8 @@ __device__ __forceinline__ uint32_t shift_of(const char* p, int64_t pitch, int64
   return ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)row * (uint32_t)pitch) & 15u;
 }
 
-template <int DT, int ROWS>
-__global__ void __maxnreg__(kForwardRegs)
+template <int DT, int ROWS, int REGS>
+__global__ void __maxnreg__(REGS)
     rms_forward_ring_kernel(const __grid_constant__ RmsArgs a) {
   using namespace sm100;
   constexpr int V = Elem<DT>::V, K = kCols / V;
@@ -549,8 +554,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512)
 
 // The same through the ring: dy and h are read from the stage in both passes,
 // so that a thread keeps gamma and the column sums alone.
-template <int DT, bool CKPT, int ROWS>
-__global__ void __maxnreg__(kBackwardRegs)
+template <int DT, bool CKPT, int ROWS, int REGS>
+__global__ void __maxnreg__(REGS)
     rms_backward_ring_kernel(const __grid_constant__ RmsArgs a) {
   using namespace sm100;
   constexpr int V = Elem<DT>::V, K = kCols / V, H = V / 2;
@@ -767,6 +772,7 @@ Shape pick(int64_t units, int64_t rows, int sms, int most, int deep, int per_sm)
 // memory.
 struct RingPlan {
   int threads, per_sm;  // threads of the rows; 0: not this way
+  int regs;             // which of the two
   unsigned smem;
 };
 
@@ -778,11 +784,12 @@ int64_t block_smem(int n) { return 228 * 1024 / n / 128 * 128 - 1024 - kStaticSm
 
 RingPlan plan_ring(const gc_ctx* ctx, RmsArgs& a, int dtype, bool back) {
   RingPlan p{};
-  const int warps = 65536 / (32 * (back ? kBackwardRegs : kForwardRegs));  // per SM
   const int64_t c = ckpt_codes_pitch(a.cols);
-  if (a.rows <= ctx->num_sms || c * elem_size(dtype) <= 2048 ||
-      c > (std::min(warps, 32) - 1) * 32 * kCols)
-    return p;
+  const int threads = (int)round_up(ceil_div(c, (int64_t)kCols), 32);
+  const int* regs = back ? kBackwardRegs : kForwardRegs;
+  p.regs = threads / 32 + 1 <= warps_at(regs[0]) ? 0 : 1;
+  const int warps = warps_at(regs[p.regs]);
+  if (a.rows <= ctx->num_sms || c * elem_size(dtype) <= 2048 || threads / 32 + 1 > warps) return p;
   const int64_t row = round_up(a.row_bytes + 30, 128);  // with a shifted start
   int64_t bytes = row;
   a.second_at = (uint32_t)bytes;
@@ -792,7 +799,6 @@ RingPlan plan_ring(const gc_ctx* ctx, RmsArgs& a, int dtype, bool back) {
   a.scales_at = (uint32_t)bytes;
   if (back && a.codes) bytes += round_up(a.scales_pitch, 128);
   a.stage_bytes = (uint32_t)bytes;
-  const int threads = (int)round_up(ceil_div(c, (int64_t)kCols), 32);
   p.per_sm = warps / (threads / 32 + 1);
   while (p.per_sm > 1 && 2 * bytes > block_smem(p.per_sm)) --p.per_sm;
   a.stages = (int)std::min<int64_t>(kMaxStages, block_smem(p.per_sm) / bytes);
@@ -810,15 +816,28 @@ void launch_ring(gc_ctx* ctx, const RmsArgs& a, const RingPlan& p, unsigned grid
   Kernel<<<grid, p.threads + 32, p.smem, ctx->stream>>>(a);
 }
 
+template <int DT, int REGS>
+void forward_ring(gc_ctx* ctx, const RmsArgs& a, const RingPlan& p, unsigned grid, bool aligned) {
+  if (!aligned) launch_ring<rms_forward_ring_kernel<DT, kAnywhere, REGS>>(ctx, a, p, grid);
+  else if (a.cols == (int64_t)p.threads * kCols)
+    launch_ring<rms_forward_ring_kernel<DT, kFull, REGS>>(ctx, a, p, grid);
+  else launch_ring<rms_forward_ring_kernel<DT, kEnds, REGS>>(ctx, a, p, grid);
+}
+template <int DT, bool CKPT, int REGS>
+void backward_ring(gc_ctx* ctx, const RmsArgs& a, const RingPlan& p, unsigned grid, bool aligned) {
+  if (!aligned) launch_ring<rms_backward_ring_kernel<DT, CKPT, kAnywhere, REGS>>(ctx, a, p, grid);
+  else if (a.cols == (int64_t)p.threads * kCols)
+    launch_ring<rms_backward_ring_kernel<DT, CKPT, kFull, REGS>>(ctx, a, p, grid);
+  else launch_ring<rms_backward_ring_kernel<DT, CKPT, kEnds, REGS>>(ctx, a, p, grid);
+}
+
 template <int DT, bool ALIGNED>
 void forward(gc_ctx* ctx, RmsArgs& a) {
   if (const RingPlan p = plan_ring(ctx, a, DT, false); p.threads) {
     LaunchScope L(ctx, GC_PHASE_RMS_FORWARD);
     const unsigned g = (unsigned)std::min<int64_t>(a.rows, (int64_t)ctx->num_sms * p.per_sm);
-    if (!ALIGNED) launch_ring<rms_forward_ring_kernel<DT, kAnywhere>>(ctx, a, p, g);
-    else if (a.cols == (int64_t)p.threads * kCols)
-      launch_ring<rms_forward_ring_kernel<DT, kFull>>(ctx, a, p, g);
-    else launch_ring<rms_forward_ring_kernel<DT, kEnds>>(ctx, a, p, g);
+    if (p.regs) forward_ring<DT, kForwardRegs[1]>(ctx, a, p, g, ALIGNED);
+    else forward_ring<DT, kForwardRegs[0]>(ctx, a, p, g, ALIGNED);
     return;
   }
   const Shape s = pick(ceil_div(a.row_bytes, (int64_t)16), a.rows, ctx->num_sms, 1024, 2, 1024);
@@ -843,10 +862,8 @@ gc_status backward(gc_ctx* ctx, RmsArgs& a) {
     s.wide = false;
     s.grid = (unsigned)std::min<int64_t>(
         {a.rows, (int64_t)ctx->num_sms * p.per_sm, kMaxParts});
-    if (!ALIGNED) launch_ring<rms_backward_ring_kernel<DT, CKPT, kAnywhere>>(ctx, a, p, s.grid);
-    else if (a.cols == (int64_t)p.threads * kCols)
-      launch_ring<rms_backward_ring_kernel<DT, CKPT, kFull>>(ctx, a, p, s.grid);
-    else launch_ring<rms_backward_ring_kernel<DT, CKPT, kEnds>>(ctx, a, p, s.grid);
+    if (p.regs) backward_ring<DT, CKPT, kBackwardRegs[1]>(ctx, a, p, s.grid, ALIGNED);
+    else backward_ring<DT, CKPT, kBackwardRegs[0]>(ctx, a, p, s.grid, ALIGNED);
   } else {
     LaunchScope L(ctx, GC_PHASE_RMS_BACKWARD);
     const auto kernel =
