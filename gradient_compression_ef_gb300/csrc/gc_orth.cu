@@ -452,20 +452,23 @@ __device__ __forceinline__ bool join_parts(const ProductArgs& a, float (&sum)[N]
   if (before != (uint32_t)a.parts - 1u) return false;
   __threadfence();
   if (lane == 0) *count = 0u;  // as it was, for the next product
-  constexpr int kBatch = 16;  // loads in flight
+#pragma unroll
+  for (int c = 0; c < N; ++c) sum[c] = 0.0f;
   for (int p = 0; p < a.parts; ++p) {
+    const float4* src = at(p);
+    constexpr int kBatch = 16;  // loads in flight
 #pragma unroll
     for (int c0 = 0; c0 < N; c0 += 4 * kBatch) {
       float4 f[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) f[k] = __ldcg(at(p) + (c0 + 4 * k) * 8);
+      for (int k = 0; k < kBatch; ++k) f[k] = __ldcg(src + (c0 + 4 * k) * 8);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         float* t = sum + c0 + 4 * k;
-        t[0] = p ? t[0] + f[k].x : f[k].x;
-        t[1] = p ? t[1] + f[k].y : f[k].y;
-        t[2] = p ? t[2] + f[k].z : f[k].z;
-        t[3] = p ? t[3] + f[k].w : f[k].w;
+        t[0] += f[k].x;
+        t[1] += f[k].y;
+        t[2] += f[k].z;
+        t[3] += f[k].w;
       }
     }
   }
