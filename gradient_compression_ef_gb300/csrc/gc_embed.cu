@@ -4,15 +4,26 @@
 //   gradient  dtable[v] (+)= scale sum of dy[t] over the tokens t with
 //             ids[t] = v, in ascending order of t
 //
-// The gradient sorts (id, token) pairs, stable, then sums runs of one id:
-//   sort      few tokens: each pair's place is the number of pairs before it,
-//             counted; more: radix passes of 8 bits (counts, their sums, places)
-//   sum       a warp takes 64 sorted tokens and 512 bytes of their rows, and
-//             stores each run's sum once: to the table's row where the run lies
-//             inside the 64, else to a partial row; warps of their own write
-//             zeros to the rows of ids that do not occur
+// Up to 256 tokens take one launch: the first token of each id sums the rows of
+// all that have it.  More are sorted as (id, token) pairs, stable, and runs of
+// one id are summed:
+//   sort      up to 8192 tokens: each pair's place is the number of pairs
+//             before it, counted (5003 tokens 13 us, two radix passes 17);
+//             more: radix passes of up to 9 bits, each of which makes the next
+//             one's counts on its way (16384 tokens 18 us)
+//   sum       a warp takes 8 to 64 sorted tokens and 512 bytes of their rows,
+//             and stores each run's sum once: to the table's row where the run
+//             lies inside its tokens, else to a partial row; blocks of their own
+//             write zeros to the rows of ids that do not occur
 //   join      the partial rows of a run that crosses chunks, in their order
-// No atomics on floats: an order of additions that the ids alone decide.
+// The order of additions is one that ids and sizes alone decide; what is added
+// to the table goes by reductions in L2, one for each place and call.
+//
+// Measured (plain copy: 6.79 TB/s): 16384 tokens, table of 32768 x 4096 bf16:
+// lookup 34 us (4.9 TB/s), sort 18, sums and zeros 107 (6.2 TB/s), join 8;
+// together 172 (floor 126).  5003 x 1001 fp32 on 4-byte boundaries, added to
+// 50021 rows: 12 + 13 + 20 + 7 us, launches and round trips, not bytes (floor
+// 10).  100 tokens x 512: 3.9 + 6.1 us, of which fetching code is a third.
 #include <algorithm>
 #include <type_traits>
 

@@ -8,11 +8,23 @@
 //             dx_j = rstd (d_j - n_j sum(d n) / cols) + dres_j,
 //             dgamma_j = sum over rows of dy_j n_j
 //
-// A row lives in the registers of the threads that own it (a warp, or a
-// block), so each input is read once; the next row is loaded while this one's
-// sum is taken.  Sums are fp32, in an order that sizes alone decide.  Bound by
-// memory: forward 2 inputs and up to 2 outputs with their codes, backward 3
-// inputs and one output, 10 to 20 instructions per element.
+// Each input is read once; sums are fp32, in an order that sizes alone decide.
+// Bound by memory: forward 2 inputs and up to 2 outputs with their codes,
+// backward 3 inputs and one output, 10 to 20 instructions per element.
+//   more rows than SMs, 2 KB  a block walks over rows that bulk copies bring
+//   to 11776 (forward 15872)  into a ring of stages, a producer warp ahead of
+//   columns, two rows fit     it; 16 columns per thread, gamma and the column
+//                             sums in registers; backward the second pass reads
+//                             the stage again
+//   narrower, or few rows     a row in the registers of a warp or a block, the
+//                             next one loaded ahead
+//   wider still               the row is read again from L2
+//
+// Measured (plain copy: 6.79 TB/s), forward and backward: 16384 x 4096 bf16 with
+// checkpoints 109 us (6.2 TB/s) and 76 + 5 (6.2); 3001 x 4099 fp32 on 4-byte
+// boundaries 50 (4.1) and 44 + 5 (4.5), the shifting of each unit into place;
+// 2048 x 11008 fp16 43 (4.2) and 40 + 6 (4.0), one block per SM, whose sum over
+// 22 warps nothing hides.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>

@@ -748,8 +748,9 @@ GC_API int64_t gc_rmsnorm_scratch_bytes(int64_t rows, int64_t cols);
  *   dx = rstd * (d - n * sum(d * n) / cols) + dres   (the gradient of x and of
  *   res), dgamma (+)= sum over rows of dy * n.
  * dres: the gradient that arrives at h along the residual stream, or NULL (0).
- * rstd: the forward call's.  dgamma: fp32[cols] or NULL.  GC_ERR_WORKSPACE when
- * less than gc_rmsnorm_scratch_bytes is reserved (and dgamma is asked for).
+ * rstd: the forward call's.  dgamma: fp32[cols] or NULL.  No output may alias
+ * an input.  GC_ERR_WORKSPACE when less than gc_rmsnorm_scratch_bytes is
+ * reserved (and dgamma is asked for).
  */
 GC_API gc_status gc_rmsnorm_backward(gc_ctx* ctx, const void* dy, int64_t lddy, const void* dres,
                                      int64_t lddres, const void* h, int64_t ldh,
@@ -780,8 +781,8 @@ GC_API int64_t gc_embedding_scratch_bytes(int64_t tokens, int64_t vocab, int64_t
  * the flat gradient; without accumulate the rows of ids that do not occur are
  * set to zero, with it they are not touched.  Tokens whose id is `pad` add
  * nothing, nor do those outside the table, which set the device status as
- * above.  The tokens are sorted by id (stable) and added in an order that the
- * ids alone decide: the same bits on every call.  GC_ERR_WORKSPACE when less
+ * above.  An id's tokens are added in ascending order, in runs that the ids and
+ * sizes alone decide: the same bits on every call.  GC_ERR_WORKSPACE when less
  * than gc_embedding_scratch_bytes is reserved; GC_ERR_UNSUPPORTED above 2^31
  * blocks of 64 tokens x 4096 bytes.
  */
@@ -805,7 +806,8 @@ GC_API int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n);
  * steps >= 1.  g: [m, n] of type dtype; out: [m, n] of type odtype; either may
  * start at any element (a slice of the flat gradient), and out may be g itself.
  * The iterates are held in 22 bits and products are added in fp32: the error is
- * that of fp32 products, as long as no element of X, A = X X^T or
+ * that of fp32 products (a bf16 out takes X and B of the last step with 11 bits,
+ * which adds up to 5e-4 of its norm to its own rounding's 1.7e-3), as long as no element of X, A = X X^T or
  * a I + b A + c A A reaches 16 in magnitude (it comes out as infinity and then
  * NaN); with |X_0| <= 1 a polynomial that keeps singular values below 2 stays
  * far from it.  A g of zeros gives zeros; one with an infinity or NaN gives NaN
