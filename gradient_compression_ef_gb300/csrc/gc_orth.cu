@@ -1395,10 +1395,10 @@ gc_status product(gc_ctx* ctx, const Planes& x, const Planes& y, const Planes& d
 }
 
 // Scratch of the tiles in parts: at most kMaxPairs items of work, and no more
-// than kMaxPartsOfTile for each tile of 128 columns.
+// than kMaxPartsOfTile for each tile, of 256 columns or of twice as many of 128.
 int64_t parts_bytes(int64_t s, int64_t l) {
-  const int64_t tiles = count_tiles(s, l, 128, false);
-  return std::min<int64_t>(kMaxPairs * 2, kMaxPartsOfTile * tiles) * kTM * 128 * 4;
+  const int64_t tiles = count_tiles(s, l, 256, false);
+  return std::min<int64_t>(kMaxPairs, kMaxPartsOfTile * tiles) * kTM * 256 * 4;
 }
 constexpr int64_t kTopBytes = kMaxParts * 4 + 256;  // and phi
 constexpr int64_t kArrivedBytes = kMaxPairs * 2 * kReadWarps * 4;
