@@ -20,9 +20,9 @@
 // to the table goes by reductions in L2, one for each place and call.
 //
 // Measured (plain copy: 6.79 TB/s): 16384 tokens, table of 32768 x 4096 bf16:
-// lookup 34 us (4.9 TB/s), sort 18, sums and zeros 107 (6.2 TB/s), join 8;
-// together 172 (floor 126).  5003 x 1001 fp32 on 4-byte boundaries, added to
-// 50021 rows: 12 + 13 + 20 + 7 us, launches and round trips, not bytes (floor
+// lookup 28 us (5.9 TB/s), sort 18, sums and zeros 107 (6.2 TB/s), join 8;
+// together 167 (floor 126).  5003 x 1001 fp32 on 4-byte boundaries, added to
+// 50021 rows: 11 + 13 + 20 + 6 us, launches and round trips, not bytes (floor
 // 10).  100 tokens x 512: 3.9 + 6.1 us, of which fetching code is a third.
 #include <algorithm>
 #include <type_traits>
@@ -587,12 +587,20 @@ unsigned warps_grid(const gc_ctx* ctx, int64_t warps, int per_sm) {
   return (unsigned)std::min<int64_t>(ceil_div(warps, (int64_t)8), (int64_t)ctx->num_sms * per_sm);
 }
 
+template <int DT, int U>
+void lookup_runs(gc_ctx* ctx, const EmbedArgs& a, bool aligned) {
+  const unsigned g = warps_grid(ctx, a.tokens * ceil_div(a.row_bytes, (int64_t)(512 * U)), 8);
+  if (aligned) embed_forward_kernel<DT, U, true><<<g, 256, 0, ctx->stream>>>(a);
+  else embed_forward_kernel<DT, U, false><<<g, 256, 0, ctx->stream>>>(a);
+}
+// Runs of 2 KB where rows have as many and there is one for every warp that the
+// GPU takes (16384 x 4096 bf16: 28 us, by runs of 1 KB 34), of 1 KB elsewhere.
 template <int DT>
 void lookup(gc_ctx* ctx, const EmbedArgs& a, bool aligned) {
   LaunchScope L(ctx, GC_PHASE_EMBED_FORWARD);
-  const unsigned g = warps_grid(ctx, a.tokens * ceil_div(a.row_bytes, (int64_t)1024), 8);
-  if (aligned) embed_forward_kernel<DT, 2, true><<<g, 256, 0, ctx->stream>>>(a);
-  else embed_forward_kernel<DT, 2, false><<<g, 256, 0, ctx->stream>>>(a);
+  const bool wide = a.row_bytes >= 2048 && a.tokens * a.row_bytes >= (int64_t)ctx->num_sms * 64 * 2048;
+  if (wide) lookup_runs<DT, 4>(ctx, a, aligned);
+  else lookup_runs<DT, 2>(ctx, a, aligned);
 }
 template <int PT, int DT>
 void lookup_cast(gc_ctx* ctx, const EmbedArgs& a, bool aligned) {
