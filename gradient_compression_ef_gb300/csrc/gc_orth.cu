@@ -985,18 +985,32 @@ __device__ __forceinline__ void slice_place(const SmallArgs& a, int chunks, int 
   c = a.tall ? w / a.s16 : w % chunks;
 }
 
-// The slice's sum of squares (a thread's part).  (Loops that are not unrolled:
-// in a kernel that runs once through its code, fetching the code counts.)
+// The slice's sum of squares (a thread's part); the elements are kept at `hold`
+// (shared memory), if that is not 0, in fp32.  (Loops that are not unrolled: in
+// a kernel that runs once through its code, fetching the code counts.)
 template <int DT>
-__device__ __forceinline__ double slice_squares(const SmallArgs& a, int64_t c0, int chunks) {
+__device__ __forceinline__ double slice_squares(const SmallArgs& a, int64_t c0, int chunks,
+                                                uint32_t hold) {
+  const int total = a.s16 * chunks;
   double sum = 0.0;
 #pragma unroll 1
-  for (int w = threadIdx.x; w < a.s16 * chunks; w += 256) {
-    int r, c;
-    slice_place(a, chunks, w, r, c);
-    float v[8];
-    get_slice<DT>(v, a, r, c0 + c * 8);
-    sum += sum_squares(v);
+  for (int w0 = threadIdx.x; w0 < total; w0 += 4 * 256) {
+    float v[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      int r, c;
+      slice_place(a, chunks, w0 + k * 256, r, c);
+      get_slice<DT>(v[k], a, r, c0 + c * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int w = w0 + k * 256;
+      if (w >= total) break;  // another slice's, or nothing
+      sum += sum_squares(v[k]);
+      if (!hold) continue;
+      sm100::sts128(hold + w * 32, make_float4(v[k][0], v[k][1], v[k][2], v[k][3]));
+      sm100::sts128(hold + w * 32 + 16, make_float4(v[k][4], v[k][5], v[k][6], v[k][7]));
+    }
   }
   return sum;
 }
@@ -1004,13 +1018,19 @@ __device__ __forceinline__ double slice_squares(const SmallArgs& a, int64_t c0, 
 // The slice, in units, to its planes.
 template <int DT>
 __device__ __forceinline__ void slice_planes(const SmallArgs& a, int64_t c0, int chunks, float2 f,
-                                             uint32_t xs) {
+                                             uint32_t xs, uint32_t hold) {
 #pragma unroll 1
   for (int w = threadIdx.x; w < a.s16 * chunks; w += 256) {
     int r, c;
     slice_place(a, chunks, w, r, c);
     float v[8];
-    get_slice<DT>(v, a, r, c0 + c * 8);
+    if (hold) {
+      const float4 p = sm100::lds128(hold + w * 32), q = sm100::lds128(hold + w * 32 + 16);
+      v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
+      v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+    } else {
+      get_slice<DT>(v, a, r, c0 + c * 8);
+    }
     const int64_t left = r < a.s ? a.l - c0 - c * 8 : 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = e < left ? in_units(v[e], f) : 0.0f;
@@ -1101,9 +1121,11 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
 
   // the slice's sum of squares
   const int chunks = xpad / 8;
-  double sum = a.dtype == GC_F32    ? slice_squares<GC_F32>(a, c0, chunks)
-               : a.dtype == GC_BF16 ? slice_squares<GC_BF16>(a, c0, chunks)
-                                    : slice_squares<GC_F16>(a, c0, chunks);
+  // A's place holds g's slice until the planes are made, where it fits
+  const uint32_t hold = a.s16 * xpad * 4 <= (int)(2 * kAPlane) ? as : 0u;
+  double sum = a.dtype == GC_F32    ? slice_squares<GC_F32>(a, c0, chunks, hold)
+               : a.dtype == GC_BF16 ? slice_squares<GC_BF16>(a, c0, chunks, hold)
+                                    : slice_squares<GC_F16>(a, c0, chunks, hold);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) norm_part[warp] = sum;
@@ -1131,9 +1153,9 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
   }
   __syncthreads();
   const float2 f = factors;
-  if (a.dtype == GC_F32) slice_planes<GC_F32>(a, c0, chunks, f, xs);
-  else if (a.dtype == GC_BF16) slice_planes<GC_BF16>(a, c0, chunks, f, xs);
-  else slice_planes<GC_F16>(a, c0, chunks, f, xs);
+  if (a.dtype == GC_F32) slice_planes<GC_F32>(a, c0, chunks, f, xs, hold);
+  else if (a.dtype == GC_BF16) slice_planes<GC_BF16>(a, c0, chunks, f, xs, hold);
+  else slice_planes<GC_F16>(a, c0, chunks, f, xs, hold);
 
   auto idesc = [](int n, bool mn) {
     return (1u << 4) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
