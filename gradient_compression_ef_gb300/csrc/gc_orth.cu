@@ -68,6 +68,7 @@ static_assert(8 * kReadRegs + 4 * kOtherRegs <= 12 * kLaunchRegs);
 constexpr long long kWaitCycles = 4000000000ll;  // bound on each wait: ~2 s
 constexpr uint32_t kWarpStage = 4096;  // of a read-out warp, for its stores
 constexpr int kMaxPartsOfTile = 4, kMaxPairs = 80;
+constexpr int kMaxParts = 608;       // blocks of the norm's kernel
 constexpr float kUnit = 4096.0f;     // planes hold v * kUnit
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
@@ -748,19 +749,28 @@ __device__ __forceinline__ void get8(float (&v)[8], const InputArgs& a, int64_t 
   for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? get<DT>(a.g, r * a.ld + c + e) : 0.0f;
 }
 
-// Sum of eight squares: in fp32 where they keep clear of its range's ends, in
-// binary64 where not.
-__device__ __forceinline__ double sum_squares(const float (&v)[8]) {
-  float top = 0.0f, q = 0.0f;
+// Sum of N times eight squares: in fp32 where they keep clear of its range's
+// ends, in binary64 (a small fraction of fp32's rate) where not.
+template <int N>
+__device__ __forceinline__ double sum_squares(const float (&v)[N][8]) {
+  float top = 0.0f, q[N];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    top = fmaxf(top, fabsf(v[e]));
-    q = fmaf(v[e], v[e], q);
+  for (int k = 0; k < N; ++k) {
+    q[k] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      top = fmaxf(top, fabsf(v[k][e]));
+      q[k] = fmaf(v[k][e], v[k][e], q[k]);
+    }
   }
-  if (top == 0.0f || (top > 0x1p-50f && top < 0x1p60f)) return (double)q;
-  double t = 0.0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t += (double)v[e] * (double)v[e];
+  for (int h = 1; h < N; h *= 2)
+#pragma unroll
+    for (int k = 0; k + h < N; k += 2 * h) q[k] += q[k + h];
+  if (top == 0.0f || (top > 0x1p-50f && top < 0x1p58f)) return (double)q[0];
+  double t = 0.0;
+  for (int k = 0; k < N; ++k)
+    for (int e = 0; e < 8; ++e) t += (double)v[k][e] * (double)v[k][e];
   return t;
 }
 
@@ -801,14 +811,20 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
   let_next_begin();
   if (blockIdx.x == 0)
     for (int k = threadIdx.x; k < kMaxPairs * 2 * kReadWarps; k += 256) a.arrived[k] = 0u;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < total; w += (int64_t)gridDim.x * 8) {
-    const int64_t r = w / segs;
-    float v[8];
-    get8<DT, VEC>(v, a, r, (w - r * segs) * 256 + lane * 8);
-    sum += sum_squares(v);
+  const int64_t step = (int64_t)gridDim.x * 8;
+  for (int64_t w0 = (int64_t)blockIdx.x * 8 + warp; w0 < total; w0 += 4 * step) {
+    float v[4][8];  // four loads on their way
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t w = w0 + k * step, r = w / segs;
+      get8<DT, VEC>(v[k], a, r, w < total ? (w - r * segs) * 256 + lane * 8 : a.n);
+    }
+    sum += sum_squares<4>(v);
     if (DT != GC_F32) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[k][e]) & 0x7FFFFFFFu);
     }
   }
 #pragma unroll
@@ -840,10 +856,15 @@ __device__ __forceinline__ float2 plane_factors(const InputArgs& a) {
   if (threadIdx.x < 32) {
     double t = 0.0;
     uint32_t top = 0u;
-    for (int p = threadIdx.x; p < a.parts; p += 32) {
-      t += a.part[p];
-      if (DT != GC_F32) top = max(top, a.top[p]);
+    double d[kMaxParts / 32];
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 32; ++k) {
+      const int p = k * 32 + threadIdx.x;
+      d[k] = p < a.parts ? a.part[p] : 0.0;
+      if (DT != GC_F32 && p < a.parts) top = max(top, a.top[p]);
     }
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 32; ++k) t += d[k];
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (DT != GC_F32) top = __reduce_max_sync(0xffffffffu, top);
@@ -892,7 +913,7 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const __grid_constant__
 }
 
 // The same for m > n, transposed: tiles of 64 x 64 through shared memory.
-template <int DT>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) orth_turn_kernel(const __grid_constant__ InputArgs a) {
   __shared__ float t[64][65];
   after_previous();
@@ -902,10 +923,19 @@ __global__ void __launch_bounds__(256) orth_turn_kernel(const __grid_constant__ 
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const int64_t r0 = w / ct * 64, c0 = (w % ct) * 64;
     __syncthreads();
-#pragma unroll 4
-    for (int k = threadIdx.x; k < 64 * 64; k += 256) {
-      const int64_t r = r0 + (k >> 6), c = c0 + (k & 63);
-      t[k >> 6][k & 63] = r < a.m && c < a.n ? in_units(get<DT>(a.g, r * a.ld + c), f) : 0.0f;
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = h * 256 + threadIdx.x;
+      const int64_t r = r0 + (k >> 3);
+      if (r < a.m) get8<DT, VEC>(v[h], a, r, c0 + (k & 7) * 8);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = h * 256 + threadIdx.x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        t[k >> 3][(k & 7) * 8 + e] = r0 + (k >> 3) < a.m ? in_units(v[h][e], f) : 0.0f;
     }
     __syncthreads();
     for (int k = threadIdx.x; k < 64 * 8; k += 256) {
@@ -1005,12 +1035,15 @@ __device__ __forceinline__ double slice_squares(const SmallArgs& a, int64_t c0, 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int w = w0 + k * 256;
-      if (w >= total) break;  // another slice's, or nothing
-      sum += sum_squares(v[k]);
-      if (!hold) continue;
-      sm100::sts128(hold + w * 32, make_float4(v[k][0], v[k][1], v[k][2], v[k][3]));
-      sm100::sts128(hold + w * 32 + 16, make_float4(v[k][4], v[k][5], v[k][6], v[k][7]));
+      if (w >= total) {  // another slice's, or nothing
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+      } else if (hold) {
+        sm100::sts128(hold + w * 32, make_float4(v[k][0], v[k][1], v[k][2], v[k][3]));
+        sm100::sts128(hold + w * 32 + 16, make_float4(v[k][4], v[k][5], v[k][6], v[k][7]));
+      }
     }
+    sum += sum_squares<4>(v);
   }
   return sum;
 }
@@ -1297,7 +1330,6 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
 
 // --- host ----------------------------------------------------------------------------------------
 
-constexpr int kMaxParts = 608;
 
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1437,9 +1469,9 @@ gc_status input(gc_ctx* ctx, const InputArgs& a) {
   cudaError_t e;
   if (a.m > a.n) {
     const int64_t tiles = ceil_div(a.m, (int64_t)64) * ceil_div(a.n, (int64_t)64);
-    e = launch_early(orth_turn_kernel<DT>,
-                     dim3((unsigned)std::min<int64_t>(tiles, (int64_t)ctx->num_sms * 8)), 256, 0,
-                     ctx->stream, a);
+    const dim3 g((unsigned)std::min<int64_t>(tiles, (int64_t)ctx->num_sms * 8));
+    e = vec ? launch_early(orth_turn_kernel<DT, true>, g, 256, 0, ctx->stream, a)
+            : launch_early(orth_turn_kernel<DT, false>, g, 256, 0, ctx->stream, a);
   } else {
     const int64_t warps = a.m * ceil_div(a.n, (int64_t)256);
     const dim3 g((unsigned)std::min<int64_t>(ceil_div(warps, (int64_t)8), (int64_t)ctx->num_sms * 8));
