@@ -35,12 +35,12 @@
 // over every kSegBlocks blocks and adds in registers, rounded to nearest.
 // (Two or four blocks: 2 and 4 % faster, with two and five times the error.)
 //
-// Measured: 4096 x 4096 fp32, five steps 2765 us (4.12 Tflop in fp16 products:
-// 1490 Tflop/s; cuBLAS bf16 1912 for a burst, 1698 sustained): the board's power
+// Measured: 4096 x 4096 fp32, five steps 2765 to 2840 us from card to card (4.12
+// Tflop in fp16 products: 1450 to 1490 Tflop/s; cuBLAS bf16 1912 for a burst, 1698 sustained): the board's power
 // limit lowers the clock to 1.75 GHz within a product, where a block of 256 x 256
 // x 64 x 3 takes 0.897 us, 98 % of what that clock gives; the rest is the last
-// round's idle pairs and a tile's epilogue, 3 to 5 us.  11008 x 4096 bf16 5003
-// us.  1001 x 2051: 229 us, 15 dependent launches of 13 us, a third of it on the
+// round's idle pairs and a tile's epilogue, 3 to 5 us.  11008 x 4096 bf16 5000 to
+// 5110 us.  1001 x 2051: 230 us, 15 dependent launches of 13 us, a third of it on the
 // tensor cores.  128 x 64: 29 us in one kernel.
 #include <cudaTypedefs.h>
 
@@ -799,26 +799,41 @@ struct Unit {
   }
 };
 
+// Segment `seg` of 256 columns of row r, every `step`-th of all: without a
+// division for each.
+struct Walk {
+  int64_t r, seg, segs, step_r, step_seg;
+  __device__ __forceinline__ Walk(int64_t first, int64_t step, int64_t segs_)
+      : r(first / segs_), seg(first - r * segs_), segs(segs_), step_r(step / segs_),
+        step_seg(step - step_r * segs_) {}
+  __device__ __forceinline__ void next() {
+    r += step_r;
+    seg += step_seg;
+    if (seg >= segs) {
+      seg -= segs;
+      ++r;
+    }
+  }
+};
+
 // Sums of squares, a double per block.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ InputArgs a) {
   __shared__ double s[8];
   __shared__ uint32_t tops[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
+  const int64_t segs = ceil_div(a.n, (int64_t)256);
   double sum = 0.0;
   uint32_t top = 0u;
   let_next_begin();
   if (blockIdx.x == 0)
     for (int k = threadIdx.x; k < kMaxPairs * 2 * kReadWarps; k += 256) a.arrived[k] = 0u;
-  const int64_t step = (int64_t)gridDim.x * 8;
-  for (int64_t w0 = (int64_t)blockIdx.x * 8 + warp; w0 < total; w0 += 4 * step) {
+  Walk at((int64_t)blockIdx.x * 8 + warp, (int64_t)gridDim.x * 8, segs);
+  while (at.r < a.m) {
     float v[4][8];  // four loads on their way
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t w = w0 + k * step, r = w / segs;
-      get8<DT, VEC>(v[k], a, r, w < total ? (w - r * segs) * 256 + lane * 8 : a.n);
-    }
+    for (int k = 0; k < 4; ++k, at.next())
+      get8<DT, VEC>(v[k], a, at.r, at.r < a.m ? at.seg * 256 + lane * 8 : a.n);
     sum += sum_squares<4>(v);
     if (DT != GC_F32) {
 #pragma unroll
@@ -895,9 +910,9 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const __grid_constant__
   let_next_begin();
   const float2 f = plane_factors<DT>(a);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t segs = ceil_div(a.n, (int64_t)256), total = a.m * segs;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < total; w += (int64_t)gridDim.x * 8) {
-    const int64_t r = w / segs, c = (w - r * segs) * 256 + lane * 8;
+  for (Walk at((int64_t)blockIdx.x * 8 + warp, (int64_t)gridDim.x * 8, ceil_div(a.n, (int64_t)256));
+       at.r < a.m; at.next()) {
+    const int64_t r = at.r, c = at.seg * 256 + lane * 8;
     if (c >= a.n) continue;
     float v[8];
     get8<DT, VEC>(v, a, r, c);
