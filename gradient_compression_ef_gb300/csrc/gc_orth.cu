@@ -13,13 +13,16 @@
 // of a converging polynomial stay below 16, and an entry below 2^-15 loses
 // bits only against 2^-37.
 //
-// An input in 16 bits is exact in one plane (times a power of two; what X_0 is
-// beyond that is one factor for the whole matrix, put in when the sums are
-// stored): the first step's A takes one product, its B X two.  A result in bf16
-// is rounded to 8 bits: the last step's A and B X use their operands' first
-// planes alone, 11 bits, which adds 3 to 5e-4 of the result's norm to the
-// rounding's 1.66e-3 (together 1.69e-3 to 1.72e-3; 11008 x 4096: both together
-// 6160 -> 5165 us).  fp16 and fp32 results keep both planes throughout.
+// An input in 16 bits is held in one plane, times the power of two that brings
+// its largest element to 2^14 .. 2^15 (what X_0 is beyond that is one factor for
+// the whole matrix, put in when the sums are stored): the first step's A takes
+// one product, its B X two.  That is exact for elements down to 2^-31 (bf16) or
+// 2^-28 (fp16) of the largest; those below are held to 2^-39 of it.
+//
+// The result's type decides the last rounding alone: a bf16 result is the fp32
+// one, rounded.  (X and B of the last step with 11 bits took 13 % off 11008 x
+// 4096 bf16, but where few singular directions carry the update their roundings
+// are coherent, and add as much as the rounding to bf16.)
 //
 // A and B are symmetric: tiles below the diagonal are not computed, what lies
 // above it is stored twice, mirrored.  a is put on B's diagonal, so that
@@ -40,7 +43,7 @@
 // 1698 sustained): the board's power limit lowers the clock to 1.75 GHz within a
 // product, where a block of 256 x 256 x 64 x 3 takes 0.897 us, 98 % of what that
 // clock gives; the rest is the last round's idle pairs and a tile's epilogue, 3
-// to 5 us.  11008 x 4096 bf16 5000 to 5110 us.  1001 x 2051: 230 us, 15 dependent
+// to 5 us.  11008 x 4096 bf16 5793 us.  1001 x 2051: 230 us, 15 dependent
 // launches of 13 us, a third of it on the tensor cores.  128 x 64: 29 us in one
 // kernel.
 #include <cudaTypedefs.h>
@@ -864,8 +867,7 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
 
 // What g's elements are multiplied by, from the blocks' sums; the whole block
 // calls it.  fp32: kUnit / (|g| + eps).  16-bit types: the power of two that
-// brings the largest magnitude to 2^14 .. 2^15 (elements below 2^-39 of it lose
-// bits), the rest of the factor being phi.
+// brings the largest magnitude to 2^14 .. 2^15, the rest of the factor being phi.
 template <int DT>
 __device__ __forceinline__ float2 plane_factors(const InputArgs& a) {
   __shared__ float2 f;
@@ -1596,10 +1598,9 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
     ProductArgs a{};
     a.part = part;
     a.arrived = in.arrived;
-    const bool exact = k == 0 && dtype != GC_F32;             // X is one plane
-    const bool rough = k + 1 == steps && odtype == GC_BF16;  // X and B by one plane
-    a.phi = exact ? in.phi : nullptr;
-    a.a_planes = a.b_planes = exact || rough ? 1 : 2;
+    const bool one = k == 0 && dtype != GC_F32;  // X is one plane
+    a.phi = one ? in.phi : nullptr;
+    a.a_planes = a.b_planes = one ? 1 : 2;
     st = product<kGram>(ctx, x, x, gram, a);
     if (st != GC_OK) break;
     a.a = coefs[3 * k];
@@ -1609,8 +1610,7 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
     a.a_planes = a.b_planes = 2;
     st = product<kPoly>(ctx, gram, gram, poly, a);
     if (st != GC_OK) break;
-    a.a_planes = rough ? 1 : 2;
-    a.b_planes = exact || rough ? 1 : 2;
+    a.b_planes = one ? 1 : 2;
     if (k + 1 < steps) {
       st = product<kApply>(ctx, poly, x, next, a);
       std::swap(x, next);

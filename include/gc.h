@@ -806,12 +806,13 @@ GC_API int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n);
  * steps >= 1.  g: [m, n] of type dtype; out: [m, n] of type odtype; either may
  * start at any element (a slice of the flat gradient), and out may be g itself.
  * The iterates are held in 22 bits and products are added in fp32: the error is
- * that of fp32 products (a bf16 out takes X and B of the last step with 11 bits,
- * which adds up to 5e-4 of its norm to its own rounding's 1.7e-3), as long as no element of X, A = X X^T or
- * a I + b A + c A A reaches 16 in magnitude (it comes out as infinity and then
- * NaN); with |X_0| <= 1 a polynomial that keeps singular values below 2 stays
- * far from it.  A g of zeros gives zeros; one with an infinity or NaN gives NaN
- * everywhere.  m, n <= 2^30.  GC_ERR_WORKSPACE when less than
+ * that of fp32 products, whatever odtype is (a bf16 out is the fp32 one, rounded),
+ * as long as no element of X, A = X X^T or a I + b A + c A A reaches 16 in
+ * magnitude (it comes out as infinity and then NaN); with |X_0| <= 1 a polynomial
+ * that keeps singular values below 2 stays far from it.  A 16-bit g's elements
+ * below 2^-31 (bf16) or 2^-28 (fp16) of its largest are held to 2^-39 of that.  A
+ * g of zeros gives zeros; one with an infinity or NaN gives NaN everywhere.
+ * m, n <= 2^30.  GC_ERR_WORKSPACE when less than
  * gc_orthogonalize_scratch_bytes is reserved.
  */
 GC_API gc_status gc_orthogonalize(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n,
