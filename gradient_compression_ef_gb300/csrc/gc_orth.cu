@@ -7,11 +7,14 @@
 // Every singular value x of X goes to x (a + b x^2 + c x^4) in each step and
 // the singular vectors stay.  Directions far below the largest one grow by a
 // factor of a each step, and so do errors in them, so that the iterates carry
-// 22 bits: each is held as two fp16 planes, v 2^12 = hi + lo, and a product is
-// hi hi + hi lo + lo hi on the tensor cores (tcgen05, exact products, fp32
-// accumulation; lo lo is below 2^-22 and left out).  Magnitudes: X, A and B
-// of a converging polynomial stay below 16, and an entry below 2^-15 loses
-// bits only against 2^-37.
+// 22 bits: each is held as two fp16 planes, v 2^12 = hi + lo 2^-11, and a product
+// is hi hi + 2^-11 (hi lo + lo hi) on the tensor cores (tcgen05, exact products,
+// fp32 accumulation; lo lo is below 2^-22 and left out).  The products with lo
+// come first, and the first hi hi multiplies the sum so far by 2^-11.  Magnitudes:
+// X, A and B of a converging polynomial stay below 16; small entries keep their
+// digits down to 2^-48 absolute, half of fp16's smallest step in lo.  (With v 2^12
+// = hi + lo that was 2^-37: a row of an update 10^8 times below another one came
+// out to 5e-3 of its size.)
 //
 // An input in 16 bits is held in one plane, times the power of two that brings
 // its largest element to 2^14 .. 2^15 (what X_0 is beyond that is one factor for
@@ -35,8 +38,8 @@
 //   issuer     one warp of the leader CTA: the MMAs of the pair
 //   read-out   8 warps: tensor memory -> running sums in registers -> planes
 // The tensor cores round their running sums towards zero; read-out takes them
-// over every kSegBlocks blocks and adds in registers, rounded to nearest.
-// (Two or four blocks: 2 and 4 % faster, with two and five times the error.)
+// over block by block and adds in registers, rounded to nearest.  (By two or four
+// blocks: 2 and 4 % faster, with two and five times the error.)
 //
 // Measured: 4096 x 4096 fp32, five steps 2765 to 2840 us from card to card (4.12
 // Tflop in fp16 products: 1450 to 1490 Tflop/s; cuBLAS bf16 1912 for a burst,
@@ -62,7 +65,6 @@ namespace {
 constexpr int kTM = 256;             // rows of a pair's tile
 constexpr int kBK = 64;              // of the sum's axis, per block
 constexpr uint32_t kABytes = 128 * kBK * 2;  // one plane, one CTA
-constexpr int kSegBlocks = 1;        // blocks per accumulator
 constexpr int kReadWarps = 8, kProducerWarp = 8, kIssuerWarp = 9;
 constexpr int kThreads = 384;
 // Registers a thread: as launched, and (tiles of 256 columns) of the read-out
@@ -74,6 +76,8 @@ constexpr uint32_t kWarpStage = 4096;  // of a read-out warp, for its stores
 constexpr int kMaxPartsOfTile = 4, kMaxPairs = 80;
 constexpr int kMaxParts = 608;       // blocks of the norm's kernel
 constexpr float kUnit = 4096.0f;     // planes hold v * kUnit
+constexpr int kLoBits = 11;          // the second plane's units are so many bits smaller
+constexpr float kLo = 1 << kLoBits;
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
@@ -150,18 +154,19 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// v = hi + lo as two fp16 values each, of a pair: hi the nearest, lo the rest.
+// v = hi + lo / kLo as two fp16 values each, of a pair: hi the nearest, lo the
+// nearest to the rest.
 __device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(v0, v1);
   const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(__fsub_rn(v0, f.x), __fsub_rn(v1, f.y));
+  const __half2 l = __floats2half2_rn(__fsub_rn(v0, f.x) * kLo, __fsub_rn(v1, f.y) * kLo);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 __device__ __forceinline__ float2 join2(uint32_t hi, uint32_t lo) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  return make_float2(h.x + l.x, h.y + l.y);
+  return make_float2(fmaf(l.x, 1.0f / kLo, h.x), fmaf(l.y, 1.0f / kLo, h.y));
 }
 
 // Tiles by rows of tiles, outputs of neighbouring columns next to one another;
@@ -396,9 +401,10 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N]
           unpack2<GC_F16>(sm100::lds_u128(staged(stage, lane, k)), f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            const float b = p ? a.b * (1.0f / kLo) : a.b;
             float* t = sum + c0 + k * 8 + 2 * e;
-            t[0] = fmaf(a.b, f[e].x, t[0]);
-            t[1] = fmaf(a.b, f[e].y, t[1]);
+            t[0] = fmaf(b, f[e].x, t[0]);
+            t[1] = fmaf(b, f[e].y, t[1]);
           }
         }
       }
@@ -434,7 +440,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N]
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float* t = sum + c0 + k * 8 + 2 * e;
-        const __half2 w = __floats2half2_rn(t[0], t[1]);
+        const __half2 w = __floats2half2_rn(t[0] * kLo, t[1] * kLo);
         l[e] = *reinterpret_cast<const uint32_t*>(&w);
       }
       sts_u128(staged(stage, lane, k), l[0], l[1], l[2], l[3]);
@@ -546,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float sum[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) sum[c] = 0.0f;
-      for (int32_t k = item.k0; k < item.k1; k += kSegBlocks, ++seg) {
+      for (int32_t k = item.k0; k < item.k1; ++k, ++seg) {
         const uint32_t buf = seg & 1u;
         const bool got = mbar_wait_cluster(&s.acc_full[buf], (seg >> 1) & 1u, kWaitCycles);
         if (__any_sync(0xffffffffu, !got)) {
@@ -645,10 +651,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t ph = 0, seg = 0;
         for (int64_t t = pair; ok && t < a.items; t += pairs) {
           const Item<TN, kSym> item(a, t, blocks);
-          int in_seg = 0;
-          for (int32_t k = item.k0; k < item.k1; ++k) {
+          for (int32_t k = item.k0; k < item.k1; ++k, ++seg) {
             const uint32_t buf = seg & 1u;
-            if (in_seg == 0 && seg >= 2 &&
+            if (seg >= 2 &&
                 !mbar_wait_cluster(&s.acc_empty[buf], ((seg >> 1) - 1u) & 1u, kWaitCycles))
               ok = false;
             if (ok && !mbar_wait_cluster(&s.full[st], ph, kWaitCycles)) ok = false;
@@ -657,11 +662,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after_sync();
-            const bool last = in_seg == kSegBlocks - 1 || k + 1 == item.k1;
             if (elect_one()) {
               const uint32_t off = (uint32_t)st * (S::kStage >> 4), d = tmem + buf * TN;
-              // the small products first: the sum is large only once hi hi is in it
-              uint32_t more = in_seg ? 1u : 0u;
+              // the products with lo first, kLoBits ahead of the others (a block
+              // has the accumulator to itself)
+              uint32_t more = 0u;
               auto multiply = [&](uint32_t a_at, uint32_t b_at) {
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk) {
@@ -672,14 +677,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               };
               if (a.a_planes == 2) multiply(kALo, 0u);
               if (a.b_planes == 2) multiply(0u, kBLo);
-              multiply(0u, 0u);
+              if (more) mma_f16_pair_behind<kLoBits>(d, a0 + off, b0 + off, hi, idesc);
+              else mma_f16_pair(d, a0 + off, b0 + off, hi, idesc, 0u);
+#pragma unroll
+              for (int kk = 1; kk < kBK / 16; ++kk)
+                mma_f16_pair(d, a0 + off + kk * kAStep, b0 + off + kk * kBStep, hi, idesc, 1u);
               mma_commit_pair(&s.empty[st]);
-              if (last) mma_commit_pair(&s.acc_full[buf]);
-            }
-            ++in_seg;
-            if (last) {
-              ++seg;
-              in_seg = 0;
+              mma_commit_pair(&s.acc_full[buf]);
             }
             if (++st == S::kStages) {
               st = 0;
@@ -1140,7 +1144,9 @@ __device__ __forceinline__ void small_product(uint32_t tmem, uint32_t cols, uint
       mma_f16_one(d, a0 + (a_plane >> 4) + a_step(k), b0 + b_step(k), hi, idesc, k > k0);
     for (int k = k0; k < k1; ++k)
       mma_f16_one(d, a0 + a_step(k), b0 + (b_plane >> 4) + b_step(k), hi, idesc, 1u);
-    for (int k = k0; k < k1; ++k) mma_f16_one(d, a0 + a_step(k), b0 + b_step(k), hi, idesc, 1u);
+    mma_f16_one_behind<kLoBits>(d, a0 + a_step(k0), b0 + b_step(k0), hi, idesc);
+    for (int k = k0 + 1; k < k1; ++k)
+      mma_f16_one(d, a0 + a_step(k), b0 + b_step(k), hi, idesc, 1u);
   }
 }
 

@@ -418,6 +418,22 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint32_t a_lo, uin
       : "memory");
 }
 
+// D = A * B + D * 2^-S over the pair: the first of the products that the sums so
+// far are S bits behind.
+template <int S>
+__device__ __forceinline__ void mma_f16_pair_behind(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                    uint32_t desc_hi, uint32_t idesc) {
+  static_assert(S > 0 && S < 16);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p, %5;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "n"(S)
+      : "memory");
+}
+
 // The same within one CTA: A's 128 rows, B and D its own.
 __device__ __forceinline__ void mma_f16_one(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                             uint32_t desc_hi, uint32_t idesc,
@@ -429,6 +445,20 @@ __device__ __forceinline__ void mma_f16_one(uint32_t d_tmem, uint32_t a_lo, uint
       "mov.b64 b, {%2, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int S>
+__device__ __forceinline__ void mma_f16_one_behind(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                   uint32_t desc_hi, uint32_t idesc) {
+  static_assert(S > 0 && S < 16);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p, %5;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "n"(S)
       : "memory");
 }
 

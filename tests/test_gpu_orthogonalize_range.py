@@ -1,8 +1,15 @@
-"""Results of an orthogonalisation in bf16 against those in fp32, of updates of
-full rank and of few directions.
+"""Orthogonalisation at the ends of what its iterates hold: results in bf16
+against those in fp32, updates of few directions, elements of very different sizes.
 
-A result in bf16 is the fp32 one rounded once: the same bits.  The fp32 one is
-compared with the 64-bit reference within the bounds of its products.
+Tolerances.  A result in bf16 is the fp32 one rounded once: the same bits.  Of
+few directions: the bounds of the products.
+Where the polynomial is a X (coefficients (a, 0, 0), or singular values so small
+that b A X is below every rounding), each sum has one term: its roundings are the
+operands' (2^-22 each: B's diagonal, X), at most 12 of the running sum towards
+zero (2^-23 each), what is put back for them (3 2^-25), and a few in registers:
+STEP = 2^-18 of the value for each step, together with the rounding of X_0.  Below
+that the second plane ends, at 2^-48: fp16's smallest step is 2^-24; the planes
+hold X_0 2^12, the second one 2^11 more; half a step.
 """
 import pytest
 
@@ -10,6 +17,8 @@ from tests.gpu_helpers import torch_cuda
 from tests.test_gpu_orthogonalize import F32_QUINTIC, check, dt, reference, update
 
 pytestmark = pytest.mark.gpu
+
+STEP = 2.0 ** -18
 
 
 @pytest.fixture(scope="module")
@@ -58,3 +67,58 @@ def test_few_directions(gc, ctx, m, n, k):
         gc.orthogonalize(ctx, g, out, steps=steps)
         want, err = reference(g, [F32_QUINTIC] * steps, 1e-7, 1.0)
         check(out, want, err, "f32")
+
+
+@pytest.mark.parametrize("m,n", [(64, 90), (120, 1000), (300, 512), (520, 264)])
+@pytest.mark.parametrize("what", ["row", "column", "element"])
+def test_beside_something_dominant(gc, ctx, m, n, what):
+    """One row, column or element 10^8 times the others: these keep their digits.  The terms of a step are at most
+    |a| + 2 |b| + 3 |c| = 19 times X, each within STEP, where the small ones grow by |a|: 6 STEP of them.  What the
+    large ones are off after a step (19 STEP) comes into the small ones through A and A A in the next: (2 |b| + 4 |c|)
+    19 / |a| = 97 STEP."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n)
+    g = torch.randn(m, n, generator=gen, device="cuda")
+    rest = torch.ones(m, n, dtype=torch.bool, device="cuda")
+    if what == "row":
+        g[m // 3] *= 1e8
+        rest[m // 3] = False
+    elif what == "column":
+        g[:, n // 3] *= 1e8
+        rest[:, n // 3] = False
+    else:
+        g[m // 3, n // 3] = 1e9
+        rest[m // 3] = False
+        rest[:, n // 3] = False
+    for steps, room in ((1, 6 * STEP), (2, 110 * STEP)):
+        o = torch.empty_like(g)
+        gc.orthogonalize(ctx, g, o, steps=steps)
+        want, _ = reference(g, [F32_QUINTIC] * steps, 1e-7, 1.0)
+        off = float(torch.linalg.norm((o.double() - want)[rest]) / torch.linalg.norm(want[rest]))
+        x0 = g.double() / torch.linalg.norm(g.double())
+        floor = 2.0 ** -48 / float(x0[rest].square().mean().sqrt())
+        assert off <= room + steps * floor, (off, floor)
+    ctx.check()
+
+
+@pytest.mark.parametrize("m,n", [(64, 90), (120, 1000), (300, 512), (520, 264)])
+@pytest.mark.parametrize("dtype,bits", [("f32", 46), ("bf16", 36), ("f16", 24)])
+def test_every_element_by_itself(gc, ctx, m, n, dtype, bits):
+    """With the polynomial 1 X the result is X_0, element by element: of elements down to 2^-bits of the largest.
+    A 16-bit matrix is held in one plane, to 2^-39 of its largest element; an fp32 one in two, to 2^-48."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(m)
+    spread = torch.exp2(-bits * torch.rand(m, n, generator=gen, device="cuda", dtype=torch.float64))
+    g = (spread * torch.sign(torch.randn(m, n, generator=gen, device="cuda"))).to(dt(dtype))
+    o = torch.empty(m, n, device="cuda")
+    x0 = g.double() / torch.linalg.norm(g.double())
+    top = float(x0.abs().max())
+    for steps in (1, 4):
+        gc.orthogonalize(ctx, g, o, steps=steps, coefs=(1.0, 0.0, 0.0), eps=0.0)
+        room = (steps + 1) * STEP * x0.abs() + steps * 2.0 ** -48
+        if dtype != "f32" and min(m, n) > 128:
+            room += 2.0 ** -39 * top
+        assert bool(((o.double() - x0).abs() <= room).all()), float(((o.double() - x0).abs() / room).max())
+    ctx.check()
