@@ -16,10 +16,14 @@
 // = hi + lo that was 2^-37: a row of an update 10^8 times below another one came
 // out to 5e-3 of its size.)
 //
+// An update far below eps makes X far below 1: X is 2^e times its planes, one e <=
+// 0 for the whole matrix and step, from a bound r on its largest singular value,
+// r_0 = |g| / (|g| + eps), r <- r (|a| + |b| r^2 + |c| r^4).  From a bound of 1/2 on
+// e is 0.  The powers of two are put in when sums are stored.
+//
 // An input in 16 bits is held in one plane, times the power of two that brings
-// its largest element to 2^14 .. 2^15 (what X_0 is beyond that is one factor for
-// the whole matrix, put in when the sums are stored): the first step's A takes
-// one product, its B X two.  That is exact for elements down to 2^-31 (bf16) or
+// its largest element to 2^14 .. 2^15 (what X_0 is beyond that is one more factor,
+// f, put in likewise): the first step's A takes one product, its B X two.  That is exact for elements down to 2^-31 (bf16) or
 // 2^-28 (fp16) of the largest; those below are held to 2^-39 of it.
 //
 // The result's type decides the last rounding alone: a bf16 result is the fp32
@@ -81,6 +85,39 @@ constexpr float kLo = 1 << kLoBits;
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
+// What a step's planes stand for: X = f 2^e times them (over kUnit).
+struct Range {
+  float gram;   // f^2 4^e: of A's sums
+  float apply;  // f 2^(e - the next step's e): of B X's, written by A's kernel
+  float f;
+  float unit;   // 2^e
+  float r;      // bound on X's largest singular value
+  int e;
+};
+// The power of two that holds values up to r, from -126 to 0; a NaN's is 0.
+__device__ __forceinline__ int exponent_of(float r) {
+  return r < 0.5f ? (int)(__float_as_uint(r) >> 23) - 126 : 0;
+}
+__device__ __forceinline__ float power2(int e) {  // of -126 .. 127
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+__device__ __forceinline__ Range make_range(float f, float r, int e) {
+  const float unit = power2(e);
+  return {f * f * unit * unit, 0.0f, f, unit, r, e};
+}
+// The bound after a step; what A's kernel writes: the next step's range and the
+// factor of B X.
+__device__ __forceinline__ float grown(float r, float a, float b, float c) {
+  const float q = r * r;
+  return r * fmaf(q, fmaf(q, fabsf(c), fabsf(b)), fabsf(a));
+}
+__device__ __forceinline__ void next_range(Range* now, Range* next, float a, float b, float c) {
+  const float r = grown(now->r, a, b, c);
+  const int e = exponent_of(r);
+  now->apply = now->f * power2(now->e - e);
+  *next = make_range(1.0f, r, e);
+}
+
 // What a sum over a block of 16 k elements loses on average to the tensor
 // cores' roundings towards zero, as a share of its value: put back when it is
 // read.  Measured as the mean of sum(x^2) - 1 over unit vectors x; in B X,
@@ -114,7 +151,7 @@ struct ProductArgs {
   const uint16_t* prev;    // kPoly: A's planes
   int64_t pitch, plane_size;  // elements
   int a_planes, b_planes;  // of the operands: 2, or their first alone
-  const float* phi;        // X stands for phi times its planes, or NULL: 1
+  Range *range, *next_range;  // of this step and of the next
   float a, b, c;
   void* out;               // kLast
   int64_t ldo;
@@ -127,6 +164,7 @@ struct Smem {
   uint32_t stage0, out0;
   uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
   uint32_t* tmem_slot;
+  float* factors;  // of the sums, of the result
 };
 template <int TN>
 __device__ __forceinline__ Smem carve(unsigned char* base) {
@@ -142,6 +180,7 @@ __device__ __forceinline__ Smem carve(unsigned char* base) {
   s.acc_empty = s.acc_full + 2;
   s.drain = s.acc_empty + 2;
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.drain + 1);
+  s.factors = reinterpret_cast<float*>(s.tmem_slot + 1);
   return s;
 }
 
@@ -284,7 +323,7 @@ __device__ __forceinline__ void store_plane(const ProductArgs& a, uint16_t* dst,
 // A warp's part of an output of type DT, rows from i, columns from j on, by
 // rows: through the stage, 128 bytes of each row at a time.
 template <int DT, int N>
-__device__ __forceinline__ void store_rows(const ProductArgs& a, const float (&v)[N],
+__device__ __forceinline__ void store_rows(const ProductArgs& a, const float (&v)[N], float scale,
                                            uint32_t stage, int64_t i, int64_t j) {
   constexpr int E = elem_size(DT), C = 128 / E, V = Elem<DT>::V;
   using T = typename Elem<DT>::T;
@@ -297,7 +336,7 @@ __device__ __forceinline__ void store_rows(const ProductArgs& a, const float (&v
     for (int k = 0; k < 8; ++k) {
       float u[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = __fmul_rn(v[c0 + k * V + e], a.scale);
+      for (int e = 0; e < V; ++e) u[e] = __fmul_rn(v[c0 + k * V + e], scale);
       const uint4 r = Elem<DT>::pack(u);
       sts_u128(staged(stage, lane, k), r.x, r.y, r.z, r.w);
     }
@@ -336,36 +375,34 @@ __device__ __forceinline__ void store_rows(const ProductArgs& a, const float (&v
 }
 template <int DT, int N>
 __device__ __forceinline__ void store_result(const ProductArgs& a, const float (&v)[N],
-                                             uint32_t stage, int64_t i, int64_t j) {
+                                             float scale, uint32_t stage, int64_t i, int64_t j) {
   if (!a.transposed) {
-    store_rows<DT, N>(a, v, stage, i, j);
+    store_rows<DT, N>(a, v, scale, stage, i, j);
     return;
   }
   const int64_t r = i + (threadIdx.x & 31);
   if (r >= a.rows) return;
 #pragma unroll
   for (int c = 0; c < N; ++c)
-    if (j + c < a.cols) put<DT>(a.out, (j + c) * a.ldo + r, __fmul_rn(v[c], a.scale));
+    if (j + c < a.cols) put<DT>(a.out, (j + c) * a.ldo + r, __fmul_rn(v[c], scale));
 }
 
 // A warp's part of a tile, 32 rows from i, N columns from j on, from the sums.
 template <int MODE, int N>
-__device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N], uint32_t stage,
-                                           int64_t i, int64_t j) {
+__device__ __forceinline__ void store_tile(const ProductArgs& a, float (&sum)[N],
+                                           const float* factors, uint32_t stage, int64_t i,
+                                           int64_t j) {
   constexpr bool kSym = MODE == kGram || MODE == kPoly;
   const int lane = threadIdx.x & 31;
   if (i >= a.rows) return;
-  float unit = MODE == kLast ? 1.0f / (kUnit * kUnit) : 1.0f / kUnit;
-  if (MODE != kPoly && a.phi) {
-    const float phi = __ldcg(a.phi);
-    unit *= MODE == kGram ? phi * phi : phi;
-  }
+  const float unit = MODE == kPoly ? 1.0f / kUnit : factors[0];
 #pragma unroll
   for (int c = 0; c < N; ++c) sum[c] = fmaf(sum[c], lost(kBK / 16, MODE), sum[c]) * unit;
   if (MODE == kLast) {
-    if (a.odtype == GC_F32) store_result<GC_F32, N>(a, sum, stage, i, j);
-    else if (a.odtype == GC_BF16) store_result<GC_BF16, N>(a, sum, stage, i, j);
-    else store_result<GC_F16, N>(a, sum, stage, i, j);
+    const float scale = factors[1];
+    if (a.odtype == GC_F32) store_result<GC_F32, N>(a, sum, scale, stage, i, j);
+    else if (a.odtype == GC_BF16) store_result<GC_BF16, N>(a, sum, scale, stage, i, j);
+    else store_result<GC_F16, N>(a, sum, scale, stage, i, j);
     return;
   }
 #pragma unroll
@@ -546,6 +583,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t q = (uint32_t)warp & 3u, ch = (uint32_t)warp >> 2;
     const uint32_t acc_empty0 = map_to_rank(smem_u32(s.acc_empty), 0);
     after_previous();
+    // fetched while the first blocks come, kept in shared memory (every warp
+    // writes the same for itself)
+    if (MODE != kPoly && lane == 0) {
+      if (MODE == kGram) s.factors[0] = __ldcg(&a.range->gram) * (1.0f / kUnit);
+      if (MODE == kApply) s.factors[0] = __ldcg(&a.range->apply) * (1.0f / kUnit);
+      if (MODE == kLast) {
+        s.factors[0] = __ldcg(&a.range->f) * (1.0f / (kUnit * kUnit));
+        s.factors[1] = a.scale * __ldcg(&a.range->unit);
+      }
+    }
+    __syncwarp();
     uint32_t seg = 0;
     for (int64_t t = pair; ok && t < a.items; t += pairs) {
       const Item<TN, kSym> item(a, t, blocks);
@@ -574,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (item.split < 0 || join_parts<N>(a, sum, item.split, item.part, rank))
-        store_tile<MODE, N>(a, sum, s.out0 + warp * kWarpStage,
+        store_tile<MODE, N>(a, sum, s.factors, s.out0 + warp * kWarpStage,
                             item.i * kTM + rank * 128 + q * 32, item.j * TN + ch * N);
       __syncwarp();
     }
@@ -693,6 +741,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) mma_commit_pair(s.drain);
       }
+    } else if (MODE == kGram && blockIdx.x == 0 && warp == kIssuerWarp + 1 && lane == 0) {
+      after_previous();
+      next_range(a.range, a.next_range, a.a, a.b, a.c);
     }
   }
   // MMAs still in flight read both CTAs' shared memory: the producers, which
@@ -726,7 +777,7 @@ struct InputArgs {
   float eps;
   uint16_t* dst;
   uint32_t* top;         // the blocks' largest magnitudes, as bits (16-bit types)
-  float* phi;            // 16-bit types: X_0 is phi times its plane
+  Range* range;          // of X_0
   uint32_t* arrived;     // the products' counters, set to zero
 };
 
@@ -782,26 +833,31 @@ __device__ __forceinline__ double sum_squares(const float (&v)[N][8]) {
   return t;
 }
 
-// kUnit / (|g| + eps) = n 2^-k: the sum of squares is m 4^k with 1 <= m < 4,
-// so that root and quotient are fp32 ones (binary64's take thousands of
-// cycles).  n = 0 where g is zero, NaN where it is not finite.
+// X_0's factor: kUnit / (|g| + eps) = n 2^(e - k), where 2^e holds r = |g| / (|g| +
+// eps).  The sum of squares is m 4^k with 1 <= m < 4, so that root and quotient
+// are fp32 ones (binary64's take thousands of cycles).  n = 0 where g is zero (or
+// eps beyond binary32's range times it), NaN where g is not finite.
 struct Unit {
-  float n;
-  int k;
-  __device__ __forceinline__ Unit(double squares, float eps) : n(0.0f), k(0) {
+  float n, r;
+  int k, e;
+  __device__ __forceinline__ Unit(double squares, float eps) : n(0.0f), r(0.0f), k(0), e(0) {
     if (squares == 0.0) return;
     if (!(squares <= 1.0e300)) {
       n = NAN;
       return;
     }
     const long long bits = __double_as_longlong(squares);
-    const int e = (int)(bits >> 52) - 1023;
-    k = e >> 1;
+    const int x = (int)(bits >> 52) - 1023;
+    k = x >> 1;
     const float m = (float)__longlong_as_double((bits & 0xFFFFFFFFFFFFFll) |
-                                                ((long long)(1023 + e - 2 * k) << 52));
-    n = kUnit / (sqrtf(m) + ldexpf(eps, -k));
+                                                ((long long)(1023 + x - 2 * k) << 52));
+    const float root = sqrtf(m), t = root + ldexpf(eps, -k);
+    r = root / t;
+    e = exponent_of(r);
+    n = kUnit / t * power2(-e);
   }
-  // as two factors, each inside binary32's range whatever the norm
+  // of g's elements, for planes that stand for 2^e times them: as two factors,
+  // each inside binary32's range whatever the norm
   __device__ __forceinline__ float2 factors() const {
     return make_float2(ldexpf(1.0f, -(k / 2)), ldexpf(n, -(k - k / 2)));
   }
@@ -870,8 +926,9 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const __grid_constant__ 
 }
 
 // What g's elements are multiplied by, from the blocks' sums; the whole block
-// calls it.  fp32: kUnit / (|g| + eps).  16-bit types: the power of two that
-// brings the largest magnitude to 2^14 .. 2^15, the rest of the factor being phi.
+// calls it, and the first one writes X_0's range.  fp32: Unit's factors.  16-bit
+// types: the power of two that brings the largest magnitude to 2^14 .. 2^15, the
+// rest being the range's f.
 template <int DT>
 __device__ __forceinline__ float2 plane_factors(const InputArgs& a) {
   __shared__ float2 f;
@@ -892,14 +949,16 @@ __device__ __forceinline__ float2 plane_factors(const InputArgs& a) {
     if (DT != GC_F32) top = __reduce_max_sync(0xffffffffu, top);
     if (threadIdx.x == 0) {
       const Unit u(t, a.eps);
+      float rest = 1.0f;
       if (DT == GC_F32) {
         f = u.factors();
       } else {
         const bool some = u.n > 0.0f;  // neither zero nor NaN
-        const int e = some ? 14 - ilogbf(__uint_as_float(top)) : 0;
-        f = make_float2(ldexpf(1.0f, e / 2), ldexpf(1.0f, e - e / 2));
-        if (blockIdx.x == 0) *a.phi = some ? ldexpf(u.n, -u.k - e) : u.n;
+        const int p = some ? 14 - ilogbf(__uint_as_float(top)) : 0;
+        f = make_float2(ldexpf(1.0f, p / 2), ldexpf(1.0f, p - p / 2));
+        rest = some ? ldexpf(u.n, -u.k - p) : u.n;
       }
+      if (blockIdx.x == 0) *a.range = make_range(rest, u.r, u.e);
     }
   }
   __syncthreads();
@@ -1096,12 +1155,12 @@ __device__ __forceinline__ void slice_planes(const SmallArgs& a, int64_t c0, int
 // 16 columns of a row of the result.
 template <int DT>
 __device__ __forceinline__ void put_slice(const SmallArgs& a, int i, int64_t j,
-                                          const float (&v)[16]) {
+                                          const float (&v)[16], float scale) {
   const int64_t at = a.tall ? j * a.ldo + i : i * a.ldo + j, step = a.tall ? a.ldo : 1;
 #pragma unroll
   for (int e = 0; e < 16; ++e)
     if (j + e < a.l)
-      put<DT>(a.out, at + e * step, __fmul_rn(v[e] * (1.0f / kUnit), a.scale));
+      put<DT>(a.out, at + e * step, __fmul_rn(v[e] * (1.0f / kUnit), scale));
 }
 
 // Every CTA of the grid is here, and what it wrote is visible; false when the
@@ -1157,6 +1216,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
   __shared__ uint32_t tmem_slot;
   __shared__ double norm_part[8];
   __shared__ float2 factors;
+  __shared__ float bound;  // on X_0's largest singular value
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t xs = (smem_u32(small_smem) + 1023u) & ~1023u, as = xs + 2 * kXPlane;
   const int64_t c0 = (int64_t)blockIdx.x * kSmallCols;
@@ -1206,10 +1266,15 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
       sum = norm_part[lane];
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) factors = Unit(sum, a.eps).factors();
+    if (lane == 0) {
+      const Unit u(sum, a.eps);
+      factors = u.factors();
+      bound = u.r;
+    }
   }
   __syncthreads();
   const float2 f = factors;
+  float r = bound;
   if (a.dtype == GC_F32) slice_planes<GC_F32>(a, c0, chunks, f, xs, hold);
   else if (a.dtype == GC_BF16) slice_planes<GC_BF16>(a, c0, chunks, f, xs, hold);
   else slice_planes<GC_F16>(a, c0, chunks, f, xs, hold);
@@ -1238,8 +1303,8 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     phase ^= 1u;
     tc_fence_after_sync();
   };
-  // 16 columns from c on of this thread's row, from `parts` accumulators.
-  auto take = [&](float (&v)[16], int c, int mode, int sixteens, uint32_t apart) {
+  // 16 columns from c on of this thread's row, from `parts` accumulators, in units.
+  auto take = [&](float (&v)[16], int c, int mode, int sixteens, uint32_t apart, float unit) {
     const int parts = (sixteens + 3) / 4;
     const float back = lost(sixteens, mode);
     tmem_ld16(tmem + (row0 << 16) + c, v);
@@ -1250,7 +1315,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
       for (int e = 0; e < 16; ++e) v[e] += w[e];
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = fmaf(v[e], back, v[e]) * (1.0f / kUnit);
+    for (int e = 0; e < 16; ++e) v[e] = fmaf(v[e], back, v[e]) * unit;
   };
   auto store16 = [&](uint32_t at, uint32_t plane, int c, const float (&v)[16]) {
 #pragma unroll
@@ -1264,9 +1329,14 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
 
   for (int step = 0; step < a.steps && ok; ++step) {
     multiply(kGram);
+    // X is 2^e times its planes, and 2^next the next one
+    const int e = exponent_of(r);
+    r = grown(r, a.coefs[step][0], a.coefs[step][1], a.coefs[step][2]);
+    const int next = exponent_of(r);
+    const float unit = power2(e);
     for (int c = half * 16; c < a.s16; c += 32) {
       float v[16];
-      take(v, c, kGram, x16, 128);
+      take(v, c, kGram, x16, 128, unit * unit * (1.0f / kUnit));
       if (!mine) continue;
       if (gridDim.x == 1) {
         store16(as, kAPlane, c, v);
@@ -1307,7 +1377,7 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     const float ca = a.coefs[step][0] * kUnit, cb = a.coefs[step][1], cc = a.coefs[step][2];
     for (int c = half * 16; c < a.s16; c += 32) {
       float v[16];
-      take(v, c, kPoly, a.s16 / 16, 128);
+      take(v, c, kPoly, a.s16 / 16, 128, 1.0f / kUnit);
       if (!mine) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1329,17 +1399,18 @@ __global__ void __launch_bounds__(256, 1) orth_small_kernel(const __grid_constan
     }
     multiply(kApply);
     const bool last = step + 1 == a.steps;
+    const float to_next = (last ? 1.0f : power2(e - next)) * (1.0f / kUnit);
     ok = !__syncthreads_or(!ok);  // a wait that ran out ends the call for every thread
     for (int c = half * 16; c < xpad; c += 32) {
       float v[16];
-      take(v, c, kApply, a.s16 / 16, 256);
+      take(v, c, kApply, a.s16 / 16, 256, to_next);
       if (!mine) continue;
       if (!last) {
         store16(xs, kXPlane, c, v);
       } else if (i < a.s) {
-        if (a.odtype == GC_F32) put_slice<GC_F32>(a, i, c0 + c, v);
-        else if (a.odtype == GC_BF16) put_slice<GC_BF16>(a, i, c0 + c, v);
-        else put_slice<GC_F16>(a, i, c0 + c, v);
+        if (a.odtype == GC_F32) put_slice<GC_F32>(a, i, c0 + c, v, a.scale * unit);
+        else if (a.odtype == GC_BF16) put_slice<GC_BF16>(a, i, c0 + c, v, a.scale * unit);
+        else put_slice<GC_F16>(a, i, c0 + c, v, a.scale * unit);
       }
     }
   }
@@ -1478,7 +1549,8 @@ int64_t parts_bytes(int64_t s, int64_t l) {
   const int64_t tiles = count_tiles(s, l, 256, false);
   return std::min<int64_t>(kMaxPairs, kMaxPartsOfTile * tiles) * kTM * 256 * 4;
 }
-constexpr int64_t kTopBytes = kMaxParts * 4 + 256;  // and phi
+constexpr int64_t kTopBytes = kMaxParts * 4 + 256;  // and two ranges
+static_assert(2 * sizeof(Range) <= 256);
 constexpr int64_t kArrivedBytes = kMaxPairs * 2 * kReadWarps * 4;
 
 template <int DT>
@@ -1574,7 +1646,8 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
   in.part = reinterpret_cast<double*>(at);
   at += kMaxParts * 8;
   in.top = reinterpret_cast<uint32_t*>(at);
-  in.phi = reinterpret_cast<float*>(in.top + kMaxParts);
+  Range* const ranges = reinterpret_cast<Range*>(in.top + kMaxParts);
+  in.range = ranges;
   at += kTopBytes;
   in.arrived = reinterpret_cast<uint32_t*>(at);
   at += round_up(kArrivedBytes, 256);
@@ -1605,13 +1678,14 @@ gc_status launch_orth(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t 
     a.part = part;
     a.arrived = in.arrived;
     const bool one = k == 0 && dtype != GC_F32;  // X is one plane
-    a.phi = one ? in.phi : nullptr;
+    a.range = ranges + (k & 1);
+    a.next_range = ranges + (~k & 1);
     a.a_planes = a.b_planes = one ? 1 : 2;
-    st = product<kGram>(ctx, x, x, gram, a);
-    if (st != GC_OK) break;
     a.a = coefs[3 * k];
     a.b = coefs[3 * k + 1];
     a.c = coefs[3 * k + 2];
+    st = product<kGram>(ctx, x, x, gram, a);
+    if (st != GC_OK) break;
     a.prev = gram.at;
     a.a_planes = a.b_planes = 2;
     st = product<kPoly>(ctx, gram, gram, poly, a);

@@ -805,14 +805,15 @@ GC_API int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n);
  * vectors stay.  coefs: HOST array of 3 * steps floats, read during the call;
  * steps >= 1.  g: [m, n] of type dtype; out: [m, n] of type odtype; either may
  * start at any element (a slice of the flat gradient), and out may be g itself.
- * The iterates are held in 22 bits, elements below 2^-26 to 2^-48, and products
- * are added in fp32: the error is that of fp32 products, whatever odtype is (a
- * bf16 out is the fp32 one, rounded), as long as no element of X, A = X X^T or
- * a I + b A + c A A reaches 16 in magnitude (it comes out as infinity and then
+ * The iterates are held in 22 bits, elements below 2^-26 to 2^-48 (of 1, or where
+ * |g|_F is far below eps of the power of two that holds X's singular values), and
+ * products are added in fp32: the error is that of fp32 products, whatever odtype
+ * is (a bf16 out is the fp32 one, rounded), as long as no element of X, A = X X^T
+ * or a I + b A + c A A reaches 16 in magnitude (it comes out as infinity and then
  * NaN); with |X_0| <= 1 a polynomial that keeps singular values below 2 stays far
- * from it.  A 16-bit g's elements
- * below 2^-31 (bf16) or 2^-28 (fp16) of its largest are held to 2^-39 of that.  A
- * g of zeros gives zeros; one with an infinity or NaN gives NaN everywhere.
+ * from it.  A 16-bit g's elements below 2^-31 (bf16) or 2^-28 (fp16) of its largest
+ * are held to 2^-39 of that.  A g of zeros gives zeros; one with an infinity or NaN
+ * gives NaN everywhere.
  * m, n <= 2^30.  GC_ERR_WORKSPACE when less than
  * gc_orthogonalize_scratch_bytes is reserved.
  */

@@ -1,5 +1,6 @@
 """Orthogonalisation at the ends of what its iterates hold: results in bf16
-against those in fp32, updates of few directions, elements of very different sizes.
+against those in fp32, updates of few directions or far below eps, elements of very
+different sizes.
 
 Tolerances.  A result in bf16 is the fp32 one rounded once: the same bits.  Of
 few directions: the bounds of the products.
@@ -8,9 +9,11 @@ that b A X is below every rounding), each sum has one term: its roundings are th
 operands' (2^-22 each: B's diagonal, X), at most 12 of the running sum towards
 zero (2^-23 each), what is put back for them (3 2^-25), and a few in registers:
 STEP = 2^-18 of the value for each step, together with the rounding of X_0.  Below
-that the second plane ends, at 2^-48: fp16's smallest step is 2^-24; the planes
-hold X_0 2^12, the second one 2^11 more; half a step.
+that the second plane ends, at 2^-48 of the power of two that holds the largest
+singular value: fp16's smallest step is 2^-24; the planes hold X_0 2^12, the second
+one 2^11 more; half a step.
 """
+import numpy as np
 import pytest
 
 from tests.gpu_helpers import torch_cuda
@@ -67,6 +70,44 @@ def test_few_directions(gc, ctx, m, n, k):
         gc.orthogonalize(ctx, g, out, steps=steps)
         want, err = reference(g, [F32_QUINTIC] * steps, 1e-7, 1.0)
         check(out, want, err, "f32")
+
+
+@pytest.mark.parametrize("m,n", [(60, 77), (77, 60), (128, 2000), (300, 512), (520, 264), (1024, 1024)])
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "f32"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("ratio", [1e-2, 1e-4, 1e-6, 1e-13, 1e-25])
+def test_far_below_eps(gc, ctx, m, n, dtype, out, ratio):
+    import torch
+    g = update(m, m, n, dtype, 1e-2)
+    eps = float(np.float32(float(torch.linalg.norm(g.double())) / ratio))
+    for steps in (1, 3, 5):
+        o = torch.empty(m, n, dtype=dt(out), device="cuda")
+        gc.orthogonalize(ctx, g, o, steps=steps, eps=eps, scale=0.5 / ratio)
+        want, _ = reference(g, [F32_QUINTIC] * steps, eps, float(np.float32(0.5 / ratio)))
+        off = float(torch.linalg.norm(o.double() - want) / torch.linalg.norm(want))
+        assert off <= (steps + 1) * STEP + (2.0 ** -8 if out == "bf16" else 0.0), off
+    ctx.check()
+
+
+@pytest.mark.parametrize("m,n", [(64, 90), (300, 512), (520, 264)])
+def test_growing_out_of_the_depths(gc, ctx, m, n):
+    """From 1e-9 of eps to singular values of order one: the iterates' power of two follows them.  While they are
+    small an error stays what it is of them; above, the slopes (at most |a| where the values grow by |a|) hold it."""
+    import torch
+    g = update(m, m, n, size=1e-2)
+    eps = float(np.float32(float(torch.linalg.norm(g.double())) * 1e9))
+    steps = 20
+    o = torch.empty_like(g)
+    gc.orthogonalize(ctx, g, o, steps=steps, eps=eps)
+    want, _ = reference(g, [F32_QUINTIC] * steps, eps, 1.0)
+    off = float(torch.linalg.norm(o.double() - want) / torch.linalg.norm(want))
+    assert float(torch.linalg.norm(want)) > 0.3 * min(m, n) ** 0.5
+    x, _ = reference(g, [F32_QUINTIC] * 14, eps, 1.0)
+    x14 = float(torch.linalg.norm(x))
+    assert x14 < 0.2
+    # 14 steps of STEP each in front, grown by |a| at most in each of the last six; these as the reference bounds
+    # them for such an X (divided by a norm of 1: |X| + 1 - |X|)
+    _, bound = reference(x, [F32_QUINTIC] * 6, 1.0 - x14, 1.0)
+    assert off <= (15 * STEP * x14 * 3.4445 ** 6 + bound) / float(torch.linalg.norm(want)) + 2.0 ** -24, off
 
 
 @pytest.mark.parametrize("m,n", [(64, 90), (120, 1000), (300, 512), (520, 264)])
