@@ -977,15 +977,23 @@ gc_status gc_embedding_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
                                 dtable, ldd, accumulate, ctx->scratch);
 }
 
+namespace {
+// Sizes of an update: its planes' bytes stay inside 64 bits.
+bool valid_update(int64_t m, int64_t n) {
+  return m >= 0 && n >= 0 && m <= kMaxCols && n <= kMaxCols && m * n <= (int64_t)1 << 48;
+}
+}  // namespace
+
 int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n) {
-  if (m < 0 || n < 0 || m > kMaxCols || n > kMaxCols) return -1;
+  if (!valid_update(m, n)) return -1;
   return gc::orth_scratch_bytes(m, n);
 }
 
 gc_status gc_orthogonalize(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n,
                            int64_t ldg, int steps, const float* coefs, float eps, float scale,
                            void* out, int odtype, int64_t ldo) {
-  if (!ctx || steps < 1 || !coefs || !(eps >= 0.0f) || m > kMaxCols) return GC_ERR_INVALID_ARG;
+  if (!ctx || steps < 1 || !coefs || !(eps >= 0.0f) || !valid_update(m, n))
+    return GC_ERR_INVALID_ARG;
   GC_TRY(check_matrix(m, n, dtype, ldg));
   GC_TRY(check_matrix(m, n, odtype, ldo));
   if (m == 0 || n == 0) return GC_OK;

@@ -814,8 +814,9 @@ GC_API int64_t gc_orthogonalize_scratch_bytes(int64_t m, int64_t n);
  * from it.  A 16-bit g's elements below 2^-31 (bf16) or 2^-28 (fp16) of its largest
  * are held to 2^-39 of that.  A g of zeros gives zeros; one with an infinity or NaN
  * gives NaN everywhere.
- * m, n <= 2^30.  GC_ERR_WORKSPACE when less than
- * gc_orthogonalize_scratch_bytes is reserved.
+ * m, n <= 2^30 and m n <= 2^48.  GC_ERR_WORKSPACE when less than
+ * gc_orthogonalize_scratch_bytes is reserved (two copies of X and one of A and of B
+ * in 4 bytes an element, rows padded to 64).
  */
 GC_API gc_status gc_orthogonalize(gc_ctx* ctx, const void* g, int dtype, int64_t m, int64_t n,
                                   int64_t ldg, int steps, const float* coefs, float eps,
