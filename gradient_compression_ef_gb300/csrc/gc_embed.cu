@@ -16,13 +16,12 @@
 //             lies inside its tokens, else to a partial row; blocks of their own
 //             write zeros to the rows of ids that do not occur
 //   join      the partial rows of a run that crosses chunks, in their order
-// The order of additions is one that ids and sizes alone decide; what is added
-// to the table goes by reductions in L2, one for each place and call.
+// The order of additions is one that ids and sizes alone decide.
 //
 // Measured (plain copy: 6.79 TB/s): 16384 tokens, table of 32768 x 4096 bf16:
 // lookup 28 us (5.9 TB/s), sort 18, sums and zeros 107 (6.2 TB/s), join 8;
 // together 167 (floor 126).  5003 x 1001 fp32 on 4-byte boundaries, added to
-// 50021 rows: 11 + 13 + 20 + 6 us, launches and round trips, not bytes (floor
+// 50021 rows: 11 + 13 + 24 + 7 us, launches and round trips, not bytes (floor
 // 10).  100 tokens x 512: 3.9 + 6.1 us, of which fetching code is a third.
 #include <algorithm>
 #include <type_traits>
@@ -307,8 +306,8 @@ __global__ void __launch_bounds__(kBins)
 // --- sums ----------------------------------------------------------------------------------------
 
 // A lane's sum of a run to columns c .. of a row (c a multiple of 4).  Added by
-// a reduction in L2, which nothing waits for: every place is written once in a
-// call, so there is no order to depend on.
+// a load and a store: every place is written once in a call.  (Reductions in L2
+// would not have to be waited for, but they flush subnormal values to zero.)
 template <int V>
 __device__ __forceinline__ void put_row(float* row, const float2 (&s)[V / 2], float scale,
                                         int64_t c, int64_t cols, bool add) {
@@ -317,23 +316,33 @@ __device__ __forceinline__ void put_row(float* row, const float2 (&s)[V / 2], fl
   for (int j = 0; j < V; ++j) v[j] = __fmul_rn(j & 1 ? s[j / 2].y : s[j / 2].x, scale);
   row += c;
   if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0 && c + V <= cols) {
+    if (add) {
+      float4 old[V / 4];
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      if (add)
-        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(row + j),
-                     "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3])
-                     : "memory");
-      else
-        *reinterpret_cast<float4*>(row + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      for (int j = 0; j < V / 4; ++j) old[j] = __ldcg(reinterpret_cast<const float4*>(row) + j);
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) {
+        v[4 * j] += old[j].x;
+        v[4 * j + 1] += old[j].y;
+        v[4 * j + 2] += old[j].z;
+        v[4 * j + 3] += old[j].w;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<float4*>(row + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     return;
   }
+  if (add) {
+    float old[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (c + j >= cols) continue;
-    if (add) atomicAdd(row + j, v[j]);
-    else row[j] = v[j];
+    for (int j = 0; j < V; ++j) old[j] = c + j < cols ? __ldcg(row + j) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += old[j];
   }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (c + j < cols) row[j] = v[j];
 }
 
 // Zeros to rows v0 + i of the table, i the bits of `todo`; a warp.
@@ -416,7 +425,10 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const __grid_constant__ 
   put_row<V>(a.dtable + (int64_t)key * a.ldd, s, a.scale, c, a.cols, a.accumulate);
 }
 
-template <int DT, bool ALIGNED>
+// ADD: to what is there, which is brought to L2 while the run is summed (5003
+// tokens of 50021 x 1001 fp32, the whole call: 60 -> 56 us).  One kernel for both
+// costs 5 us of 166 where nothing is added.
+template <int DT, bool ALIGNED, bool ADD>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ EmbedArgs a) {
   constexpr int V = Elem<DT>::V, H = V / 2, kDeep = 8;
   after_previous();
@@ -467,7 +479,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
     float* part = a.part + chunk * 2 * a.part_pitch;
     if (opens) put_row<V>(part, s, 1.0f, c, a.cols, false);
     else if (goes_on) put_row<V>(part + a.part_pitch, s, 1.0f, c, a.cols, false);
-    else put_row<V>(a.dtable + (int64_t)run * a.ldd, s, a.scale, c, a.cols, a.accumulate);
+    else  // (asked again at run time: without that the compiler's code takes 74 us, not 56)
+      put_row<V>(a.dtable + (int64_t)run * a.ldd, s, a.scale, c, a.cols, ADD && a.accumulate);
   };
   for (int i0 = 0; i0 < n; i0 += kDeep) {
     uint4 r[kDeep];
@@ -477,8 +490,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
       k[i] = __shfl_sync(0xffffffffu, i0 < 32 ? key[0] : key[1], (i0 + i) & 31);
       const uint32_t t = __shfl_sync(0xffffffffu, i0 < 32 ? tok[0] : tok[1], (i0 + i) & 31);
       r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (k[i] != none)
+      if (k[i] != none) {
         r[i] = load_unit<DT, ALIGNED>(a.table + (int64_t)t * a.tpitch, off, a.row_bytes, a.tend);
+        // what the run's sum will be added to
+        if (ADD && (i == 0 || k[i] != k[i - 1]) && c < a.cols)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dtable + (int64_t)k[i] * a.ldd + c));
+      }
     }
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
@@ -750,10 +767,14 @@ gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
   if (st != GC_OK) return st;
   {
     LaunchScope L(ctx, GC_PHASE_EMBED_SUM);
-    const auto kernel =
-        dtype == GC_F32    ? (al ? embed_sum_kernel<GC_F32, true> : embed_sum_kernel<GC_F32, false>)
-        : dtype == GC_BF16 ? (al ? embed_sum_kernel<GC_BF16, true> : embed_sum_kernel<GC_BF16, false>)
-                           : (al ? embed_sum_kernel<GC_F16, true> : embed_sum_kernel<GC_F16, false>);
+    auto pick = [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      return accumulate ? (al ? embed_sum_kernel<DT, true, true> : embed_sum_kernel<DT, false, true>)
+                        : (al ? embed_sum_kernel<DT, true, false> : embed_sum_kernel<DT, false, false>);
+    };
+    const auto kernel = dtype == GC_F32    ? pick(std::integral_constant<int, GC_F32>{})
+                        : dtype == GC_BF16 ? pick(std::integral_constant<int, GC_BF16>{})
+                                           : pick(std::integral_constant<int, GC_F16>{});
     if (launch_early(kernel, dim3((unsigned)(sum_blocks + a.zero_blocks)), 256, 0, ctx->stream,
                      a) != cudaSuccess)
       return GC_ERR_CUDA;

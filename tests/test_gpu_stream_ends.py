@@ -1,0 +1,54 @@
+"""Embedding at the ends of the range: subnormal sums added to a table.
+
+Sums of a few equal values and one addition to what is there are compared with
+the same fp32 operations on the host, bit for bit (subnormals kept).
+"""
+import numpy as np
+import pytest
+
+from tests.gpu_helpers import torch_cuda
+from tests.test_gpu_backward import matrix, out_matrix, pad_untouched
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gc():
+    torch_cuda()
+    from gradient_compression_ef_gb300 import gc as binding
+    return binding
+
+
+@pytest.fixture(scope="module")
+def ctx(gc):
+    with gc.Context(0) as c:
+        c.reserve_scratch(64 << 20)
+        yield c
+
+
+@pytest.mark.parametrize("tokens,vocab", [(3, 5), (200, 40), (1000, 7), (1000, 900), (9000, 3000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("cols,pad", [(64, 0), (33, 0), (300, 4), (4096, 0)])
+def test_added_subnormals(gc, ctx, tokens, vocab, dtype, cols, pad):
+    """Subnormal sums, and subnormal values in the rows that they are added to."""
+    import torch
+    r = np.random.default_rng(tokens + cols)
+    scale = 2.0 ** -120 if dtype == "f16" else 1.0
+    dy, _, _ = matrix(r.integers(-8, 9, (tokens, cols)) * (2.0 ** -20 if dtype == "f16" else 2.0 ** -133), dtype, pad)
+    ids = torch.from_numpy(r.integers(0, vocab, tokens)).cuda()
+    first, _ = out_matrix(vocab, cols, "f32", pad)
+    gc.embedding_wgrad(ctx, dy, ids, scale, first)
+    sums = first.cpu().numpy()
+    assert ((sums != 0) & (np.abs(sums) < 2.0 ** -126)).any()
+    base = (r.integers(-2 ** 20, 2 ** 20, (vocab, cols)) * 2.0 ** -149).astype(np.float32)
+    base[:, ::3] = r.integers(-3, 4, base[:, ::3].shape) * np.float32(2.0 ** -126)
+    d, buf = out_matrix(vocab, cols, "f32", pad)
+    d.copy_(torch.from_numpy(base))
+    gc.embedding_wgrad(ctx, dy, ids, scale, d, accumulate=True)
+    used = np.zeros((vocab, 1), bool)
+    used[ids.cpu().numpy()] = True
+    want = np.where(used, base + sums, base)
+    got = d.cpu().numpy()
+    assert np.array_equal(got, want), "%d differ" % int((got != want).sum())
+    pad_untouched(buf, cols)
+    ctx.check()
