@@ -966,7 +966,7 @@ gc_status gc_embedding_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
   GC_TRY(check_ids(ids, itype, tokens, vocab));
   GC_TRY(check_matrix(tokens, cols, dtype, lddy));
   GC_TRY(check_matrix(vocab, cols, GC_F32, ldd));
-  const bool used = tokens > 0 && cols > 0 && vocab > 0;
+  const bool used = tokens > 0 && cols > 0;  // a table without rows: ids are looked at
   GC_TRY(check_buf(dy, used));
   GC_TRY(check_floats(dtable, cols > 0 && vocab > 0));
   if (used && ctx->scratch_bytes < gc::embed_scratch_bytes(tokens, vocab, cols))

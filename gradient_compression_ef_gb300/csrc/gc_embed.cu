@@ -719,9 +719,9 @@ gc_status launch_embed_wgrad(gc_ctx* ctx, const void* dy, int64_t lddy, int dtyp
                              int itype, int64_t tokens, int64_t pad, int64_t vocab, int64_t cols,
                              float scale, float* dtable, int64_t ldd, int accumulate,
                              void* scratch) {
-  if (vocab == 0 || cols == 0) return GC_OK;
+  if (cols == 0) return GC_OK;
   if (tokens == 0) {
-    if (accumulate) return GC_OK;
+    if (accumulate || vocab == 0) return GC_OK;
     return cudaMemset2DAsync(dtable, ldd * 4, 0, cols * 4, vocab, ctx->stream) == cudaSuccess
                ? GC_OK
                : GC_ERR_CUDA;

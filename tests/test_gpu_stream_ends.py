@@ -1,4 +1,5 @@
-"""Embedding at the ends of the range: subnormal sums added to a table.
+"""Embedding at the ends of the range: subnormal sums added to a
+table, tables without rows.
 
 Sums of a few equal values and one addition to what is there are compared with
 the same fp32 operations on the host, bit for bit (subnormals kept).
@@ -52,3 +53,23 @@ def test_added_subnormals(gc, ctx, tokens, vocab, dtype, cols, pad):
     assert np.array_equal(got, want), "%d differ" % int((got != want).sum())
     pad_untouched(buf, cols)
     ctx.check()
+
+
+@pytest.mark.parametrize("tokens", [3, 300, 9000])
+def test_ids_of_a_table_without_rows(gc, ctx, tokens):
+    """Every id that is not padding is outside it: the gradient's call says so too."""
+    import torch
+    ids = torch.full((tokens,), 4, device="cuda")
+    table = torch.empty(0, 8, device="cuda")
+    y = torch.ones(tokens, 8, device="cuda")
+    for accumulate in (False, True):
+        gc.embedding_wgrad(ctx, y, ids, 1.0, table, accumulate=accumulate)
+        with pytest.raises(gc.GCError) as e:
+            ctx.check()
+        assert e.value.status == gc.ERR_DEVICE_CHECK
+        gc.embedding_wgrad(ctx, y, ids, 1.0, table, pad=4, accumulate=accumulate)
+        ctx.check()
+    gc.embedding_forward(ctx, ids, table, 1.0, y)
+    assert bool((y == 0).all())
+    with pytest.raises(gc.GCError):
+        ctx.check()
