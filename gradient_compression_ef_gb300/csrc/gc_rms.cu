@@ -105,9 +105,11 @@ __device__ __forceinline__ Rstd rstd_of(float sum, const Count& n, float eps) {
 }
 
 // y's unit from h's: h rstd as two terms, times gamma, rounded once to fp32.
-template <int DT>
-__device__ __forceinline__ uint4 scale_unit(const uint4& r, const Rstd& rstd,
-                                            const float (&g)[Elem<DT>::V]) {
+// CLAMP: the small term is kept finite: where gamma or rstd is infinite it would
+// be a NaN, or an infinity of the other sign, beside the large one.
+template <int DT, bool CLAMP>
+__device__ __forceinline__ uint4 scaled(const uint4& r, const Rstd& rstd,
+                                        const float (&g)[Elem<DT>::V]) {
   constexpr int H = Elem<DT>::V / 2;
   float2 v[H];
   unpack2<DT>(r, v);
@@ -116,10 +118,34 @@ __device__ __forceinline__ uint4 scale_unit(const uint4& r, const Rstd& rstd,
     const float2 w = make_float2(g[2 * j], g[2 * j + 1]);
     const float2 p = __fmul2_rn(v[j], both(rstd.hi));
     const float2 minus = make_float2(-p.x, -p.y);
-    const float2 q = __ffma2_rn(v[j], both(rstd.lo), __ffma2_rn(v[j], both(rstd.hi), minus));
-    v[j] = __ffma2_rn(p, w, __fmul2_rn(q, w));
+    float2 q = __ffma2_rn(v[j], both(rstd.lo), __ffma2_rn(v[j], both(rstd.hi), minus));
+    q = __fmul2_rn(q, w);
+    if (CLAMP)
+      q = make_float2(fminf(fmaxf(q.x, -FLT_MAX), FLT_MAX), fminf(fmaxf(q.y, -FLT_MAX), FLT_MAX));
+    v[j] = __ffma2_rn(p, w, q);
   }
   return pack2<DT>(v);
+}
+// Whether a thread's parameters are all finite.
+template <int V>
+__device__ __forceinline__ bool all_finite(const float (&g)[V]) {
+  bool yes = true;
+#pragma unroll
+  for (int j = 0; j < V; ++j) yes = yes && fabsf(g[j]) <= FLT_MAX;
+  return yes;
+}
+template <int K, int V>
+__device__ __forceinline__ bool all_finite(const float (&g)[K][V]) {
+  bool yes = true;
+#pragma unroll
+  for (int i = 0; i < K; ++i) yes = yes && all_finite(g[i]);
+  return yes;
+}
+// (Clamping everywhere: 16384 x 4096 bf16, forward and backward, 229 -> 232 us.)
+template <int DT>
+__device__ __forceinline__ uint4 scale_unit(const uint4& r, const Rstd& rstd,
+                                            const float (&g)[Elem<DT>::V], bool finite) {
+  return finite && rstd.hi <= FLT_MAX ? scaled<DT, false>(r, rstd, g) : scaled<DT, true>(r, rstd, g);
 }
 
 // A row per team: a warp (U units per lane), or a block.
@@ -146,6 +172,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
 #pragma unroll
   for (int i = 0; i < U; ++i)
     load_params<V>(g[i], a.gamma, a.ptype, c0 + i * 32 * V, a.cols, 1.0f);
+  const bool finite = all_finite(g);
   for (; row < a.rows; row += step) {
     uint4 h[U];
 #pragma unroll
@@ -167,7 +194,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
                       c0 + i * 32 * V, a.codes_pitch);
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i) h[i] = scale_unit<DT>(h[i], rstd, g[i]);
+    for (int i = 0; i < U; ++i) h[i] = scale_unit<DT>(h[i], rstd, g[i], finite);
     if (a.y) store_run<DT, ALIGNED>(a.y + row * a.ypitch, at, inner, a.row_bytes, h);
     if (a.ycodes) {
 #pragma unroll
@@ -209,7 +236,7 @@ __global__ void __launch_bounds__(1024)
                       a.codes_pitch);
       float g[V];
       load_params<V>(g, a.gamma, a.ptype, c, a.cols, 1.0f);
-      const uint4 y = scale_unit<DT>(h, rstd, g);
+      const uint4 y = scale_unit<DT>(h, rstd, g, all_finite(g));
       if (a.y) store_unit<DT, ALIGNED>(a.y + row * a.ypitch, off, a.row_bytes, y);
       if (a.ycodes)
         save_unit<DT>(a.ycodes + row * a.codes_pitch, a.yscales + row * a.scales_pitch, y, c,
@@ -334,6 +361,7 @@ __global__ void __maxnreg__(REGS)
     const int64_t u = u1 + i * 32;
     load_params<V>(g[i], a.gamma, a.ptype, u * V, a.cols, 1.0f);
   }
+  const bool finite = all_finite(g);
   bool ok = true;
   RingPos ring;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -374,7 +402,7 @@ __global__ void __maxnreg__(REGS)
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       keep_packed(h[i]);
-      h[i] = scale_unit<DT>(h[i], rstd, g[i]);
+      h[i] = scale_unit<DT>(h[i], rstd, g[i], finite);
     }
     if (a.y) put_units<DT, ROWS>(a.y + row * a.ypitch, u0, a.row_bytes, h);
     if (a.ycodes) {

@@ -1,5 +1,5 @@
-"""Embedding at the ends of the range: subnormal sums added to a
-table, tables without rows.
+"""Embedding and RMS norm at the ends of the range: subnormal sums added to a
+table, tables without rows, infinite parameters.
 
 Sums of a few equal values and one addition to what is there are compared with
 the same fp32 operations on the host, bit for bit (subnormals kept).
@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 
 from tests.gpu_helpers import torch_cuda
-from tests.test_gpu_backward import matrix, out_matrix, pad_untouched
+from tests.test_gpu_backward import ckpt, f64, matrix, out_matrix, pad_untouched
+from tests.test_gpu_rmsnorm import EPS, same_ckpt
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,37 @@ def test_ids_of_a_table_without_rows(gc, ctx, tokens):
     assert bool((y == 0).all())
     with pytest.raises(gc.GCError):
         ctx.check()
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 40), (300, 200), (5, 700), (5, 4100), (300, 4099), (300, 4096), (200, 11008),
+                                       (4, 20001)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("ptype", ["f32", "bf16", "f16"])
+def test_infinite_parameters(gc, ctx, rows, cols, dtype, ptype):
+    """y is infinite, with h's sign times gamma's, where gamma is; NaN where h is 0 or gamma NaN; elsewhere what it is
+    without such parameters."""
+    import torch
+    r = np.random.default_rng(cols)
+    v = r.standard_normal((rows, cols))
+    v[:, 0] = 0.0
+    x, _, _ = matrix(v, dtype, 3 if cols % 2 else 0)
+    pt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[ptype]
+    gamma = torch.from_numpy(1.0 + 0.3 * r.standard_normal(cols)).to(pt).cuda()
+    plain, _ = out_matrix(rows, cols, dtype)
+    rstd = torch.empty(rows, device="cuda")
+    gc.rmsnorm_forward(ctx, x, None, gamma, EPS, None, plain, rstd)
+    inf = float("inf")
+    bad = {0: inf, 1: inf, cols // 2: -inf, cols - 2: inf, cols - 1: float("nan"), cols // 3: -inf}
+    for c, b in bad.items():
+        gamma[c] = b
+    y, _ = out_matrix(rows, cols, dtype)
+    yc = ckpt(rows, cols)
+    gc.rmsnorm_forward(ctx, x, None, gamma, EPS, None, y, rstd, None, None, *yc)
+    want = plain.clone()
+    for c, b in bad.items():
+        want[:, c] = x[:, c] * b
+    assert bool(want[:, 0].isnan().all()) and bool(want[:, 1].isinf().all())
+    assert torch.equal(y.isnan(), want.isnan())
+    assert torch.equal(y.nan_to_num(0.0, inf, -inf), want.nan_to_num(0.0, inf, -inf))
+    same_ckpt(yc, f64(y))
+    ctx.check()
