@@ -8,7 +8,8 @@
 // all that have it.  More are sorted as (id, token) pairs, stable, and runs of
 // one id are summed:
 //   sort      up to 8192 tokens: each pair's place is the number of pairs
-//             before it, counted (5003 tokens 13 us, two radix passes 17);
+//             before it, counted (1000, 2500, 5003, 8192 tokens, each launch
+//             timed by events: 7, 8, 15, 21 us; two radix passes 23 to 24);
 //             more: radix passes of up to 9 bits, each of which makes the next
 //             one's counts on its way (16384 tokens 18 us)
 //   sum       a warp takes 8 to 64 sorted tokens and 512 bytes of their rows,
@@ -19,7 +20,8 @@
 // The order of additions is one that ids and sizes alone decide.
 //
 // Measured (plain copy: 6.79 TB/s): 16384 tokens, table of 32768 x 4096 bf16:
-// lookup 28 us (5.9 TB/s), sort 18, sums and zeros 107 (6.2 TB/s), join 8;
+// lookup 28 us (5.9 TB/s; a table in another type, fp32 to bf16 or back, 72 to 76,
+// 4.8 to 4.9), sort 18, sums and zeros 107 (6.2 TB/s), join 8;
 // together 167 (floor 126).  5003 x 1001 fp32 on 4-byte boundaries, added to
 // 50021 rows: 11 + 13 + 24 + 7 us, launches and round trips, not bytes (floor
 // 10).  100 tokens x 512: 3.9 + 6.1 us, of which fetching code is a third.
@@ -180,7 +182,7 @@ __device__ __forceinline__ uint32_t key_of(const EmbedArgs& a, int64_t t) {
 // A block places 32 tokens: warp w counts, for the 32 tokens (one per lane),
 // the pairs of its share of all tokens that come before.
 __global__ void __launch_bounds__(1024) embed_count_kernel(const __grid_constant__ EmbedArgs a) {
-  extern __shared__ __align__(16) uint32_t keys[];  // all keys, then the warps' counts
+  extern __shared__ __align__(16) uint32_t keys[];  // all keys
   const int n = (int)a.tokens, padded = (int)round_up(n, 128);
   __shared__ uint32_t before[32][33];
   let_next_begin();

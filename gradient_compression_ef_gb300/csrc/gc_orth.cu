@@ -45,14 +45,14 @@
 // over block by block and adds in registers, rounded to nearest.  (By two or four
 // blocks: 2 and 4 % faster, with two and five times the error.)
 //
-// Measured: 4096 x 4096 fp32, five steps 2765 to 2840 us from card to card (4.12
-// Tflop in fp16 products: 1450 to 1490 Tflop/s; cuBLAS bf16 1912 for a burst,
+// Measured: 4096 x 4096 fp32, five steps 2830 to 2920 us from card to card (4.12
+// Tflop in fp16 products: 1410 to 1460 Tflop/s; cuBLAS bf16 1912 for a burst,
 // 1698 sustained): the board's power limit lowers the clock to 1.75 GHz within a
 // product, where a block of 256 x 256 x 64 x 3 takes 0.897 us, 98 % of what that
 // clock gives; the rest is the last round's idle pairs and a tile's epilogue, 3
-// to 5 us.  11008 x 4096 bf16 5793 us.  1001 x 2051: 230 us, 15 dependent
-// launches of 13 us, a third of it on the tensor cores.  128 x 64: 29 us in one
-// kernel.
+// to 5 us.  11008 x 4096 bf16 5730 to 5900 us (8.60 Tflop).  1001 x 2051: 233 to
+// 238 us, 15 dependent launches of 13 us, a third of it on the tensor cores.  128
+// x 64: 29 us in one kernel.
 #include <cudaTypedefs.h>
 
 #include <algorithm>

@@ -10,7 +10,8 @@
 //
 // Each input is read once; sums are fp32, in an order that sizes alone decide.
 // Bound by memory: forward 2 inputs and up to 2 outputs with their codes,
-// backward 3 inputs and one output, 10 to 20 instructions per element.
+// backward 3 inputs and one output, 40 and 25 instructions per element (fp32 rows
+// off 16-byte boundaries 78 and 51).
 //   more rows than SMs, 2 KB  a block walks over rows that bulk copies bring
 //   to 11776 (forward 15872)  into a ring of stages, a producer warp ahead of
 //   columns, two rows fit     it; 16 columns per thread, gamma and the column
@@ -21,10 +22,11 @@
 //   wider still               the row is read again from L2
 //
 // Measured (plain copy: 6.79 TB/s), forward and backward: 16384 x 4096 bf16 with
-// checkpoints 109 us (6.2 TB/s) and 76 + 5 (6.2); 3001 x 4099 fp32 on 4-byte
+// checkpoints 110 us (6.1 TB/s) and 76 + 5 (6.2); 3001 x 4099 fp32 on 4-byte
 // boundaries 50 (4.1) and 44 + 5 (4.5), the shifting of each unit into place;
-// 2048 x 11008 fp16 43 (4.2) and 40 + 6 (4.0), one block per SM, whose sum over
-// 22 warps nothing hides.
+// 2048 x 11008 fp16 44 (4.1) and 40 + 6 (4.0), one block per SM, whose sum over
+// 22 warps nothing hides.  Without the ring, bf16 with checkpoints: 4096 x 16384
+// 166 (4.1) and 163 (2.9), 4096 x 12288 backward 146 (2.4), 64 x 4096 forward 8.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
