@@ -23,8 +23,9 @@
 //
 // An input in 16 bits is held in one plane, times the power of two that brings
 // its largest element to 2^14 .. 2^15 (what X_0 is beyond that is one more factor,
-// f, put in likewise): the first step's A takes one product, its B X two.  That is exact for elements down to 2^-31 (bf16) or
-// 2^-28 (fp16) of the largest; those below are held to 2^-39 of it.
+// f, put in likewise): the first step's A takes one product, its B X two.  That is
+// exact for elements down to 2^-31 (bf16) or 2^-28 (fp16) of the largest; those
+// below are held to 2^-39 of it.
 //
 // The result's type decides the last rounding alone: a bf16 result is the fp32
 // one, rounded.  (X and B of the last step with 11 bits took 13 % off 11008 x
@@ -112,9 +113,9 @@ __device__ __forceinline__ float grown(float r, float a, float b, float c) {
   return r * fmaf(q, fmaf(q, fabsf(c), fabsf(b)), fabsf(a));
 }
 __device__ __forceinline__ void next_range(Range* now, Range* next, float a, float b, float c) {
-  const float r = grown(now->r, a, b, c);
+  const float r = grown(__ldcg(&now->r), a, b, c);
   const int e = exponent_of(r);
-  now->apply = now->f * power2(now->e - e);
+  now->apply = __ldcg(&now->f) * power2(__ldcg(&now->e) - e);
   *next = make_range(1.0f, r, e);
 }
 
